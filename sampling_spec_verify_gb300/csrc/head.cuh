@@ -1,0 +1,465 @@
+// The vocabulary head's losses without its logits: matrix products on the
+// tensor cores with the softmax in their epilogues.
+//
+//   z = X W^T / T                 X [N, H] hidden states, W [V, H] head
+//   pass 1   per 256-token tile and row: maximum and sum of 2^z', z' = z log2(e)
+//   pass 2   per piece of the vocabulary, C tokens wide:
+//     D  = (softmax(z) - t) w     recomputed from X and W, 16 bits, [N, C]
+//     dX += D W_piece             fp32, one partial per split of the piece
+//     dW_piece = D^T X
+//
+// D is rounded to the operands' 16-bit type because the products that consume
+// it take that type: one rounding of half a step per entry, the size of the
+// rounding of a 16-bit result.  Row weights are divided by the largest one and,
+// for fp16, D is scaled by 2^15, so that probabilities down to 2^-29 keep
+// their precision in fp16's short exponent.
+//
+// One kernel does all four products.  Bound: tensor cores (2 N V H operations
+// a product).  A CTA pair owns a 256 x 256 tile: each CTA stages 128 rows of A
+// and 128 of B per 64-deep step (32 KB, six stages), one thread of the even
+// CTA issues tcgen05.mma for both, accumulators take half of tensor memory so
+// that the epilogue of a tile overlaps the products of the next.
+#pragma once
+
+#include "loss_common.cuh"
+#include "tc05.cuh"
+
+namespace ssv {
+
+constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
+constexpr int kStages = 6;
+constexpr int kStageBytes = 2 * 128 * kTileK * 2;  // A and B halves of a CTA
+constexpr int kEpiWarps = 4;
+constexpr int kHeadThreads = 64 + 32 * kEpiWarps;
+constexpr int kStageOut = 4096;  // per epilogue warp and buffer: 32 rows x 128 bytes
+constexpr int kHeadSmem = kStages * kStageBytes + kEpiWarps * 2 * kStageOut + 1024;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+enum HeadOp {
+  kHeadNorm,    // pass 1: row statistics of X W^T per tile
+  kHeadGrad,    // D
+  kHeadHidden,  // dX partials
+  kHeadWeight   // dW
+};
+
+struct HeadParams {
+  int M, N, K;       // rows, columns, depth of the product
+  int tiles_m, tiles_n, splits;
+  int ksteps;        // 64-deep steps of the whole product
+  int b_off;         // the piece's start among the rows of B
+  int bf16;
+  float s;           // log2(e) / T
+  // kHeadNorm
+  float2* part;      // [tiles_n, M]
+  // kHeadGrad
+  const float* lse2; // [M] log2 of the normaliser
+  const float* weight;
+  const uint8_t* keep;
+  float store_scale;
+  // kHeadHidden
+  int first;         // store (not add) the partials
+  int slot_rows;     // rows between the partials of two splits
+  const LossScalars* scalars;
+  uint32_t* status;
+};
+
+template <HeadOp OP>
+struct HeadTraits {  // operand rows run along K, or (mn) along the other dimension
+  static constexpr bool a_mn = OP == kHeadWeight;
+  static constexpr bool b_mn = OP == kHeadHidden || OP == kHeadWeight;
+};
+
+// Tile `i` of the launch: bands of eight tile rows, down the rows first, so
+// that the tiles in flight share operands in L2.
+struct TileAt {
+  int m, n, split;
+};
+__device__ __forceinline__ TileAt tile_at(int i, int tiles_m, int tiles_n) {
+  const int per = tiles_m * tiles_n;
+  TileAt t;
+  t.split = i / per;
+  i -= t.split * per;
+  constexpr int kBand = 8;
+  const int band = i / (kBand * tiles_n);
+  const int rows = min(kBand, tiles_m - band * kBand);
+  i -= band * kBand * tiles_n;
+  t.m = band * kBand + i % rows;
+  t.n = i / rows;
+  return t;
+}
+
+// Writes 16 bytes of a row into a 128-byte-swizzled staging tile.
+__device__ __forceinline__ void stage_write(uint32_t base, int row, int unit, uint32_t a, uint32_t b, uint32_t c,
+                                            uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + row * 128 + ((unit ^ (row & 7)) << 4)), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack16(float a, float b, bool bf16) {
+  return bf16 ? Elem<__nv_bfloat16>::pack(a, b) : Elem<__half>::pack(a, b);
+}
+
+// OUT32: the result of kHeadWeight is fp32.
+template <HeadOp OP, bool OUT32>
+__global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
+    head_kernel(const __grid_constant__ HeadParams P, const __grid_constant__ CUtensorMap map_a,
+                const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_out) {
+  using T = HeadTraits<OP>;
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
+  __shared__ uint32_t tmem_slot;
+
+  const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const uint32_t tiles0 = (smem_addr(raw) + 1023u) & ~1023u;
+  const uint32_t out0 = tiles0 + kStages * kStageBytes;
+  const uint32_t bar_full = smem_addr(bars), bar_empty = bar_full + 8 * kStages;
+  const uint32_t bar_done = bar_empty + 8 * kStages;  // accumulators written, two
+  const uint32_t bar_free = bar_done + 16;            // accumulators read, two
+  const uint32_t bar_drain = bar_free + 16;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar_full + 8 * i, 1);
+      mbar_init(bar_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_done + 8 * i, 1);
+      mbar_init(bar_free + 8 * i, 2 * kEpiWarps);
+    }
+    mbar_init(bar_drain, 1);
+    fence_mbar_init();
+    prefetch_map(&map_a);
+    prefetch_map(&map_b);
+  }
+  if (wid == 0) {
+    tmem_alloc_pair(smem_addr(&tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  const int tiles = P.tiles_m * P.tiles_n * P.splits;
+  const int clusters = gridDim.x / 2, first_tile = blockIdx.x / 2;
+
+  if (wid == 0) {
+    // ---- loads: one thread of each CTA ----
+    if (lane == 0) {
+      const uint32_t full0 = map_rank(bar_full, 0);
+      uint32_t step = 0;
+      bool ok = true;
+      for (int i = first_tile; ok && i < tiles; i += clusters) {
+        const TileAt t = tile_at(i, P.tiles_m, P.tiles_n);
+        const int k0 = (int)((long long)P.ksteps * t.split / P.splits);
+        const int k1 = (int)((long long)P.ksteps * (t.split + 1) / P.splits);
+        const int row_a = t.m * kTileM + (int)rank * 128, row_b = t.n * kTileN + (int)rank * 128;
+        for (int k = k0; k < k1; ++k, ++step) {
+          const uint32_t s = step % kStages, use = step / kStages;
+          if (use > 0 && !mbar_wait_bounded(bar_empty + 8 * s, (use - 1) & 1u, kWaitNs)) {
+            ok = false;
+            break;
+          }
+          const uint32_t a = tiles0 + s * kStageBytes, b = a + kStageBytes / 2;
+          if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * s, 2 * kStageBytes);
+          const uint32_t full = full0 + 8 * s;
+          if (T::a_mn) {
+            tma_load_pair(a, &map_a, row_a, k * kTileK, full);
+            tma_load_pair(a + 8192, &map_a, row_a + 64, k * kTileK, full);
+          } else {
+            tma_load_pair(a, &map_a, k * kTileK, row_a, full);
+          }
+          if (T::b_mn) {
+            tma_load_pair(b, &map_b, row_b, P.b_off + k * kTileK, full);
+            tma_load_pair(b + 8192, &map_b, row_b + 64, P.b_off + k * kTileK, full);
+          } else {
+            tma_load_pair(b, &map_b, k * kTileK, P.b_off + row_b, full);
+          }
+        }
+      }
+      if (!ok) {
+        raise(P.status, SPEC_DEV_TIMEOUT);
+        // the copies in flight of the pair end on the even CTA's barriers
+        if (rank == 0)
+          for (int i = 0; i < kStages && step > 0; ++i, --step)
+            mbar_wait_bounded(bar_full + 8 * ((step - 1) % kStages), ((step - 1) / kStages) & 1u, 10000000ull);
+      }
+    }
+  } else if (wid == 1) {
+    // ---- products: one thread of the even CTA ----
+    if (rank == 0 && lane == 0) {
+      const uint32_t idesc = mma_idesc(P.bf16 != 0, T::a_mn, T::b_mn);
+      constexpr uint64_t da = T::a_mn ? smem_desc_base(8192, 1024) : smem_desc_base(16, 1024);
+      constexpr uint64_t db = T::b_mn ? smem_desc_base(8192, 1024) : smem_desc_base(16, 1024);
+      constexpr uint32_t ka = T::a_mn ? 2048 : 32, kb = T::b_mn ? 2048 : 32;  // bytes of 16 K steps
+      uint32_t step = 0, it = 0;
+      bool ok = true;
+      for (int i = first_tile; ok && i < tiles; i += clusters, ++it) {
+        const TileAt t = tile_at(i, P.tiles_m, P.tiles_n);
+        const int k0 = (int)((long long)P.ksteps * t.split / P.splits);
+        const int k1 = (int)((long long)P.ksteps * (t.split + 1) / P.splits);
+        const uint32_t acc = it & 1, use = it >> 1;
+        if (use > 0 && !mbar_wait_bounded(bar_free + 8 * acc, (use - 1) & 1u, kWaitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + acc * kTileN;
+        for (int k = k0; k < k1; ++k, ++step) {
+          const uint32_t s = step % kStages;
+          if (!mbar_wait_bounded(bar_full + 8 * s, (step / kStages) & 1u, kWaitNs)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = tiles0 + s * kStageBytes, b = a + kStageBytes / 2;
+#pragma unroll
+          for (int j = 0; j < kTileK / 16; ++j)
+            mma_pair(d, smem_desc(da, a + j * ka), smem_desc(db, b + j * kb), idesc, (k > k0 || j > 0) ? 1u : 0u);
+          mma_commit_pair(bar_empty + 8 * s);
+        }
+        if (ok) mma_commit_pair(bar_done + 8 * acc);
+      }
+      if (!ok) {
+        raise(P.status, SPEC_DEV_TIMEOUT);
+        mma_commit_pair(bar_drain);
+        mbar_wait_bounded(bar_drain, 0, 10000000ull);
+      }
+    }
+  } else {
+    // ---- epilogue: a thread per row of this CTA's half of the tile ----
+    const int quad = wid & 3;  // the tensor-memory lanes that this warp may read
+    const uint32_t stage = out0 + (wid - 2) * 2 * kStageOut;
+    const uint32_t free0 = map_rank(bar_free, 0);
+    uint32_t it = 0, buf = 0;
+    for (int i = first_tile; i < tiles; i += clusters, ++it) {
+      const TileAt t = tile_at(i, P.tiles_m, P.tiles_n);
+      const uint32_t acc = it & 1, use = it >> 1;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_done + 8 * acc, use & 1u, kWaitNs))) {
+        raise(P.status, SPEC_DEV_TIMEOUT);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t src = tmem + acc * kTileN + ((uint32_t)(quad * 32) << 16);
+      const int row0 = t.m * kTileM + (int)rank * 128 + quad * 32, row = row0 + lane;
+      const int col0 = t.n * kTileN;
+
+      if constexpr (OP == kHeadNorm) {
+        // running maximum and sum over the tile's columns, in powers of two
+        float m = -INFINITY, sum = 0.0f;
+        for (int c = 0; c < kTileN; c += 32) {
+          float v[32];
+          tmem_load32(src + c, v);
+          float cm = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            v[j] = col0 + c + j < P.N ? v[j] * P.s : -INFINITY;
+            cm = max_nan(cm, v[j]);
+          }
+          const float nm = max_nan(m, cm);
+          if (nm > -INFINITY) {
+            float a = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) a += ex2(v[j] - nm);
+            sum = sum * ex2(m - nm) + a;
+            m = nm;
+          } else if (!(nm < INFINITY)) {
+            m = nm;  // NaN passes on
+          }
+        }
+        if (row < P.M) P.part[(long long)t.n * P.M + row] = make_float2(m, sum);
+      } else {
+        float lse = 0.0f, cf = 0.0f, mul = 1.0f;
+        if constexpr (OP == kHeadGrad) {
+          if (row < P.M && P.keep[row]) {
+            lse = P.lse2[row];
+            cf = (P.weight ? P.weight[row] : 1.0f) * P.scalars->inv_wmax * P.store_scale;
+          }
+        } else if constexpr (OP == kHeadWeight) {
+          mul = P.scalars->grad_mul;
+        }
+        constexpr bool wide = OP == kHeadHidden || (OP == kHeadWeight && OUT32);  // fp32 out
+        constexpr int kCols = wide ? 32 : 64;  // columns of 128 bytes
+        for (int c = 0; c < kTileN; c += kCols) {
+          if (col0 + c >= P.N) break;
+          const uint32_t dst = stage + buf * kStageOut;
+          buf ^= 1;
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < kCols; h += 32) {
+            float v[32];
+            tmem_load32(src + c + h, v);
+            if constexpr (OP == kHeadGrad) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = cf != 0.0f ? ex2(fmaf(v[j], P.s, -lse)) * cf : 0.0f;
+            } else if constexpr (OP == kHeadWeight) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] *= mul;
+            }
+            if constexpr (wide) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4)
+                stage_write(dst, lane, j / 4, __float_as_uint(v[j]), __float_as_uint(v[j + 1]),
+                            __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3]));
+            } else {
+              const bool bf = P.bf16 != 0;
+#pragma unroll
+              for (int j = 0; j < 32; j += 8)
+                stage_write(dst, lane, (h + j) / 8, pack16(v[j], v[j + 1], bf), pack16(v[j + 2], v[j + 3], bf),
+                            pack16(v[j + 4], v[j + 5], bf), pack16(v[j + 6], v[j + 7], bf));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < P.M) {
+              const int y = OP == kHeadHidden ? t.split * P.slot_rows + row0 : row0;
+              if (OP == kHeadHidden && !P.first)
+                tma_reduce_add(&map_out, dst, col0 + c, y);
+              else
+                tma_store(&map_out, dst, col0 + c, y);
+            }
+            bulk_commit();
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(free0 + 8 * acc);
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (wid == 0) tmem_free_pair(tmem, 512);
+}
+
+// ---- the listed tokens -----------------------------------------------------------
+
+// Raw logits of the listed tokens, zi[n, i] = X_n . W_id: one warp each, fp32
+// sums of exact products.
+template <class E>
+__global__ void __launch_bounds__(256) listed_logits_kernel(const E* x, const E* w, const int32_t* ids,
+                                                            const uint8_t* keep, int N, int H, int k, float* zi) {
+  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (i >= (long long)N * k) return;
+  const long long n = i / k;
+  const int id = ids[i];
+  float acc = 0.0f;
+  if (keep[n] && id >= 0) {
+    const uint4* a = reinterpret_cast<const uint4*>(x + n * H);
+    const uint4* b = reinterpret_cast<const uint4*>(w + (long long)id * H);
+    for (int j = lane; j < H / 8; j += 32) {
+      float fa[8], fb[8];
+      Elem<E>::unpack(a[j], fa);
+      Elem<E>::unpack(b[j], fb);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc = fmaf(fa[e], fb[e], acc);
+    }
+    acc = warp_sum(acc);
+  }
+  if (lane == 0) zi[i] = acc;
+}
+
+// Puts the listed tokens' entries into a piece of D (tokens [v0, v0 + C)).
+struct ListedParams {
+  const int32_t* ids;
+  const float* t;
+  const float* zi;
+  const float* lse2;
+  const float* weight;
+  const uint8_t* keep;
+  const LossScalars* scalars;
+  int N, k, v0, C;
+  long long ld;
+  double s;  // log2(e) / T
+  float store_scale;
+};
+template <class E>
+__global__ void __launch_bounds__(256) listed_grads_kernel(const ListedParams P, E* d) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (long long)P.N * P.k) return;
+  const long long n = i / P.k;
+  const int id = P.ids[i];
+  if (id < P.v0 || id >= P.v0 + P.C || !P.keep[n]) return;
+  const float cf = (P.weight ? P.weight[n] : 1.0f) * P.scalars->inv_wmax * P.store_scale;
+  const float q = exp2f((float)((double)P.zi[i] * P.s - (double)P.lse2[n]));
+  d[n * P.ld + (id - P.v0)] = Elem<E>::from_f32(cf == 0.0f ? 0.0f : (q - P.t[i]) * cf);
+}
+
+// ---- normalisers, row losses, their sum --------------------------------------------
+
+// 32 rows per CTA: the eight warps share the tiles, lane = row; then a warp per row.
+__global__ void __launch_bounds__(256) head_finish_kernel(const FinishParams P, const float2* part, int tiles_n,
+                                                          float* lse_out, float* lse2) {
+  __shared__ float2 sh[8][32];
+  __shared__ double lse_sh[32];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long base = (long long)blockIdx.x * 32, n = base + lane;
+  float m = -INFINITY, sum = 0.0f;
+  if (n < P.N) {
+    for (int t = w; t < tiles_n; t += 8) {
+      const float2 v = __ldcs(part + (long long)t * P.N + n);
+      const float nm = max_nan(m, v.x);
+      if (nm > -INFINITY) {
+        sum = (m > -INFINITY ? sum * exp2f(m - nm) : 0.0f) + (v.x > -INFINITY ? v.y * exp2f(v.x - nm) : 0.0f);
+        m = nm;
+      } else if (!(nm < INFINITY)) {
+        m = nm;
+      }
+    }
+  }
+  sh[w][lane] = make_float2(m, sum);
+  __syncthreads();
+  if (w == 0 && n < P.N) {
+    m = -INFINITY;
+    for (int i = 0; i < 8; ++i) m = max_nan(m, sh[i][lane].x);
+    double z = 0.0;
+    for (int i = 0; i < 8; ++i)
+      if (sh[i][lane].x > -INFINITY) z += (double)sh[i][lane].y * exp2((double)(sh[i][lane].x - m));
+    const bool bad = !(m < INFINITY) || !(m > -INFINITY);
+    const double l2 = bad ? NAN : (double)m + log2(z);
+    if (bad && P.keep[n]) raise(P.status, SPEC_DEV_BAD_LOGITS);
+    const double l = l2 * 0.69314718055994530942;
+    lse_sh[lane] = l;
+    lse2[n] = (float)l2;
+    if (lse_out) lse_out[n] = (float)l;
+  }
+  __syncthreads();
+  for (int r = w; r < 32; r += 8) {
+    const long long row = base + r;
+    if (row >= P.N) break;
+    const float loss = P.keep[row] ? row_loss_warp(P, row, lane, lse_sh[r], 0.0) : 0.0f;
+    if (lane == 0) P.row_loss[row] = loss;
+  }
+  finish_total(P, 256);
+}
+
+// grad_hidden = grad_mul * sum of the partials, in slot order.
+template <class O>
+__global__ void __launch_bounds__(256) hidden_out_kernel(const float* part, int slots, long long slot_elems,
+                                                         long long elems, const LossScalars* scalars, O* out) {
+  const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= elems) return;
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int s = 0; s < slots; ++s) {
+    const float4 v = __ldcs(reinterpret_cast<const float4*>(part + s * slot_elems + i));
+    a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+  }
+  const float mul = scalars->grad_mul;
+  if constexpr (sizeof(O) == 4) {
+    *reinterpret_cast<float4*>(out + i) = make_float4(a.x * mul, a.y * mul, a.z * mul, a.w * mul);
+  } else {
+    uint2 v;
+    v.x = Elem<O>::pack(a.x * mul, a.y * mul);
+    v.y = Elem<O>::pack(a.z * mul, a.w * mul);
+    *reinterpret_cast<uint2*>(out + i) = v;
+  }
+}
+
+}  // namespace ssv
