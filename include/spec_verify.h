@@ -53,7 +53,8 @@ typedef enum {
   SPEC_ERR_CUDA = 3         /* the CUDA runtime reported an error */
 } spec_status_t;
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype_t;
+/* SPEC_F16: the drafter-training losses only. */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype_t;
 
 /* Bits OR-ed into *dev_status by the kernels. */
 #define SPEC_DEV_BAD_TOKEN 1u      /* a drafted token outside [0, V) (treated as rejected) */
@@ -412,6 +413,120 @@ spec_status_t spec_schedule_lengths(const float* survival, int R, int L,
                                     const float* sps, int sps_len,
                                     int32_t* lengths, float* objective,
                                     uint32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Losses for training a drafter.
+ *
+ * "读 Qwen Bebop 与 DeepSeek DSpark", section "Bebop 的解法" (drafters are trained
+ * with cross entropy or KL; the E2E-TV loss above is the alternative that
+ * targets acceptance); "SpecOPD", method step (6) (only the draft side is
+ * differentiated, the target is a constant).
+ *
+ * Rules shared by these entry points
+ *  - reduction: loss = (1 / count) sum_n w_n L_n (SPEC_MEAN, count = the rows
+ *    that count, 0 if there are none) or sum_n w_n L_n (SPEC_SUM); w_n =
+ *    row_weight[n], or 1 where row_weight is NULL.  Gradients are those of
+ *    grad_scale * loss.
+ *  - A row that is left out has row_loss 0 and no part in loss, count or any
+ *    gradient.
+ *  - A row that counts and whose logits hold NaN or +inf, or no finite value,
+ *    sets SPEC_DEV_BAD_LOGITS; its results are NaN.
+ *  - Results do not depend on timing: the same inputs give the same bits.
+ *  - The workspace needs NO initial contents and holds none to rely on
+ *    afterwards: unlike the other entry points' workspaces it is not
+ *    zero-filled by the call, so it must not be shared with them.
+ *    It must lie on a 256-byte boundary.
+ *  - N == 0 gives loss 0 and a zero head gradient.
+ *  - Listed teacher tokens: teacher_ids [N, k] int32, 1 <= k <= 256, -1 marks
+ *    an unused slot; teacher_logits [N, k] float32.  A row without a used
+ *    slot is left out.  An id outside [-1, V) or listed twice sets
+ *    SPEC_DEV_BAD_TOKEN, and teacher values that cannot be normalised (NaN,
+ *    +inf, nothing but -inf) set SPEC_DEV_BAD_LOGITS; both leave the row out.
+ */
+typedef enum { SPEC_MEAN = 0, SPEC_SUM = 1 } spec_reduction_t;
+
+/* Cross entropy of a vocabulary head, in pieces of the vocabulary, without
+ * keeping the logits z_n = hidden_n . weight^T / T:
+ *   L_n = logsumexp(z_n) - z_n[label_n]
+ *
+ * hidden     [N, H], weight [V, H]: dtype SPEC_BF16 or SPEC_F16 (products are
+ *            summed in fp32), contiguous, 16-byte aligned, H a multiple of 8.
+ * labels     [N] int32; a row whose label is ignore_index is left out, and so
+ *            is one whose label is otherwise outside [0, V), which also sets
+ *            SPEC_DEV_BAD_TOKEN.
+ * loss_out   [1], row_loss [N] or NULL, lse_out [N] or NULL (natural log of
+ *            the normaliser, of every row): float32.
+ * grad_hidden [N, H], grad_weight [V, H] or NULL (not computed), of
+ *            grad_dtype = dtype or SPEC_F32, 16-byte aligned.  The gradient of
+ *            the logits is rounded once to dtype on its way into the products.
+ * The workspace size covers the gradients that are asked for.
+ */
+size_t spec_linear_loss_workspace_bytes(int N, int V, int H, int k, int want_grad_hidden, int want_grad_weight);
+
+spec_status_t spec_linear_cross_entropy(const void* hidden, const void* weight, spec_dtype_t dtype, int N, int V,
+                                        int H, float temperature, const int32_t* labels, int ignore_index,
+                                        const float* row_weight, spec_reduction_t reduction, float* loss_out,
+                                        float* row_loss, float* lse_out, uint32_t* dev_status, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+spec_status_t spec_linear_cross_entropy_fwd_bwd(const void* hidden, const void* weight, spec_dtype_t dtype, int N,
+                                                int V, int H, float temperature, float grad_scale,
+                                                const int32_t* labels, int ignore_index, const float* row_weight,
+                                                spec_reduction_t reduction, float* loss_out, float* row_loss,
+                                                float* lse_out, void* grad_hidden, void* grad_weight,
+                                                spec_dtype_t grad_dtype, uint32_t* dev_status, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
+/* Distillation from a teacher's top logits through the head: with t =
+ * softmax(teacher_logits / T) over the row's used slots and q = softmax(z),
+ *   L_n = sum_i t_i (log t_i - log q_i)
+ * Other arguments as above (workspace with this call's k). */
+spec_status_t spec_linear_topk_distill(const void* hidden, const void* weight, spec_dtype_t dtype, int N, int V, int H,
+                                       int k, float temperature, const int32_t* teacher_ids,
+                                       const float* teacher_logits, const float* row_weight,
+                                       spec_reduction_t reduction, float* loss_out, float* row_loss, float* lse_out,
+                                       uint32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream);
+
+spec_status_t spec_linear_topk_distill_fwd_bwd(const void* hidden, const void* weight, spec_dtype_t dtype, int N,
+                                               int V, int H, int k, float temperature, float grad_scale,
+                                               const int32_t* teacher_ids, const float* teacher_logits,
+                                               const float* row_weight, spec_reduction_t reduction, float* loss_out,
+                                               float* row_loss, float* lse_out, void* grad_hidden, void* grad_weight,
+                                               spec_dtype_t grad_dtype, uint32_t* dev_status, void* workspace,
+                                               size_t workspace_bytes, void* stream);
+
+/* Distillation of given student logits from a teacher's top logits.
+ *
+ * student [N, V] dtype (SPEC_F32, SPEC_BF16 or SPEC_F16), row-contiguous, any
+ * alignment of the element's size; -inf marks dropped tokens.
+ * q = softmax(student / T) over the whole vocabulary.
+ * teacher_lse NULL: t = softmax(teacher_logits / T) over the used slots, and
+ *   L_n = sum_i t_i (log t_i - log q_i)
+ * teacher_lse [N] float32 (logsumexp of the teacher's whole row / T): t_i =
+ * exp(teacher_logits_i / T - teacher_lse), and what both sides leave over
+ * counts as one more token,
+ *   L_n = sum_i t_i (log t_i - log q_i) + t_r (log t_r - log q_r),
+ * t_r = 1 - sum_i t_i (0 where that is below 1e-6, the rounding of the sum),
+ * q_r = 1 - sum_i q_i.
+ * With M = sum_i t_i + t_r the gradient is (M q_i - t_i) / T on the listed
+ * tokens and q_v (M - t_r / q_r) / T on the others.
+ * loss_out [1], row_loss [N] or NULL: float32.  grad [N, V] of grad_dtype =
+ * dtype or SPEC_F32.
+ * Limit: V * elem_size up to about 3.5 MB (16 CTAs' shared memory).
+ */
+size_t spec_topk_distill_workspace_bytes(int N, int V, int k);
+
+spec_status_t spec_topk_distill(const void* student, spec_dtype_t dtype, int N, int V, int k, float temperature,
+                                const int32_t* teacher_ids, const float* teacher_logits, const float* teacher_lse,
+                                const float* row_weight, spec_reduction_t reduction, float* loss_out, float* row_loss,
+                                uint32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream);
+
+spec_status_t spec_topk_distill_fwd_bwd(const void* student, spec_dtype_t dtype, int N, int V, int k,
+                                        float temperature, float grad_scale, const int32_t* teacher_ids,
+                                        const float* teacher_logits, const float* teacher_lse,
+                                        const float* row_weight, spec_reduction_t reduction, float* loss_out,
+                                        float* row_loss, void* grad, spec_dtype_t grad_dtype, uint32_t* dev_status,
+                                        void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Failure-path self-test of the bounded wait.

@@ -14,7 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libspec_verify.so")
-SOURCES = ["spec_api.cu", "spec_noalloc.cu"]
+SOURCES = ["spec_api.cu", "spec_noalloc.cu", "loss_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

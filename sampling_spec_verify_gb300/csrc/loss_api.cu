@@ -1,0 +1,704 @@
+// Host side of the drafter-training losses: argument checks, workspace layout,
+// launch shapes and launches.  No entry point allocates device memory or
+// synchronises the stream.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "distill.cuh"
+#include "head.cuh"
+#include "spec_verify.h"
+
+namespace ssv {
+cudaError_t count_launch(cudaError_t e);  // spec_api.cu
+}
+
+namespace {
+
+using ssv::count_launch;
+
+constexpr double kLog2e = 1.4426950408889634074;
+constexpr int kMaxDevices = 64;
+
+spec_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA; }
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+int elem_size(spec_dtype_t dt) { return dt == SPEC_F32 ? 4 : 2; }
+bool any_dtype(spec_dtype_t dt) { return dt == SPEC_F32 || dt == SPEC_BF16 || dt == SPEC_F16; }
+
+struct Device {
+  int sms = 0, smem_optin = 0;
+};
+bool device(Device* out, int* id) {
+  static Device cache[kMaxDevices];
+  static std::once_flag once[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  std::call_once(once[dev], [dev]() {
+    cudaDeviceGetAttribute(&cache[dev].sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaDeviceGetAttribute(&cache[dev].smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  });
+  *out = cache[dev];
+  *id = dev;
+  return out->sms > 0 && out->smem_optin > 0;
+}
+
+// Launch facts of one kernel instantiation, looked up once per device, cluster
+// size and shared-memory size: a fixed table, so that no lookup can throw.
+struct Residency {
+  struct Entry {
+    int S, smem, clusters;
+  };
+  static constexpr int kEntries = 64;
+  std::mutex mu;
+  bool attrs[kMaxDevices] = {};
+  Entry e[kMaxDevices][kEntries] = {};
+  int n[kMaxDevices] = {};
+};
+
+// Clusters of S CTAs that fit on the device at once; sets the kernel's
+// attributes on first use.  0 on failure.
+int resident_clusters(Residency& r, const void* fn, int S, int smem, int threads, int dev, int smem_optin) {
+  std::lock_guard<std::mutex> g(r.mu);
+  for (int i = 0; i < r.n[dev]; ++i)
+    if (r.e[dev][i].S == S && r.e[dev][i].smem == smem) return r.e[dev][i].clusters;
+  if (!r.attrs[dev]) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, fn) != cudaSuccess) return 0;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem_optin - (int)fa.sharedSizeBytes) != cudaSuccess)
+      return 0;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return 0;
+    r.attrs[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)S);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)S;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (r.n[dev] < Residency::kEntries) r.e[dev][r.n[dev]++] = {S, smem, n};
+  return n;
+}
+
+// Carves a workspace into 256-byte-aligned parts; with a null base it measures.
+struct Carver {
+  char* base;
+  size_t used = 0;
+  template <class T>
+  T* take(size_t n) {
+    T* p = base ? reinterpret_cast<T*>(base + used) : nullptr;
+    used += (n * sizeof(T) + 255) & ~size_t(255);
+    return p;
+  }
+};
+
+// Factor of an exponent in powers of two, hi rounded down so that lo > 0 and
+// -inf * lo stays -inf.
+void split_scale(double s, float* hi, float* lo) {
+  float h = (float)s;
+  if ((double)h > s) h = std::nextafter(h, 0.0f);
+  float l = (float)(s - (double)h);
+  if (!(l > 0.0f)) l = 1e-30f;
+  *hi = h;
+  *lo = l;
+}
+
+bool temperature_ok(float t) { return t > 0.0f && std::isfinite(t) && std::isfinite((float)(kLog2e / (double)t)); }
+
+// ---- distillation of given logits ------------------------------------------------
+
+struct DistillWs {
+  ssv::LossScalars* scalars;
+  float* t;
+  ssv::RowTeacher* row;
+  uint8_t* keep;
+  float* zi;
+  ssv::RowNorm* norm;
+  float* row_loss;
+  size_t total;
+};
+DistillWs distill_ws(void* base, size_t N, size_t k) {
+  Carver c{static_cast<char*>(base)};
+  DistillWs w;
+  w.scalars = c.take<ssv::LossScalars>(1);
+  w.t = c.take<float>(N * k);
+  w.row = c.take<ssv::RowTeacher>(N);
+  w.keep = c.take<uint8_t>(N);
+  w.zi = c.take<float>(N * k);
+  w.norm = c.take<ssv::RowNorm>(N);
+  w.row_loss = c.take<float>(N);
+  w.total = c.used;
+  return w;
+}
+
+// Slices of a row: small enough for two stages of two resident CTAs, else of
+// one, else for one stage.  Short batches spread a row over more CTAs.
+struct DistillShape {
+  int S = 0, nst = 0;
+  uint32_t cap = 0;
+};
+DistillShape distill_shape(long long row_bytes, int N, int sms) {
+  const long long budget[3] = {52 * 1024, 108 * 1024, 216 * 1024};
+  DistillShape d;
+  for (int level = 0; level < 3 && !d.S; ++level)
+    for (int s = 1; s <= ssv::kDMaxCluster; s *= 2)
+      if ((row_bytes + s - 1) / s + 32 <= budget[level]) {
+        d.S = s;
+        d.nst = level == 2 ? 1 : 2;
+        break;
+      }
+  if (!d.S) return d;
+  while (d.S < 8 && (long long)N * d.S < sms && row_bytes / d.S > 8192) d.S *= 2;
+  d.cap = (uint32_t)((((row_bytes / 16) / d.S + 2) * 16 + 127) & ~127ll);
+  return d;
+}
+
+template <class E, class O>
+spec_status_t launch_distill(ssv::DistillParams P, cudaStream_t st) {
+  static Residency res;
+  const void* fn = (const void*)ssv::distill_kernel<E, O>;
+  Device d;
+  int dev = 0;
+  if (!device(&d, &dev)) return SPEC_ERR_CUDA;
+  const DistillShape sh = distill_shape((long long)P.V * (long long)sizeof(E), P.N, d.sms);
+  if (!sh.S) return SPEC_ERR_UNSUPPORTED;
+  P.nst = sh.nst;
+  P.cap = sh.cap;
+  const int smem = (int)(sh.cap * (uint32_t)sh.nst);
+  const int fit = resident_clusters(res, fn, sh.S, smem, ssv::kDThreads, dev, d.smem_optin);
+  if (fit <= 0) return SPEC_ERR_CUDA;
+  const int G = P.N < fit ? P.N : fit;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(G * sh.S));
+  cfg.blockDim = dim3(ssv::kDThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)sh.S;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return from_cuda(count_launch(cudaLaunchKernelEx(&cfg, ssv::distill_kernel<E, O>, P)));
+}
+
+spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int k, float temperature,
+                      float grad_scale, const int32_t* ids, const float* logits, const float* lse,
+                      const float* weight, spec_reduction_t reduction, float* loss, float* row_loss, bool want_grad,
+                      void* grad, spec_dtype_t grad_dtype, uint32_t* status, void* workspace, size_t bytes,
+                      void* stream) {
+  if (N < 0 || V < 1 || k < 1 || !any_dtype(dtype)) return SPEC_ERR_INVALID_ARG;
+  if (reduction != SPEC_MEAN && reduction != SPEC_SUM) return SPEC_ERR_INVALID_ARG;
+  if (!temperature_ok(temperature) || !std::isfinite(grad_scale)) return SPEC_ERR_INVALID_ARG;
+  if (want_grad && grad_dtype != dtype && grad_dtype != SPEC_F32) return SPEC_ERR_INVALID_ARG;
+  if (!loss) return SPEC_ERR_INVALID_ARG;
+  if (k > ssv::kMaxEntries || !distill_shape((long long)V * elem_size(dtype), N, 1).S) return SPEC_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (N == 0) return from_cuda(cudaMemsetAsync(loss, 0, sizeof(float), st));
+  if (!student || !ids || !logits || (want_grad && !grad)) return SPEC_ERR_INVALID_ARG;
+  if (!aligned(student, elem_size(dtype)) || (want_grad && !aligned(grad, elem_size(grad_dtype))))
+    return SPEC_ERR_INVALID_ARG;
+  const DistillWs ws = distill_ws(workspace, (size_t)N, (size_t)k);
+  if (!workspace || bytes < ws.total || !aligned(workspace, 256)) return SPEC_ERR_INVALID_ARG;
+
+  ssv::TargetParams tp = {};
+  tp.ids = ids;
+  tp.logits = logits;
+  tp.lse = lse;
+  tp.N = N;
+  tp.V = V;
+  tp.k = k;
+  tp.inv_t = 1.0 / (double)temperature;
+  tp.t = ws.t;
+  tp.row = ws.row;
+  tp.keep = ws.keep;
+  tp.scalars = ws.scalars;
+  tp.status = status;
+  const unsigned row_grid = (unsigned)((N + ssv::kTargetWarps - 1) / ssv::kTargetWarps);
+  ssv::targets_kernel<<<row_grid, ssv::kTargetWarps * 32, 0, st>>>(tp);
+  if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
+
+  ssv::DistillParams P = {};
+  P.z = student;
+  P.grad = grad;
+  P.N = N;
+  P.V = V;
+  P.k = k;
+  P.skew = (int)((reinterpret_cast<uintptr_t>(student) & 15) / (uintptr_t)elem_size(dtype));
+  if (want_grad) {
+    const uintptr_t o = reinterpret_cast<uintptr_t>(grad) - (uintptr_t)P.skew * (uintptr_t)elem_size(grad_dtype);
+    P.out_vec = (o & 15) == 0;
+  }
+  split_scale(kLog2e / (double)temperature, &P.s_hi, &P.s_lo);
+  P.ids = ids;
+  P.t = ws.t;
+  P.row = ws.row;
+  P.keep = ws.keep;
+  P.weight = weight;
+  P.mean = reduction == SPEC_MEAN;
+  P.tail = lse != nullptr;
+  P.gscale = (float)((double)grad_scale / (double)temperature);
+  P.zi = ws.zi;
+  P.norm = ws.norm;
+  P.status = status;
+  spec_status_t r;
+  const bool wide = want_grad && grad_dtype == SPEC_F32;
+  using B = __nv_bfloat16;
+  using Hf = __half;
+  if (dtype == SPEC_F32)
+    r = want_grad ? launch_distill<float, float>(P, st) : launch_distill<float, ssv::NoGrad>(P, st);
+  else if (dtype == SPEC_BF16)
+    r = !want_grad ? launch_distill<B, ssv::NoGrad>(P, st)
+                   : (wide ? launch_distill<B, float>(P, st) : launch_distill<B, B>(P, st));
+  else
+    r = !want_grad ? launch_distill<Hf, ssv::NoGrad>(P, st)
+                   : (wide ? launch_distill<Hf, float>(P, st) : launch_distill<Hf, Hf>(P, st));
+  if (r != SPEC_OK) return r;
+
+  ssv::FinishParams F = {};
+  F.N = N;
+  F.k = k;
+  F.inv_t = tp.inv_t;
+  F.logits = logits;
+  F.t = ws.t;
+  F.row = ws.row;
+  F.keep = ws.keep;
+  F.weight = weight;
+  F.zi = ws.zi;
+  F.mean = P.mean;
+  F.grad_scale = P.gscale;
+  F.store_scale = 1.0f;
+  F.loss = loss;
+  F.row_loss = row_loss ? row_loss : ws.row_loss;
+  F.scalars = ws.scalars;
+  F.status = status;
+  ssv::distill_finish_kernel<<<row_grid, ssv::kTargetWarps * 32, 0, st>>>(F, ws.norm);
+  return from_cuda(count_launch(cudaGetLastError()));
+}
+
+// ---- losses through the head --------------------------------------------------------
+
+constexpr int kPairs = 76;                       // CTA pairs in flight, for the split rule
+constexpr size_t kPieceBytes = (size_t)256 << 20;  // of a piece of D
+
+// How a call is cut: pieces of the vocabulary and splits of a piece's depth in
+// the product that gives the hidden states' gradient.
+struct HeadPlan {
+  int piece;       // tokens per piece, a multiple of 256
+  int pieces;
+  int splits;
+  int slot_rows;
+};
+HeadPlan head_plan(int N, int V, int H) {
+  HeadPlan p;
+  const long long vt = ((long long)V + 255) / 256;
+  long long cap = (long long)(kPieceBytes / 2 / (size_t)N) / 256;  // tiles of tokens
+  if (cap < 8) cap = 8;
+  p.pieces = (int)((vt + cap - 1) / cap);
+  p.piece = (int)((vt + p.pieces - 1) / p.pieces) * 256;
+  p.pieces = (int)(((long long)V + p.piece - 1) / p.piece);
+  p.slot_rows = (N + 255) / 256 * 256;
+  // The tiles of N x H may be far fewer than the CTA pairs: the depth is split
+  // until the last wave is full, at no less than 1024 tokens a split.
+  const long long tiles = (long long)(p.slot_rows / 256) * ((H + 255) / 256);
+  double best = 0.0;
+  p.splits = 1;
+  for (int s = 1; s <= 32 && (s == 1 || p.piece / s >= 1024); ++s) {
+    const long long n = tiles * s;
+    const double waves = (double)((n + kPairs - 1) / kPairs);
+    const double eff = (double)n / (waves * kPairs) / (1.0 + 0.01 * s);
+    if (eff > best) {
+      best = eff;
+      p.splits = s;
+    }
+  }
+  return p;
+}
+
+struct HeadWs {
+  ssv::LossScalars* scalars;
+  float* t;
+  ssv::RowTeacher* row;
+  uint8_t* keep;
+  float* zi;
+  float* row_loss;
+  float* lse2;
+  float2* part;
+  float* hidden;
+  uint16_t* d;
+  size_t total;
+};
+HeadWs head_ws(void* base, size_t N, size_t V, size_t H, size_t k, bool gh, bool gw) {
+  Carver c{static_cast<char*>(base)};
+  const HeadPlan p = head_plan((int)N, (int)V, (int)H);
+  HeadWs w;
+  w.scalars = c.take<ssv::LossScalars>(1);
+  w.t = c.take<float>(N * k);
+  w.row = c.take<ssv::RowTeacher>(N);
+  w.keep = c.take<uint8_t>(N);
+  w.zi = c.take<float>(N * k);
+  w.row_loss = c.take<float>(N);
+  w.lse2 = c.take<float>(N);
+  w.part = c.take<float2>(N * ((V + 255) / 256));
+  w.hidden = gh ? c.take<float>((size_t)p.splits * (size_t)p.slot_rows * H) : nullptr;
+  w.d = gh || gw ? c.take<uint16_t>(N * (size_t)p.piece) : nullptr;
+  w.total = c.used;
+  return w;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static std::atomic<EncodeTiled> fn{nullptr};
+  EncodeTiled f = fn.load(std::memory_order_acquire);
+  if (f) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  f = reinterpret_cast<EncodeTiled>(p);
+  fn.store(f, std::memory_order_release);
+  return f;
+}
+
+// Row-major [rows, cols] matrix, tiles of box_rows x 128 bytes, 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* base, spec_dtype_t dt, long long rows, long long cols, long long ld,
+              int box_rows) {
+  EncodeTiled enc = encode_tiled();
+  if (!enc) return false;
+  const int es = elem_size(dt);
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * (cuuint64_t)es};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows};
+  const cuuint32_t step[2] = {1, 1};
+  const CUtensorMapDataType t = dt == SPEC_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : dt == SPEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(m, t, 2, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <ssv::HeadOp OP, bool OUT32>
+spec_status_t launch_head(ssv::HeadParams P, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out,
+                          cudaStream_t st) {
+  static Residency res;
+  const void* fn = (const void*)ssv::head_kernel<OP, OUT32>;
+  Device d;
+  int dev = 0;
+  if (!device(&d, &dev)) return SPEC_ERR_CUDA;
+  const int fit = resident_clusters(res, fn, 2, ssv::kHeadSmem, ssv::kHeadThreads, dev, d.smem_optin);
+  if (fit <= 0) return SPEC_ERR_CUDA;
+  P.tiles_m = (P.M + ssv::kTileM - 1) / ssv::kTileM;
+  P.tiles_n = (P.N + ssv::kTileN - 1) / ssv::kTileN;
+  P.ksteps = (P.K + ssv::kTileK - 1) / ssv::kTileK;
+  const long long tiles = (long long)P.tiles_m * P.tiles_n * P.splits;
+  if (tiles > 0x7FFFFFF) return SPEC_ERR_UNSUPPORTED;
+  const int G = tiles < fit ? (int)tiles : fit;
+  ssv::head_kernel<OP, OUT32><<<2 * G, ssv::kHeadThreads, ssv::kHeadSmem, st>>>(P, a, b, out);
+  return from_cuda(count_launch(cudaGetLastError()));
+}
+
+struct HeadCall {
+  const void *hidden, *weight;
+  spec_dtype_t dtype;
+  int N, V, H, k;
+  float temperature, grad_scale;
+  const int32_t* ids;
+  const float* logits;  // null: cross entropy, ids are labels
+  int ignore;
+  const float* row_weight;
+  spec_reduction_t reduction;
+  float *loss, *row_loss, *lse;
+  void *grad_hidden, *grad_weight;
+  spec_dtype_t grad_dtype;
+  uint32_t* status;
+  void* workspace;
+  size_t bytes;
+  void* stream;
+};
+
+template <class E>
+spec_status_t head_run(const HeadCall& c, const HeadWs& ws) {
+  cudaStream_t st = static_cast<cudaStream_t>(c.stream);
+  const HeadPlan plan = head_plan(c.N, c.V, c.H);
+  const E* x = static_cast<const E*>(c.hidden);
+  const E* w = static_cast<const E*>(c.weight);
+  const double s = kLog2e / (double)c.temperature;
+  const float store_scale = c.dtype == SPEC_F16 ? 32768.0f : 1.0f;
+  const long long entries = (long long)c.N * c.k;
+
+  ssv::TargetParams tp = {};
+  tp.ids = c.ids;
+  tp.logits = c.logits;
+  tp.N = c.N;
+  tp.V = c.V;
+  tp.k = c.k;
+  tp.ignore = c.ignore;
+  tp.inv_t = 1.0 / (double)c.temperature;
+  tp.t = ws.t;
+  tp.row = ws.row;
+  tp.keep = ws.keep;
+  tp.scalars = ws.scalars;
+  tp.status = c.status;
+  ssv::targets_kernel<<<(unsigned)((c.N + ssv::kTargetWarps - 1) / ssv::kTargetWarps), ssv::kTargetWarps * 32, 0,
+                        st>>>(tp);
+  if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
+  ssv::listed_logits_kernel<E><<<(unsigned)((entries + 7) / 8), 256, 0, st>>>(x, w, c.ids, ws.keep, c.N, c.H, c.k,
+                                                                              ws.zi);
+  if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
+
+  CUtensorMap x_k, w_k;  // 128-row boxes along K
+  if (!make_map(&x_k, x, c.dtype, c.N, c.H, c.H, 128) || !make_map(&w_k, w, c.dtype, c.V, c.H, c.H, 128))
+    return SPEC_ERR_CUDA;
+  ssv::HeadParams P = {};
+  P.M = c.N;
+  P.N = c.V;
+  P.K = c.H;
+  P.splits = 1;
+  P.bf16 = c.dtype == SPEC_BF16;
+  P.s = (float)s;
+  P.part = ws.part;
+  P.status = c.status;
+  P.scalars = ws.scalars;
+  spec_status_t r = launch_head<ssv::kHeadNorm, false>(P, x_k, w_k, x_k, st);
+  if (r != SPEC_OK) return r;
+
+  ssv::FinishParams F = {};
+  F.N = c.N;
+  F.k = c.k;
+  F.inv_t = tp.inv_t;
+  F.logits = c.logits;
+  F.t = ws.t;
+  F.row = ws.row;
+  F.keep = ws.keep;
+  F.weight = c.row_weight;
+  F.zi = ws.zi;
+  F.mean = c.reduction == SPEC_MEAN;
+  F.grad_scale = (float)((double)c.grad_scale / (double)c.temperature);
+  F.store_scale = store_scale;
+  F.loss = c.loss;
+  F.row_loss = c.row_loss ? c.row_loss : ws.row_loss;
+  F.scalars = ws.scalars;
+  F.status = c.status;
+  ssv::head_finish_kernel<<<(unsigned)((c.N + 31) / 32), 256, 0, st>>>(F, ws.part, (c.V + 255) / 256, c.lse, ws.lse2);
+  if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (!c.grad_hidden && !c.grad_weight) return SPEC_OK;
+
+  CUtensorMap x_mn, w_mn, part_out;  // 64-row boxes along the other dimension
+  if (!make_map(&x_mn, x, c.dtype, c.N, c.H, c.H, 64) || !make_map(&w_mn, w, c.dtype, c.V, c.H, c.H, 64))
+    return SPEC_ERR_CUDA;
+  if (c.grad_hidden && !make_map(&part_out, ws.hidden, SPEC_F32, (long long)plan.splits * plan.slot_rows, c.H, c.H, 32))
+    return SPEC_ERR_CUDA;
+  int slots = 0;
+  for (int i = 0; i < plan.pieces; ++i) {
+    const int v0 = i * plan.piece;
+    const int C = c.V - v0 < plan.piece ? c.V - v0 : plan.piece;
+    CUtensorMap d_out, d_k, d_mn;
+    if (!make_map(&d_out, ws.d, c.dtype, c.N, C, plan.piece, 32) ||
+        !make_map(&d_k, ws.d, c.dtype, c.N, C, plan.piece, 128) || !make_map(&d_mn, ws.d, c.dtype, c.N, C, plan.piece, 64))
+      return SPEC_ERR_CUDA;
+
+    ssv::HeadParams D = P;
+    D.N = C;
+    D.b_off = v0;
+    D.lse2 = ws.lse2;
+    D.weight = c.row_weight;
+    D.keep = ws.keep;
+    D.store_scale = store_scale;
+    if ((r = launch_head<ssv::kHeadGrad, false>(D, x_k, w_k, d_out, st)) != SPEC_OK) return r;
+
+    ssv::ListedParams L = {};
+    L.ids = c.ids;
+    L.t = ws.t;
+    L.zi = ws.zi;
+    L.lse2 = ws.lse2;
+    L.weight = c.row_weight;
+    L.keep = ws.keep;
+    L.scalars = ws.scalars;
+    L.N = c.N;
+    L.k = c.k;
+    L.v0 = v0;
+    L.C = C;
+    L.ld = plan.piece;
+    L.s = s;
+    L.store_scale = store_scale;
+    ssv::listed_grads_kernel<E>
+        <<<(unsigned)((entries + 255) / 256), 256, 0, st>>>(L, reinterpret_cast<E*>(ws.d));
+    if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
+
+    if (c.grad_hidden) {
+      ssv::HeadParams Q = P;
+      Q.M = c.N;
+      Q.N = c.H;
+      Q.K = C;
+      Q.b_off = v0;
+      const int steps = (C + ssv::kTileK - 1) / ssv::kTileK;
+      Q.splits = plan.splits < steps ? plan.splits : steps;
+      if (i == 0) slots = Q.splits;  // later pieces are no longer than the first
+      Q.first = i == 0;
+      Q.slot_rows = plan.slot_rows;
+      if ((r = launch_head<ssv::kHeadHidden, true>(Q, d_k, w_mn, part_out, st)) != SPEC_OK) return r;
+    }
+    if (c.grad_weight) {
+      const int es = elem_size(c.grad_dtype);
+      CUtensorMap w_out;
+      if (!make_map(&w_out, static_cast<char*>(c.grad_weight) + (size_t)v0 * (size_t)c.H * (size_t)es, c.grad_dtype, C,
+                    c.H, c.H, 32))
+        return SPEC_ERR_CUDA;
+      ssv::HeadParams Q = P;
+      Q.M = C;
+      Q.N = c.H;
+      Q.K = c.N;
+      Q.b_off = 0;
+      r = c.grad_dtype == SPEC_F32 ? launch_head<ssv::kHeadWeight, true>(Q, d_mn, x_mn, w_out, st)
+                                   : launch_head<ssv::kHeadWeight, false>(Q, d_mn, x_mn, w_out, st);
+      if (r != SPEC_OK) return r;
+    }
+  }
+  if (c.grad_hidden) {
+    const long long elems = (long long)c.N * c.H;
+    const long long slot = (long long)plan.slot_rows * c.H;
+    const unsigned grid = (unsigned)((elems / 4 + 255) / 256);
+    if (c.grad_dtype == SPEC_F32)
+      ssv::hidden_out_kernel<float><<<grid, 256, 0, st>>>(ws.hidden, slots, slot, elems, ws.scalars,
+                                                          static_cast<float*>(c.grad_hidden));
+    else
+      ssv::hidden_out_kernel<E><<<grid, 256, 0, st>>>(ws.hidden, slots, slot, elems, ws.scalars,
+                                                      static_cast<E*>(c.grad_hidden));
+    if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
+  }
+  return SPEC_OK;
+}
+
+bool head_dims_ok(int N, int V, int H, int k) { return N >= 0 && V >= 1 && H >= 8 && H % 8 == 0 && k >= 1; }
+bool head_dims_fit(int N, int V, int H, int k) {
+  return N <= (1 << 20) && V <= (1 << 24) && H <= (1 << 16) && k <= ssv::kMaxEntries;
+}
+
+spec_status_t head_loss(const HeadCall& c, bool grads) {
+  if (!head_dims_ok(c.N, c.V, c.H, c.k)) return SPEC_ERR_INVALID_ARG;
+  if (c.dtype != SPEC_BF16 && c.dtype != SPEC_F16) return SPEC_ERR_INVALID_ARG;
+  if (c.reduction != SPEC_MEAN && c.reduction != SPEC_SUM) return SPEC_ERR_INVALID_ARG;
+  if (!temperature_ok(c.temperature) || !std::isfinite(c.grad_scale) || !c.loss) return SPEC_ERR_INVALID_ARG;
+  if (grads && ((!c.grad_hidden && !c.grad_weight && c.N > 0) ||
+                (c.grad_dtype != c.dtype && c.grad_dtype != SPEC_F32)))
+    return SPEC_ERR_INVALID_ARG;
+  if (!aligned(c.grad_hidden, 16) || !aligned(c.grad_weight, 16)) return SPEC_ERR_INVALID_ARG;
+  if (!head_dims_fit(c.N, c.V, c.H, c.k)) return SPEC_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(c.stream);
+  if (c.N == 0) {
+    cudaError_t e = cudaMemsetAsync(c.loss, 0, sizeof(float), st);
+    if (e == cudaSuccess && c.grad_weight)
+      e = cudaMemsetAsync(c.grad_weight, 0, (size_t)c.V * (size_t)c.H * (size_t)elem_size(c.grad_dtype), st);
+    return from_cuda(e);
+  }
+  if (!c.hidden || !c.weight || !c.ids || !aligned(c.hidden, 16) || !aligned(c.weight, 16)) return SPEC_ERR_INVALID_ARG;
+  const HeadWs ws = head_ws(c.workspace, (size_t)c.N, (size_t)c.V, (size_t)c.H, (size_t)c.k, c.grad_hidden != nullptr,
+                            c.grad_weight != nullptr);
+  if (!c.workspace || c.bytes < ws.total || !aligned(c.workspace, 256)) return SPEC_ERR_INVALID_ARG;
+  return c.dtype == SPEC_BF16 ? head_run<__nv_bfloat16>(c, ws) : head_run<__half>(c, ws);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_topk_distill_workspace_bytes(int N, int V, int k) {
+  if (N < 0 || V < 1 || k < 1 || k > ssv::kMaxEntries) return 0;
+  return distill_ws(nullptr, (size_t)N, (size_t)k).total;
+}
+
+spec_status_t spec_topk_distill(const void* student, spec_dtype_t dtype, int N, int V, int k, float temperature,
+                                const int32_t* teacher_ids, const float* teacher_logits, const float* teacher_lse,
+                                const float* row_weight, spec_reduction_t reduction, float* loss_out, float* row_loss,
+                                uint32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream) {
+  return distill(student, dtype, N, V, k, temperature, 0.0f, teacher_ids, teacher_logits, teacher_lse, row_weight,
+                 reduction, loss_out, row_loss, false, nullptr, dtype, dev_status, workspace, workspace_bytes, stream);
+}
+
+spec_status_t spec_topk_distill_fwd_bwd(const void* student, spec_dtype_t dtype, int N, int V, int k,
+                                        float temperature, float grad_scale, const int32_t* teacher_ids,
+                                        const float* teacher_logits, const float* teacher_lse,
+                                        const float* row_weight, spec_reduction_t reduction, float* loss_out,
+                                        float* row_loss, void* grad, spec_dtype_t grad_dtype, uint32_t* dev_status,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  return distill(student, dtype, N, V, k, temperature, grad_scale, teacher_ids, teacher_logits, teacher_lse,
+                 row_weight, reduction, loss_out, row_loss, true, grad, grad_dtype, dev_status, workspace,
+                 workspace_bytes, stream);
+}
+
+size_t spec_linear_loss_workspace_bytes(int N, int V, int H, int k, int want_grad_hidden, int want_grad_weight) {
+  if (!head_dims_ok(N, V, H, k) || !head_dims_fit(N, V, H, k)) return 0;
+  if (N == 0) return 256;
+  return head_ws(nullptr, (size_t)N, (size_t)V, (size_t)H, (size_t)k, want_grad_hidden != 0, want_grad_weight != 0)
+      .total;
+}
+
+spec_status_t spec_linear_cross_entropy_fwd_bwd(const void* hidden, const void* weight, spec_dtype_t dtype, int N,
+                                                int V, int H, float temperature, float grad_scale,
+                                                const int32_t* labels, int ignore_index, const float* row_weight,
+                                                spec_reduction_t reduction, float* loss_out, float* row_loss,
+                                                float* lse_out, void* grad_hidden, void* grad_weight,
+                                                spec_dtype_t grad_dtype, uint32_t* dev_status, void* workspace,
+                                                size_t workspace_bytes, void* stream) {
+  const HeadCall c{hidden,     weight,      dtype,        N,          V,          H,         1,        temperature,
+                   grad_scale, labels,      nullptr,      ignore_index, row_weight, reduction, loss_out, row_loss,
+                   lse_out,    grad_hidden, grad_weight,  grad_dtype, dev_status, workspace, workspace_bytes, stream};
+  return head_loss(c, true);
+}
+
+spec_status_t spec_linear_cross_entropy(const void* hidden, const void* weight, spec_dtype_t dtype, int N, int V,
+                                        int H, float temperature, const int32_t* labels, int ignore_index,
+                                        const float* row_weight, spec_reduction_t reduction, float* loss_out,
+                                        float* row_loss, float* lse_out, uint32_t* dev_status, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  const HeadCall c{hidden,  weight,  dtype,   N,            V,          H,         1,        temperature,
+                   0.0f,    labels,  nullptr, ignore_index, row_weight, reduction, loss_out, row_loss,
+                   lse_out, nullptr, nullptr, dtype,        dev_status, workspace, workspace_bytes, stream};
+  return head_loss(c, false);
+}
+
+spec_status_t spec_linear_topk_distill_fwd_bwd(const void* hidden, const void* weight, spec_dtype_t dtype, int N,
+                                               int V, int H, int k, float temperature, float grad_scale,
+                                               const int32_t* teacher_ids, const float* teacher_logits,
+                                               const float* row_weight, spec_reduction_t reduction, float* loss_out,
+                                               float* row_loss, float* lse_out, void* grad_hidden, void* grad_weight,
+                                               spec_dtype_t grad_dtype, uint32_t* dev_status, void* workspace,
+                                               size_t workspace_bytes, void* stream) {
+  if (N > 0 && !teacher_logits) return SPEC_ERR_INVALID_ARG;
+  const HeadCall c{hidden,     weight,      dtype,          N,          V,          H,         k,        temperature,
+                   grad_scale, teacher_ids, teacher_logits, -1,         row_weight, reduction, loss_out, row_loss,
+                   lse_out,    grad_hidden, grad_weight,    grad_dtype, dev_status, workspace, workspace_bytes, stream};
+  return head_loss(c, true);
+}
+
+spec_status_t spec_linear_topk_distill(const void* hidden, const void* weight, spec_dtype_t dtype, int N, int V, int H,
+                                       int k, float temperature, const int32_t* teacher_ids,
+                                       const float* teacher_logits, const float* row_weight,
+                                       spec_reduction_t reduction, float* loss_out, float* row_loss, float* lse_out,
+                                       uint32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream) {
+  if (N > 0 && !teacher_logits) return SPEC_ERR_INVALID_ARG;
+  const HeadCall c{hidden,  weight,      dtype,          N,     V,          H,         k,        temperature,
+                   0.0f,    teacher_ids, teacher_logits, -1,    row_weight, reduction, loss_out, row_loss,
+                   lse_out, nullptr,     nullptr,        dtype, dev_status, workspace, workspace_bytes, stream};
+  return head_loss(c, false);
+}
+
+}  // extern "C"

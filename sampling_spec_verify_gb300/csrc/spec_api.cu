@@ -19,6 +19,11 @@
 #include "schedule.cuh"
 #include "tree.cuh"
 
+// Counts a launch made by another translation unit of the library.
+namespace ssv {
+cudaError_t count_launch(cudaError_t e);
+}
+
 namespace {
 
 using ssv::Bf16;
@@ -44,6 +49,12 @@ cudaError_t counted(cudaError_t e) {
   if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
   return e;
 }
+
+}  // namespace
+
+cudaError_t ssv::count_launch(cudaError_t e) { return counted(e); }
+
+namespace {
 
 struct DevInfo {
   int sms = 0;
