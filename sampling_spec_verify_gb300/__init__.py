@@ -23,7 +23,14 @@ Entry points (same names as the C ABI, see include/spec_verify.h):
 * ``truncate_logits`` -- top-k / top-p truncation, to apply identically to
                          target and draft logits before ``verify``;
 * ``schedule_lengths`` -- verify lengths maximising tau * SPS(B) over prefix
-                         survivals and a throughput table.
+                         survivals and a throughput table;
+* ``linear_cross_entropy``, ``linear_cross_entropy_fwd_bwd`` -- cross entropy
+                         of a vocabulary head from hidden states, without
+                         keeping its logits, and its gradients;
+* ``topk_distill``, ``topk_distill_fwd_bwd`` -- distillation of draft logits
+                         from a teacher's top logits, and its gradient;
+* ``linear_topk_distill``, ``linear_topk_distill_fwd_bwd`` -- the same from
+                         hidden states, through the head.
 """
 
 from __future__ import annotations
@@ -36,8 +43,11 @@ from typing import Optional
 import torch
 
 __all__ = [
-    "SpecError", "lib", "verify", "verify_ragged", "verify_relaxed", "tree_mask", "tree_verify_greedy", "overlap", "e2e_tv_fwd_bwd", "diagnostics", "truncate_logits", "schedule_lengths", "selftest_bounded_wait", "launch_shape", "kernel_launches", "set_kernel_override",
+    "SpecError", "lib", "verify", "verify_ragged", "verify_relaxed", "tree_mask", "tree_verify_greedy", "overlap", "e2e_tv_fwd_bwd", "diagnostics", "truncate_logits", "schedule_lengths", "linear_cross_entropy",
+    "linear_cross_entropy_fwd_bwd", "topk_distill", "topk_distill_fwd_bwd", "linear_topk_distill",
+    "linear_topk_distill_fwd_bwd", "selftest_bounded_wait", "launch_shape", "kernel_launches", "set_kernel_override",
     "set_launch_override", "VerifyOutput", "OverlapOutput", "E2EOutput", "DiagOutput", "TreeOutput", "HostVerifier",
+    "LinearLossOutput", "DistillOutput",
     "DEV_BAD_TOKEN", "DEV_BAD_LOGITS", "DEV_BAD_UNIFORM", "DEV_TIMEOUT", "DEV_EMPTY_RESIDUAL", "DEV_BAD_OFFSETS",
     "SPEC_OK", "SPEC_ERR_INVALID_ARG", "SPEC_ERR_UNSUPPORTED", "SPEC_ERR_CUDA",
 ]
@@ -46,7 +56,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libspec_verify.so")
 
 SPEC_OK, SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA = 0, 1, 2, 3
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_F16 = 0, 1, 2
+SPEC_MEAN, SPEC_SUM = 0, 1
 DEV_BAD_TOKEN, DEV_BAD_LOGITS, DEV_BAD_UNIFORM, DEV_TIMEOUT, DEV_EMPTY_RESIDUAL = 1, 2, 4, 8, 16
 DEV_BAD_OFFSETS = 32
 
@@ -117,6 +128,26 @@ def lib():
     L.spec_set_launch_override.argtypes = [i32, i32]
     L.spec_set_kernel_override.restype = None
     L.spec_set_kernel_override.argtypes = [i32]
+    head = [vp, vp, i32, i32, i32, i32]                 # hidden, weight, dtype, N, V, H
+    tail = [vp, vp, sz, vp]                             # status, workspace, bytes, stream
+    L.spec_linear_loss_workspace_bytes.restype = sz
+    L.spec_linear_loss_workspace_bytes.argtypes = [i32] * 6
+    L.spec_linear_cross_entropy.restype = i32
+    L.spec_linear_cross_entropy.argtypes = head + [f32, vp, i32, vp, i32, vp, vp, vp] + tail
+    L.spec_linear_cross_entropy_fwd_bwd.restype = i32
+    L.spec_linear_cross_entropy_fwd_bwd.argtypes = head + [f32, f32, vp, i32, vp, i32, vp, vp, vp, vp, vp, i32] + tail
+    L.spec_linear_topk_distill.restype = i32
+    L.spec_linear_topk_distill.argtypes = head + [i32, f32, vp, vp, vp, i32, vp, vp, vp] + tail
+    L.spec_linear_topk_distill_fwd_bwd.restype = i32
+    L.spec_linear_topk_distill_fwd_bwd.argtypes = head + [i32, f32, f32, vp, vp, vp, i32, vp, vp, vp, vp, vp,
+                                                          i32] + tail
+    L.spec_topk_distill_workspace_bytes.restype = sz
+    L.spec_topk_distill_workspace_bytes.argtypes = [i32, i32, i32]
+    L.spec_topk_distill.restype = i32
+    L.spec_topk_distill.argtypes = [vp, i32, i32, i32, i32, f32, vp, vp, vp, vp, i32, vp, vp] + tail
+    L.spec_topk_distill_fwd_bwd.restype = i32
+    L.spec_topk_distill_fwd_bwd.argtypes = [vp, i32, i32, i32, i32, f32, f32, vp, vp, vp, vp, i32, vp, vp, vp,
+                                            i32] + tail
     _lib = L
     return L
 
@@ -545,6 +576,271 @@ def schedule_lengths(survival: torch.Tensor, sps: torch.Tensor, *, status: Optio
                                   _ptr(status), sh)
     _check(st, "spec_schedule_lengths")
     return lengths, objective
+
+
+# ---------------------------------------------------------------------------
+# losses for training a drafter
+# ---------------------------------------------------------------------------
+
+_SCRATCH = {}
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace of the training losses, cached per (device, stream).  Its
+    contents are never zeroed, so it is not the one of the other calls."""
+    key = (device.index, stream.cuda_stream)
+    ws = _SCRATCH.get(key)
+    if ws is None or ws.numel() < nbytes:
+        _SCRATCH.pop(key, None)
+        ws = None  # the old one goes before the new one comes
+        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        _SCRATCH[key] = ws
+    return ws
+
+
+_LOSS_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+
+
+def _reduction_code(reduction: str) -> int:
+    if reduction not in ("mean", "sum"):
+        raise ValueError(f"reduction must be 'mean' or 'sum', got {reduction!r}")
+    return SPEC_MEAN if reduction == "mean" else SPEC_SUM
+
+
+def _grad_code(grad_dtype, dtype, name: str):
+    grad_dtype = dtype if grad_dtype is None else grad_dtype
+    if grad_dtype not in (dtype, torch.float32):
+        raise TypeError(f"grad_dtype must be float32 or the dtype of {name}, got {grad_dtype}")
+    return grad_dtype, _LOSS_DTYPES[grad_dtype]
+
+
+def _need_out(t: Optional[torch.Tensor], name: str, dtype, shape, device):
+    if t is not None:
+        _need(t, f"out.{name}", dtype=dtype, shape=shape, device=device)
+
+
+@dataclass
+class LinearLossOutput:
+    loss: torch.Tensor                    # float32 [1]
+    row_loss: torch.Tensor                # float32 [N]
+    lse: torch.Tensor                     # float32 [N]: log of the normaliser, every row
+    grad_hidden: Optional[torch.Tensor]   # [N, H]
+    grad_weight: Optional[torch.Tensor]   # [V, H]
+    status: torch.Tensor                  # int32 [1] device status word
+
+
+@dataclass
+class DistillOutput:
+    loss: torch.Tensor            # float32 [1]
+    row_loss: torch.Tensor        # float32 [N]
+    grad: Optional[torch.Tensor]  # [N, V]
+    status: torch.Tensor          # int32 [1] device status word
+
+
+def _linear_loss(what, hidden, weight, ids, logits, ignore_index, temperature, grad_scale, row_weight, reduction,
+                 want_hidden, want_weight, grad_dtype, out, workspace, stream):
+    L = lib()
+    _need(hidden, "hidden")
+    if hidden.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"hidden must be bfloat16 or float16, got {hidden.dtype}")
+    if hidden.dim() != 2:
+        raise ValueError("hidden must be [N, H]")
+    N, H = hidden.shape
+    dev = hidden.device
+    _need(weight, "weight", dtype=hidden.dtype, device=dev)
+    if weight.dim() != 2 or weight.shape[1] != H:
+        raise ValueError(f"weight must be [V, {H}], got {tuple(weight.shape)}")
+    V = weight.shape[0]
+    if logits is None:
+        k = 1
+        _need(ids, "labels", dtype=torch.int32, shape=(N,), device=dev)
+    else:
+        _need(ids, "teacher_ids", dtype=torch.int32, device=dev)
+        if ids.dim() != 2 or ids.shape[0] != N:
+            raise ValueError(f"teacher_ids must be [{N}, k], got {tuple(ids.shape)}")
+        k = ids.shape[1]
+        _need(logits, "teacher_logits", dtype=torch.float32, shape=(N, k), device=dev)
+    if row_weight is not None:
+        _need(row_weight, "row_weight", dtype=torch.float32, shape=(N,), device=dev)
+    grads = want_hidden or want_weight
+    gdt, gcode = _grad_code(grad_dtype, hidden.dtype, "hidden")
+    red = _reduction_code(reduction)
+    if out is None:
+        f = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+        out = LinearLossOutput(f(1), f(N), f(N), f(N, H, dtype=gdt) if want_hidden else None,
+                               f(V, H, dtype=gdt) if want_weight else None,
+                               torch.zeros((1,), dtype=torch.int32, device=dev))
+    else:
+        _need(out.loss, "out.loss", dtype=torch.float32, shape=(1,), device=dev)
+        _need_out(out.row_loss, "row_loss", torch.float32, (N,), dev)
+        _need_out(out.lse, "lse", torch.float32, (N,), dev)
+        _need_out(out.status, "status", torch.int32, (1,), dev)
+        if grads:
+            if (out.grad_hidden is None) == want_hidden or (out.grad_weight is None) == want_weight:
+                raise ValueError("out must hold exactly the gradients that are asked for")
+            _need_out(out.grad_hidden, "grad_hidden", gdt, (N, H), dev)
+            _need_out(out.grad_weight, "grad_weight", gdt, (V, H), dev)
+    sh, s = _stream_handle(stream, dev)
+    need = L.spec_linear_loss_workspace_bytes(N, V, H, k, int(want_hidden), int(want_weight))
+    ws = workspace if workspace is not None else _scratch(need, dev, s)
+    dims = (_ptr(hidden), _ptr(weight), _LOSS_DTYPES[hidden.dtype], N, V, H)
+    rows = (_ptr(row_weight), red, _ptr(out.loss), _ptr(out.row_loss), _ptr(out.lse))
+    end = (_ptr(out.status), _ptr(ws), ws.numel() * ws.element_size(), sh)
+    t, gs = float(temperature), float(grad_scale)
+    if logits is None:
+        if grads:
+            st = L.spec_linear_cross_entropy_fwd_bwd(*dims, t, gs, _ptr(ids), int(ignore_index), *rows,
+                                                     _ptr(out.grad_hidden), _ptr(out.grad_weight), gcode, *end)
+        else:
+            st = L.spec_linear_cross_entropy(*dims, t, _ptr(ids), int(ignore_index), *rows, *end)
+    elif grads:
+        st = L.spec_linear_topk_distill_fwd_bwd(*dims, k, t, gs, _ptr(ids), _ptr(logits), *rows,
+                                                _ptr(out.grad_hidden), _ptr(out.grad_weight), gcode, *end)
+    else:
+        st = L.spec_linear_topk_distill(*dims, k, t, _ptr(ids), _ptr(logits), *rows, *end)
+    _check(st, what)
+    return out
+
+
+def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor, temperature: float = 1.0, *,
+                         row_weight: Optional[torch.Tensor] = None, ignore_index: int = -100,
+                         reduction: str = "mean", out: Optional[LinearLossOutput] = None,
+                         workspace: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None) -> LinearLossOutput:
+    """Cross entropy of softmax(hidden weight^T / temperature) against labels
+    without keeping the logits (see spec_linear_cross_entropy in the C
+    header).  hidden [N, H] and weight [V, H] (bf16 or fp16, H a multiple of
+    8), labels int32 [N], row_weight float32 [N].  ``row_loss`` is unweighted
+    (minus the label's log-probability); ``loss`` is the weighted sum, over
+    the rows whose label is not ``ignore_index``, divided by their number
+    unless reduction is "sum"."""
+    return _linear_loss("spec_linear_cross_entropy", hidden, weight, labels, None, ignore_index, temperature, 0.0,
+                        row_weight, reduction, False, False, None, out, workspace, stream)
+
+
+def linear_cross_entropy_fwd_bwd(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor,
+                                 temperature: float = 1.0, grad_scale: float = 1.0, *,
+                                 row_weight: Optional[torch.Tensor] = None, ignore_index: int = -100,
+                                 reduction: str = "mean", want_grad_hidden: bool = True,
+                                 want_grad_weight: bool = True, grad_dtype: Optional[torch.dtype] = None,
+                                 out: Optional[LinearLossOutput] = None, workspace: Optional[torch.Tensor] = None,
+                                 stream: Optional[torch.cuda.Stream] = None) -> LinearLossOutput:
+    """``linear_cross_entropy`` and grad_scale times its gradients with respect
+    to hidden and weight (of ``grad_dtype``: float32 or, by default, the dtype
+    of hidden).  A frozen head saves its product with
+    ``want_grad_weight=False``."""
+    if not (want_grad_hidden or want_grad_weight):
+        raise ValueError("no gradient asked for: call linear_cross_entropy")
+    return _linear_loss("spec_linear_cross_entropy_fwd_bwd", hidden, weight, labels, None, ignore_index, temperature,
+                        grad_scale, row_weight, reduction, want_grad_hidden, want_grad_weight, grad_dtype, out,
+                        workspace, stream)
+
+
+def linear_topk_distill(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor,
+                        teacher_logits: torch.Tensor, temperature: float = 1.0, *,
+                        row_weight: Optional[torch.Tensor] = None, reduction: str = "mean",
+                        out: Optional[LinearLossOutput] = None, workspace: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> LinearLossOutput:
+    """KL(t || q) of the teacher's renormalised top logits against
+    q = softmax(hidden weight^T / temperature), without keeping the logits (see
+    spec_linear_topk_distill in the C header).  teacher_ids int32 [N, k] (-1:
+    unused slot) and teacher_logits float32 [N, k], k <= 256."""
+    if teacher_logits is None:
+        raise TypeError("teacher_logits must be a torch.Tensor")
+    return _linear_loss("spec_linear_topk_distill", hidden, weight, teacher_ids, teacher_logits, -1, temperature, 0.0,
+                        row_weight, reduction, False, False, None, out, workspace, stream)
+
+
+def linear_topk_distill_fwd_bwd(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor,
+                                teacher_logits: torch.Tensor, temperature: float = 1.0, grad_scale: float = 1.0, *,
+                                row_weight: Optional[torch.Tensor] = None, reduction: str = "mean",
+                                want_grad_hidden: bool = True, want_grad_weight: bool = True,
+                                grad_dtype: Optional[torch.dtype] = None, out: Optional[LinearLossOutput] = None,
+                                workspace: Optional[torch.Tensor] = None,
+                                stream: Optional[torch.cuda.Stream] = None) -> LinearLossOutput:
+    """``linear_topk_distill`` and grad_scale times its gradients, as
+    ``linear_cross_entropy_fwd_bwd`` gives them."""
+    if teacher_logits is None:
+        raise TypeError("teacher_logits must be a torch.Tensor")
+    if not (want_grad_hidden or want_grad_weight):
+        raise ValueError("no gradient asked for: call linear_topk_distill")
+    return _linear_loss("spec_linear_topk_distill_fwd_bwd", hidden, weight, teacher_ids, teacher_logits, -1,
+                        temperature, grad_scale, row_weight, reduction, want_grad_hidden, want_grad_weight,
+                        grad_dtype, out, workspace, stream)
+
+
+def _distill(what, student, ids, logits, lse, temperature, grad_scale, row_weight, reduction, want_grad, grad_dtype,
+             out, workspace, stream):
+    L = lib()
+    _need(student, "student")
+    if student.dtype not in _LOSS_DTYPES:
+        raise TypeError(f"student must be bfloat16, float16 or float32, got {student.dtype}")
+    if student.dim() != 2:
+        raise ValueError("student must be [N, V]")
+    N, V = student.shape
+    dev = student.device
+    _need(ids, "teacher_ids", dtype=torch.int32, device=dev)
+    if ids.dim() != 2 or ids.shape[0] != N:
+        raise ValueError(f"teacher_ids must be [{N}, k], got {tuple(ids.shape)}")
+    k = ids.shape[1]
+    _need(logits, "teacher_logits", dtype=torch.float32, shape=(N, k), device=dev)
+    if lse is not None:
+        _need(lse, "teacher_lse", dtype=torch.float32, shape=(N,), device=dev)
+    if row_weight is not None:
+        _need(row_weight, "row_weight", dtype=torch.float32, shape=(N,), device=dev)
+    gdt, gcode = _grad_code(grad_dtype, student.dtype, "student")
+    red = _reduction_code(reduction)
+    if out is None:
+        f = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+        out = DistillOutput(f(1), f(N), f(N, V, dtype=gdt) if want_grad else None,
+                            torch.zeros((1,), dtype=torch.int32, device=dev))
+    else:
+        _need(out.loss, "out.loss", dtype=torch.float32, shape=(1,), device=dev)
+        _need_out(out.row_loss, "row_loss", torch.float32, (N,), dev)
+        _need_out(out.status, "status", torch.int32, (1,), dev)
+        if want_grad:
+            _need(out.grad, "out.grad", dtype=gdt, shape=(N, V), device=dev)
+    sh, s = _stream_handle(stream, dev)
+    need = L.spec_topk_distill_workspace_bytes(N, V, k)
+    ws = workspace if workspace is not None else _scratch(need, dev, s)
+    end = (_ptr(out.status), _ptr(ws), ws.numel() * ws.element_size(), sh)
+    common = (_ptr(ids), _ptr(logits), _ptr(lse), _ptr(row_weight), red, _ptr(out.loss), _ptr(out.row_loss))
+    dims = (_ptr(student), _LOSS_DTYPES[student.dtype], N, V, k, float(temperature))
+    if want_grad:
+        st = L.spec_topk_distill_fwd_bwd(*dims, float(grad_scale), *common, _ptr(out.grad), gcode, *end)
+    else:
+        st = L.spec_topk_distill(*dims, *common, *end)
+    _check(st, what)
+    return out
+
+
+def topk_distill(student: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                 temperature: float = 1.0, *, teacher_lse: Optional[torch.Tensor] = None,
+                 row_weight: Optional[torch.Tensor] = None, reduction: str = "mean",
+                 out: Optional[DistillOutput] = None, workspace: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> DistillOutput:
+    """KL(t || q) of a teacher's top logits against q = softmax(student /
+    temperature) (see spec_topk_distill in the C header).  student [N, V]
+    (bf16, fp16 or fp32), teacher_ids int32 [N, k] (-1: unused slot),
+    teacher_logits float32 [N, k], k <= 256.  Without ``teacher_lse`` the
+    listed logits are renormalised; with it (float32 [N], logsumexp of the
+    teacher's whole row / temperature) the remaining mass of both sides counts
+    as one more token."""
+    return _distill("spec_topk_distill", student, teacher_ids, teacher_logits, teacher_lse, temperature, 0.0,
+                    row_weight, reduction, False, None, out, workspace, stream)
+
+
+def topk_distill_fwd_bwd(student: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                         temperature: float = 1.0, grad_scale: float = 1.0, *,
+                         teacher_lse: Optional[torch.Tensor] = None, row_weight: Optional[torch.Tensor] = None,
+                         reduction: str = "mean", grad_dtype: Optional[torch.dtype] = None,
+                         out: Optional[DistillOutput] = None, workspace: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None) -> DistillOutput:
+    """``topk_distill`` and grad_scale times its gradient with respect to the
+    student logits (of ``grad_dtype``: float32 or, by default, the student's
+    dtype)."""
+    return _distill("spec_topk_distill_fwd_bwd", student, teacher_ids, teacher_logits, teacher_lse, temperature,
+                    grad_scale, row_weight, reduction, True, grad_dtype, out, workspace, stream)
 
 
 # ---------------------------------------------------------------------------
