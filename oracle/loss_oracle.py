@@ -37,10 +37,8 @@ class LossResult:
 
 
 def logsumexp(a):
-    m = np.max(a, axis=1, keepdims=True)
-    m = np.where(np.isneginf(m), 0.0, m)
     with np.errstate(divide="ignore"):
-        return (m + np.log(np.exp(a - m).sum(axis=1, keepdims=True)))[:, 0]
+        return np.log(np.exp(a).sum(axis=1))
 
 
 def dense_teacher(ids, logits, temperature, V, lse=None):
@@ -95,6 +93,11 @@ def listed_loss(z, target, temperature, *, row_weight=None, reduction="mean", gr
     t, listed, rest, keep = target
     a = np.asarray(z, dtype=np.float64) / float(temperature)
     N, V = a.shape
+    # each row's maximum comes off first: beside the lowest value of a type the
+    # logarithm of a sum would be lost
+    top = np.max(a, axis=1) if N else np.zeros(0)
+    top = np.where(np.isneginf(top), 0.0, top)
+    a = a - top[:, None]
     lse = logsumexp(a) if N else np.zeros(0)
     with np.errstate(divide="ignore", invalid="ignore"):
         logq = a - lse[:, None]
@@ -112,7 +115,7 @@ def listed_loss(z, target, temperature, *, row_weight=None, reduction="mean", gr
     with np.errstate(invalid="ignore"):
         g = np.where(listed, mass * q - t, q * (mass - ratio[:, None]))
         g = np.where(keep[:, None], g * (coef / float(temperature))[:, None], 0.0)
-    return LossResult(float((w * row)[keep].sum() / den), row, lse, keep, coef, q, t, listed, rest, g)
+    return LossResult(float((w * row)[keep].sum() / den), row, top + lse, keep, coef, q, t, listed, rest, g)
 
 
 def head_loss(hidden, weight, target, temperature, **kw):

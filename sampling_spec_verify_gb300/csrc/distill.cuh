@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kTargetWarps * 32) distill_finish_kernel(const
     float loss = 0.0f;
     if (P.keep[n]) {
       const RowNorm r = norm[n];
-      const double lse = (double)r.m * P.inv_t + log((double)r.z);
+      const double logz = log((double)r.z);
       double log_qr = 0.0;
       if (P.row[n].rest > 0.0f) {
         // from the listed tokens' mass where that is the smaller part
@@ -385,9 +385,9 @@ __global__ void __launch_bounds__(kTargetWarps * 32) distill_finish_kernel(const
         if (ql < 0.5)
           log_qr = log1p(-ql);
         else
-          log_qr = r.mr > -INFINITY ? (double)r.mr * P.inv_t + log((double)r.zr) - lse : -INFINITY;
+          log_qr = r.mr > -INFINITY ? ((double)r.mr - (double)r.m) * P.inv_t + log((double)r.zr) - logz : -INFINITY;
       }
-      loss = row_loss_warp(P, n, lane, lse, log_qr);
+      loss = row_loss_warp(P, n, lane, (double)r.m, logz, log_qr);
     }
     if (lane == 0) P.row_loss[n] = loss;
   }

@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const FinishParams P, 
   for (int r = w; r < 32; r += 8) {
     const long long row = base + r;
     if (row >= P.N) break;
-    const float loss = P.keep[row] ? row_loss_warp(P, row, lane, lse_sh[r], 0.0) : 0.0f;
+    const float loss = P.keep[row] ? row_loss_warp(P, row, lane, 0.0, lse_sh[r], 0.0) : 0.0f;
     if (lane == 0) P.row_loss[row] = loss;
   }
   finish_total(P, 256);

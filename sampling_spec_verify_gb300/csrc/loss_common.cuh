@@ -275,9 +275,10 @@ struct FinishParams {
   uint32_t* status;
 };
 
-// Loss of row n, by one warp (every lane gets it): lse is the student's
-// normaliser, log_qr the log of the unlisted tokens' mass.
-__device__ __forceinline__ float row_loss_warp(const FinishParams& P, long long n, int lane, double lse,
+// Loss of row n, by one warp (every lane gets it): log q_i = (z_i - m) / T -
+// logz, log_qr the log of the unlisted tokens' mass.  The maximum is taken off
+// first: rows masked with the type's lowest value would lose logz beside it.
+__device__ __forceinline__ float row_loss_warp(const FinishParams& P, long long n, int lane, double m, double logz,
                                                double log_qr) {
   const RowTeacher r = P.row[n];
   float acc = 0.0f;
@@ -285,7 +286,7 @@ __device__ __forceinline__ float row_loss_warp(const FinishParams& P, long long 
     const float t = P.t[n * P.k + i];
     if (t > 0.0f) {
       const double lt = P.logits ? (double)P.logits[n * P.k + i] * P.inv_t - r.shift : 0.0;
-      acc += t * (float)(lt - ((double)P.zi[n * P.k + i] * P.inv_t - lse));
+      acc += t * (float)(lt - (((double)P.zi[n * P.k + i] - m) * P.inv_t - logz));
     }
   }
   acc = warp_sum(acc);
@@ -293,7 +294,7 @@ __device__ __forceinline__ float row_loss_warp(const FinishParams& P, long long 
     const double lr = r.sum < 0.5f ? log1p(-(double)r.sum) : log((double)r.rest);
     acc += (float)((double)r.rest * (lr - log_qr));
   }
-  if (isnan(lse)) acc = NAN;  // also where the entries weigh nothing
+  if (isnan(logz)) acc = NAN;  // also where the entries weigh nothing
   return acc;
 }
 
