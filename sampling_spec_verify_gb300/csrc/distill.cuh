@@ -13,7 +13,10 @@
 //
 // Bound: HBM.  A row is read once and its gradient written once; a row of
 // 151936 bf16 logits is 304 KB, more than one SM holds, so a cluster of S CTAs
-// keeps it in shared memory between the normaliser and the gradient.
+// holds it between the normaliser and the gradient, each CTA a slice in its
+// registers (NV vectors a thread; NV = 0: in shared memory, for slices that do
+// not fit).  Slices land in shared memory by bulk copies, up to two rows ahead;
+// two CTAs share an SM, so that one's exchange hides behind the other's work.
 #pragma once
 
 #include <type_traits>
@@ -25,16 +28,17 @@ namespace ssv {
 constexpr int kDThreads = 512;
 constexpr int kDWarps = kDThreads / 32;
 constexpr int kDMaxCluster = 16;
+constexpr int kDVecs = 6;  // vectors of a slice held by a thread
 
 struct DistillParams {
   const void* z;
   void* grad;
   int N, V, k;
-  int nst;            // shared-memory stages (2: the next row's slice is prefetched)
+  int nst;            // shared-memory stages: rows of this cluster in flight
   uint32_t cap;       // bytes of a stage
   int skew;           // elements by which the base lies past a 16-byte boundary
-  int out_vec;        // gradient vectors may be written 16 bytes at a time
-  float s_hi, s_lo;   // log2(e) / T
+  int out_vec;        // bytes that a gradient store may write at a time: 32, 16 or (0) one element
+  float s;            // log2(e) / T
   const int32_t* ids; // [N, k]
   const float* t;     // [N, k]
   const RowTeacher* row;
@@ -49,24 +53,44 @@ struct DistillParams {
 
 struct NoGrad {};
 
-// Writes PV gradients of consecutive tokens.
+__device__ __forceinline__ void st_async_f4(uint32_t addr, float a, float b, float c, float d, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                   addr),
+               "f"(a), "f"(b), "f"(c), "f"(d), "r"(bar)
+               : "memory");
+}
+
+// Writes the gradients of a vector's tokens.  32-byte stores where fp32
+// gradients come from 16-bit logits: two 16-byte stores a thread would each
+// touch half of every sector.
 template <class O, int PV>
-__device__ __forceinline__ void store_grads(O* dst, const float (&g)[PV], bool vec) {
-  if (vec) {
-    if constexpr (sizeof(O) == 4) {
+__device__ __forceinline__ void store_grads(O* dst, const f32x2 (&g)[PV / 2], int bytes) {
+  float x[PV];
 #pragma unroll
-      for (int i = 0; i < PV; i += 4)
-        __stcs(reinterpret_cast<float4*>(dst + i), make_float4(g[i], g[i + 1], g[i + 2], g[i + 3]));
-    } else {
+  for (int i = 0; i < PV / 2; ++i) f2_split(g[i], x[2 * i], x[2 * i + 1]);
+  if (bytes >= 16) {
+    if constexpr (sizeof(O) == 2) {
       static_assert(PV == 8, "16-bit gradients come from 16-bit logits");
       uint4 w;
-      w.x = Elem<O>::pack(g[0], g[1]), w.y = Elem<O>::pack(g[2], g[3]);
-      w.z = Elem<O>::pack(g[4], g[5]), w.w = Elem<O>::pack(g[6], g[7]);
+      w.x = Elem<O>::pack(x[0], x[1]), w.y = Elem<O>::pack(x[2], x[3]);
+      w.z = Elem<O>::pack(x[4], x[5]), w.w = Elem<O>::pack(x[6], x[7]);
       __stcs(reinterpret_cast<uint4*>(dst), w);
+    } else {
+      if constexpr (PV == 8) {
+        if (bytes == 32) {
+          asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(x[0]), "f"(x[1]),
+                       "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                       : "memory");
+          return;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < PV; i += 4)
+        __stcs(reinterpret_cast<float4*>(dst + i), make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < PV; ++i) dst[i] = Elem<O>::from_f32(g[i]);
+    for (int i = 0; i < PV; ++i) dst[i] = Elem<O>::from_f32(x[i]);
   }
 }
 
@@ -83,30 +107,30 @@ template <int PV>
 __device__ __forceinline__ Slice slice_of(long long n, int V, int skew, uint32_t rank, uint32_t S) {
   Slice s;
   s.f0 = n * V;
-  int lead = (int)((PV - (s.f0 + skew) % PV) % PV);
+  int lead = (PV - (int)((s.f0 + skew) & (PV - 1))) & (PV - 1);
   if (lead > V) lead = V;
-  const int nv = (V - lead) / PV;
+  const uint32_t nv = (uint32_t)(V - lead) / PV;
   s.a0 = lead;
-  s.a1 = lead + nv * PV;
-  s.v0 = (int)((long long)nv * rank / S);
-  s.v1 = (int)((long long)nv * (rank + 1) / S);
+  s.a1 = lead + (int)nv * PV;
+  s.v0 = (int)(nv * rank / S);  // nv * S < 2^31: rows of at most 16 slices of shared memory
+  s.v1 = (int)(nv * (rank + 1) / S);
   s.head = rank == 0 ? lead : 0;
   s.tail = rank == S - 1 ? V - s.a1 : 0;
   return s;
 }
 
-template <class E, class O>
-__global__ void __launch_bounds__(kDThreads, 2) distill_kernel(const __grid_constant__ DistillParams P) {
+template <class E, class O, int NV>
+__global__ void __launch_bounds__(kDThreads, NV ? 2 : 1) distill_kernel(const __grid_constant__ DistillParams P) {
   using T = Elem<E>;
   constexpr int PV = T::PV;
   constexpr bool kGrad = !std::is_same<O, NoGrad>::value;
   using OG = typename std::conditional<kGrad, O, float>::type;
   extern __shared__ __align__(128) unsigned char stage_mem[];
-  __shared__ __align__(8) uint64_t bars[2];
-  __shared__ float4 warp_part[kDWarps];    // {m, s} of the unlisted, {m, s} of the listed tokens
-  __shared__ float4 box[2][kDMaxCluster];  // the same per CTA, pushed by every CTA of the cluster
-  __shared__ float edge[16];               // odd elements: 0..7 before, 8..15 after the aligned part
-  __shared__ RowNorm shared_norm;
+  // {m, s} of the unlisted and {m, s} of the listed tokens, per warp of the
+  // cluster, pushed by every CTA into every CTA; two rows in turn
+  __shared__ float4 box[2][kDMaxCluster * kDWarps];
+  __shared__ __align__(8) uint64_t bars[4];      // stages, boxes
+  __shared__ float edge[16];  // odd elements: 0..7 before, 8..15 after the aligned part
   __shared__ uint32_t shared_count[kDWarps];
   __shared__ uint32_t abort_flag;
 
@@ -116,14 +140,58 @@ __global__ void __launch_bounds__(kDThreads, 2) distill_kernel(const __grid_cons
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
   const int G = gridDim.x / S, c = blockIdx.x / S;
   const E* z = static_cast<const E*>(P.z);
-  const uint32_t bar0 = smem_addr(bars);
+  const uint32_t bar0 = smem_addr(bars), xbar0 = bar0 + 16;
   if (tid == 0) {
-    mbar_init(bar0, 1);
-    mbar_init(bar0 + 8, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(bar0 + 8 * i, 1);
     fence_mbar_init();
     abort_flag = 0;
   }
 
+  const uint64_t policy = l2_evict_first_policy();
+  // Starts the copy of row n's slice into stage st (thread 0; rows that are
+  // left out are not read).
+  auto fetch = [&](long long n, int st, bool on) {
+    if (tid != 0 || n >= P.N || !on) return;
+    const Slice s = slice_of<PV>(n, P.V, P.skew, rank, S);
+    const uint32_t bytes = (uint32_t)(s.v1 - s.v0) * 16u;
+    mbar_arrive_expect_tx(bar0 + 8 * st, bytes);
+    if (bytes)
+      bulk_load(smem_addr(stage_mem) + st * P.cap, z + s.f0 + s.a0 + (long long)s.v0 * PV, bytes, bar0 + 8 * st,
+                policy);
+  };
+
+  // Per-row values, loaded a row ahead and independently of one another.
+  struct Row {
+    int id;
+    float t, w, sum, rest, edge;
+    bool live;
+  };
+  auto row_values = [&](long long n) {
+    Row r{-1, 0.0f, 0.0f, 0.0f, 0.0f, -INFINITY, false};
+    if (n < P.N) {
+      r.live = P.keep[n];
+      if (tid < P.k) {
+        r.id = P.ids[n * P.k + tid];
+        r.t = P.t[n * P.k + tid];
+      }
+      const RowTeacher rt = P.row[n];
+      r.sum = rt.sum;
+      r.rest = rt.rest;
+      r.w = P.weight ? P.weight[n] : 1.0f;
+      if (tid < 16) {
+        const Slice s = slice_of<PV>(n, P.V, P.skew, rank, S);
+        if (tid < s.head) r.edge = T::to_f32(z[s.f0 + tid]);
+        if (tid >= 8 && tid - 8 < s.tail) r.edge = T::to_f32(z[s.f0 + s.a1 + tid - 8]);
+      }
+    }
+    return r;
+  };
+
+  if (tid == 0) {
+    fetch(c, 0, P.keep[c]);
+    if (P.nst == 2 && c + G < P.N) fetch((long long)c + G, 1, P.keep[c + G]);
+  }
+  Row cur = row_values(c);
   float coef0 = P.gscale;
   if (kGrad && P.mean) {  // rows that count
     uint32_t cnt = 0;
@@ -139,99 +207,67 @@ __global__ void __launch_bounds__(kDThreads, 2) distill_kernel(const __grid_cons
     coef0 = cnt ? coef0 / (float)cnt : 0.0f;
   }
 
-  const uint64_t policy = l2_evict_first_policy();
-  // Starts the copy of row n's slice into stage st; rows that are left out are
-  // not read.
-  auto fetch = [&](long long n, int st) {
-    if (tid != 0 || n >= P.N || !P.keep[n]) return;
-    const Slice s = slice_of<PV>(n, P.V, P.skew, rank, S);
-    const uint32_t bytes = (uint32_t)(s.v1 - s.v0) * 16u;
-    mbar_arrive_expect_tx(bar0 + 8 * st, bytes);
-    if (bytes)
-      bulk_load(smem_addr(stage_mem) + st * P.cap, z + s.f0 + s.a0 + (long long)s.v0 * PV, bytes, bar0 + 8 * st,
-                policy);
-  };
-
-  // per-row values of the row about to be processed
-  int my_id;
-  float my_t, w, my_edge;
-  bool live;
-  RowTeacher rt;
-  auto row_values = [&](long long n) {
-    live = n < P.N && P.keep[n];
-    my_id = -1;
-    my_t = w = 0.0f;
-    rt = RowTeacher{0.0, 0.0f, 0.0f};
-    my_edge = -INFINITY;
-    if (live) {
-      if (tid < P.k) {
-        my_id = P.ids[n * P.k + tid];
-        my_t = P.t[n * P.k + tid];
-      }
-      rt = P.row[n];
-      w = P.weight ? P.weight[n] : 1.0f;
-      if (tid < 16) {
-        const Slice s = slice_of<PV>(n, P.V, P.skew, rank, S);
-        if (tid < s.head) my_edge = T::to_f32(z[s.f0 + tid]);
-        if (tid >= 8 && tid - 8 < s.tail) my_edge = T::to_f32(z[s.f0 + s.a1 + tid - 8]);
-      }
-    }
-  };
-
   uint32_t par = 0;  // phase parity of each stage, one bit per stage
-  fetch(c, 0);
-  if (P.nst == 2) fetch((long long)c + G, 1);
-  row_values(c);
-  int it = 0, ex = 0;
-  uint32_t failed = 0;
+  uint32_t it = 0, ex = 0, failed = 0;
+  OG* late = nullptr;  // a listed token's gradient, written after the next barrier: its place
+  float late_v = 0.0f;  // is first written, as 0, by the thread that holds its vector
   for (long long n = c; n < P.N; n += G, ++it) {
-    const int st = P.nst == 2 ? (it & 1) : 0;
+    const int st = P.nst == 2 ? (int)(it & 1) : 0;
     const Slice s = slice_of<PV>(n, P.V, P.skew, rank, S);
     const int nvl = s.v1 - s.v0;
     OG* out = kGrad ? static_cast<OG*>(P.grad) + s.f0 : nullptr;
-    if (!live) {  // left out: no gradient
+    const long long n_fetch = n + (long long)P.nst * G;
+    const bool fetch_on = tid == 0 && n_fetch < P.N && P.keep[n_fetch];
+    const uint4 low = make_uint4(T::kLow, T::kLow, T::kLow, T::kLow);
+    if (!cur.live) {  // left out: no gradient
       if (kGrad) {
-        float zero[PV] = {};
-        for (int i = tid; i < nvl; i += kDThreads) store_grads<OG, PV>(out + s.a0 + (s.v0 + i) * PV, zero, P.out_vec);
+        const f32x2 zero[PV / 2] = {};
+        for (int i = tid; i < nvl; i += kDThreads)
+          store_grads<OG, PV>(out + s.a0 + (s.v0 + i) * PV, zero, P.out_vec);
         if (tid < s.head) out[tid] = Elem<OG>::from_f32(0.0f);
         if (tid >= 8 && tid - 8 < s.tail) out[s.a1 + tid - 8] = Elem<OG>::from_f32(0.0f);
       }
-      fetch(n + (long long)P.nst * G, st);
-      row_values(n + G);
+      fetch(n_fetch, st, fetch_on);
+      cur = row_values(n + G);
       continue;
     }
     E* buf = reinterpret_cast<E*>(stage_mem + st * P.cap);
     const uint4* vec = reinterpret_cast<const uint4*>(buf);
-    const float coef = coef0 * w;
+    const uint32_t slot = ex & 1, xpar = (ex >> 1) & 1;
+    ++ex;
+    if (tid == 0) mbar_arrive_expect_tx(xbar0 + 8 * slot, S * kDWarps * 16);
 
-    if (tid < 16) edge[tid] = my_edge;
     // after a wait that ran out, the later ones are short: the call ends soon
-    const bool got = mbar_wait_bounded(bar0 + 8 * st, (par >> st) & 1u, failed ? 100000ull : 2000000000ull);
+    const uint64_t limit = failed ? 100000ull : 2000000000ull;
+    if (!mbar_wait_bounded(bar0 + 8 * st, (par >> st) & 1u, limit)) failed = abort_flag = 1;
     par ^= 1u << st;
-    if (!got) failed = abort_flag = 1;
-    __syncthreads();  // edges written
+    const bool odd = s.a0 > 0 || s.a1 < P.V;
+    if (odd) {
+      if (tid < 16) edge[tid] = cur.edge;
+      __syncthreads();
+    }
 
     // the listed tokens: taken out of the row, their logits kept by their threads
     float my_z = -INFINITY;
     bool mine = false;
-    if (my_id >= 0) {
-      if (my_id < s.a0) {
+    if (cur.id >= 0) {
+      if (cur.id < s.a0) {
         mine = rank == 0;
         if (mine) {
-          my_z = edge[my_id];
-          edge[my_id] = -INFINITY;
+          my_z = edge[cur.id];
+          edge[cur.id] = -INFINITY;
         }
-      } else if (my_id >= s.a1) {
+      } else if (cur.id >= s.a1) {
         mine = rank == S - 1;
         if (mine) {
-          my_z = edge[8 + my_id - s.a1];
-          edge[8 + my_id - s.a1] = -INFINITY;
+          my_z = edge[8 + cur.id - s.a1];
+          edge[8 + cur.id - s.a1] = -INFINITY;
         }
       } else {
-        const int v = (my_id - s.a0) / PV;
+        const int v = (cur.id - s.a0) / PV;
         mine = v >= s.v0 && v < s.v1;
         if (mine) {
-          E* p = buf + (my_id - s.a0 - s.v0 * PV);
+          E* p = buf + (cur.id - s.a0 - s.v0 * PV);
           my_z = T::to_f32(*p);
           *p = T::neg_inf();
         }
@@ -239,159 +275,198 @@ __global__ void __launch_bounds__(kDThreads, 2) distill_kernel(const __grid_cons
       if (mine) P.zi[n * P.k + tid] = my_z;
     }
     __syncthreads();
+    if (kGrad && late) *late = Elem<OG>::from_f32(late_v);
+    late = nullptr;
+
+    // the slice, from here on in registers
+    uint4 v[NV ? NV : 1];
+    uint4 top = low;
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int i = tid + j * kDThreads;
+        v[j] = i < nvl ? vec[i] : low;
+      }
+    }
+    const float my_edge = odd && tid < 16 ? edge[tid] : -INFINITY;
+    const Row next = row_values(n + G);  // travels while this row is worked on
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) top = T::vmax(top, v[j]);
+    } else {
+      for (int i = tid; i < nvl; i += kDThreads) top = T::vmax(top, vec[i]);
+    }
 
     // normalisers: each warp relative to its own maximum
-    float m = -INFINITY;
-    for (int i = tid; i < nvl; i += kDThreads) {
-      float x[PV];
-      T::unpack(vec[i], x);
-#pragma unroll
-      for (int j = 0; j < PV; ++j) m = max_nan(m, x[j]);
-    }
-    if (tid < 16) m = max_nan(m, edge[tid]);
-    m = redux_max_nan(m);
-    float sum = 0.0f;
+    float m = redux_max_nan(max_nan(T::hmax(top), my_edge)), sum = 0.0f;
     if (m > -INFINITY && m < INFINITY) {
-      for (int i = tid; i < nvl; i += kDThreads) {
-        float x[PV];
-        T::unpack(vec[i], x);
-        float a = 0.0f;
+      const f32x2 s2 = f2(P.s, P.s), m2 = f2(-m, -m);
+      f32x2 a0 = f2(0.0f, 0.0f), a1 = a0;
+      auto add = [&](const uint4& u) {
+        f32x2 p[PV / 2];
+        T::pairs(u, p);
 #pragma unroll
-        for (int j = 0; j < PV; ++j) {
-          const float d = x[j] - m;
-          a += ex2(fmaf(d, P.s_hi, d * P.s_lo));
+        for (int i = 0; i < PV / 2; ++i) {
+          float x, y;
+          f2_split(f2_mul(f2_add(p[i], m2), s2), x, y);
+          const f32x2 e = f2(ex2(x), ex2(y));
+          if (i & 1)
+            a1 = f2_add(a1, e);
+          else
+            a0 = f2_add(a0, e);
         }
-        sum += a;
+      };
+      if constexpr (NV > 0) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (j * kDThreads < nvl) add(v[j]);
+      } else {
+        for (int i = tid; i < nvl; i += kDThreads) add(vec[i]);
       }
-      if (tid < 16) sum += exp2_scaled(edge[tid] - m, P.s_hi, P.s_lo);
-      sum = warp_sum(sum);
+      sum = warp_sum(f2_hsum(f2_add(a0, a1)) + exp2_scaled(my_edge - m, P.s));
     } else if (!(m < INFINITY)) {  // NaN or +inf among the logits
       sum = NAN;
       m = 0.0f;
     }
     float mk = redux_max_nan(my_z), sk = 0.0f;
     if (mk > -INFINITY && mk < INFINITY) {
-      sk = warp_sum(exp2_scaled(my_z - mk, P.s_hi, P.s_lo));
+      sk = warp_sum(exp2_scaled(my_z - mk, P.s));
     } else if (!(mk < INFINITY)) {
       sk = NAN;
       mk = 0.0f;
     }
-    if (lane == 0) warp_part[wid] = make_float4(m, sum, mk, sk);
-    __syncthreads();
-    const int slot = ex & 1;
-    ++ex;
-    // joins the {m, s} pairs of the lanes of a warp
-    auto join = [&](float& mm, float& ss) {
-      const float top = redux_max_nan(mm);
-      ss = warp_sum(mm > -INFINITY ? ss * exp2_scaled(mm - top, P.s_hi, P.s_lo) : 0.0f);
-      mm = top;
-    };
-    if (wid == 0) {
-      float4 v = lane < kDWarps ? warp_part[lane] : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
-      join(v.x, v.y);
-      join(v.z, v.w);
-      if (lane < (int)S) st_cluster_v4(map_rank(smem_addr(&box[slot][rank]), lane), v.x, v.y, v.z, v.w);
+    if (lane < (int)S)
+      st_async_f4(map_rank(smem_addr(&box[slot][rank * kDWarps + wid]), lane), m, sum, mk, sk,
+                  map_rank(xbar0 + 8 * slot, lane));
+    if constexpr (NV > 0) {  // the stage is free: everyone has its part in registers
+      fence_proxy_async_smem();
+      __syncthreads();
+      fetch(n_fetch, st, fetch_on);
     }
-    cluster_sync();
-    if (wid == 0) {
-      float4 v = lane < (int)S ? box[slot][lane] : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
-      join(v.x, v.y);
-      join(v.z, v.w);
-      if (lane == 0) {
-        const float top = fmaxf(v.x, v.z);
-        RowNorm r;
-        r.m = top;
-        r.mr = v.x;
-        r.zr = v.y;
-        r.zl = v.z > -INFINITY ? v.w * exp2_scaled(v.z - top, P.s_hi, P.s_lo) : 0.0f;
-        r.z = (v.x > -INFINITY ? v.y * exp2_scaled(v.x - top, P.s_hi, P.s_lo) : 0.0f) + r.zl;
-        if (!(top > -INFINITY)) r.z = NAN;  // no finite logit
-        shared_norm = r;
-        if (rank == 0) {
-          P.norm[n] = r;
-          if (!(r.z < INFINITY)) raise(P.status, SPEC_DEV_BAD_LOGITS);
-        }
-      }
-    }
-    __syncthreads();
 
-    // the next row's scalars travel while this one's gradient is written
-    const int id = my_id;
-    const float t = my_t;
-    const RowTeacher rc = rt;
-    row_values(n + G);
+    // the cluster's pairs, joined by every warp in the same order
+    if (!mbar_wait_bounded(xbar0 + 8 * slot, xpar, limit)) failed = abort_flag = 1;
+    RowNorm r;
+    {
+      const int entries = (int)S * kDWarps;
+      float mu = -INFINITY, ml = -INFINITY;
+      for (int i = lane; i < entries; i += 32) {
+        const float4 b = box[slot][i];
+        mu = max_nan(mu, b.x);
+        ml = max_nan(ml, b.z);
+      }
+      mu = redux_max_nan(mu);
+      ml = redux_max_nan(ml);
+      float su = 0.0f, sl = 0.0f;
+      for (int i = lane; i < entries; i += 32) {
+        const float4 b = box[slot][i];
+        if (b.x > -INFINITY) su += b.y * exp2_scaled(b.x - mu, P.s);
+        if (b.z > -INFINITY) sl += b.w * exp2_scaled(b.z - ml, P.s);
+      }
+      su = warp_sum(su);
+      sl = warp_sum(sl);
+      r.m = fmaxf(mu, ml);
+      r.mr = mu;
+      r.zr = su;
+      r.zl = ml > -INFINITY ? sl * exp2_scaled(ml - r.m, P.s) : 0.0f;
+      r.z = (mu > -INFINITY ? su * exp2_scaled(mu - r.m, P.s) : 0.0f) + r.zl;
+      if (!(r.m > -INFINITY)) r.z = NAN;  // no finite logit
+    }
+    if (rank == 0 && tid == 0) {
+      P.norm[n] = r;
+      if (!(r.z < INFINITY)) raise(P.status, SPEC_DEV_BAD_LOGITS);
+    }
 
     if (kGrad) {
-      const RowNorm r = shared_norm;
-      const float mass = rc.sum + rc.rest;
+      const float coef = coef0 * cur.w;
+      const float mass = cur.sum + cur.rest;
       const float inv_z = 1.0f / r.z;
       const bool some = r.mr > -INFINITY;
-      const float rest_scale = some ? exp2_scaled(r.mr - r.m, P.s_hi, P.s_lo) : 0.0f;
+      const float rest_scale = some ? exp2_scaled(r.mr - r.m, P.s) : 0.0f;
       const float mr = some ? r.mr : 0.0f;
       float cb;  // factor of 2^((z - mr) s) for tokens that are not listed
       if (P.tail) {
         const float ql = r.zl * inv_z;
-        const float diff = ql < 0.5f ? rc.sum - mass * ql : mass * (r.zr * rest_scale * inv_z) - rc.rest;
+        const float diff = ql < 0.5f ? cur.sum - mass * ql : mass * (r.zr * rest_scale * inv_z) - cur.rest;
         cb = some ? coef * diff / r.zr : coef * (r.z - r.z);
       } else {
         cb = coef * mass * rest_scale * inv_z;
       }
-      for (int i = tid; i < nvl; i += kDThreads) {
-        float x[PV], g[PV];
-        T::unpack(vec[i], x);
+      const f32x2 s2 = f2(P.s, P.s), m2 = f2(-mr, -mr), c2 = f2(cb, cb);
+      auto grads = [&](const uint4& u, int i) {
+        f32x2 p[PV / 2];
+        T::pairs(u, p);
 #pragma unroll
-        for (int j = 0; j < PV; ++j) {
-          const float d = x[j] - mr;
-          g[j] = ex2(fmaf(d, P.s_hi, d * P.s_lo)) * cb;
+        for (int j = 0; j < PV / 2; ++j) {
+          float x, y;
+          f2_split(f2_mul(f2_add(p[j], m2), s2), x, y);
+          p[j] = f2_mul(f2(ex2(x), ex2(y)), c2);
         }
-        store_grads<OG, PV>(out + s.a0 + (s.v0 + i) * PV, g, P.out_vec);
+        store_grads<OG, PV>(out + s.a0 + (s.v0 + i) * PV, p, P.out_vec);
+      };
+      if constexpr (NV > 0) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int i = tid + j * kDThreads;
+          if (i < nvl) grads(v[j], i);
+        }
+      } else {
+        for (int i = tid; i < nvl; i += kDThreads) grads(vec[i], i);
       }
       if (tid < 16) {
-        const float g = exp2_scaled(edge[tid] - mr, P.s_hi, P.s_lo) * cb;
+        const float g = exp2_scaled(my_edge - mr, P.s) * cb;
         if (tid < s.head) out[tid] = Elem<OG>::from_f32(g);
         if (tid >= 8 && tid - 8 < s.tail) out[s.a1 + tid - 8] = Elem<OG>::from_f32(g);
       }
-      fence_proxy_async_smem();
-      __syncthreads();  // the slice has been read, and the listed tokens' places hold 0
       if (mine) {
-        const float q = exp2_scaled(my_z - r.m, P.s_hi, P.s_lo) * inv_z;
-        out[id] = Elem<OG>::from_f32(coef * (mass * q - t));
+        late = out + cur.id;
+        late_v = coef * (mass * (exp2_scaled(my_z - r.m, P.s) * inv_z) - cur.t);
       }
-    } else {
+    }
+    if constexpr (NV == 0) {
       fence_proxy_async_smem();
       __syncthreads();
+      fetch(n_fetch, st, fetch_on);
     }
-    fetch(n + (long long)P.nst * G, st);
+    cur = next;
   }
   __syncthreads();
+  if (kGrad && late) *late = Elem<OG>::from_f32(late_v);
   if (tid == 0 && abort_flag) raise(P.status, SPEC_DEV_TIMEOUT);
   cluster_sync();  // no CTA leaves while others may still push into it
 }
 
-// Row losses and their sum: one warp per row.
-__global__ void __launch_bounds__(kTargetWarps * 32) distill_finish_kernel(const FinishParams P,
-                                                                          const RowNorm* norm) {
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long n = (long long)blockIdx.x * kTargetWarps + w;
-  if (n < P.N) {
-    float loss = 0.0f;
-    if (P.keep[n]) {
+// Row losses and their sum: 32 rows a CTA.
+__global__ void __launch_bounds__(256) distill_finish_kernel(const FinishParams P, const RowNorm* norm) {
+  __shared__ RowLog sh[32];
+  const long long base = (long long)blockIdx.x * 32;
+  if (threadIdx.x < 32) {
+    const long long n = base + threadIdx.x;
+    if (n < P.N && P.keep[n]) {
       const RowNorm r = norm[n];
-      const double logz = log((double)r.z);
-      double log_qr = 0.0;
-      if (P.row[n].rest > 0.0f) {
-        // from the listed tokens' mass where that is the smaller part
+      const RowTeacher t = P.row[n];
+      const double logz = log((double)r.z), b = logz - (double)t.shift - (double)t.shift_lo;
+      RowLog g;
+      g.m = r.m;
+      g.base.hi = (float)b;
+      g.base.lo = (float)(b - (double)g.base.hi);
+      g.extra = 0.0f;
+      if (t.rest > 0.0f) {
+        // each side from the listed tokens' mass where that is the smaller part
+        const double lt = t.sum < 0.5f ? log1p(-(double)t.sum) : log((double)t.rest);
         const double ql = (double)r.zl / (double)r.z;
+        double lq = -INFINITY;
         if (ql < 0.5)
-          log_qr = log1p(-ql);
-        else
-          log_qr = r.mr > -INFINITY ? ((double)r.mr - (double)r.m) * P.inv_t + log((double)r.zr) - logz : -INFINITY;
+          lq = log1p(-ql);
+        else if (r.mr > -INFINITY)
+          lq = ((double)r.mr - (double)r.m) * ((double)P.c.hi + (double)P.c.lo) + log((double)r.zr) - logz;
+        g.extra = (float)((double)t.rest * (lt - lq));
       }
-      loss = row_loss_warp(P, n, lane, (double)r.m, logz, log_qr);
+      sh[threadIdx.x] = g;
     }
-    if (lane == 0) P.row_loss[n] = loss;
   }
-  finish_total(P, kTargetWarps * 32);
+  __syncthreads();
+  finish_rows(P, base, sh);
 }
 
 }  // namespace ssv

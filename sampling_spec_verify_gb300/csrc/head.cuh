@@ -394,50 +394,75 @@ __global__ void __launch_bounds__(256) listed_grads_kernel(const ListedParams P,
 
 // ---- normalisers, row losses, their sum --------------------------------------------
 
-// 32 rows per CTA: the eight warps share the tiles, lane = row; then a warp per row.
+// 32 rows per CTA.  The tiles' statistics of a row are joined by 32 threads,
+// 8 rows at a time (64 contiguous bytes of every tile), each thread's loads
+// independent of one another; the sums are then the row's in log2.
 __global__ void __launch_bounds__(256) head_finish_kernel(const FinishParams P, const float2* part, int tiles_n,
                                                           float* lse_out, float* lse2) {
-  __shared__ float2 sh[8][32];
-  __shared__ double lse_sh[32];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long base = (long long)blockIdx.x * 32, n = base + lane;
-  float m = -INFINITY, sum = 0.0f;
-  if (n < P.N) {
-    for (int t = w; t < tiles_n; t += 8) {
-      const float2 v = __ldcs(part + (long long)t * P.N + n);
-      const float nm = max_nan(m, v.x);
-      if (nm > -INFINITY) {
-        sum = (m > -INFINITY ? sum * exp2f(m - nm) : 0.0f) + (v.x > -INFINITY ? v.y * exp2f(v.x - nm) : 0.0f);
-        m = nm;
-      } else if (!(nm < INFINITY)) {
+  __shared__ float2 sh[32][8];
+  __shared__ RowLog logs[32];
+  const int r8 = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const long long base = (long long)blockIdx.x * 32;
+  for (int q = 0; q < 32; q += 8) {
+    const long long n = base + q + r8;
+    float m = -INFINITY, sum = 0.0f;
+    if (n < P.N) {
+      for (int t0 = g; t0 < tiles_n; t0 += 32 * 8) {
+        float2 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int t = t0 + 32 * j;
+          v[j] = t < tiles_n ? __ldcs(part + (long long)t * P.N + n) : make_float2(-INFINITY, 0.0f);
+        }
+        float nm = m;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) nm = max_nan(nm, v[j].x);
+        if (nm > -INFINITY && nm < INFINITY) {
+          sum *= exp2f(m - nm);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum += v[j].y * exp2f(v[j].x - nm);
+        }
         m = nm;
       }
     }
+    __syncthreads();
+    sh[g][r8] = make_float2(m, sum);
+    __syncthreads();
+    if (threadIdx.x < 64) {  // eight threads a row
+      const int row = threadIdx.x >> 3, i = threadIdx.x & 7;
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max_nan(top, sh[i + 8 * j][row].x);
+#pragma unroll
+      for (int o = 4; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      float z = 0.0f;
+      const bool fine = top > -INFINITY && top < INFINITY;
+      if (fine) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z += sh[i + 8 * j][row].y * exp2f(sh[i + 8 * j][row].x - top);
+      }
+#pragma unroll
+      for (int o = 4; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+      const long long n2 = base + q + row;
+      if (i == 0 && n2 < P.N) {
+        const double l2 = fine ? (double)top + (double)log2f(z) : NAN;
+        if (!fine && P.keep[n2]) raise(P.status, SPEC_DEV_BAD_LOGITS);
+        const double l = l2 * 0.69314718055994530942;
+        lse2[n2] = (float)l2;
+        if (lse_out) lse_out[n2] = (float)l;
+        const RowTeacher t = P.row[n2];
+        const double b = l - (double)t.shift - (double)t.shift_lo;
+        RowLog o;
+        o.m = 0.0f;
+        o.base.hi = (float)b;
+        o.base.lo = (float)(b - (double)o.base.hi);
+        o.extra = 0.0f;
+        logs[q + row] = o;
+      }
+    }
   }
-  sh[w][lane] = make_float2(m, sum);
   __syncthreads();
-  if (w == 0 && n < P.N) {
-    m = -INFINITY;
-    for (int i = 0; i < 8; ++i) m = max_nan(m, sh[i][lane].x);
-    double z = 0.0;
-    for (int i = 0; i < 8; ++i)
-      if (sh[i][lane].x > -INFINITY) z += (double)sh[i][lane].y * exp2((double)(sh[i][lane].x - m));
-    const bool bad = !(m < INFINITY) || !(m > -INFINITY);
-    const double l2 = bad ? NAN : (double)m + log2(z);
-    if (bad && P.keep[n]) raise(P.status, SPEC_DEV_BAD_LOGITS);
-    const double l = l2 * 0.69314718055994530942;
-    lse_sh[lane] = l;
-    lse2[n] = (float)l2;
-    if (lse_out) lse_out[n] = (float)l;
-  }
-  __syncthreads();
-  for (int r = w; r < 32; r += 8) {
-    const long long row = base + r;
-    if (row >= P.N) break;
-    const float loss = P.keep[row] ? row_loss_warp(P, row, lane, 0.0, lse_sh[r], 0.0) : 0.0f;
-    if (lane == 0) P.row_loss[row] = loss;
-  }
-  finish_total(P, 256);
+  finish_rows(P, base, logs);
 }
 
 // grad_hidden = grad_mul * sum of the partials, in slot order.

@@ -21,7 +21,7 @@ namespace {
 
 using ssv::count_launch;
 
-constexpr double kLog2e = 1.4426950408889634074;
+constexpr double kLog2e = 1.4426950408889634074, kLn2 = 0.69314718055994530942;
 constexpr int kMaxDevices = 64;
 
 spec_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA; }
@@ -105,15 +105,9 @@ struct Carver {
   }
 };
 
-// Factor of an exponent in powers of two, hi rounded down so that lo > 0 and
-// -inf * lo stays -inf.
-void split_scale(double s, float* hi, float* lo) {
-  float h = (float)s;
-  if ((double)h > s) h = std::nextafter(h, 0.0f);
-  float l = (float)(s - (double)h);
-  if (!(l > 0.0f)) l = 1e-30f;
-  *hi = h;
-  *lo = l;
+ssv::F2 split(double v) {
+  const float hi = (float)v;
+  return {hi, (float)(v - (double)hi)};
 }
 
 bool temperature_ok(float t) { return t > 0.0f && std::isfinite(t) && std::isfinite((float)(kLog2e / (double)t)); }
@@ -128,6 +122,7 @@ struct DistillWs {
   float* zi;
   ssv::RowNorm* norm;
   float* row_loss;
+  double* part;
   size_t total;
 };
 DistillWs distill_ws(void* base, size_t N, size_t k) {
@@ -140,41 +135,42 @@ DistillWs distill_ws(void* base, size_t N, size_t k) {
   w.zi = c.take<float>(N * k);
   w.norm = c.take<ssv::RowNorm>(N);
   w.row_loss = c.take<float>(N);
+  w.part = c.take<double>(3 * ((N + 31) / 32));
   w.total = c.used;
   return w;
 }
 
-// Slices of a row: small enough for two stages of two resident CTAs, else of
-// one, else for one stage.  Short batches spread a row over more CTAs.
+// Slices of a row: what 512 threads hold in registers, with two stages and two
+// resident CTAs; rows too long for 16 such slices stay in shared memory, with
+// two stages or one.  Short batches spread a row over more CTAs.
 struct DistillShape {
   int S = 0, nst = 0;
+  bool regs = false;
   uint32_t cap = 0;
 };
 DistillShape distill_shape(long long row_bytes, int N, int sms) {
-  const long long budget[3] = {52 * 1024, 108 * 1024, 216 * 1024};
+  const long long budget[3] = {ssv::kDVecs * ssv::kDThreads * 16, 104 * 1024, 208 * 1024};
   DistillShape d;
   for (int level = 0; level < 3 && !d.S; ++level)
     for (int s = 1; s <= ssv::kDMaxCluster; s *= 2)
-      if ((row_bytes + s - 1) / s + 32 <= budget[level]) {
+      if ((row_bytes / 16 + s - 1) / s * 16 <= budget[level]) {
         d.S = s;
+        d.regs = level == 0;
         d.nst = level == 2 ? 1 : 2;
         break;
       }
   if (!d.S) return d;
   while (d.S < 8 && (long long)N * d.S < sms && row_bytes / d.S > 8192) d.S *= 2;
-  d.cap = (uint32_t)((((row_bytes / 16) / d.S + 2) * 16 + 127) & ~127ll);
+  d.cap = (uint32_t)((((row_bytes / 16 + d.S - 1) / d.S) * 16 + 127) & ~127ll);
+  if (!d.cap) d.cap = 128;
   return d;
 }
 
-template <class E, class O>
-spec_status_t launch_distill(ssv::DistillParams P, cudaStream_t st) {
+template <class E, class O, int NV>
+spec_status_t launch_distill_nv(ssv::DistillParams P, const DistillShape& sh, const Device& d, int dev,
+                                cudaStream_t st) {
   static Residency res;
-  const void* fn = (const void*)ssv::distill_kernel<E, O>;
-  Device d;
-  int dev = 0;
-  if (!device(&d, &dev)) return SPEC_ERR_CUDA;
-  const DistillShape sh = distill_shape((long long)P.V * (long long)sizeof(E), P.N, d.sms);
-  if (!sh.S) return SPEC_ERR_UNSUPPORTED;
+  const void* fn = (const void*)ssv::distill_kernel<E, O, NV>;
   P.nst = sh.nst;
   P.cap = sh.cap;
   const int smem = (int)(sh.cap * (uint32_t)sh.nst);
@@ -192,7 +188,18 @@ spec_status_t launch_distill(ssv::DistillParams P, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return from_cuda(count_launch(cudaLaunchKernelEx(&cfg, ssv::distill_kernel<E, O>, P)));
+  return from_cuda(count_launch(cudaLaunchKernelEx(&cfg, ssv::distill_kernel<E, O, NV>, P)));
+}
+
+template <class E, class O>
+spec_status_t launch_distill(const ssv::DistillParams& P, cudaStream_t st) {
+  Device d;
+  int dev = 0;
+  if (!device(&d, &dev)) return SPEC_ERR_CUDA;
+  const DistillShape sh = distill_shape((long long)P.V * (long long)sizeof(E), P.N, d.sms);
+  if (!sh.S) return SPEC_ERR_UNSUPPORTED;
+  return sh.regs ? launch_distill_nv<E, O, ssv::kDVecs>(P, sh, d, dev, st)
+                 : launch_distill_nv<E, O, 0>(P, sh, d, dev, st);
 }
 
 spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int k, float temperature,
@@ -221,7 +228,7 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
   tp.N = N;
   tp.V = V;
   tp.k = k;
-  tp.inv_t = 1.0 / (double)temperature;
+  tp.inv_t = split(1.0 / (double)temperature);
   tp.t = ws.t;
   tp.row = ws.row;
   tp.keep = ws.keep;
@@ -240,9 +247,9 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
   P.skew = (int)((reinterpret_cast<uintptr_t>(student) & 15) / (uintptr_t)elem_size(dtype));
   if (want_grad) {
     const uintptr_t o = reinterpret_cast<uintptr_t>(grad) - (uintptr_t)P.skew * (uintptr_t)elem_size(grad_dtype);
-    P.out_vec = (o & 15) == 0;
+    P.out_vec = (o & 31) == 0 ? 32 : ((o & 15) == 0 ? 16 : 0);
   }
-  split_scale(kLog2e / (double)temperature, &P.s_hi, &P.s_lo);
+  P.s = (float)(kLog2e / (double)temperature);
   P.ids = ids;
   P.t = ws.t;
   P.row = ws.row;
@@ -272,6 +279,8 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
   F.N = N;
   F.k = k;
   F.inv_t = tp.inv_t;
+  F.c = split((double)P.s * kLn2);  // the exponents' own factor
+  F.part = ws.part;
   F.logits = logits;
   F.t = ws.t;
   F.row = ws.row;
@@ -285,7 +294,7 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
   F.row_loss = row_loss ? row_loss : ws.row_loss;
   F.scalars = ws.scalars;
   F.status = status;
-  ssv::distill_finish_kernel<<<row_grid, ssv::kTargetWarps * 32, 0, st>>>(F, ws.norm);
+  ssv::distill_finish_kernel<<<(unsigned)((N + 31) / 32), 256, 0, st>>>(F, ws.norm);
   return from_cuda(count_launch(cudaGetLastError()));
 }
 
@@ -336,6 +345,7 @@ struct HeadWs {
   float* zi;
   float* row_loss;
   float* lse2;
+  double* sums;
   float2* part;
   float* hidden;
   uint16_t* d;
@@ -352,6 +362,7 @@ HeadWs head_ws(void* base, size_t N, size_t V, size_t H, size_t k, bool gh, bool
   w.zi = c.take<float>(N * k);
   w.row_loss = c.take<float>(N);
   w.lse2 = c.take<float>(N);
+  w.sums = c.take<double>(3 * ((N + 31) / 32));
   w.part = c.take<float2>(N * ((V + 255) / 256));
   w.hidden = gh ? c.take<float>((size_t)p.splits * (size_t)p.slot_rows * H) : nullptr;
   w.d = gh || gw ? c.take<uint16_t>(N * (size_t)p.piece) : nullptr;
@@ -451,7 +462,7 @@ spec_status_t head_run(const HeadCall& c, const HeadWs& ws) {
   tp.V = c.V;
   tp.k = c.k;
   tp.ignore = c.ignore;
-  tp.inv_t = 1.0 / (double)c.temperature;
+  tp.inv_t = split(1.0 / (double)c.temperature);
   tp.t = ws.t;
   tp.row = ws.row;
   tp.keep = ws.keep;
@@ -484,6 +495,8 @@ spec_status_t head_run(const HeadCall& c, const HeadWs& ws) {
   F.N = c.N;
   F.k = c.k;
   F.inv_t = tp.inv_t;
+  F.c = split((double)P.s * kLn2);  // the exponents' own factor
+  F.part = ws.sums;
   F.logits = c.logits;
   F.t = ws.t;
   F.row = ws.row;
@@ -537,7 +550,7 @@ spec_status_t head_run(const HeadCall& c, const HeadWs& ws) {
     L.v0 = v0;
     L.C = C;
     L.ld = plan.piece;
-    L.s = s;
+    L.s = (double)P.s;
     L.store_scale = store_scale;
     ssv::listed_grads_kernel<E>
         <<<(unsigned)((entries + 255) / 256), 256, 0, st>>>(L, reinterpret_cast<E*>(ws.d));

@@ -21,10 +21,10 @@ constexpr int kMaxEntries = 256;  // listed teacher tokens per row
 constexpr int kTargetWarps = 8;   // rows per CTA of the kernels with a warp per row
 constexpr int kHashSlots = 512;   // per row, at least twice kMaxEntries
 
-struct RowTeacher {
-  double shift;  // log of the teacher's normaliser: log t_i = x_i / T - shift
-  float sum;     // sum of t_i
-  float rest;    // t_r
+struct __align__(16) RowTeacher {
+  float shift, shift_lo;  // log of the teacher's normaliser: log t_i = x_i / T - (shift + shift_lo)
+  float sum;              // sum of t_i
+  float rest;             // t_r
 };
 
 struct RowNorm {  // of the student: sums of 2^((z - m) s), s = log2(e) / T
@@ -41,6 +41,18 @@ struct LossScalars {
   float grad_mul;  // factor of the stored logit gradients in the results
 };
 
+// Maximum of a float over the warp; NaN if any lane holds NaN.
+__device__ __forceinline__ float redux_max_nan(float v) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // ---- elements ---------------------------------------------------------------------
 
 template <class E>
@@ -56,6 +68,26 @@ struct Elem<__nv_bfloat16> {
       x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
     }
   }
+  // The 8 values as 4 packed pairs in element order (exact widening).
+  __device__ static __forceinline__ void pairs(const uint4& w, f32x2 (&p)[4]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = f2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
+  }
+  // Elementwise maximum of two vectors; NaN passes on.
+  __device__ static __forceinline__ uint4 vmax(const uint4& a, const uint4& b) {
+    return make_uint4(max2(a.x, b.x), max2(a.y, b.y), max2(a.z, b.z), max2(a.w, b.w));
+  }
+  __device__ static __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  __device__ static __forceinline__ float hmax(const uint4& w) {
+    const uint32_t m = max2(max2(w.x, w.y), max2(w.z, w.w));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  }
+  static constexpr uint32_t kLow = 0xFF80FF80u;  // -inf in every element
   __device__ static __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
   __device__ static __forceinline__ __nv_bfloat16 neg_inf() { return __ushort_as_bfloat16(0xFF80u); }
   __device__ static __forceinline__ uint32_t pack(float a, float b) {
@@ -76,6 +108,27 @@ struct Elem<__half> {
       x[2 * i + 1] = f.y;
     }
   }
+  __device__ static __forceinline__ void pairs(const uint4& w, f32x2 (&p)[4]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+      p[i] = f2(f.x, f.y);
+    }
+  }
+  __device__ static __forceinline__ uint4 vmax(const uint4& a, const uint4& b) {
+    return make_uint4(max2(a.x, b.x), max2(a.y, b.y), max2(a.z, b.z), max2(a.w, b.w));
+  }
+  __device__ static __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __half2 m = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  __device__ static __forceinline__ float hmax(const uint4& w) {
+    const uint32_t m = max2(max2(w.x, w.y), max2(w.z, w.w));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    return max_nan(f.x, f.y);
+  }
+  static constexpr uint32_t kLow = 0xFC00FC00u;
   __device__ static __forceinline__ float to_f32(__half v) { return __half2float(v); }
   __device__ static __forceinline__ __half neg_inf() { return __ushort_as_half(0xFC00u); }
   __device__ static __forceinline__ uint32_t pack(float a, float b) {
@@ -91,6 +144,20 @@ struct Elem<float> {
     x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y);
     x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
   }
+  __device__ static __forceinline__ void pairs(const uint4& w, f32x2 (&p)[2]) {
+    p[0] = f2(__uint_as_float(w.x), __uint_as_float(w.y));
+    p[1] = f2(__uint_as_float(w.z), __uint_as_float(w.w));
+  }
+  __device__ static __forceinline__ uint4 vmax(const uint4& a, const uint4& b) {
+    return make_uint4(max1(a.x, b.x), max1(a.y, b.y), max1(a.z, b.z), max1(a.w, b.w));
+  }
+  __device__ static __forceinline__ uint32_t max1(uint32_t a, uint32_t b) {
+    return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+  }
+  __device__ static __forceinline__ float hmax(const uint4& w) {
+    return __uint_as_float(max1(max1(w.x, w.y), max1(w.z, w.w)));
+  }
+  static constexpr uint32_t kLow = 0xFF800000u;
   __device__ static __forceinline__ float to_f32(float v) { return v; }
   __device__ static __forceinline__ float neg_inf() { return -INFINITY; }
   __device__ static __forceinline__ float from_f32(float v) { return v; }
@@ -98,26 +165,35 @@ struct Elem<float> {
 
 // ---- arithmetic ---------------------------------------------------------------------
 
-// 2^(d (hi + lo)) to a few ulp: the rounding of the product is carried along.
-// hi + lo = log2(e) / T with lo > 0 (the host rounds hi down), so that a logit
-// of -inf stays -inf through d * hi + d * lo.
-__device__ __forceinline__ float exp2_scaled(float d, float hi, float lo) {
-  const float p = d * hi;
-  if (!(fabsf(p) < INFINITY)) return p < 0.0f ? 0.0f : p;  // d = -inf; NaN and +inf pass on
-  const float e = fmaf(d, lo, fmaf(d, hi, -p));
-  return exp2f(p) * fmaf(e, 0.69314718f, 1.0f);
+__device__ __forceinline__ f32x2 f2_mul(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
-// Maximum of a float over the warp; NaN if any lane holds NaN.
-__device__ __forceinline__ float redux_max_nan(float v) {
-  float r;
-  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
+// 2^(d s) to a few ulp: the rounding of the product is carried along.
+__device__ __forceinline__ float exp2_scaled(float d, float s) {
+  const float p = d * s;
+  if (!(fabsf(p) < INFINITY)) return p < 0.0f ? 0.0f : p;  // d = -inf; NaN and +inf pass on
+  return exp2f(p) * fmaf(fmaf(d, s, -p), 0.69314718f, 1.0f);
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
+
+// A sum of two floats kept as value and rounding error.
+struct F2 {
+  float hi, lo;
+};
+__device__ __forceinline__ F2 two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ F2 two_mul(float a, F2 b) {
+  const float p = a * b.hi;
+  return {p, fmaf(a, b.lo, fmaf(a, b.hi, -p))};
+}
+__device__ __forceinline__ F2 pair_add(F2 a, F2 b) {
+  F2 s = two_sum(a.hi, b.hi);
+  s.lo += a.lo + b.lo;
+  return s;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -143,7 +219,7 @@ struct TargetParams {
   const float* lse;      // [N] teacher normaliser, or null
   int N, V, k;
   int ignore;            // label of rows that are left out
-  double inv_t;
+  F2 inv_t;
   float* t;              // [N, k] out: teacher probabilities, 0 in unused slots
   RowTeacher* row;       // [N] out
   uint8_t* keep;         // [N] out: the row counts
@@ -156,8 +232,9 @@ struct TargetParams {
 // and is reported.  Duplicates are found with a hash set in shared memory: k
 // inserts, against k^2 / 2 compares.
 //
-// log t_i is formed in fp64 (a few adds and multiplies per entry) because the
-// loss is a small difference of such logarithms; the exponential is fp32.
+// log t_i is formed with its rounding carried along, because the loss is a
+// small difference of such logarithms.  (In fp64 the same cost 7 us of the
+// 2 fused operations a clock that an SM has.)
 __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const TargetParams P) {
   __shared__ int hash[kTargetWarps][kHashSlots];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -172,7 +249,7 @@ __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const Target
       if (!ok && id != P.ignore) raise(P.status, SPEC_DEV_BAD_TOKEN);
       P.keep[n] = ok;
       P.t[n] = ok ? 1.0f : 0.0f;
-      P.row[n] = RowTeacher{0.0, ok ? 1.0f : 0.0f, 0.0f};
+      P.row[n] = RowTeacher{0.0f, 0.0f, ok ? 1.0f : 0.0f, 0.0f};
     }
     return;
   }
@@ -211,7 +288,7 @@ __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const Target
   any = __any_sync(0xffffffffu, any);
   m = redux_max_nan(m);
   uint32_t bits = bad ? SPEC_DEV_BAD_TOKEN : 0u;
-  double shift = 0.0;
+  F2 shift{0.0f, 0.0f};
   bool ok = any && !bad;
   const float lse = P.lse ? P.lse[n] : 0.0f;
   if (ok && (!(m < INFINITY) || (P.lse ? !(fabsf(lse) < INFINITY) : m == -INFINITY))) {
@@ -220,12 +297,15 @@ __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const Target
   }
   float sum = 0.0f;
   if (ok) {
-    shift = P.lse ? (double)lse : (double)m * P.inv_t;
+    shift = P.lse ? F2{lse, 0.0f} : two_mul(m, P.inv_t);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {  // x becomes the (unnormalised) probability
-      const double d = (double)x[j] * P.inv_t - shift;  // -inf where unused
-      const float hi = (float)d;
-      x[j] = hi > -INFINITY ? expf(hi) * (1.0f + (float)(d - (double)hi)) : 0.0f;
+      if (x[j] > -INFINITY) {
+        const F2 d = pair_add(two_mul(x[j], P.inv_t), F2{-shift.hi, -shift.lo});
+        x[j] = expf(d.hi) * (1.0f + d.lo);
+      } else {
+        x[j] = 0.0f;
+      }
       sum += x[j];
     }
     sum = warp_sum(sum);
@@ -233,7 +313,7 @@ __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const Target
       const float inv = 1.0f / sum;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) x[j] *= inv;
-      shift += log((double)sum);
+      shift = pair_add(shift, F2{logf(sum), 0.0f});
     }
   }
 #pragma unroll
@@ -243,7 +323,7 @@ __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const Target
   }
   if (lane == 0) {
     raise(P.status, bits);
-    RowTeacher r{shift, 0.0f, 0.0f};
+    RowTeacher r{shift.hi, shift.lo, 0.0f, 0.0f};
     if (ok) {
       r.sum = P.lse ? sum : 1.0f;
       const float rest = 1.0f - sum;
@@ -259,7 +339,8 @@ __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const Target
 
 struct FinishParams {
   int N, k;
-  double inv_t;
+  F2 inv_t;             // teacher side
+  F2 c;                 // student side: log q_i = (z_i - m) c - log Z
   const float* logits;  // [N, k] teacher logits, or null (cross entropy)
   const float* t;       // [N, k]
   const RowTeacher* row;
@@ -269,64 +350,95 @@ struct FinishParams {
   int mean;
   float grad_scale;     // times 1 / T
   float store_scale;    // of the stored logit gradients (head losses)
+  double* part;         // [CTAs, 3] sums of a CTA's rows
   float* loss;          // [1]
   float* row_loss;      // [N]
   LossScalars* scalars;
   uint32_t* status;
 };
 
-// Loss of row n, by one warp (every lane gets it): log q_i = (z_i - m) / T -
-// logz, log_qr the log of the unlisted tokens' mass.  The maximum is taken off
-// first: rows masked with the type's lowest value would lose logz beside it.
-__device__ __forceinline__ float row_loss_warp(const FinishParams& P, long long n, int lane, double m, double logz,
-                                               double log_qr) {
-  const RowTeacher r = P.row[n];
-  float acc = 0.0f;
-  for (int i = lane; i < P.k; i += 32) {
-    const float t = P.t[n * P.k + i];
-    if (t > 0.0f) {
-      const double lt = P.logits ? (double)P.logits[n * P.k + i] * P.inv_t - r.shift : 0.0;
-      acc += t * (float)(lt - (((double)P.zi[n * P.k + i] - m) * P.inv_t - logz));
+// What one thread prepares of a row.
+struct RowLog {
+  float m;        // taken off the student's logits first: rows masked with a
+                  // type's lowest value would lose log Z beside it
+  F2 base;        // log Z - (log of the teacher's normaliser)
+  float extra;    // t_r (log t_r - log q_r)
+};
+
+// Row losses of the 32 rows from `base`, eight warps, after lane r of warp 0
+// has put row base + r into sh[r]; then the CTA's sums, and in the last CTA to
+// arrive the call's, all in fixed orders.  256 threads.
+//   L_n = sum_i t_i ((x_i / T - shift) - ((z_i - m) c - log Z)) + extra
+// with every difference carrying its rounding: the terms are small differences
+// of logarithms near 10.
+__device__ __forceinline__ void finish_rows(const FinishParams& P, long long base, const RowLog* sh) {
+  __shared__ float row_sh[32];
+  __shared__ uint32_t last;
+  __shared__ double red[3][8];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = w; r < 32; r += 8) {
+    const long long n = base + r;
+    if (n >= P.N) break;
+    float loss = 0.0f;
+    if (P.keep[n]) {
+      const RowLog g = sh[r];
+      float acc = 0.0f;
+#pragma unroll 4
+      for (int i = lane; i < P.k; i += 32) {
+        const float t = P.t[n * P.k + i], z = P.zi[n * P.k + i];
+        const float x = P.logits ? P.logits[n * P.k + i] : 0.0f;
+        if (t > 0.0f) {
+          const F2 d = two_sum(z, -g.m);
+          F2 lq = two_mul(d.hi, P.c);
+          lq.lo = fmaf(d.lo, P.c.hi, lq.lo);
+          F2 v = pair_add(two_mul(x, P.inv_t), F2{-lq.hi, -lq.lo});
+          v = pair_add(v, g.base);
+          acc = fmaf(t, lq.hi > -INFINITY ? v.hi + v.lo : INFINITY, acc);
+        }
+      }
+      loss = warp_sum(acc) + g.extra;
+      if (isnan(g.base.hi)) loss = NAN;  // also where the entries weigh nothing
+    }
+    if (lane == 0) {
+      P.row_loss[n] = loss;
+      row_sh[r] = loss;
     }
   }
-  acc = warp_sum(acc);
-  if (r.rest > 0.0f) {
-    const double lr = r.sum < 0.5f ? log1p(-(double)r.sum) : log((double)r.rest);
-    acc += (float)((double)r.rest * (lr - log_qr));
-  }
-  if (isnan(logz)) acc = NAN;  // also where the entries weigh nothing
-  return acc;
-}
-
-// The last CTA to arrive sums the rows in one fixed order, in fp64.
-__device__ __forceinline__ void finish_total(const FinishParams& P, int threads) {
-  __shared__ uint32_t last;
-  __shared__ double red[3][32];
-  __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(&P.scalars->ticket, 1u) == gridDim.x - 1;
+  if (w == 0) {
+    const long long n = base + lane;
+    const bool on = n < P.N && P.keep[n];
+    const float rw = on ? (P.weight ? P.weight[n] : 1.0f) : 0.0f;
+    const double sum = warp_sum(on ? (double)rw * (double)row_sh[lane] : 0.0);
+    const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, on));
+    const float wmax = redux_max_nan(fabsf(rw));
+    if (lane == 0) {
+      double* p = P.part + 3ll * blockIdx.x;
+      p[0] = sum, p[1] = (double)cnt, p[2] = (double)wmax;
+      __threadfence();
+      last = atomicAdd(&P.scalars->ticket, 1u) == gridDim.x - 1;
+    }
+  }
   __syncthreads();
   if (!last) return;
   __threadfence();
   double sum = 0.0, cnt = 0.0;
   float wmax = 0.0f;
-  for (int n = threadIdx.x; n < P.N; n += threads) {
-    if (!P.keep[n]) continue;
-    const float w = P.weight ? P.weight[n] : 1.0f;
-    sum += (double)w * (double)__ldcg(P.row_loss + n);
-    cnt += 1.0;
-    wmax = max_nan(wmax, fabsf(w));
+  for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) {
+    const double* p = P.part + 3ll * i;
+    sum += __ldcg(p);
+    cnt += __ldcg(p + 1);
+    wmax = max_nan(wmax, (float)__ldcg(p + 2));
   }
   sum = warp_sum(sum);
   cnt = warp_sum(cnt);
   wmax = redux_max_nan(wmax);
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = threads >> 5;
   if (lane == 0) red[0][w] = sum, red[1][w] = cnt, red[2][w] = (double)wmax;
   __syncthreads();
   if (threadIdx.x == 0) {
     sum = cnt = 0.0;
     wmax = 0.0f;
-    for (int i = 0; i < nw; ++i) sum += red[0][i], cnt += red[1][i], wmax = max_nan(wmax, (float)red[2][i]);
+    for (int i = 0; i < 8; ++i) sum += red[0][i], cnt += red[1][i], wmax = max_nan(wmax, (float)red[2][i]);
     const double den = P.mean ? (cnt > 0.0 ? cnt : 1.0) : 1.0;
     P.loss[0] = (float)(sum / den);
     P.scalars->count = (uint32_t)cnt;
