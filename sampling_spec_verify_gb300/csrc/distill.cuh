@@ -25,10 +25,10 @@
 
 namespace ssv {
 
-constexpr int kDThreads = 512;
+constexpr int kDThreads = 256;
 constexpr int kDWarps = kDThreads / 32;
 constexpr int kDMaxCluster = 16;
-constexpr int kDVecs = 6;  // vectors of a slice held by a thread
+constexpr int kDVecs = 10;  // vectors of a slice held by a thread
 
 struct DistillParams {
   const void* z;
@@ -37,6 +37,7 @@ struct DistillParams {
   int nst;            // shared-memory stages: rows of this cluster in flight
   uint32_t cap;       // bytes of a stage
   int skew;           // elements by which the base lies past a 16-byte boundary
+  int odd;            // rows may start off one
   int out_vec;        // bytes that a gradient store may write at a time: 32, 16 or (0) one element
   float s;            // log2(e) / T
   const int32_t* ids; // [N, k]
@@ -120,7 +121,7 @@ __device__ __forceinline__ Slice slice_of(long long n, int V, int skew, uint32_t
 }
 
 template <class E, class O, int NV>
-__global__ void __launch_bounds__(kDThreads, NV ? 2 : 1) distill_kernel(const __grid_constant__ DistillParams P) {
+__global__ void __launch_bounds__(kDThreads, NV ? 3 : 1) distill_kernel(const __grid_constant__ DistillParams P) {
   using T = Elem<E>;
   constexpr int PV = T::PV;
   constexpr bool kGrad = !std::is_same<O, NoGrad>::value;
@@ -131,6 +132,8 @@ __global__ void __launch_bounds__(kDThreads, NV ? 2 : 1) distill_kernel(const __
   __shared__ float4 box[2][kDMaxCluster * kDWarps];
   __shared__ __align__(8) uint64_t bars[4];      // stages, boxes
   __shared__ float edge[16];  // odd elements: 0..7 before, 8..15 after the aligned part
+  __shared__ float4 grad_of;  // {mr, cb, factor of a listed token's 2^((z - m) s), m}, see below
+  __shared__ float grad_w;    // the row's coefficient
   __shared__ uint32_t shared_count[kDWarps];
   __shared__ uint32_t abort_flag;
 
@@ -160,7 +163,8 @@ __global__ void __launch_bounds__(kDThreads, NV ? 2 : 1) distill_kernel(const __
                 policy);
   };
 
-  // Per-row values, loaded a row ahead and independently of one another.
+  // Per-row values, loaded a row ahead and independently of one another; the
+  // row's own scalars by warp 0 alone.
   struct Row {
     int id;
     float t, w, sum, rest, edge;
@@ -172,13 +176,15 @@ __global__ void __launch_bounds__(kDThreads, NV ? 2 : 1) distill_kernel(const __
       r.live = P.keep[n];
       if (tid < P.k) {
         r.id = P.ids[n * P.k + tid];
-        r.t = P.t[n * P.k + tid];
+        if (kGrad) r.t = P.t[n * P.k + tid];
       }
-      const RowTeacher rt = P.row[n];
-      r.sum = rt.sum;
-      r.rest = rt.rest;
-      r.w = P.weight ? P.weight[n] : 1.0f;
-      if (tid < 16) {
+      if (kGrad && wid == 0) {
+        const RowTeacher rt = P.row[n];
+        r.sum = rt.sum;
+        r.rest = rt.rest;
+        r.w = P.weight ? P.weight[n] : 1.0f;
+      }
+      if (P.odd && tid < 16) {
         const Slice s = slice_of<PV>(n, P.V, P.skew, rank, S);
         if (tid < s.head) r.edge = T::to_f32(z[s.f0 + tid]);
         if (tid >= 8 && tid - 8 < s.tail) r.edge = T::to_f32(z[s.f0 + s.a1 + tid - 8]);
@@ -211,9 +217,11 @@ __global__ void __launch_bounds__(kDThreads, NV ? 2 : 1) distill_kernel(const __
   uint32_t it = 0, ex = 0, failed = 0;
   OG* late = nullptr;  // a listed token's gradient, written after the next barrier: its place
   float late_v = 0.0f;  // is first written, as 0, by the thread that holds its vector
+  Slice s = slice_of<PV>(c, P.V, P.skew, rank, S);
   for (long long n = c; n < P.N; n += G, ++it) {
     const int st = P.nst == 2 ? (int)(it & 1) : 0;
-    const Slice s = slice_of<PV>(n, P.V, P.skew, rank, S);
+    if (P.odd) s = slice_of<PV>(n, P.V, P.skew, rank, S);
+    s.f0 = n * P.V;
     const int nvl = s.v1 - s.v0;
     OG* out = kGrad ? static_cast<OG*>(P.grad) + s.f0 : nullptr;
     const long long n_fetch = n + (long long)P.nst * G;
@@ -241,8 +249,7 @@ __global__ void __launch_bounds__(kDThreads, NV ? 2 : 1) distill_kernel(const __
     const uint64_t limit = failed ? 100000ull : 2000000000ull;
     if (!mbar_wait_bounded(bar0 + 8 * st, (par >> st) & 1u, limit)) failed = abort_flag = 1;
     par ^= 1u << st;
-    const bool odd = s.a0 > 0 || s.a1 < P.V;
-    if (odd) {
+    if (P.odd) {
       if (tid < 16) edge[tid] = cur.edge;
       __syncthreads();
     }
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(kDThreads, NV ? 2 : 1) distill_kernel(const __
         v[j] = i < nvl ? vec[i] : low;
       }
     }
-    const float my_edge = odd && tid < 16 ? edge[tid] : -INFINITY;
+    const float my_edge = P.odd && tid < 16 ? edge[tid] : -INFINITY;
     const Row next = row_values(n + G);  // travels while this row is worked on
     if constexpr (NV > 0) {
 #pragma unroll
@@ -323,17 +330,22 @@ __global__ void __launch_bounds__(kDThreads, NV ? 2 : 1) distill_kernel(const __
       } else {
         for (int i = tid; i < nvl; i += kDThreads) add(vec[i]);
       }
-      sum = warp_sum(f2_hsum(f2_add(a0, a1)) + exp2_scaled(my_edge - m, P.s));
+      sum = f2_hsum(f2_add(a0, a1));
+      if (P.odd) sum += exp2_scaled(my_edge - m, P.s);
+      sum = warp_sum(sum);
     } else if (!(m < INFINITY)) {  // NaN or +inf among the logits
       sum = NAN;
       m = 0.0f;
     }
-    float mk = redux_max_nan(my_z), sk = 0.0f;
-    if (mk > -INFINITY && mk < INFINITY) {
-      sk = warp_sum(exp2_scaled(my_z - mk, P.s));
-    } else if (!(mk < INFINITY)) {
-      sk = NAN;
-      mk = 0.0f;
+    float mk = -INFINITY, sk = 0.0f;
+    if (wid * 32 < P.k) {
+      mk = redux_max_nan(my_z);
+      if (mk > -INFINITY && mk < INFINITY) {
+        sk = warp_sum(exp2_scaled(my_z - mk, P.s));
+      } else if (!(mk < INFINITY)) {
+        sk = NAN;
+        mk = 0.0f;
+      }
     }
     if (lane < (int)S)
       st_async_f4(map_rank(smem_addr(&box[slot][rank * kDWarps + wid]), lane), m, sum, mk, sk,
@@ -344,10 +356,11 @@ __global__ void __launch_bounds__(kDThreads, NV ? 2 : 1) distill_kernel(const __
       fetch(n_fetch, st, fetch_on);
     }
 
-    // the cluster's pairs, joined by every warp in the same order
-    if (!mbar_wait_bounded(xbar0 + 8 * slot, xpar, limit)) failed = abort_flag = 1;
-    RowNorm r;
-    {
+    // Warp 0 joins the cluster's pairs, in the same order in every CTA.  (Done
+    // by every warp, this was a third of the kernel's instructions.)
+    if (wid == 0) {
+      if (!mbar_wait_bounded(xbar0 + 8 * slot, xpar, limit)) failed = abort_flag = 1;
+      __syncwarp();
       const int entries = (int)S * kDWarps;
       float mu = -INFINITY, ml = -INFINITY;
       for (int i = lane; i < entries; i += 32) {
@@ -365,34 +378,42 @@ __global__ void __launch_bounds__(kDThreads, NV ? 2 : 1) distill_kernel(const __
       }
       su = warp_sum(su);
       sl = warp_sum(sl);
+      const bool some = mu > -INFINITY;
+      RowNorm r;
       r.m = fmaxf(mu, ml);
       r.mr = mu;
       r.zr = su;
+      const float rest_scale = some ? exp2_scaled(mu - r.m, P.s) : 0.0f;
       r.zl = ml > -INFINITY ? sl * exp2_scaled(ml - r.m, P.s) : 0.0f;
-      r.z = (mu > -INFINITY ? su * exp2_scaled(mu - r.m, P.s) : 0.0f) + r.zl;
+      r.z = (some ? su * rest_scale : 0.0f) + r.zl;
       if (!(r.m > -INFINITY)) r.z = NAN;  // no finite logit
-    }
-    if (rank == 0 && tid == 0) {
-      P.norm[n] = r;
-      if (!(r.z < INFINITY)) raise(P.status, SPEC_DEV_BAD_LOGITS);
+      if (rank == 0 && lane == 0) {
+        P.norm[n] = r;
+        if (!(r.z < INFINITY)) raise(P.status, SPEC_DEV_BAD_LOGITS);
+      }
+      if (kGrad && lane == 0) {
+        const float coef = coef0 * cur.w;
+        const float mass = cur.sum + cur.rest;
+        const float inv_z = 1.0f / r.z;
+        float cb;  // factor of 2^((z - mr) s) for tokens that are not listed
+        if (P.tail) {
+          const float ql = r.zl * inv_z;
+          const float diff = ql < 0.5f ? cur.sum - mass * ql : mass * (r.zr * rest_scale * inv_z) - cur.rest;
+          cb = some ? coef * diff / r.zr : coef * (r.z - r.z);
+        } else {
+          cb = coef * mass * rest_scale * inv_z;
+        }
+        grad_of = make_float4(some ? mu : 0.0f, cb, mass * inv_z, r.m);
+        grad_w = coef;
+      }
     }
 
     if (kGrad) {
-      const float coef = coef0 * cur.w;
-      const float mass = cur.sum + cur.rest;
-      const float inv_z = 1.0f / r.z;
-      const bool some = r.mr > -INFINITY;
-      const float rest_scale = some ? exp2_scaled(r.mr - r.m, P.s) : 0.0f;
-      const float mr = some ? r.mr : 0.0f;
-      float cb;  // factor of 2^((z - mr) s) for tokens that are not listed
-      if (P.tail) {
-        const float ql = r.zl * inv_z;
-        const float diff = ql < 0.5f ? cur.sum - mass * ql : mass * (r.zr * rest_scale * inv_z) - cur.rest;
-        cb = some ? coef * diff / r.zr : coef * (r.z - r.z);
-      } else {
-        cb = coef * mass * rest_scale * inv_z;
-      }
-      const f32x2 s2 = f2(P.s, P.s), m2 = f2(-mr, -mr), c2 = f2(cb, cb);
+      __syncthreads();
+      const float4 go = grad_of;
+      const float coef = grad_w;
+      const f32x2 s2 = f2(P.s, P.s), m2 = f2(-go.x, -go.x), c2 = f2(go.y, go.y);
+      OG* dst = out + s.a0 + (s.v0 + tid) * PV;
       auto grads = [&](const uint4& u, int i) {
         f32x2 p[PV / 2];
         T::pairs(u, p);
@@ -402,25 +423,23 @@ __global__ void __launch_bounds__(kDThreads, NV ? 2 : 1) distill_kernel(const __
           f2_split(f2_mul(f2_add(p[j], m2), s2), x, y);
           p[j] = f2_mul(f2(ex2(x), ex2(y)), c2);
         }
-        store_grads<OG, PV>(out + s.a0 + (s.v0 + i) * PV, p, P.out_vec);
+        store_grads<OG, PV>(dst + i * PV, p, P.out_vec);
       };
       if constexpr (NV > 0) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int i = tid + j * kDThreads;
-          if (i < nvl) grads(v[j], i);
-        }
+        for (int j = 0; j < NV; ++j)
+          if (tid + j * kDThreads < nvl) grads(v[j], j * kDThreads);
       } else {
-        for (int i = tid; i < nvl; i += kDThreads) grads(vec[i], i);
+        for (int i = 0; tid + i < nvl; i += kDThreads) grads(vec[tid + i], i);
       }
-      if (tid < 16) {
-        const float g = exp2_scaled(my_edge - mr, P.s) * cb;
+      if (P.odd && tid < 16) {
+        const float g = exp2_scaled(my_edge - go.x, P.s) * go.y;
         if (tid < s.head) out[tid] = Elem<OG>::from_f32(g);
         if (tid >= 8 && tid - 8 < s.tail) out[s.a1 + tid - 8] = Elem<OG>::from_f32(g);
       }
       if (mine) {
         late = out + cur.id;
-        late_v = coef * (mass * (exp2_scaled(my_z - r.m, P.s) * inv_z) - cur.t);
+        late_v = coef * (exp2_scaled(my_z - go.w, P.s) * go.z - cur.t);
       }
     }
     if constexpr (NV == 0) {

@@ -156,7 +156,7 @@ DistillShape distill_shape(long long row_bytes, int N, int sms) {
       if ((row_bytes / 16 + s - 1) / s * 16 <= budget[level]) {
         d.S = s;
         d.regs = level == 0;
-        d.nst = level == 2 ? 1 : 2;
+        d.nst = level == 1 ? 2 : 1;
         break;
       }
   if (!d.S) return d;
@@ -245,6 +245,7 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
   P.V = V;
   P.k = k;
   P.skew = (int)((reinterpret_cast<uintptr_t>(student) & 15) / (uintptr_t)elem_size(dtype));
+  P.odd = P.skew != 0 || ((long long)V * elem_size(dtype)) % 16 != 0;
   if (want_grad) {
     const uintptr_t o = reinterpret_cast<uintptr_t>(grad) - (uintptr_t)P.skew * (uintptr_t)elem_size(grad_dtype);
     P.out_vec = (o & 31) == 0 ? 32 : ((o & 15) == 0 ? 16 : 0);

@@ -171,11 +171,12 @@ __device__ __forceinline__ f32x2 f2_mul(f32x2 a, f32x2 b) {
   return r;
 }
 
-// 2^(d s) to a few ulp: the rounding of the product is carried along.
+// 2^(d s) within 2^-21: the rounding of the product is carried along.  d = -inf
+// gives 0; NaN and +inf pass on.
 __device__ __forceinline__ float exp2_scaled(float d, float s) {
   const float p = d * s;
-  if (!(fabsf(p) < INFINITY)) return p < 0.0f ? 0.0f : p;  // d = -inf; NaN and +inf pass on
-  return exp2f(p) * fmaf(fmaf(d, s, -p), 0.69314718f, 1.0f);
+  const float e = fabsf(p) < INFINITY ? fmaf(d, s, -p) : 0.0f;
+  return ex2(p) * fmaf(e, 0.69314718f, 1.0f);
 }
 
 // A sum of two floats kept as value and rounding error.
