@@ -121,7 +121,7 @@ __device__ __forceinline__ Slice slice_of(long long n, int V, int skew, uint32_t
 }
 
 template <class E, class O, int NV>
-__global__ void __launch_bounds__(kDThreads, NV ? 3 : 1) distill_kernel(const __grid_constant__ DistillParams P) {
+__global__ void __launch_bounds__(kDThreads, NV == 0 ? 1 : (std::is_same<O, NoGrad>::value ? 4 : 3)) distill_kernel(const __grid_constant__ DistillParams P) {
   using T = Elem<E>;
   constexpr int PV = T::PV;
   constexpr bool kGrad = !std::is_same<O, NoGrad>::value;
@@ -455,37 +455,38 @@ __global__ void __launch_bounds__(kDThreads, NV ? 3 : 1) distill_kernel(const __
   cluster_sync();  // no CTA leaves while others may still push into it
 }
 
-// Row losses and their sum: 32 rows a CTA.
+// Row losses and their sum: a warp per row.
 __global__ void __launch_bounds__(256) distill_finish_kernel(const FinishParams P, const RowNorm* norm) {
-  __shared__ RowLog sh[32];
-  const long long base = (long long)blockIdx.x * 32;
-  if (threadIdx.x < 32) {
-    const long long n = base + threadIdx.x;
-    if (n < P.N && P.keep[n]) {
-      const RowNorm r = norm[n];
-      const RowTeacher t = P.row[n];
-      const double logz = log((double)r.z), b = logz - (double)t.shift - (double)t.shift_lo;
-      RowLog g;
-      g.m = r.m;
-      g.base.hi = (float)b;
-      g.base.lo = (float)(b - (double)g.base.hi);
-      g.extra = 0.0f;
-      if (t.rest > 0.0f) {
-        // each side from the listed tokens' mass where that is the smaller part
-        const double lt = t.sum < 0.5f ? log1p(-(double)t.sum) : log((double)t.rest);
-        const double ql = (double)r.zl / (double)r.z;
-        double lq = -INFINITY;
-        if (ql < 0.5)
-          lq = log1p(-ql);
-        else if (r.mr > -INFINITY)
-          lq = ((double)r.mr - (double)r.m) * ((double)P.c.hi + (double)P.c.lo) + log((double)r.zr) - logz;
-        g.extra = (float)((double)t.rest * (lt - lq));
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long n = (long long)blockIdx.x * 8 + w;
+  const bool on = n < P.N && P.keep[n];
+  float loss = 0.0f, weight = 0.0f;
+  if (on) {
+    const RowNorm r = norm[n];
+    const RowTeacher t = P.row[n];
+    weight = P.weight ? P.weight[n] : 1.0f;
+    const F2 logz = log_pair(r.z);
+    RowLog g;
+    g.m = r.m;
+    g.base = pair_add(logz, F2{-t.shift, -t.shift_lo});
+    g.extra = 0.0f;
+    if (t.rest > 0.0f) {
+      // each side from the listed tokens' mass where that is the smaller part
+      const float lt = t.sum < 0.5f ? log1pf(-t.sum) : logf(t.rest);
+      const float ql = r.zl / r.z;
+      float lq = -INFINITY;
+      if (ql < 0.5f) {
+        lq = log1pf(-ql);
+      } else if (r.mr > -INFINITY) {
+        const F2 v = pair_add(pair_add(log_pair(r.zr), F2{-logz.hi, -logz.lo}), two_mul(r.mr - r.m, P.c));
+        lq = v.hi + v.lo;
       }
-      sh[threadIdx.x] = g;
+      g.extra = t.rest * (lt - lq);
     }
+    loss = row_loss_warp(P, n, lane, g);
   }
-  __syncthreads();
-  finish_rows(P, base, sh);
+  if (lane == 0 && n < P.N) P.row_loss[n] = loss;
+  finish_sums(P, loss, on, weight);
 }
 
 }  // namespace ssv

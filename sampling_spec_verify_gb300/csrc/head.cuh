@@ -394,75 +394,63 @@ __global__ void __launch_bounds__(256) listed_grads_kernel(const ListedParams P,
 
 // ---- normalisers, row losses, their sum --------------------------------------------
 
-// 32 rows per CTA.  The tiles' statistics of a row are joined by 32 threads,
-// 8 rows at a time (64 contiguous bytes of every tile), each thread's loads
-// independent of one another; the sums are then the row's in log2.
+// 8 rows per CTA.  The tiles' statistics of a row are joined by 32 threads (64
+// contiguous bytes of every tile), each thread's loads independent of one
+// another; then a warp per row.
 __global__ void __launch_bounds__(256) head_finish_kernel(const FinishParams P, const float2* part, int tiles_n,
                                                           float* lse_out, float* lse2) {
-  __shared__ float2 sh[32][8];
-  __shared__ RowLog logs[32];
+  __shared__ float2 sh[32][9];
   const int r8 = threadIdx.x & 7, g = threadIdx.x >> 3;
-  const long long base = (long long)blockIdx.x * 32;
-  for (int q = 0; q < 32; q += 8) {
-    const long long n = base + q + r8;
-    float m = -INFINITY, sum = 0.0f;
-    if (n < P.N) {
-      for (int t0 = g; t0 < tiles_n; t0 += 32 * 8) {
-        float2 v[8];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long base = (long long)blockIdx.x * 8;
+  float m = -INFINITY, sum = 0.0f;
+  if (base + r8 < P.N) {
+    for (int t0 = g; t0 < tiles_n; t0 += 32 * 8) {
+      float2 v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int t = t0 + 32 * j;
-          v[j] = t < tiles_n ? __ldcs(part + (long long)t * P.N + n) : make_float2(-INFINITY, 0.0f);
-        }
-        float nm = m;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) nm = max_nan(nm, v[j].x);
-        if (nm > -INFINITY && nm < INFINITY) {
-          sum *= exp2f(m - nm);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sum += v[j].y * exp2f(v[j].x - nm);
-        }
-        m = nm;
+      for (int j = 0; j < 8; ++j) {
+        const int t = t0 + 32 * j;
+        v[j] = t < tiles_n ? __ldcs(part + (long long)t * P.N + base + r8) : make_float2(-INFINITY, 0.0f);
       }
-    }
-    __syncthreads();
-    sh[g][r8] = make_float2(m, sum);
-    __syncthreads();
-    if (threadIdx.x < 64) {  // eight threads a row
-      const int row = threadIdx.x >> 3, i = threadIdx.x & 7;
-      float top = -INFINITY;
+      float nm = m;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) top = max_nan(top, sh[i + 8 * j][row].x);
+      for (int j = 0; j < 8; ++j) nm = max_nan(nm, v[j].x);
+      if (nm > -INFINITY && nm < INFINITY) {
+        sum *= exp2f(m - nm);
 #pragma unroll
-      for (int o = 4; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-      float z = 0.0f;
-      const bool fine = top > -INFINITY && top < INFINITY;
-      if (fine) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) z += sh[i + 8 * j][row].y * exp2f(sh[i + 8 * j][row].x - top);
+        for (int j = 0; j < 8; ++j) sum += v[j].y * exp2f(v[j].x - nm);
       }
-#pragma unroll
-      for (int o = 4; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-      const long long n2 = base + q + row;
-      if (i == 0 && n2 < P.N) {
-        const double l2 = fine ? (double)top + (double)log2f(z) : NAN;
-        if (!fine && P.keep[n2]) raise(P.status, SPEC_DEV_BAD_LOGITS);
-        const double l = l2 * 0.69314718055994530942;
-        lse2[n2] = (float)l2;
-        if (lse_out) lse_out[n2] = (float)l;
-        const RowTeacher t = P.row[n2];
-        const double b = l - (double)t.shift - (double)t.shift_lo;
-        RowLog o;
-        o.m = 0.0f;
-        o.base.hi = (float)b;
-        o.base.lo = (float)(b - (double)o.base.hi);
-        o.extra = 0.0f;
-        logs[q + row] = o;
-      }
+      m = nm;
     }
   }
+  sh[g][r8] = make_float2(m, sum);
   __syncthreads();
-  finish_rows(P, base, logs);
+  const long long n = base + w;
+  const bool in = n < P.N, on = in && P.keep[n];
+  float loss = 0.0f, weight = 0.0f;
+  if (in) {
+    const float2 v = sh[lane][w];
+    const float top = redux_max_nan(v.x);
+    const bool fine = top > -INFINITY && top < INFINITY;
+    const float z = warp_sum(fine ? v.y * exp2f(v.x - top) : 0.0f);
+    // log2 Z as a pair: the maximum and a small logarithm
+    const F2 l2 = fine ? two_sum(top, log2f(z)) : F2{NAN, 0.0f};
+    const F2 ln2{0.693147182f, -1.90465421e-9f};
+    F2 l = two_mul(l2.hi, ln2);
+    l.lo = fmaf(l2.lo, ln2.hi, l.lo);
+    if (lane == 0) {
+      if (!fine && on) raise(P.status, SPEC_DEV_BAD_LOGITS);
+      lse2[n] = l2.hi;
+      if (lse_out) lse_out[n] = l.hi + l.lo;
+    }
+    if (on) {
+      const RowTeacher t = P.row[n];
+      weight = P.weight ? P.weight[n] : 1.0f;
+      loss = row_loss_warp(P, n, lane, RowLog{0.0f, pair_add(l, F2{-t.shift, -t.shift_lo}), 0.0f});
+    }
+    if (lane == 0) P.row_loss[n] = loss;
+  }
+  finish_sums(P, loss, on, weight);
 }
 
 // grad_hidden = grad_mul * sum of the partials, in slot order.

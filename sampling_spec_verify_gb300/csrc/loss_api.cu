@@ -135,7 +135,7 @@ DistillWs distill_ws(void* base, size_t N, size_t k) {
   w.zi = c.take<float>(N * k);
   w.norm = c.take<ssv::RowNorm>(N);
   w.row_loss = c.take<float>(N);
-  w.part = c.take<double>(3 * ((N + 31) / 32));
+  w.part = c.take<double>(3 * ((N + 7) / 8));
   w.total = c.used;
   return w;
 }
@@ -295,7 +295,7 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
   F.row_loss = row_loss ? row_loss : ws.row_loss;
   F.scalars = ws.scalars;
   F.status = status;
-  ssv::distill_finish_kernel<<<(unsigned)((N + 31) / 32), 256, 0, st>>>(F, ws.norm);
+  ssv::distill_finish_kernel<<<(unsigned)((N + 7) / 8), 256, 0, st>>>(F, ws.norm);
   return from_cuda(count_launch(cudaGetLastError()));
 }
 
@@ -363,7 +363,7 @@ HeadWs head_ws(void* base, size_t N, size_t V, size_t H, size_t k, bool gh, bool
   w.zi = c.take<float>(N * k);
   w.row_loss = c.take<float>(N);
   w.lse2 = c.take<float>(N);
-  w.sums = c.take<double>(3 * ((N + 31) / 32));
+  w.sums = c.take<double>(3 * ((N + 7) / 8));
   w.part = c.take<float2>(N * ((V + 255) / 256));
   w.hidden = gh ? c.take<float>((size_t)p.splits * (size_t)p.slot_rows * H) : nullptr;
   w.d = gh || gw ? c.take<uint16_t>(N * (size_t)p.piece) : nullptr;
@@ -511,7 +511,7 @@ spec_status_t head_run(const HeadCall& c, const HeadWs& ws) {
   F.row_loss = c.row_loss ? c.row_loss : ws.row_loss;
   F.scalars = ws.scalars;
   F.status = c.status;
-  ssv::head_finish_kernel<<<(unsigned)((c.N + 31) / 32), 256, 0, st>>>(F, ws.part, (c.V + 255) / 256, c.lse, ws.lse2);
+  ssv::head_finish_kernel<<<(unsigned)((c.N + 7) / 8), 256, 0, st>>>(F, ws.part, (c.V + 255) / 256, c.lse, ws.lse2);
   if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
   if (!c.grad_hidden && !c.grad_weight) return SPEC_OK;
 

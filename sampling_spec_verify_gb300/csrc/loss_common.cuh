@@ -358,7 +358,7 @@ struct FinishParams {
   uint32_t* status;
 };
 
-// What one thread prepares of a row.
+// What a row's loss needs of the student.
 struct RowLog {
   float m;        // taken off the student's logits first: rows masked with a
                   // type's lowest value would lose log Z beside it
@@ -366,65 +366,68 @@ struct RowLog {
   float extra;    // t_r (log t_r - log q_r)
 };
 
-// Row losses of the 32 rows from `base`, eight warps, after lane r of warp 0
-// has put row base + r into sh[r]; then the CTA's sums, and in the last CTA to
-// arrive the call's, all in fixed orders.  256 threads.
+// log z of a normal z > 0 within 2^-25: the exponent's part is exact in the high word,
+// the mantissa's logarithm is below 0.41.
+__device__ __forceinline__ F2 log_pair(float z) {
+  int e;
+  float f = frexpf(z, &e);  // [0.5, 1)
+  if (f < 0.75f) f *= 2.0f, e -= 1;
+  const float x = (float)e;
+  // ln 2 = 0.693145751953125 (16 bits) + 1.42860682030941723e-6
+  return two_sum(x * 0.693145751953125f, fmaf(x, 1.428606820309417e-6f, logf(f)));
+}
+
+// Row loss of row n, by one warp:
 //   L_n = sum_i t_i ((x_i / T - shift) - ((z_i - m) c - log Z)) + extra
 // with every difference carrying its rounding: the terms are small differences
 // of logarithms near 10.
-__device__ __forceinline__ void finish_rows(const FinishParams& P, long long base, const RowLog* sh) {
-  __shared__ float row_sh[32];
-  __shared__ uint32_t last;
-  __shared__ double red[3][8];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = w; r < 32; r += 8) {
-    const long long n = base + r;
-    if (n >= P.N) break;
-    float loss = 0.0f;
-    if (P.keep[n]) {
-      const RowLog g = sh[r];
-      float acc = 0.0f;
+__device__ __forceinline__ float row_loss_warp(const FinishParams& P, long long n, int lane, const RowLog& g) {
+  float acc = 0.0f;
 #pragma unroll 4
-      for (int i = lane; i < P.k; i += 32) {
-        const float t = P.t[n * P.k + i], z = P.zi[n * P.k + i];
-        const float x = P.logits ? P.logits[n * P.k + i] : 0.0f;
-        if (t > 0.0f) {
-          const F2 d = two_sum(z, -g.m);
-          F2 lq = two_mul(d.hi, P.c);
-          lq.lo = fmaf(d.lo, P.c.hi, lq.lo);
-          F2 v = pair_add(two_mul(x, P.inv_t), F2{-lq.hi, -lq.lo});
-          v = pair_add(v, g.base);
-          acc = fmaf(t, lq.hi > -INFINITY ? v.hi + v.lo : INFINITY, acc);
-        }
-      }
-      loss = warp_sum(acc) + g.extra;
-      if (isnan(g.base.hi)) loss = NAN;  // also where the entries weigh nothing
-    }
-    if (lane == 0) {
-      P.row_loss[n] = loss;
-      row_sh[r] = loss;
+  for (int i = lane; i < P.k; i += 32) {
+    const float t = P.t[n * P.k + i], z = P.zi[n * P.k + i];
+    const float x = P.logits ? P.logits[n * P.k + i] : 0.0f;
+    if (t > 0.0f) {
+      const F2 d = two_sum(z, -g.m);
+      F2 lq = two_mul(d.hi, P.c);
+      lq.lo = fmaf(d.lo, P.c.hi, lq.lo);
+      F2 v = pair_add(two_mul(x, P.inv_t), F2{-lq.hi, -lq.lo});
+      v = pair_add(v, g.base);
+      acc = fmaf(t, lq.hi > -INFINITY ? v.hi + v.lo : INFINITY, acc);
     }
   }
+  acc = warp_sum(acc) + g.extra;
+  return isnan(g.base.hi) ? NAN : acc;  // also where the entries weigh nothing
+}
+
+// Sums of the CTA's eight rows (warp w's loss in every lane of it), and in the
+// last CTA to arrive the call's, all in fixed orders.  256 threads.
+__device__ __forceinline__ void finish_sums(const FinishParams& P, float loss, bool on, float weight) {
+  __shared__ double red[3][8];
+  __shared__ uint32_t last;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) {
+    red[0][w] = on ? (double)weight * (double)loss : 0.0;
+    red[1][w] = on ? 1.0 : 0.0;
+    red[2][w] = on ? (double)fabsf(weight) : 0.0;
+  }
   __syncthreads();
-  if (w == 0) {
-    const long long n = base + lane;
-    const bool on = n < P.N && P.keep[n];
-    const float rw = on ? (P.weight ? P.weight[n] : 1.0f) : 0.0f;
-    const double sum = warp_sum(on ? (double)rw * (double)row_sh[lane] : 0.0);
-    const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, on));
-    const float wmax = redux_max_nan(fabsf(rw));
-    if (lane == 0) {
-      double* p = P.part + 3ll * blockIdx.x;
-      p[0] = sum, p[1] = (double)cnt, p[2] = (double)wmax;
-      __threadfence();
-      last = atomicAdd(&P.scalars->ticket, 1u) == gridDim.x - 1;
-    }
+  if (threadIdx.x == 0) {
+    double sum = 0.0, cnt = 0.0;
+    float wmax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += red[0][i], cnt += red[1][i], wmax = max_nan(wmax, (float)red[2][i]);
+    double* p = P.part + 3ll * blockIdx.x;
+    p[0] = sum, p[1] = cnt, p[2] = (double)wmax;
+    __threadfence();
+    last = atomicAdd(&P.scalars->ticket, 1u) == gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
   double sum = 0.0, cnt = 0.0;
   float wmax = 0.0f;
+#pragma unroll 4
   for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) {
     const double* p = P.part + 3ll * i;
     sum += __ldcg(p);
@@ -439,12 +442,14 @@ __device__ __forceinline__ void finish_rows(const FinishParams& P, long long bas
   if (threadIdx.x == 0) {
     sum = cnt = 0.0;
     wmax = 0.0f;
+#pragma unroll
     for (int i = 0; i < 8; ++i) sum += red[0][i], cnt += red[1][i], wmax = max_nan(wmax, (float)red[2][i]);
-    const double den = P.mean ? (cnt > 0.0 ? cnt : 1.0) : 1.0;
-    P.loss[0] = (float)(sum / den);
+    const float den = P.mean && cnt > 0.0 ? (float)cnt : 1.0f;  // at most 2^20 rows through a head; a
+                                                                // count beyond 2^24 is rounded
+    P.loss[0] = (float)sum / den;
     P.scalars->count = (uint32_t)cnt;
     P.scalars->inv_wmax = wmax == 0.0f ? 0.0f : 1.0f / wmax;
-    P.scalars->grad_mul = (float)((double)P.grad_scale * (double)wmax / (den * (double)P.store_scale));
+    P.scalars->grad_mul = P.grad_scale * wmax / (den * P.store_scale);
   }
 }
 
