@@ -4,9 +4,14 @@
 //   z = X W^T / T                 X [N, H] hidden states, W [V, H] head
 //   pass 1   per 256-token tile and row: maximum and sum of 2^z', z' = z log2(e)
 //   pass 2   per piece of the vocabulary, C tokens wide:
-//     D  = (softmax(z) - t) w     recomputed from X and W, 16 bits, [N, C]
+//     D  = (softmax(z) - t) w     16 bits, [N, C]
 //     dX += D W_piece             fp32, one partial per split of the piece
 //     dW_piece = D^T X
+//
+// The piece lies in a workspace of bounded size.  Where the whole vocabulary is
+// one piece, pass 1 leaves its unnormalised probabilities there and D is a
+// rescaling of them (4 bytes of traffic an entry); otherwise D is recomputed
+// from X and W piece by piece, a fourth product.
 //
 // D is rounded to the operands' 16-bit type because the products that consume
 // it take that type: one rounding of half a step per entry, the size of the
@@ -36,55 +41,64 @@ constexpr int kHeadSmem = kStages * kStageBytes + kEpiWarps * 2 * kStageOut + 10
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 enum HeadOp {
-  kHeadNorm,    // pass 1: row statistics of X W^T per tile
-  kHeadGrad,    // D
-  kHeadHidden,  // dX partials
-  kHeadWeight   // dW
+  kHeadNorm,  // pass 1: row statistics of X W^T per tile
+  kHeadKeep,  // pass 1, keeping the unnormalised probabilities
+  kHeadGrad,  // D of a piece, recomputed
+  kHeadBack   // dX partials (product 0) and dW (product 1) of a piece
 };
 
-struct HeadParams {
-  int M, N, K;       // rows, columns, depth of the product
+// One product of a launch.  Rows of A and B run along K, or (mn) along the
+// other dimension.
+struct Product {
+  int M, N;     // rows and columns
   int tiles_m, tiles_n, splits;
-  int ksteps;        // 64-deep steps of the whole product
-  int b_off;         // the piece's start among the rows of B
+  int ksteps;   // 64-deep steps
+  int b_off;    // the piece's start among the rows of B
+};
+
+struct HeadLaunch {
+  CUtensorMap a[2], b[2], out[2];
+  Product p[2];
+  int tiles0, tiles;  // of product 0, of the launch
   int bf16;
-  float s;           // log2(e) / T
-  // kHeadNorm
-  float2* part;      // [tiles_n, M]
+  float s;            // log2(e) / T
+  // kHeadNorm, kHeadKeep
+  float2* part;       // [tiles_n, M]
   // kHeadGrad
-  const float* lse2; // [M] log2 of the normaliser
+  const float* lse2;  // [M] log2 of the normaliser
   const float* weight;
   const uint8_t* keep;
   float store_scale;
-  // kHeadHidden
-  int first;         // store (not add) the partials
-  int slot_rows;     // rows between the partials of two splits
+  // kHeadBack
+  int first;          // store (not add) the partials
+  int slot_rows;      // rows between the partials of two splits
   const LossScalars* scalars;
   uint32_t* status;
-};
-
-template <HeadOp OP>
-struct HeadTraits {  // operand rows run along K, or (mn) along the other dimension
-  static constexpr bool a_mn = OP == kHeadWeight;
-  static constexpr bool b_mn = OP == kHeadHidden || OP == kHeadWeight;
 };
 
 // Tile `i` of the launch: bands of eight tile rows, down the rows first, so
 // that the tiles in flight share operands in L2.
 struct TileAt {
-  int m, n, split;
+  int second;  // which product
+  int m, n, split, k0, k1;
 };
-__device__ __forceinline__ TileAt tile_at(int i, int tiles_m, int tiles_n) {
-  const int per = tiles_m * tiles_n;
+template <HeadOp OP>
+__device__ __forceinline__ TileAt tile_at(const HeadLaunch& L, int i) {
   TileAt t;
+  t.second = OP == kHeadBack && i >= L.tiles0;
+  const Product& p = L.p[t.second];
+  if (t.second) i -= L.tiles0;
+  const int per = p.tiles_m * p.tiles_n;
   t.split = i / per;
   i -= t.split * per;
   constexpr int kBand = 8;
-  const int band = i / (kBand * tiles_n);
-  const int rows = min(kBand, tiles_m - band * kBand);
-  i -= band * kBand * tiles_n;
+  const int band = i / (kBand * p.tiles_n);
+  const int rows = min(kBand, p.tiles_m - band * kBand);
+  i -= band * kBand * p.tiles_n;
   t.m = band * kBand + i % rows;
   t.n = i / rows;
+  t.k0 = (int)((long long)p.ksteps * t.split / p.splits);
+  t.k1 = (int)((long long)p.ksteps * (t.split + 1) / p.splits);
   return t;
 }
 
@@ -100,12 +114,16 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, bool bf16) {
   return bf16 ? Elem<__nv_bfloat16>::pack(a, b) : Elem<__half>::pack(a, b);
 }
 
-// OUT32: the result of kHeadWeight is fp32.
+// Unnormalised probabilities are kept as fp16 2^(z' - m + 15), m the row's
+// maximum in the tile: 11 bits down to 2^-29 of the largest, so that rounding D
+// to the operands' type afterwards stays the one rounding that counts.  (Calls
+// that keep none use the same exponents, for the same bits.)
+constexpr float kKeepShift = 15.0f;
+
+// OUT32: dW is fp32.
 template <HeadOp OP, bool OUT32>
 __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
-    head_kernel(const __grid_constant__ HeadParams P, const __grid_constant__ CUtensorMap map_a,
-                const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_out) {
-  using T = HeadTraits<OP>;
+    head_kernel(const __grid_constant__ HeadLaunch L) {
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
   __shared__ uint32_t tmem_slot;
@@ -130,8 +148,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
     }
     mbar_init(bar_drain, 1);
     fence_mbar_init();
-    prefetch_map(&map_a);
-    prefetch_map(&map_b);
+    prefetch_map(&L.a[0]);
+    prefetch_map(&L.b[0]);
   }
   if (wid == 0) {
     tmem_alloc_pair(smem_addr(&tmem_slot), 512);
@@ -141,8 +159,6 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-
-  const int tiles = P.tiles_m * P.tiles_n * P.splits;
   const int clusters = gridDim.x / 2, first_tile = blockIdx.x / 2;
 
   if (wid == 0) {
@@ -151,12 +167,13 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
       const uint32_t full0 = map_rank(bar_full, 0);
       uint32_t step = 0;
       bool ok = true;
-      for (int i = first_tile; ok && i < tiles; i += clusters) {
-        const TileAt t = tile_at(i, P.tiles_m, P.tiles_n);
-        const int k0 = (int)((long long)P.ksteps * t.split / P.splits);
-        const int k1 = (int)((long long)P.ksteps * (t.split + 1) / P.splits);
+      for (int i = first_tile; ok && i < L.tiles; i += clusters) {
+        const TileAt t = tile_at<OP>(L, i);
+        const CUtensorMap *map_a = &L.a[t.second], *map_b = &L.b[t.second];
+        const int b_off = L.p[t.second].b_off;
+        const bool a_mn = t.second, b_mn = OP == kHeadBack;
         const int row_a = t.m * kTileM + (int)rank * 128, row_b = t.n * kTileN + (int)rank * 128;
-        for (int k = k0; k < k1; ++k, ++step) {
+        for (int k = t.k0; k < t.k1; ++k, ++step) {
           const uint32_t s = step % kStages, use = step / kStages;
           if (use > 0 && !mbar_wait_bounded(bar_empty + 8 * s, (use - 1) & 1u, kWaitNs)) {
             ok = false;
@@ -165,22 +182,22 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
           const uint32_t a = tiles0 + s * kStageBytes, b = a + kStageBytes / 2;
           if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * s, 2 * kStageBytes);
           const uint32_t full = full0 + 8 * s;
-          if (T::a_mn) {
-            tma_load_pair(a, &map_a, row_a, k * kTileK, full);
-            tma_load_pair(a + 8192, &map_a, row_a + 64, k * kTileK, full);
+          if (a_mn) {
+            tma_load_pair(a, map_a, row_a, k * kTileK, full);
+            tma_load_pair(a + 8192, map_a, row_a + 64, k * kTileK, full);
           } else {
-            tma_load_pair(a, &map_a, k * kTileK, row_a, full);
+            tma_load_pair(a, map_a, k * kTileK, row_a, full);
           }
-          if (T::b_mn) {
-            tma_load_pair(b, &map_b, row_b, P.b_off + k * kTileK, full);
-            tma_load_pair(b + 8192, &map_b, row_b + 64, P.b_off + k * kTileK, full);
+          if (b_mn) {
+            tma_load_pair(b, map_b, row_b, b_off + k * kTileK, full);
+            tma_load_pair(b + 8192, map_b, row_b + 64, b_off + k * kTileK, full);
           } else {
-            tma_load_pair(b, &map_b, k * kTileK, P.b_off + row_b, full);
+            tma_load_pair(b, map_b, k * kTileK, b_off + row_b, full);
           }
         }
       }
       if (!ok) {
-        raise(P.status, SPEC_DEV_TIMEOUT);
+        raise(L.status, SPEC_DEV_TIMEOUT);
         // the copies in flight of the pair end on the even CTA's barriers
         if (rank == 0)
           for (int i = 0; i < kStages && step > 0; ++i, --step)
@@ -190,16 +207,17 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (wid == 1) {
     // ---- products: one thread of the even CTA ----
     if (rank == 0 && lane == 0) {
-      const uint32_t idesc = mma_idesc(P.bf16 != 0, T::a_mn, T::b_mn);
-      constexpr uint64_t da = T::a_mn ? smem_desc_base(8192, 1024) : smem_desc_base(16, 1024);
-      constexpr uint64_t db = T::b_mn ? smem_desc_base(8192, 1024) : smem_desc_base(16, 1024);
-      constexpr uint32_t ka = T::a_mn ? 2048 : 32, kb = T::b_mn ? 2048 : 32;  // bytes of 16 K steps
+      constexpr uint64_t desc_k = smem_desc_base(16, 1024), desc_mn = smem_desc_base(8192, 1024);
+      constexpr bool b_mn = OP == kHeadBack;
+      constexpr uint64_t db = b_mn ? desc_mn : desc_k;
+      constexpr uint32_t kb = b_mn ? 2048 : 32;  // bytes of 16 K steps
       uint32_t step = 0, it = 0;
       bool ok = true;
-      for (int i = first_tile; ok && i < tiles; i += clusters, ++it) {
-        const TileAt t = tile_at(i, P.tiles_m, P.tiles_n);
-        const int k0 = (int)((long long)P.ksteps * t.split / P.splits);
-        const int k1 = (int)((long long)P.ksteps * (t.split + 1) / P.splits);
+      for (int i = first_tile; ok && i < L.tiles; i += clusters, ++it) {
+        const TileAt t = tile_at<OP>(L, i);
+        const uint32_t idesc = mma_idesc(L.bf16 != 0, t.second, b_mn);
+        const uint64_t da = t.second ? desc_mn : desc_k;
+        const uint32_t ka = t.second ? 2048 : 32;
         const uint32_t acc = it & 1, use = it >> 1;
         if (use > 0 && !mbar_wait_bounded(bar_free + 8 * acc, (use - 1) & 1u, kWaitNs)) {
           ok = false;
@@ -207,7 +225,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + acc * kTileN;
-        for (int k = k0; k < k1; ++k, ++step) {
+        for (int k = t.k0; k < t.k1; ++k, ++step) {
           const uint32_t s = step % kStages;
           if (!mbar_wait_bounded(bar_full + 8 * s, (step / kStages) & 1u, kWaitNs)) {
             ok = false;
@@ -217,13 +235,13 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
           const uint32_t a = tiles0 + s * kStageBytes, b = a + kStageBytes / 2;
 #pragma unroll
           for (int j = 0; j < kTileK / 16; ++j)
-            mma_pair(d, smem_desc(da, a + j * ka), smem_desc(db, b + j * kb), idesc, (k > k0 || j > 0) ? 1u : 0u);
+            mma_pair(d, smem_desc(da, a + j * ka), smem_desc(db, b + j * kb), idesc, (k > t.k0 || j > 0) ? 1u : 0u);
           mma_commit_pair(bar_empty + 8 * s);
         }
         if (ok) mma_commit_pair(bar_done + 8 * acc);
       }
       if (!ok) {
-        raise(P.status, SPEC_DEV_TIMEOUT);
+        raise(L.status, SPEC_DEV_TIMEOUT);
         mma_commit_pair(bar_drain);
         mbar_wait_bounded(bar_drain, 0, 10000000ull);
       }
@@ -234,96 +252,138 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t stage = out0 + (wid - 2) * 2 * kStageOut;
     const uint32_t free0 = map_rank(bar_free, 0);
     uint32_t it = 0, buf = 0;
-    for (int i = first_tile; i < tiles; i += clusters, ++it) {
-      const TileAt t = tile_at(i, P.tiles_m, P.tiles_n);
+    // The next of the warp's two staging buffers, once its last store has read it.
+    auto next_buffer = [&]() {
+      const uint32_t dst = stage + buf * kStageOut;
+      buf ^= 1;
+      if (lane == 0) bulk_wait_read<1>();
+      __syncwarp();
+      return dst;
+    };
+    // Sends a staged 32-row block of 128-byte rows to the result.
+    auto send = [&](const CUtensorMap* map, uint32_t src, int x, int y, bool in, bool add) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (in) {
+          if (add)
+            tma_reduce_add(map, src, x, y);
+          else
+            tma_store(map, src, x, y);
+        }
+        bulk_commit();
+      }
+    };
+    auto stage16 = [&](uint32_t dst, int unit, const float (&v)[32], bool bf) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 8)
+        stage_write(dst, lane, unit + j / 8, pack16(v[j], v[j + 1], bf), pack16(v[j + 2], v[j + 3], bf),
+                    pack16(v[j + 4], v[j + 5], bf), pack16(v[j + 6], v[j + 7], bf));
+    };
+    auto stage32 = [&](uint32_t dst, const float (&v)[32]) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        stage_write(dst, lane, j / 4, __float_as_uint(v[j]), __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]),
+                    __float_as_uint(v[j + 3]));
+    };
+
+    for (int i = first_tile; i < L.tiles; i += clusters, ++it) {
+      const TileAt t = tile_at<OP>(L, i);
       const uint32_t acc = it & 1, use = it >> 1;
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_done + 8 * acc, use & 1u, kWaitNs))) {
-        raise(P.status, SPEC_DEV_TIMEOUT);
+        raise(L.status, SPEC_DEV_TIMEOUT);
         break;
       }
       tc_fence_after();
       const uint32_t src = tmem + acc * kTileN + ((uint32_t)(quad * 32) << 16);
+      const int M = L.p[t.second].M, N = L.p[t.second].N;
       const int row0 = t.m * kTileM + (int)rank * 128 + quad * 32, row = row0 + lane;
       const int col0 = t.n * kTileN;
 
-      if constexpr (OP == kHeadNorm) {
-        // running maximum and sum over the tile's columns, in powers of two
+      if constexpr (OP == kHeadNorm || OP == kHeadKeep) {
+        // the row's maximum over the tile, then the sum, in powers of two
+        const int cols = N - col0;
         float m = -INFINITY, sum = 0.0f;
         for (int c = 0; c < kTileN; c += 32) {
           float v[32];
           tmem_load32(src + c, v);
-          float cm = -INFINITY;
+          if (c + 32 <= cols) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            v[j] = col0 + c + j < P.N ? v[j] * P.s : -INFINITY;
-            cm = max_nan(cm, v[j]);
+            for (int j = 0; j < 32; ++j) m = max_nan(m, v[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) m = max_nan(m, c + j < cols ? v[j] : -INFINITY);
           }
-          const float nm = max_nan(m, cm);
-          if (nm > -INFINITY) {
+        }
+        m *= L.s;
+        const float off = m - kKeepShift;
+        for (int c = 0; c < kTileN; c += 64) {
+          if (c >= cols) break;
+          uint32_t dst = 0;
+          if constexpr (OP == kHeadKeep) dst = next_buffer();
+#pragma unroll
+          for (int h = 0; h < 64; h += 32) {
+            float v[32];
+            tmem_load32(src + c + h, v);
             float a = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) a += ex2(v[j] - nm);
-            sum = sum * ex2(m - nm) + a;
-            m = nm;
-          } else if (!(nm < INFINITY)) {
-            m = nm;  // NaN passes on
+            for (int j = 0; j < 32; ++j) {
+              v[j] = ex2(fmaf(v[j], L.s, -off));
+              if (c + h + 32 > cols && c + h + j >= cols) v[j] = 0.0f;
+              a += v[j];
+            }
+            sum += a;
+            if constexpr (OP == kHeadKeep) stage16(dst, h / 8, v, false);
           }
+          if constexpr (OP == kHeadKeep) send(&L.out[0], dst, col0 + c, row0, row0 < M, false);
         }
-        if (row < P.M) P.part[(long long)t.n * P.M + row] = make_float2(m, sum);
+        if (row < M) L.part[(long long)t.n * M + row] = make_float2(off, sum);
+      } else if constexpr (OP == kHeadGrad) {
+        float lse = 0.0f, cf = 0.0f;
+        if (row < M && L.keep[row]) {
+          lse = L.lse2[row];
+          cf = (L.weight ? L.weight[row] : 1.0f) * L.scalars->inv_wmax * L.store_scale;
+        }
+        for (int c = 0; c < kTileN; c += 64) {
+          if (col0 + c >= N) break;
+          const uint32_t dst = next_buffer();
+#pragma unroll
+          for (int h = 0; h < 64; h += 32) {
+            float v[32];
+            tmem_load32(src + c + h, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = cf != 0.0f ? ex2(fmaf(v[j], L.s, -lse)) * cf : 0.0f;
+            stage16(dst, h / 8, v, L.bf16 != 0);
+          }
+          send(&L.out[0], dst, col0 + c, row0, row0 < M, false);
+        }
+      } else if (!t.second) {
+        for (int c = 0; c < kTileN; c += 32) {
+          if (col0 + c >= N) break;
+          const uint32_t dst = next_buffer();
+          float v[32];
+          tmem_load32(src + c, v);
+          stage32(dst, v);
+          send(&L.out[0], dst, col0 + c, t.split * L.slot_rows + row0, row0 < M, !L.first);
+        }
       } else {
-        float lse = 0.0f, cf = 0.0f, mul = 1.0f;
-        if constexpr (OP == kHeadGrad) {
-          if (row < P.M && P.keep[row]) {
-            lse = P.lse2[row];
-            cf = (P.weight ? P.weight[row] : 1.0f) * P.scalars->inv_wmax * P.store_scale;
-          }
-        } else if constexpr (OP == kHeadWeight) {
-          mul = P.scalars->grad_mul;
-        }
-        constexpr bool wide = OP == kHeadHidden || (OP == kHeadWeight && OUT32);  // fp32 out
-        constexpr int kCols = wide ? 32 : 64;  // columns of 128 bytes
+        const float mul = L.scalars->grad_mul;
+        constexpr int kCols = OUT32 ? 32 : 64;
         for (int c = 0; c < kTileN; c += kCols) {
-          if (col0 + c >= P.N) break;
-          const uint32_t dst = stage + buf * kStageOut;
-          buf ^= 1;
-          if (lane == 0) bulk_wait_read<1>();
-          __syncwarp();
+          if (col0 + c >= N) break;
+          const uint32_t dst = next_buffer();
 #pragma unroll
           for (int h = 0; h < kCols; h += 32) {
             float v[32];
             tmem_load32(src + c + h, v);
-            if constexpr (OP == kHeadGrad) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = cf != 0.0f ? ex2(fmaf(v[j], P.s, -lse)) * cf : 0.0f;
-            } else if constexpr (OP == kHeadWeight) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] *= mul;
-            }
-            if constexpr (wide) {
-#pragma unroll
-              for (int j = 0; j < 32; j += 4)
-                stage_write(dst, lane, j / 4, __float_as_uint(v[j]), __float_as_uint(v[j + 1]),
-                            __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3]));
-            } else {
-              const bool bf = P.bf16 != 0;
-#pragma unroll
-              for (int j = 0; j < 32; j += 8)
-                stage_write(dst, lane, (h + j) / 8, pack16(v[j], v[j + 1], bf), pack16(v[j + 2], v[j + 3], bf),
-                            pack16(v[j + 4], v[j + 5], bf), pack16(v[j + 6], v[j + 7], bf));
-            }
+            for (int j = 0; j < 32; ++j) v[j] *= mul;
+            if constexpr (OUT32)
+              stage32(dst, v);
+            else
+              stage16(dst, h / 8, v, L.bf16 != 0);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (row0 < P.M) {
-              const int y = OP == kHeadHidden ? t.split * P.slot_rows + row0 : row0;
-              if (OP == kHeadHidden && !P.first)
-                tma_reduce_add(&map_out, dst, col0 + c, y);
-              else
-                tma_store(&map_out, dst, col0 + c, y);
-            }
-            bulk_commit();
-          }
+          send(&L.out[1], dst, col0 + c, row0, row0 < M, false);
         }
       }
       tc_fence_before();
@@ -390,6 +450,53 @@ __global__ void __launch_bounds__(256) listed_grads_kernel(const ListedParams P,
   const float cf = (P.weight ? P.weight[n] : 1.0f) * P.scalars->inv_wmax * P.store_scale;
   const float q = exp2f((float)((double)P.zi[i] * P.s - (double)P.lse2[n]));
   d[n * P.ld + (id - P.v0)] = Elem<E>::from_f32(cf == 0.0f ? 0.0f : (q - P.t[i]) * cf);
+}
+
+// Turns kept probabilities into D, in place: one CTA per row and kDenseCols
+// tokens (one read and one write of the piece; the listed tokens after it).
+constexpr int kDenseCols = 8192;
+template <class E>
+__global__ void __launch_bounds__(256) dense_grads_kernel(const ListedParams P, const float2* part, E* d) {
+  const long long n = blockIdx.x;
+  const int c0 = blockIdx.y * kDenseCols, c1 = min(P.C, c0 + kDenseCols);
+  const float cf = P.keep[n] ? (P.weight ? P.weight[n] : 1.0f) * P.scalars->inv_wmax * P.store_scale : 0.0f;
+  const float lse = P.lse2[n];
+  uint4* row = reinterpret_cast<uint4*>(d + n * P.ld);
+  constexpr int kPer = kDenseCols / 8 / 256;
+  uint4 v[kPer];
+  float f[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int c = c0 + (i * 256 + threadIdx.x) * 8;
+    if (c < c1) {
+      v[i] = __ldcs(row + c / 8);
+      f[i] = part[(long long)(c >> 8) * P.N + n].x;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int c = c0 + (i * 256 + threadIdx.x) * 8;
+    if (c < c1) {
+      uint4 o = make_uint4(0u, 0u, 0u, 0u);
+      if (cf != 0.0f) {
+        const float m = ex2(f[i] - lse) * cf;
+        float x[8];
+        Elem<__half>::unpack(v[i], x);
+        o.x = Elem<E>::pack(x[0] * m, x[1] * m), o.y = Elem<E>::pack(x[2] * m, x[3] * m);
+        o.z = Elem<E>::pack(x[4] * m, x[5] * m), o.w = Elem<E>::pack(x[6] * m, x[7] * m);
+      }
+      row[c / 8] = o;
+    }
+  }
+  __syncthreads();
+  if (cf == 0.0f) return;
+  for (int i = threadIdx.x; i < P.k; i += 256) {
+    const int id = P.ids[n * P.k + i];
+    if (id >= c0 && id < c1) {
+      const float q = exp2f((float)((double)P.zi[n * P.k + i] * P.s - (double)lse));
+      d[n * P.ld + id] = Elem<E>::from_f32((q - P.t[n * P.k + i]) * cf);
+    }
+  }
 }
 
 // ---- normalisers, row losses, their sum --------------------------------------------

@@ -7,6 +7,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <mutex>
 
 #include "distill.cuh"
@@ -302,21 +303,29 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
 // ---- losses through the head --------------------------------------------------------
 
 constexpr int kPairs = 76;                       // CTA pairs in flight, for the split rule
-constexpr size_t kPieceBytes = (size_t)256 << 20;  // of a piece of D
+// A bf16 batch whose probabilities fit kKeepBytes keeps them between the
+// passes (1792 x 151936 x 2048, both gradients: 2.3 ms against 2.8); the others
+// go in pieces of kPieceBytes, and so does fp16, whose own rounding the kept
+// one would double.
+constexpr size_t kKeepBytes = (size_t)1280 << 20;
+constexpr size_t kPieceBytes = (size_t)256 << 20;
 
 // How a call is cut: pieces of the vocabulary and splits of a piece's depth in
 // the product that gives the hidden states' gradient.
 struct HeadPlan {
+  bool kept;       // one piece, holding pass 1's probabilities
   int piece;       // tokens per piece, a multiple of 256
   int pieces;
   int splits;
   int slot_rows;
 };
-HeadPlan head_plan(int N, int V, int H) {
+HeadPlan head_plan(int N, int V, int H, bool may_keep) {
   HeadPlan p;
   const long long vt = ((long long)V + 255) / 256;
   long long cap = (long long)(kPieceBytes / 2 / (size_t)N) / 256;  // tiles of tokens
   if (cap < 8) cap = 8;
+  p.kept = may_keep && (size_t)N * (size_t)vt * 512 <= kKeepBytes;
+  if (p.kept) cap = vt;
   p.pieces = (int)((vt + cap - 1) / cap);
   p.piece = (int)((vt + p.pieces - 1) / p.pieces) * 256;
   p.pieces = (int)(((long long)V + p.piece - 1) / p.piece);
@@ -352,9 +361,8 @@ struct HeadWs {
   uint16_t* d;
   size_t total;
 };
-HeadWs head_ws(void* base, size_t N, size_t V, size_t H, size_t k, bool gh, bool gw) {
+HeadWs head_ws(void* base, const HeadPlan& p, size_t N, size_t V, size_t H, size_t k, bool gh, bool gw) {
   Carver c{static_cast<char*>(base)};
-  const HeadPlan p = head_plan((int)N, (int)V, (int)H);
   HeadWs w;
   w.scalars = c.take<ssv::LossScalars>(1);
   w.t = c.take<float>(N * k);
@@ -407,9 +415,23 @@ bool make_map(CUtensorMap* m, const void* base, spec_dtype_t dt, long long rows,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Sizes of a product of M x N results, K deep.
+ssv::Product product(int M, int N, int K, int splits, int b_off) {
+  ssv::Product p;
+  p.M = M;
+  p.N = N;
+  p.tiles_m = (M + ssv::kTileM - 1) / ssv::kTileM;
+  p.tiles_n = (N + ssv::kTileN - 1) / ssv::kTileN;
+  p.ksteps = (K + ssv::kTileK - 1) / ssv::kTileK;
+  p.splits = splits < p.ksteps ? splits : p.ksteps;
+  p.b_off = b_off;
+  return p;
+}
+long long tiles_of(const ssv::Product& p) { return (long long)p.tiles_m * p.tiles_n * p.splits; }
+
+// Launches the first (which & 1) and the second (which & 2) product of L.
 template <ssv::HeadOp OP, bool OUT32>
-spec_status_t launch_head(ssv::HeadParams P, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out,
-                          cudaStream_t st) {
+spec_status_t launch_head(ssv::HeadLaunch& L, int which, cudaStream_t st) {
   static Residency res;
   const void* fn = (const void*)ssv::head_kernel<OP, OUT32>;
   Device d;
@@ -417,13 +439,12 @@ spec_status_t launch_head(ssv::HeadParams P, const CUtensorMap& a, const CUtenso
   if (!device(&d, &dev)) return SPEC_ERR_CUDA;
   const int fit = resident_clusters(res, fn, 2, ssv::kHeadSmem, ssv::kHeadThreads, dev, d.smem_optin);
   if (fit <= 0) return SPEC_ERR_CUDA;
-  P.tiles_m = (P.M + ssv::kTileM - 1) / ssv::kTileM;
-  P.tiles_n = (P.N + ssv::kTileN - 1) / ssv::kTileN;
-  P.ksteps = (P.K + ssv::kTileK - 1) / ssv::kTileK;
-  const long long tiles = (long long)P.tiles_m * P.tiles_n * P.splits;
-  if (tiles > 0x7FFFFFF) return SPEC_ERR_UNSUPPORTED;
-  const int G = tiles < fit ? (int)tiles : fit;
-  ssv::head_kernel<OP, OUT32><<<2 * G, ssv::kHeadThreads, ssv::kHeadSmem, st>>>(P, a, b, out);
+  const long long t0 = (which & 1) ? tiles_of(L.p[0]) : 0, t1 = (which & 2) ? tiles_of(L.p[1]) : 0;
+  if (t0 + t1 > 0x7FFFFFF) return SPEC_ERR_UNSUPPORTED;
+  L.tiles0 = (int)t0;
+  L.tiles = (int)(t0 + t1);
+  const int G = L.tiles < fit ? L.tiles : fit;
+  ssv::head_kernel<OP, OUT32><<<2 * G, ssv::kHeadThreads, ssv::kHeadSmem, st>>>(L);
   return from_cuda(count_launch(cudaGetLastError()));
 }
 
@@ -447,9 +468,8 @@ struct HeadCall {
 };
 
 template <class E>
-spec_status_t head_run(const HeadCall& c, const HeadWs& ws) {
+spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws) {
   cudaStream_t st = static_cast<cudaStream_t>(c.stream);
-  const HeadPlan plan = head_plan(c.N, c.V, c.H);
   const E* x = static_cast<const E*>(c.hidden);
   const E* w = static_cast<const E*>(c.weight);
   const double s = kLog2e / (double)c.temperature;
@@ -476,27 +496,33 @@ spec_status_t head_run(const HeadCall& c, const HeadWs& ws) {
                                                                               ws.zi);
   if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
 
-  CUtensorMap x_k, w_k;  // 128-row boxes along K
-  if (!make_map(&x_k, x, c.dtype, c.N, c.H, c.H, 128) || !make_map(&w_k, w, c.dtype, c.V, c.H, c.H, 128))
+  const bool grads = c.grad_hidden || c.grad_weight;
+  const bool kept = grads && plan.kept;
+  ssv::HeadLaunch L;
+  std::memset(&L, 0, sizeof(L));
+  L.bf16 = c.dtype == SPEC_BF16;
+  L.s = (float)s;
+  L.part = ws.part;
+  L.status = c.status;
+  L.scalars = ws.scalars;
+  L.lse2 = ws.lse2;
+  L.weight = c.row_weight;
+  L.keep = ws.keep;
+  L.store_scale = store_scale;
+  L.slot_rows = plan.slot_rows;
+  // 128-row boxes along K
+  if (!make_map(&L.a[0], x, c.dtype, c.N, c.H, c.H, 128) || !make_map(&L.b[0], w, c.dtype, c.V, c.H, c.H, 128))
     return SPEC_ERR_CUDA;
-  ssv::HeadParams P = {};
-  P.M = c.N;
-  P.N = c.V;
-  P.K = c.H;
-  P.splits = 1;
-  P.bf16 = c.dtype == SPEC_BF16;
-  P.s = (float)s;
-  P.part = ws.part;
-  P.status = c.status;
-  P.scalars = ws.scalars;
-  spec_status_t r = launch_head<ssv::kHeadNorm, false>(P, x_k, w_k, x_k, st);
+  if (kept && !make_map(&L.out[0], ws.d, SPEC_F16, c.N, c.V, plan.piece, 32)) return SPEC_ERR_CUDA;
+  L.p[0] = product(c.N, c.V, c.H, 1, 0);
+  spec_status_t r = kept ? launch_head<ssv::kHeadKeep, false>(L, 1, st) : launch_head<ssv::kHeadNorm, false>(L, 1, st);
   if (r != SPEC_OK) return r;
 
   ssv::FinishParams F = {};
   F.N = c.N;
   F.k = c.k;
   F.inv_t = tp.inv_t;
-  F.c = split((double)P.s * kLn2);  // the exponents' own factor
+  F.c = split((double)L.s * kLn2);  // the exponents' own factor
   F.part = ws.sums;
   F.logits = c.logits;
   F.t = ws.t;
@@ -513,78 +539,64 @@ spec_status_t head_run(const HeadCall& c, const HeadWs& ws) {
   F.status = c.status;
   ssv::head_finish_kernel<<<(unsigned)((c.N + 7) / 8), 256, 0, st>>>(F, ws.part, (c.V + 255) / 256, c.lse, ws.lse2);
   if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
-  if (!c.grad_hidden && !c.grad_weight) return SPEC_OK;
+  if (!grads) return SPEC_OK;
 
-  CUtensorMap x_mn, w_mn, part_out;  // 64-row boxes along the other dimension
-  if (!make_map(&x_mn, x, c.dtype, c.N, c.H, c.H, 64) || !make_map(&w_mn, w, c.dtype, c.V, c.H, c.H, 64))
+  // the backward products: 64-row boxes along the other dimension
+  ssv::HeadLaunch B = L;
+  if (!make_map(&B.b[0], w, c.dtype, c.V, c.H, c.H, 64) || !make_map(&B.b[1], x, c.dtype, c.N, c.H, c.H, 64))
     return SPEC_ERR_CUDA;
-  if (c.grad_hidden && !make_map(&part_out, ws.hidden, SPEC_F32, (long long)plan.splits * plan.slot_rows, c.H, c.H, 32))
+  if (c.grad_hidden &&
+      !make_map(&B.out[0], ws.hidden, SPEC_F32, (long long)plan.splits * plan.slot_rows, c.H, c.H, 32))
     return SPEC_ERR_CUDA;
+  ssv::ListedParams Q = {};
+  Q.ids = c.ids;
+  Q.t = ws.t;
+  Q.zi = ws.zi;
+  Q.lse2 = ws.lse2;
+  Q.weight = c.row_weight;
+  Q.keep = ws.keep;
+  Q.scalars = ws.scalars;
+  Q.N = c.N;
+  Q.k = c.k;
+  Q.ld = plan.piece;
+  Q.s = (double)L.s;
+  Q.store_scale = store_scale;
+  E* d = reinterpret_cast<E*>(ws.d);
   int slots = 0;
   for (int i = 0; i < plan.pieces; ++i) {
     const int v0 = i * plan.piece;
     const int C = c.V - v0 < plan.piece ? c.V - v0 : plan.piece;
-    CUtensorMap d_out, d_k, d_mn;
-    if (!make_map(&d_out, ws.d, c.dtype, c.N, C, plan.piece, 32) ||
-        !make_map(&d_k, ws.d, c.dtype, c.N, C, plan.piece, 128) || !make_map(&d_mn, ws.d, c.dtype, c.N, C, plan.piece, 64))
-      return SPEC_ERR_CUDA;
-
-    ssv::HeadParams D = P;
-    D.N = C;
-    D.b_off = v0;
-    D.lse2 = ws.lse2;
-    D.weight = c.row_weight;
-    D.keep = ws.keep;
-    D.store_scale = store_scale;
-    if ((r = launch_head<ssv::kHeadGrad, false>(D, x_k, w_k, d_out, st)) != SPEC_OK) return r;
-
-    ssv::ListedParams L = {};
-    L.ids = c.ids;
-    L.t = ws.t;
-    L.zi = ws.zi;
-    L.lse2 = ws.lse2;
-    L.weight = c.row_weight;
-    L.keep = ws.keep;
-    L.scalars = ws.scalars;
-    L.N = c.N;
-    L.k = c.k;
-    L.v0 = v0;
-    L.C = C;
-    L.ld = plan.piece;
-    L.s = (double)P.s;
-    L.store_scale = store_scale;
-    ssv::listed_grads_kernel<E>
-        <<<(unsigned)((entries + 255) / 256), 256, 0, st>>>(L, reinterpret_cast<E*>(ws.d));
-    if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
-
-    if (c.grad_hidden) {
-      ssv::HeadParams Q = P;
-      Q.M = c.N;
-      Q.N = c.H;
-      Q.K = C;
-      Q.b_off = v0;
-      const int steps = (C + ssv::kTileK - 1) / ssv::kTileK;
-      Q.splits = plan.splits < steps ? plan.splits : steps;
-      if (i == 0) slots = Q.splits;  // later pieces are no longer than the first
-      Q.first = i == 0;
-      Q.slot_rows = plan.slot_rows;
-      if ((r = launch_head<ssv::kHeadHidden, true>(Q, d_k, w_mn, part_out, st)) != SPEC_OK) return r;
+    Q.v0 = v0;
+    Q.C = C;
+    if (kept) {
+      const dim3 grid((unsigned)c.N, (unsigned)((C + ssv::kDenseCols - 1) / ssv::kDenseCols));
+      ssv::dense_grads_kernel<E><<<grid, 256, 0, st>>>(Q, ws.part, d);
+      if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
+    } else {
+      if (!make_map(&L.out[0], ws.d, c.dtype, c.N, C, plan.piece, 32)) return SPEC_ERR_CUDA;
+      L.p[0] = product(c.N, C, c.H, 1, v0);
+      if ((r = launch_head<ssv::kHeadGrad, false>(L, 1, st)) != SPEC_OK) return r;
+      ssv::listed_grads_kernel<E><<<(unsigned)((entries + 255) / 256), 256, 0, st>>>(Q, d);
+      if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
     }
+
+    if (!make_map(&B.a[0], ws.d, c.dtype, c.N, C, plan.piece, 128) ||
+        !make_map(&B.a[1], ws.d, c.dtype, c.N, C, plan.piece, 64))
+      return SPEC_ERR_CUDA;
+    B.p[0] = product(c.N, c.H, C, plan.splits, v0);
+    B.p[1] = product(C, c.H, c.N, 1, 0);
+    B.first = i == 0;
+    if (i == 0) slots = B.p[0].splits;  // later pieces are no longer than the first
     if (c.grad_weight) {
       const int es = elem_size(c.grad_dtype);
-      CUtensorMap w_out;
-      if (!make_map(&w_out, static_cast<char*>(c.grad_weight) + (size_t)v0 * (size_t)c.H * (size_t)es, c.grad_dtype, C,
-                    c.H, c.H, 32))
+      if (!make_map(&B.out[1], static_cast<char*>(c.grad_weight) + (size_t)v0 * (size_t)c.H * (size_t)es, c.grad_dtype,
+                    C, c.H, c.H, 32))
         return SPEC_ERR_CUDA;
-      ssv::HeadParams Q = P;
-      Q.M = C;
-      Q.N = c.H;
-      Q.K = c.N;
-      Q.b_off = 0;
-      r = c.grad_dtype == SPEC_F32 ? launch_head<ssv::kHeadWeight, true>(Q, d_mn, x_mn, w_out, st)
-                                   : launch_head<ssv::kHeadWeight, false>(Q, d_mn, x_mn, w_out, st);
-      if (r != SPEC_OK) return r;
     }
+    const int which = (c.grad_hidden ? 1 : 0) | (c.grad_weight ? 2 : 0);
+    r = c.grad_weight && c.grad_dtype == SPEC_F32 ? launch_head<ssv::kHeadBack, true>(B, which, st)
+                                                  : launch_head<ssv::kHeadBack, false>(B, which, st);
+    if (r != SPEC_OK) return r;
   }
   if (c.grad_hidden) {
     const long long elems = (long long)c.N * c.H;
@@ -624,10 +636,11 @@ spec_status_t head_loss(const HeadCall& c, bool grads) {
     return from_cuda(e);
   }
   if (!c.hidden || !c.weight || !c.ids || !aligned(c.hidden, 16) || !aligned(c.weight, 16)) return SPEC_ERR_INVALID_ARG;
-  const HeadWs ws = head_ws(c.workspace, (size_t)c.N, (size_t)c.V, (size_t)c.H, (size_t)c.k, c.grad_hidden != nullptr,
+  const HeadPlan plan = head_plan(c.N, c.V, c.H, c.dtype == SPEC_BF16);
+  const HeadWs ws = head_ws(c.workspace, plan, (size_t)c.N, (size_t)c.V, (size_t)c.H, (size_t)c.k, c.grad_hidden != nullptr,
                             c.grad_weight != nullptr);
   if (!c.workspace || c.bytes < ws.total || !aligned(c.workspace, 256)) return SPEC_ERR_INVALID_ARG;
-  return c.dtype == SPEC_BF16 ? head_run<__nv_bfloat16>(c, ws) : head_run<__half>(c, ws);
+  return c.dtype == SPEC_BF16 ? head_run<__nv_bfloat16>(c, plan, ws) : head_run<__half>(c, plan, ws);
 }
 
 }  // namespace
@@ -661,8 +674,16 @@ spec_status_t spec_topk_distill_fwd_bwd(const void* student, spec_dtype_t dtype,
 size_t spec_linear_loss_workspace_bytes(int N, int V, int H, int k, int want_grad_hidden, int want_grad_weight) {
   if (!head_dims_ok(N, V, H, k) || !head_dims_fit(N, V, H, k)) return 0;
   if (N == 0) return 256;
-  return head_ws(nullptr, (size_t)N, (size_t)V, (size_t)H, (size_t)k, want_grad_hidden != 0, want_grad_weight != 0)
-      .total;
+  // for either dtype: the larger of the two plans
+  size_t most = 0;
+  for (int keep = 0; keep < 2; ++keep) {
+    const HeadPlan plan = head_plan(N, V, H, keep != 0);
+    const size_t n = head_ws(nullptr, plan, (size_t)N, (size_t)V, (size_t)H, (size_t)k, want_grad_hidden != 0,
+                             want_grad_weight != 0)
+                         .total;
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 spec_status_t spec_linear_cross_entropy_fwd_bwd(const void* hidden, const void* weight, spec_dtype_t dtype, int N,

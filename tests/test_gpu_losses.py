@@ -363,9 +363,11 @@ def test_head(ssv, N, V, H, dt, gdt, T, k, red, weighted):
     assert int(o.status) == 0
 
 
-def test_head_in_pieces(ssv):
-    """A batch long enough that the vocabulary is cut: against fp64 products on the GPU."""
-    N, V, H = 70000, 4100, 64
+@pytest.mark.parametrize("N", [70000, 170000])
+def test_head_in_pieces(ssv, N):
+    """Long batches, the second one long enough that its vocabulary is cut:
+    against fp64 products on the GPU."""
+    V, H = 4100, 64
     x, w, y, _ = head_inputs(N, V, H, BF16, 5)
     y[:N // 2] = -100
     xd, wd, yd = x.to(DEV), w.to(DEV), y.to(DEV)
