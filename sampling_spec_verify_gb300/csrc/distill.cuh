@@ -14,9 +14,9 @@
 // Bound: HBM.  A row is read once and its gradient written once; a row of
 // 151936 bf16 logits is 304 KB, more than one SM holds, so a cluster of S CTAs
 // holds it between the normaliser and the gradient, each CTA a slice in its
-// registers (NV vectors a thread; NV = 0: in shared memory, for slices that do
-// not fit).  Slices land in shared memory by bulk copies, up to two rows ahead;
-// two CTAs share an SM, so that one's exchange hides behind the other's work.
+// registers (up to NV vectors a thread; NV = 0: in shared memory, for slices that
+// do not fit and gradients that start off a vector's boundary).  Slices land in
+// shared memory by bulk copies a row ahead; two CTAs share an SM, so that one's exchange hides behind the other's work.
 #pragma once
 
 #include <type_traits>
@@ -28,7 +28,14 @@ namespace ssv {
 constexpr int kDThreads = 256;
 constexpr int kDWarps = kDThreads / 32;
 constexpr int kDMaxCluster = 16;
-constexpr int kDVecs = 10;  // vectors of a slice held by a thread
+// Most vectors of a slice held by a thread.  Longer slices mean fewer warps a row
+// and so less bookkeeping; more CTAs an SM hide more of the exchange.  Measured
+// (us, 896 x 129280 bf16 with gradient; 1024 x 151936 loss alone): 10 vectors,
+// three and four CTAs an SM 104; 66.  19 vectors, two CTAs 91; 70.  The loss
+// alone takes the same slices as with its gradient, so that both give the same
+// bits.  Kernels exist for 8, 16 and 19: places beyond a slice hold -inf and are
+// worked on without a test (a branch per vector cost 10%).
+constexpr int kDVecs = 19;
 
 struct DistillParams {
   const void* z;
@@ -38,7 +45,7 @@ struct DistillParams {
   uint32_t cap;       // bytes of a stage
   int skew;           // elements by which the base lies past a 16-byte boundary
   int odd;            // rows may start off one
-  int out_vec;        // bytes that a gradient store may write at a time: 32, 16 or (0) one element
+  int wide;           // gradients may be written a vector's at a time (always where NV > 0)
   float s;            // log2(e) / T
   const int32_t* ids; // [N, k]
   const float* t;     // [N, k]
@@ -64,12 +71,12 @@ __device__ __forceinline__ void st_async_f4(uint32_t addr, float a, float b, flo
 // Writes the gradients of a vector's tokens.  32-byte stores where fp32
 // gradients come from 16-bit logits: two 16-byte stores a thread would each
 // touch half of every sector.
-template <class O, int PV>
-__device__ __forceinline__ void store_grads(O* dst, const f32x2 (&g)[PV / 2], int bytes) {
+template <class O, int PV, int bytes>
+__device__ __forceinline__ void store_grads(O* dst, const f32x2 (&g)[PV / 2]) {
   float x[PV];
 #pragma unroll
   for (int i = 0; i < PV / 2; ++i) f2_split(g[i], x[2 * i], x[2 * i + 1]);
-  if (bytes >= 16) {
+  if constexpr (bytes >= 16) {
     if constexpr (sizeof(O) == 2) {
       static_assert(PV == 8, "16-bit gradients come from 16-bit logits");
       uint4 w;
@@ -77,17 +84,15 @@ __device__ __forceinline__ void store_grads(O* dst, const f32x2 (&g)[PV / 2], in
       w.z = Elem<O>::pack(x[4], x[5]), w.w = Elem<O>::pack(x[6], x[7]);
       __stcs(reinterpret_cast<uint4*>(dst), w);
     } else {
-      if constexpr (PV == 8) {
-        if (bytes == 32) {
+      if constexpr (PV == 8 && bytes == 32) {
           asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(x[0]), "f"(x[1]),
                        "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
                        : "memory");
-          return;
-        }
-      }
+      } else {
 #pragma unroll
-      for (int i = 0; i < PV; i += 4)
-        __stcs(reinterpret_cast<float4*>(dst + i), make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+        for (int i = 0; i < PV; i += 4)
+          __stcs(reinterpret_cast<float4*>(dst + i), make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+      }
     }
   } else {
 #pragma unroll
@@ -121,7 +126,7 @@ __device__ __forceinline__ Slice slice_of(long long n, int V, int skew, uint32_t
 }
 
 template <class E, class O, int NV>
-__global__ void __launch_bounds__(kDThreads, NV == 0 ? 1 : (std::is_same<O, NoGrad>::value ? 4 : 3)) distill_kernel(const __grid_constant__ DistillParams P) {
+__global__ void __launch_bounds__(kDThreads, NV == 0 ? 1 : 2) distill_kernel(const __grid_constant__ DistillParams P) {
   using T = Elem<E>;
   constexpr int PV = T::PV;
   constexpr bool kGrad = !std::is_same<O, NoGrad>::value;
@@ -231,7 +236,7 @@ __global__ void __launch_bounds__(kDThreads, NV == 0 ? 1 : (std::is_same<O, NoGr
       if (kGrad) {
         const f32x2 zero[PV / 2] = {};
         for (int i = tid; i < nvl; i += kDThreads)
-          store_grads<OG, PV>(out + s.a0 + (s.v0 + i) * PV, zero, P.out_vec);
+          store_grads<OG, PV, 0>(out + s.a0 + (s.v0 + i) * PV, zero);
         if (tid < s.head) out[tid] = Elem<OG>::from_f32(0.0f);
         if (tid >= 8 && tid - 8 < s.tail) out[s.a1 + tid - 8] = Elem<OG>::from_f32(0.0f);
       }
@@ -291,8 +296,8 @@ __global__ void __launch_bounds__(kDThreads, NV == 0 ? 1 : (std::is_same<O, NoGr
     if constexpr (NV > 0) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int i = tid + j * kDThreads;
-        v[j] = i < nvl ? vec[i] : low;
+        v[j] = low;
+        if (tid + j * kDThreads < nvl) v[j] = vec[tid + j * kDThreads];
       }
     }
     const float my_edge = P.odd && tid < 16 ? edge[tid] : -INFINITY;
@@ -325,8 +330,7 @@ __global__ void __launch_bounds__(kDThreads, NV == 0 ? 1 : (std::is_same<O, NoGr
       };
       if constexpr (NV > 0) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-          if (j * kDThreads < nvl) add(v[j]);
+        for (int j = 0; j < NV; ++j) add(v[j]);
       } else {
         for (int i = tid; i < nvl; i += kDThreads) add(vec[i]);
       }
@@ -414,8 +418,8 @@ __global__ void __launch_bounds__(kDThreads, NV == 0 ? 1 : (std::is_same<O, NoGr
       const float coef = grad_w;
       const f32x2 s2 = f2(P.s, P.s), m2 = f2(-go.x, -go.x), c2 = f2(go.y, go.y);
       OG* dst = out + s.a0 + (s.v0 + tid) * PV;
-      auto grads = [&](const uint4& u, int i) {
-        f32x2 p[PV / 2];
+      constexpr int kWide = sizeof(OG) * PV;  // bytes of a vector's gradients
+      auto grads = [&](const uint4& u, f32x2 (&p)[PV / 2]) {
         T::pairs(u, p);
 #pragma unroll
         for (int j = 0; j < PV / 2; ++j) {
@@ -423,14 +427,22 @@ __global__ void __launch_bounds__(kDThreads, NV == 0 ? 1 : (std::is_same<O, NoGr
           f2_split(f2_mul(f2_add(p[j], m2), s2), x, y);
           p[j] = f2_mul(f2(ex2(x), ex2(y)), c2);
         }
-        store_grads<OG, PV>(dst + i * PV, p, P.out_vec);
       };
+      f32x2 p[PV / 2];
       if constexpr (NV > 0) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-          if (tid + j * kDThreads < nvl) grads(v[j], j * kDThreads);
+        for (int j = 0; j < NV; ++j) {
+          grads(v[j], p);
+          if (tid + j * kDThreads < nvl) store_grads<OG, PV, kWide>(dst + j * kDThreads * PV, p);
+        }
       } else {
-        for (int i = 0; tid + i < nvl; i += kDThreads) grads(vec[tid + i], i);
+        for (int i = tid; i < nvl; i += kDThreads) {
+          grads(vec[i], p);
+          if (P.wide)
+            store_grads<OG, PV, kWide>(out + s.a0 + (s.v0 + i) * PV, p);
+          else
+            store_grads<OG, PV, 0>(out + s.a0 + (s.v0 + i) * PV, p);
+        }
       }
       if (P.odd && tid < 16) {
         const float g = exp2_scaled(my_edge - go.x, P.s) * go.y;

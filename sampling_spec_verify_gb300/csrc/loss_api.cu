@@ -141,16 +141,16 @@ DistillWs distill_ws(void* base, size_t N, size_t k) {
   return w;
 }
 
-// Slices of a row: what 512 threads hold in registers, with two stages and two
-// resident CTAs; rows too long for 16 such slices stay in shared memory, with
+// Slices of a row: what a CTA's threads hold in registers (one stage: it is free
+// again as soon as they do); rows too long for 16 such slices stay in shared memory, with
 // two stages or one.  Short batches spread a row over more CTAs.
 struct DistillShape {
   int S = 0, nst = 0;
   bool regs = false;
   uint32_t cap = 0;
 };
-DistillShape distill_shape(long long row_bytes, int N, int sms) {
-  const long long budget[3] = {ssv::kDVecs * ssv::kDThreads * 16, 104 * 1024, 208 * 1024};
+DistillShape distill_shape(long long row_bytes, int N, int sms, bool wide) {
+  const long long budget[3] = {wide ? ssv::kDVecs * ssv::kDThreads * 16 : -1, 104 * 1024, 208 * 1024};
   DistillShape d;
   for (int level = 0; level < 3 && !d.S; ++level)
     for (int s = 1; s <= ssv::kDMaxCluster; s *= 2)
@@ -197,10 +197,13 @@ spec_status_t launch_distill(const ssv::DistillParams& P, cudaStream_t st) {
   Device d;
   int dev = 0;
   if (!device(&d, &dev)) return SPEC_ERR_CUDA;
-  const DistillShape sh = distill_shape((long long)P.V * (long long)sizeof(E), P.N, d.sms);
+  const DistillShape sh = distill_shape((long long)P.V * (long long)sizeof(E), P.N, d.sms, P.wide != 0);
   if (!sh.S) return SPEC_ERR_UNSUPPORTED;
-  return sh.regs ? launch_distill_nv<E, O, ssv::kDVecs>(P, sh, d, dev, st)
-                 : launch_distill_nv<E, O, 0>(P, sh, d, dev, st);
+  if (!sh.regs) return launch_distill_nv<E, O, 0>(P, sh, d, dev, st);
+  const int vecs = (int)(sh.cap / 16 + ssv::kDThreads - 1) / ssv::kDThreads;
+  if (vecs <= 8) return launch_distill_nv<E, O, 8>(P, sh, d, dev, st);
+  if (vecs <= 16) return launch_distill_nv<E, O, 16>(P, sh, d, dev, st);
+  return launch_distill_nv<E, O, ssv::kDVecs>(P, sh, d, dev, st);
 }
 
 spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int k, float temperature,
@@ -213,7 +216,7 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
   if (!temperature_ok(temperature) || !std::isfinite(grad_scale)) return SPEC_ERR_INVALID_ARG;
   if (want_grad && grad_dtype != dtype && grad_dtype != SPEC_F32) return SPEC_ERR_INVALID_ARG;
   if (!loss) return SPEC_ERR_INVALID_ARG;
-  if (k > ssv::kMaxEntries || !distill_shape((long long)V * elem_size(dtype), N, 1).S) return SPEC_ERR_UNSUPPORTED;
+  if (k > ssv::kMaxEntries || !distill_shape((long long)V * elem_size(dtype), N, 1, false).S) return SPEC_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (N == 0) return from_cuda(cudaMemsetAsync(loss, 0, sizeof(float), st));
   if (!student || !ids || !logits || (want_grad && !grad)) return SPEC_ERR_INVALID_ARG;
@@ -247,9 +250,10 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
   P.k = k;
   P.skew = (int)((reinterpret_cast<uintptr_t>(student) & 15) / (uintptr_t)elem_size(dtype));
   P.odd = P.skew != 0 || ((long long)V * elem_size(dtype)) % 16 != 0;
+  P.wide = 1;
   if (want_grad) {
     const uintptr_t o = reinterpret_cast<uintptr_t>(grad) - (uintptr_t)P.skew * (uintptr_t)elem_size(grad_dtype);
-    P.out_vec = (o & 31) == 0 ? 32 : ((o & 15) == 0 ? 16 : 0);
+    P.wide = (o & (dtype != SPEC_F32 && grad_dtype == SPEC_F32 ? 31 : 15)) == 0;
   }
   P.s = (float)(kLog2e / (double)temperature);
   P.ids = ids;
