@@ -583,19 +583,50 @@ def schedule_lengths(survival: torch.Tensor, sps: torch.Tensor, *, status: Optio
 # ---------------------------------------------------------------------------
 
 _SCRATCH = {}
+_STATUS = {}
+_STATUS_WORDS = 1024
 
 
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """A workspace of the training losses, cached per (device, stream).  Its
-    contents are never zeroed, so it is not the one of the other calls."""
+def _loss_buffers(device, stream, given, nbytes, workspace, empties):
+    """(status word, workspace, empty tensors) of a training-loss call, on its
+    stream.  Status words come zeroed from a block per (device, stream), one
+    for each call; workspaces are cached per (device, stream) and never zeroed,
+    so they are not the ones of the other calls.  Inside a stream capture
+    nothing is cached: the memory belongs to the graph."""
     key = (device.index, stream.cuda_stream)
-    ws = _SCRATCH.get(key)
-    if ws is None or ws.numel() < nbytes:
-        _SCRATCH.pop(key, None)
-        ws = None  # the old one goes before the new one comes
-        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _SCRATCH[key] = ws
-    return ws
+    capturing = torch.cuda.is_current_stream_capturing()
+    current = given is None
+    with _Nothing() if current else torch.cuda.stream(stream):
+        made = [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in empties]
+        status = None
+        if made:
+            if capturing:
+                status = torch.zeros((1,), dtype=torch.int32, device=device)
+            else:
+                block = _STATUS.get(key)
+                if not block:
+                    block = list(torch.zeros((_STATUS_WORDS, 1), dtype=torch.int32, device=device).unbind())
+                    _STATUS[key] = block
+                status = block.pop()
+        if workspace is None:
+            if capturing:
+                workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+            else:
+                workspace = _SCRATCH.get(key)
+                if workspace is None or workspace.numel() < nbytes:
+                    _SCRATCH.pop(key, None)
+                    workspace = None  # the old one goes before the new one comes
+                    workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+                    _SCRATCH[key] = workspace
+    return status, workspace, made
+
+
+class _Nothing:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
 
 
 _LOSS_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
@@ -665,11 +696,10 @@ def _linear_loss(what, hidden, weight, ids, logits, ignore_index, temperature, g
     grads = want_hidden or want_weight
     gdt, gcode = _grad_code(grad_dtype, hidden.dtype, "hidden")
     red = _reduction_code(reduction)
+    empties = []
     if out is None:
-        f = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
-        out = LinearLossOutput(f(1), f(N), f(N), f(N, H, dtype=gdt) if want_hidden else None,
-                               f(V, H, dtype=gdt) if want_weight else None,
-                               torch.zeros((1,), dtype=torch.int32, device=dev))
+        empties = [((1,), torch.float32), ((N,), torch.float32), ((N,), torch.float32)]
+        empties += [((N, H), gdt)] * want_hidden + [((V, H), gdt)] * want_weight
     else:
         _need(out.loss, "out.loss", dtype=torch.float32, shape=(1,), device=dev)
         _need_out(out.row_loss, "row_loss", torch.float32, (N,), dev)
@@ -682,7 +712,10 @@ def _linear_loss(what, hidden, weight, ids, logits, ignore_index, temperature, g
             _need_out(out.grad_weight, "grad_weight", gdt, (V, H), dev)
     sh, s = _stream_handle(stream, dev)
     need = L.spec_linear_loss_workspace_bytes(N, V, H, k, int(want_hidden), int(want_weight))
-    ws = workspace if workspace is not None else _scratch(need, dev, s)
+    status, ws, made = _loss_buffers(dev, s, stream, need, workspace, empties)
+    if out is None:
+        out = LinearLossOutput(made[0], made[1], made[2], made[3] if want_hidden else None,
+                               made[-1] if want_weight else None, status)
     dims = (_ptr(hidden), _ptr(weight), _LOSS_DTYPES[hidden.dtype], N, V, H)
     rows = (_ptr(row_weight), red, _ptr(out.loss), _ptr(out.row_loss), _ptr(out.lse))
     end = (_ptr(out.status), _ptr(ws), ws.numel() * ws.element_size(), sh)
@@ -790,10 +823,9 @@ def _distill(what, student, ids, logits, lse, temperature, grad_scale, row_weigh
         _need(row_weight, "row_weight", dtype=torch.float32, shape=(N,), device=dev)
     gdt, gcode = _grad_code(grad_dtype, student.dtype, "student")
     red = _reduction_code(reduction)
+    empties = []
     if out is None:
-        f = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
-        out = DistillOutput(f(1), f(N), f(N, V, dtype=gdt) if want_grad else None,
-                            torch.zeros((1,), dtype=torch.int32, device=dev))
+        empties = [((1,), torch.float32), ((N,), torch.float32)] + [((N, V), gdt)] * want_grad
     else:
         _need(out.loss, "out.loss", dtype=torch.float32, shape=(1,), device=dev)
         _need_out(out.row_loss, "row_loss", torch.float32, (N,), dev)
@@ -802,7 +834,9 @@ def _distill(what, student, ids, logits, lse, temperature, grad_scale, row_weigh
             _need(out.grad, "out.grad", dtype=gdt, shape=(N, V), device=dev)
     sh, s = _stream_handle(stream, dev)
     need = L.spec_topk_distill_workspace_bytes(N, V, k)
-    ws = workspace if workspace is not None else _scratch(need, dev, s)
+    status, ws, made = _loss_buffers(dev, s, stream, need, workspace, empties)
+    if out is None:
+        out = DistillOutput(made[0], made[1], made[2] if want_grad else None, status)
     end = (_ptr(out.status), _ptr(ws), ws.numel() * ws.element_size(), sh)
     common = (_ptr(ids), _ptr(logits), _ptr(lse), _ptr(row_weight), red, _ptr(out.loss), _ptr(out.row_loss))
     dims = (_ptr(student), _LOSS_DTYPES[student.dtype], N, V, k, float(temperature))

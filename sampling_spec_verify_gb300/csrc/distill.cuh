@@ -33,7 +33,7 @@ constexpr int kDMaxCluster = 16;
 // (us, 896 x 129280 bf16 with gradient; 1024 x 151936 loss alone): 10 vectors,
 // three and four CTAs an SM 104; 66.  19 vectors, two CTAs 91; 70.  The loss
 // alone takes the same slices as with its gradient, so that both give the same
-// bits.  Kernels exist for 8, 16 and 19: places beyond a slice hold -inf and are
+// bits.  Kernels exist for 4, 8, 13, 16 and 19: places beyond a slice hold -inf and are
 // worked on without a test (a branch per vector cost 10%).
 constexpr int kDVecs = 19;
 
@@ -154,6 +154,8 @@ __global__ void __launch_bounds__(kDThreads, NV == 0 ? 1 : 2) distill_kernel(con
     fence_mbar_init();
     abort_flag = 0;
   }
+  let_next_start();
+  follow_previous();
 
   const uint64_t policy = l2_evict_first_policy();
   // Starts the copy of row n's slice into stage st (thread 0; rows that are
@@ -469,6 +471,8 @@ __global__ void __launch_bounds__(kDThreads, NV == 0 ? 1 : 2) distill_kernel(con
 
 // Row losses and their sum: a warp per row.
 __global__ void __launch_bounds__(256) distill_finish_kernel(const FinishParams P, const RowNorm* norm) {
+  let_next_start();
+  follow_previous();
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long n = (long long)blockIdx.x * 8 + w;
   const bool on = n < P.N && P.keep[n];

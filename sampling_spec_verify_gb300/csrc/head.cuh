@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
     prefetch_map(&L.a[0]);
     prefetch_map(&L.b[0]);
   }
+  let_next_start();
   if (wid == 0) {
     tmem_alloc_pair(smem_addr(&tmem_slot), 512);
     tmem_relinquish_pair();
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
+  follow_previous();
   const uint32_t tmem = tmem_slot;
   const int clusters = gridDim.x / 2, first_tile = blockIdx.x / 2;
 
@@ -405,6 +407,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
 template <class E>
 __global__ void __launch_bounds__(256) listed_logits_kernel(const E* x, const E* w, const int32_t* ids,
                                                             const uint8_t* keep, int N, int H, int k, float* zi) {
+  let_next_start();
+  follow_previous();
   const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (i >= (long long)N * k) return;
@@ -442,6 +446,8 @@ struct ListedParams {
 };
 template <class E>
 __global__ void __launch_bounds__(256) listed_grads_kernel(const ListedParams P, E* d) {
+  let_next_start();
+  follow_previous();
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   if (i >= (long long)P.N * P.k) return;
   const long long n = i / P.k;
@@ -457,6 +463,8 @@ __global__ void __launch_bounds__(256) listed_grads_kernel(const ListedParams P,
 constexpr int kDenseCols = 8192;
 template <class E>
 __global__ void __launch_bounds__(256) dense_grads_kernel(const ListedParams P, const float2* part, E* d) {
+  let_next_start();
+  follow_previous();
   const long long n = blockIdx.x;
   const int c0 = blockIdx.y * kDenseCols, c1 = min(P.C, c0 + kDenseCols);
   const float cf = P.keep[n] ? (P.weight ? P.weight[n] : 1.0f) * P.scalars->inv_wmax * P.store_scale : 0.0f;
@@ -507,6 +515,8 @@ __global__ void __launch_bounds__(256) dense_grads_kernel(const ListedParams P, 
 __global__ void __launch_bounds__(256) head_finish_kernel(const FinishParams P, const float2* part, int tiles_n,
                                                           float* lse_out, float* lse2) {
   __shared__ float2 sh[32][9];
+  let_next_start();
+  follow_previous();
   const int r8 = threadIdx.x & 7, g = threadIdx.x >> 3;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long base = (long long)blockIdx.x * 8;
@@ -564,6 +574,8 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const FinishParams P, 
 template <class O>
 __global__ void __launch_bounds__(256) hidden_out_kernel(const float* part, int slots, long long slot_elems,
                                                          long long elems, const LossScalars* scalars, O* out) {
+  let_next_start();
+  follow_previous();
   const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= elems) return;
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);

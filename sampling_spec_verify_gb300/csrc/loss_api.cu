@@ -94,6 +94,33 @@ int resident_clusters(Residency& r, const void* fn, int S, int smem, int threads
   return n;
 }
 
+// Launches a kernel; all but the first of a call may start while the previous
+// one drains (the kernels wait for it themselves).
+template <class... P, class... A>
+cudaError_t launch(void (*fn)(P...), dim3 grid, int threads, int smem, int cluster, bool first, cudaStream_t st,
+                   const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (!first) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 0) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return count_launch(cudaLaunchKernelEx(&cfg, fn, args...));
+}
+
 // Carves a workspace into 256-byte-aligned parts; with a null base it measures.
 struct Carver {
   char* base;
@@ -178,18 +205,11 @@ spec_status_t launch_distill_nv(ssv::DistillParams P, const DistillShape& sh, co
   const int fit = resident_clusters(res, fn, sh.S, smem, ssv::kDThreads, dev, d.smem_optin);
   if (fit <= 0) return SPEC_ERR_CUDA;
   const int G = P.N < fit ? P.N : fit;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(G * sh.S));
-  cfg.blockDim = dim3(ssv::kDThreads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)sh.S;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return from_cuda(count_launch(cudaLaunchKernelEx(&cfg, ssv::distill_kernel<E, O, NV>, P)));
+  // Two CTAs take all registers of an SM: started around the previous kernel's
+  // CTAs, a full grid lands unevenly (1792 x 151936: 353 us a pass against 288).
+  const bool plain = G * sh.S > d.sms;
+  return from_cuda(launch(ssv::distill_kernel<E, O, NV>, dim3((unsigned)(G * sh.S)), ssv::kDThreads, smem, sh.S, plain,
+                          st, P));
 }
 
 template <class E, class O>
@@ -201,7 +221,9 @@ spec_status_t launch_distill(const ssv::DistillParams& P, cudaStream_t st) {
   if (!sh.S) return SPEC_ERR_UNSUPPORTED;
   if (!sh.regs) return launch_distill_nv<E, O, 0>(P, sh, d, dev, st);
   const int vecs = (int)(sh.cap / 16 + ssv::kDThreads - 1) / ssv::kDThreads;
+  if (vecs <= 4) return launch_distill_nv<E, O, 4>(P, sh, d, dev, st);
   if (vecs <= 8) return launch_distill_nv<E, O, 8>(P, sh, d, dev, st);
+  if (vecs <= 13) return launch_distill_nv<E, O, 13>(P, sh, d, dev, st);
   if (vecs <= 16) return launch_distill_nv<E, O, 16>(P, sh, d, dev, st);
   return launch_distill_nv<E, O, ssv::kDVecs>(P, sh, d, dev, st);
 }
@@ -239,8 +261,8 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
   tp.scalars = ws.scalars;
   tp.status = status;
   const unsigned row_grid = (unsigned)((N + ssv::kTargetWarps - 1) / ssv::kTargetWarps);
-  ssv::targets_kernel<<<row_grid, ssv::kTargetWarps * 32, 0, st>>>(tp);
-  if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (launch(ssv::targets_kernel, dim3(row_grid), ssv::kTargetWarps * 32, 0, 0, true, st, tp) != cudaSuccess)
+    return SPEC_ERR_CUDA;
 
   ssv::DistillParams P = {};
   P.z = student;
@@ -300,8 +322,8 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
   F.row_loss = row_loss ? row_loss : ws.row_loss;
   F.scalars = ws.scalars;
   F.status = status;
-  ssv::distill_finish_kernel<<<(unsigned)((N + 7) / 8), 256, 0, st>>>(F, ws.norm);
-  return from_cuda(count_launch(cudaGetLastError()));
+  return from_cuda(launch(ssv::distill_finish_kernel, dim3((unsigned)((N + 7) / 8)), 256, 0, 0, false, st, F,
+                          (const ssv::RowNorm*)ws.norm));
 }
 
 // ---- losses through the head --------------------------------------------------------
@@ -448,8 +470,8 @@ spec_status_t launch_head(ssv::HeadLaunch& L, int which, cudaStream_t st) {
   L.tiles0 = (int)t0;
   L.tiles = (int)(t0 + t1);
   const int G = L.tiles < fit ? L.tiles : fit;
-  ssv::head_kernel<OP, OUT32><<<2 * G, ssv::kHeadThreads, ssv::kHeadSmem, st>>>(L);
-  return from_cuda(count_launch(cudaGetLastError()));
+  return from_cuda(launch(ssv::head_kernel<OP, OUT32>, dim3((unsigned)(2 * G)), ssv::kHeadThreads, ssv::kHeadSmem, 0,
+                          false, st, L));
 }
 
 struct HeadCall {
@@ -493,12 +515,12 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   tp.keep = ws.keep;
   tp.scalars = ws.scalars;
   tp.status = c.status;
-  ssv::targets_kernel<<<(unsigned)((c.N + ssv::kTargetWarps - 1) / ssv::kTargetWarps), ssv::kTargetWarps * 32, 0,
-                        st>>>(tp);
-  if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
-  ssv::listed_logits_kernel<E><<<(unsigned)((entries + 7) / 8), 256, 0, st>>>(x, w, c.ids, ws.keep, c.N, c.H, c.k,
-                                                                              ws.zi);
-  if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (launch(ssv::targets_kernel, dim3((unsigned)((c.N + ssv::kTargetWarps - 1) / ssv::kTargetWarps)),
+             ssv::kTargetWarps * 32, 0, 0, true, st, tp) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  if (launch(ssv::listed_logits_kernel<E>, dim3((unsigned)((entries + 7) / 8)), 256, 0, 0, false, st, x, w, c.ids,
+             (const uint8_t*)ws.keep, c.N, c.H, c.k, ws.zi) != cudaSuccess)
+    return SPEC_ERR_CUDA;
 
   const bool grads = c.grad_hidden || c.grad_weight;
   const bool kept = grads && plan.kept;
@@ -541,8 +563,9 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   F.row_loss = c.row_loss ? c.row_loss : ws.row_loss;
   F.scalars = ws.scalars;
   F.status = c.status;
-  ssv::head_finish_kernel<<<(unsigned)((c.N + 7) / 8), 256, 0, st>>>(F, ws.part, (c.V + 255) / 256, c.lse, ws.lse2);
-  if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (launch(ssv::head_finish_kernel, dim3((unsigned)((c.N + 7) / 8)), 256, 0, 0, false, st, F,
+             (const float2*)ws.part, (c.V + 255) / 256, c.lse, ws.lse2) != cudaSuccess)
+    return SPEC_ERR_CUDA;
   if (!grads) return SPEC_OK;
 
   // the backward products: 64-row boxes along the other dimension
@@ -574,14 +597,15 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
     Q.C = C;
     if (kept) {
       const dim3 grid((unsigned)c.N, (unsigned)((C + ssv::kDenseCols - 1) / ssv::kDenseCols));
-      ssv::dense_grads_kernel<E><<<grid, 256, 0, st>>>(Q, ws.part, d);
-      if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
+      if (launch(ssv::dense_grads_kernel<E>, grid, 256, 0, 0, false, st, Q, (const float2*)ws.part, d) != cudaSuccess)
+        return SPEC_ERR_CUDA;
     } else {
       if (!make_map(&L.out[0], ws.d, c.dtype, c.N, C, plan.piece, 32)) return SPEC_ERR_CUDA;
       L.p[0] = product(c.N, C, c.H, 1, v0);
       if ((r = launch_head<ssv::kHeadGrad, false>(L, 1, st)) != SPEC_OK) return r;
-      ssv::listed_grads_kernel<E><<<(unsigned)((entries + 255) / 256), 256, 0, st>>>(Q, d);
-      if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
+      if (launch(ssv::listed_grads_kernel<E>, dim3((unsigned)((entries + 255) / 256)), 256, 0, 0, false, st, Q, d) !=
+          cudaSuccess)
+        return SPEC_ERR_CUDA;
     }
 
     if (!make_map(&B.a[0], ws.d, c.dtype, c.N, C, plan.piece, 128) ||
@@ -605,14 +629,16 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   if (c.grad_hidden) {
     const long long elems = (long long)c.N * c.H;
     const long long slot = (long long)plan.slot_rows * c.H;
-    const unsigned grid = (unsigned)((elems / 4 + 255) / 256);
-    if (c.grad_dtype == SPEC_F32)
-      ssv::hidden_out_kernel<float><<<grid, 256, 0, st>>>(ws.hidden, slots, slot, elems, ws.scalars,
-                                                          static_cast<float*>(c.grad_hidden));
-    else
-      ssv::hidden_out_kernel<E><<<grid, 256, 0, st>>>(ws.hidden, slots, slot, elems, ws.scalars,
-                                                      static_cast<E*>(c.grad_hidden));
-    if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
+    const dim3 grid((unsigned)((elems / 4 + 255) / 256));
+    const ssv::LossScalars* sc = ws.scalars;
+    const float* part = ws.hidden;
+    const cudaError_t e =
+        c.grad_dtype == SPEC_F32
+            ? launch(ssv::hidden_out_kernel<float>, grid, 256, 0, 0, false, st, part, slots, slot, elems, sc,
+                     static_cast<float*>(c.grad_hidden))
+            : launch(ssv::hidden_out_kernel<E>, grid, 256, 0, 0, false, st, part, slots, slot, elems, sc,
+                     static_cast<E*>(c.grad_hidden));
+    if (e != cudaSuccess) return SPEC_ERR_CUDA;
   }
   return SPEC_OK;
 }

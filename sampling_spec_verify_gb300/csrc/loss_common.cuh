@@ -208,6 +208,14 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
+// The kernels of a call follow each other by programmatic launches: a kernel
+// starts its prologue while the previous one drains, and waits here before it
+// touches anything that was written before it.
+__device__ __forceinline__ void follow_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ void raise(uint32_t* status, uint32_t bits) {
   if (status && bits) atomicOr(status, bits);
 }
@@ -252,6 +260,7 @@ __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const Target
       P.t[n] = ok ? 1.0f : 0.0f;
       P.row[n] = RowTeacher{0.0f, 0.0f, ok ? 1.0f : 0.0f, 0.0f};
     }
+    let_next_start();
     return;
   }
 
@@ -334,6 +343,7 @@ __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const Target
     P.row[n] = r;
     P.keep[n] = ok;
   }
+  let_next_start();  // not before: kernels of whole SMs would be placed around this one's CTAs
 }
 
 // ---- row losses and their sum --------------------------------------------------
