@@ -114,13 +114,14 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, bool bf16) {
   return bf16 ? Elem<__nv_bfloat16>::pack(a, b) : Elem<__half>::pack(a, b);
 }
 
-// Unnormalised probabilities are kept as fp16 2^(z' - m + 15), m the row's
-// maximum in the tile: 11 bits down to 2^-29 of the largest, so that rounding D
-// to the operands' type afterwards stays the one rounding that counts.  (Calls
-// that keep none use the same exponents, for the same bits.)
+// Unnormalised probabilities are kept as 2^(z' - m + 15), m the row's maximum in
+// the tile: for bf16 operands in fp16, whose 11 bits (down to 2^-29 of the
+// largest) leave rounding D to bf16 the one rounding that counts; for fp16
+// operands in fp32.  (Calls that keep none use the same exponents, for the same
+// bits.)
 constexpr float kKeepShift = 15.0f;
 
-// OUT32: dW is fp32.
+// OUT32: kHeadKeep keeps fp32; dW of kHeadBack is fp32.
 template <HeadOp OP, bool OUT32>
 __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
     head_kernel(const __grid_constant__ HeadLaunch L) {
@@ -319,12 +320,13 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
         }
         m *= L.s;
         const float off = m - kKeepShift;
-        for (int c = 0; c < kTileN; c += 64) {
+        constexpr int kCols = OP == kHeadKeep && OUT32 ? 32 : 64;
+        for (int c = 0; c < kTileN; c += kCols) {
           if (c >= cols) break;
           uint32_t dst = 0;
           if constexpr (OP == kHeadKeep) dst = next_buffer();
 #pragma unroll
-          for (int h = 0; h < 64; h += 32) {
+          for (int h = 0; h < kCols; h += 32) {
             float v[32];
             tmem_load32(src + c + h, v);
             float a = 0.0f;
@@ -335,7 +337,12 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
               a += v[j];
             }
             sum += a;
-            if constexpr (OP == kHeadKeep) stage16(dst, h / 8, v, false);
+            if constexpr (OP == kHeadKeep) {
+              if constexpr (OUT32)
+                stage32(dst, v);
+              else
+                stage16(dst, h / 8, v, false);
+            }
           }
           if constexpr (OP == kHeadKeep) send(&L.out[0], dst, col0 + c, row0, row0 < M, false);
         }
@@ -458,26 +465,30 @@ __global__ void __launch_bounds__(256) listed_grads_kernel(const ListedParams P,
   d[n * P.ld + (id - P.v0)] = Elem<E>::from_f32(cf == 0.0f ? 0.0f : (q - P.t[i]) * cf);
 }
 
-// Turns kept probabilities into D, in place: one CTA per row and kDenseCols
-// tokens (one read and one write of the piece; the listed tokens after it).
+// Turns kept probabilities (S; fp16 ones lie where D goes) into D: one CTA per
+// row and kDenseCols tokens (one read and one write, the listed tokens after).
 constexpr int kDenseCols = 8192;
-template <class E>
-__global__ void __launch_bounds__(256) dense_grads_kernel(const ListedParams P, const float2* part, E* d) {
+template <class E, class S>
+__global__ void __launch_bounds__(256) dense_grads_kernel(const ListedParams P, const float2* part, const S* kept,
+                                                          E* d) {
   let_next_start();
   follow_previous();
   const long long n = blockIdx.x;
   const int c0 = blockIdx.y * kDenseCols, c1 = min(P.C, c0 + kDenseCols);
   const float cf = P.keep[n] ? (P.weight ? P.weight[n] : 1.0f) * P.scalars->inv_wmax * P.store_scale : 0.0f;
   const float lse = P.lse2[n];
-  uint4* row = reinterpret_cast<uint4*>(d + n * P.ld);
+  constexpr int kWords = sizeof(S) / 2;  // 16-byte words of eight entries
+  const uint4* src = reinterpret_cast<const uint4*>(kept + n * P.ld);
+  uint4* dst = reinterpret_cast<uint4*>(d + n * P.ld);
   constexpr int kPer = kDenseCols / 8 / 256;
-  uint4 v[kPer];
+  uint4 v[kPer][kWords];
   float f[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int c = c0 + (i * 256 + threadIdx.x) * 8;
     if (c < c1) {
-      v[i] = __ldcs(row + c / 8);
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) v[i][w] = __ldcs(src + c / 8 * kWords + w);
       f[i] = part[(long long)(c >> 8) * P.N + n].x;
     }
   }
@@ -489,11 +500,19 @@ __global__ void __launch_bounds__(256) dense_grads_kernel(const ListedParams P, 
       if (cf != 0.0f) {
         const float m = ex2(f[i] - lse) * cf;
         float x[8];
-        Elem<__half>::unpack(v[i], x);
+        if constexpr (kWords == 1) {
+          Elem<S>::unpack(v[i][0], x);
+        } else {
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+            x[4 * w] = __uint_as_float(v[i][w].x), x[4 * w + 1] = __uint_as_float(v[i][w].y);
+            x[4 * w + 2] = __uint_as_float(v[i][w].z), x[4 * w + 3] = __uint_as_float(v[i][w].w);
+          }
+        }
         o.x = Elem<E>::pack(x[0] * m, x[1] * m), o.y = Elem<E>::pack(x[2] * m, x[3] * m);
         o.z = Elem<E>::pack(x[4] * m, x[5] * m), o.w = Elem<E>::pack(x[6] * m, x[7] * m);
       }
-      row[c / 8] = o;
+      dst[c / 8] = o;
     }
   }
   __syncthreads();

@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "distill.cuh"
 #include "head.cuh"
@@ -329,28 +330,30 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
 // ---- losses through the head --------------------------------------------------------
 
 constexpr int kPairs = 76;                       // CTA pairs in flight, for the split rule
-// A bf16 batch whose probabilities fit kKeepBytes keeps them between the
-// passes (1792 x 151936 x 2048, both gradients: 2.3 ms against 2.8); the others
-// go in pieces of kPieceBytes, and so does fp16, whose own rounding the kept
-// one would double.
+// A batch whose probabilities fit kKeepBytes (2 bytes an entry for bf16; 6 for
+// fp16, which keeps them in fp32 beside D) keeps them between the passes (1792 x
+// 151936 x 2048, both gradients: 2.3 ms against 2.8); the others go in pieces of
+// kPieceBytes.
 constexpr size_t kKeepBytes = (size_t)1280 << 20;
 constexpr size_t kPieceBytes = (size_t)256 << 20;
 
 // How a call is cut: pieces of the vocabulary and splits of a piece's depth in
 // the product that gives the hidden states' gradient.
 struct HeadPlan {
-  bool kept;       // one piece, holding pass 1's probabilities
+  bool kept;       // one piece, pass 1's probabilities kept
+  bool kept32;     // in fp32
   int piece;       // tokens per piece, a multiple of 256
   int pieces;
   int splits;
   int slot_rows;
 };
-HeadPlan head_plan(int N, int V, int H, bool may_keep) {
+HeadPlan head_plan(int N, int V, int H, bool bf16) {
   HeadPlan p;
   const long long vt = ((long long)V + 255) / 256;
   long long cap = (long long)(kPieceBytes / 2 / (size_t)N) / 256;  // tiles of tokens
   if (cap < 8) cap = 8;
-  p.kept = may_keep && (size_t)N * (size_t)vt * 512 <= kKeepBytes;
+  p.kept32 = !bf16;
+  p.kept = (size_t)N * (size_t)vt * (bf16 ? 512 : 1536) <= kKeepBytes;
   if (p.kept) cap = vt;
   p.pieces = (int)((vt + cap - 1) / cap);
   p.piece = (int)((vt + p.pieces - 1) / p.pieces) * 256;
@@ -385,6 +388,7 @@ struct HeadWs {
   float2* part;
   float* hidden;
   uint16_t* d;
+  float* e;  // fp32 probabilities
   size_t total;
 };
 HeadWs head_ws(void* base, const HeadPlan& p, size_t N, size_t V, size_t H, size_t k, bool gh, bool gw) {
@@ -401,6 +405,7 @@ HeadWs head_ws(void* base, const HeadPlan& p, size_t N, size_t V, size_t H, size
   w.part = c.take<float2>(N * ((V + 255) / 256));
   w.hidden = gh ? c.take<float>((size_t)p.splits * (size_t)p.slot_rows * H) : nullptr;
   w.d = gh || gw ? c.take<uint16_t>(N * (size_t)p.piece) : nullptr;
+  w.e = (gh || gw) && p.kept && p.kept32 ? c.take<float>(N * (size_t)p.piece) : nullptr;
   w.total = c.used;
   return w;
 }
@@ -539,9 +544,12 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   // 128-row boxes along K
   if (!make_map(&L.a[0], x, c.dtype, c.N, c.H, c.H, 128) || !make_map(&L.b[0], w, c.dtype, c.V, c.H, c.H, 128))
     return SPEC_ERR_CUDA;
-  if (kept && !make_map(&L.out[0], ws.d, SPEC_F16, c.N, c.V, plan.piece, 32)) return SPEC_ERR_CUDA;
+  constexpr bool kWide = std::is_same<E, __half>::value;
+  using S = typename std::conditional<kWide, float, __half>::type;  // of kept probabilities
+  const void* room = kWide ? (const void*)ws.e : (const void*)ws.d;
+  if (kept && !make_map(&L.out[0], room, kWide ? SPEC_F32 : SPEC_F16, c.N, c.V, plan.piece, 32)) return SPEC_ERR_CUDA;
   L.p[0] = product(c.N, c.V, c.H, 1, 0);
-  spec_status_t r = kept ? launch_head<ssv::kHeadKeep, false>(L, 1, st) : launch_head<ssv::kHeadNorm, false>(L, 1, st);
+  spec_status_t r = kept ? launch_head<ssv::kHeadKeep, kWide>(L, 1, st) : launch_head<ssv::kHeadNorm, false>(L, 1, st);
   if (r != SPEC_OK) return r;
 
   ssv::FinishParams F = {};
@@ -597,7 +605,8 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
     Q.C = C;
     if (kept) {
       const dim3 grid((unsigned)c.N, (unsigned)((C + ssv::kDenseCols - 1) / ssv::kDenseCols));
-      if (launch(ssv::dense_grads_kernel<E>, grid, 256, 0, 0, false, st, Q, (const float2*)ws.part, d) != cudaSuccess)
+      if (launch(ssv::dense_grads_kernel<E, S>, grid, 256, 0, 0, false, st, Q, (const float2*)ws.part,
+                 static_cast<const S*>(room), d) != cudaSuccess)
         return SPEC_ERR_CUDA;
     } else {
       if (!make_map(&L.out[0], ws.d, c.dtype, c.N, C, plan.piece, 32)) return SPEC_ERR_CUDA;

@@ -264,34 +264,37 @@ __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const Target
     return;
   }
 
-  for (int i = lane; i < kHashSlots; i += 32) hash[w][i] = -1;
-  __syncwarp();
   constexpr int kPer = kMaxEntries / 32;
   float x[kPer];
+  int id[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = lane + 32 * j;
+    id[j] = i < P.k ? P.ids[n * P.k + i] : -1;
+    x[j] = i < P.k ? P.logits[n * P.k + i] : -INFINITY;
+  }
+  for (int i = lane; i < kHashSlots; i += 32) hash[w][i] = -1;
+  __syncwarp();
   bool bad = false, any = false;
   float m = -INFINITY;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    const int i = lane + 32 * j;
-    x[j] = -INFINITY;
-    if (i < P.k) {
-      const int id = P.ids[n * P.k + i];
-      if (id < -1 || id >= P.V) bad = true;
-      if (id >= 0 && id < P.V) {
-        any = true;
-        x[j] = P.logits[n * P.k + i];
-        uint32_t s = ((uint32_t)id * 2654435761u) >> 23;  // 9 bits
-        for (int probe = 0; probe < kHashSlots; ++probe) {
-          const int old = atomicCAS(&hash[w][s], -1, id);
-          if (old == -1) break;
-          if (old == id) {
-            bad = true;
-            break;
-          }
-          s = (s + 1) & (kHashSlots - 1);
+    if (id[j] >= 0 && id[j] < P.V) {
+      any = true;
+      uint32_t s = ((uint32_t)id[j] * 2654435761u) >> 23;  // 9 bits
+      for (int probe = 0; probe < kHashSlots; ++probe) {
+        const int old = atomicCAS(&hash[w][s], -1, id[j]);
+        if (old == -1) break;
+        if (old == id[j]) {
+          bad = true;
+          break;
         }
-        m = max_nan(m, x[j]);
+        s = (s + 1) & (kHashSlots - 1);
       }
+      m = max_nan(m, x[j]);
+    } else {
+      bad |= id[j] != -1;
+      x[j] = -INFINITY;
     }
   }
   bad = __any_sync(0xffffffffu, bad);
