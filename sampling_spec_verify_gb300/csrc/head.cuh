@@ -407,6 +407,16 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
   if (wid == 0) tmem_free_pair(tmem, 512);
 }
 
+// Copies rows to a pitch of `ld` elements (16 bytes a thread).
+__global__ void __launch_bounds__(256) repitch_kernel(const uint4* src, uint4* dst, int N, int words, int ld_words) {
+  let_next_start();
+  follow_previous();
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (long long)N * words) return;
+  const long long n = i / words;
+  dst[n * ld_words + (i - n * words)] = src[i];
+}
+
 // ---- the listed tokens -----------------------------------------------------------
 
 // Raw logits of the listed tokens, zi[n, i] = X_n . W_id: one warp each, fp32

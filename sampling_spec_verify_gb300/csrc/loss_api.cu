@@ -376,7 +376,14 @@ HeadPlan head_plan(int N, int V, int H, bool bf16) {
   return p;
 }
 
+// Rows that start off a 32-byte sector cost the products a quarter of their rate
+// (1001 x 50257, bf16: H = 1536 94 us, 1544 125, 1552 103); the hidden states are
+// copied to whole lines for them.  (The head is too large to copy.)
+bool repitched(size_t H) { return H % 16 != 0; }
+size_t pitch_of(size_t H) { return repitched(H) ? (H + 63) / 64 * 64 : H; }
+
 struct HeadWs {
+  uint16_t* x;  // hidden states at pitch_of(H), where they are copied
   ssv::LossScalars* scalars;
   float* t;
   ssv::RowTeacher* row;
@@ -395,6 +402,7 @@ HeadWs head_ws(void* base, const HeadPlan& p, size_t N, size_t V, size_t H, size
   Carver c{static_cast<char*>(base)};
   HeadWs w;
   w.scalars = c.take<ssv::LossScalars>(1);
+  w.x = repitched(H) ? c.take<uint16_t>(N * pitch_of(H)) : nullptr;
   w.t = c.take<float>(N * k);
   w.row = c.take<ssv::RowTeacher>(N);
   w.keep = c.take<uint8_t>(N);
@@ -527,6 +535,15 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
              (const uint8_t*)ws.keep, c.N, c.H, c.k, ws.zi) != cudaSuccess)
     return SPEC_ERR_CUDA;
 
+  const int ldx = (int)pitch_of((size_t)c.H);
+  const void* xp = x;
+  if (ws.x) {
+    const long long words = (long long)c.N * (c.H / 8);
+    if (launch(ssv::repitch_kernel, dim3((unsigned)((words + 255) / 256)), 256, 0, 0, false, st,
+               reinterpret_cast<const uint4*>(x), reinterpret_cast<uint4*>(ws.x), c.N, c.H / 8, ldx / 8) != cudaSuccess)
+      return SPEC_ERR_CUDA;
+    xp = ws.x;
+  }
   const bool grads = c.grad_hidden || c.grad_weight;
   const bool kept = grads && plan.kept;
   ssv::HeadLaunch L;
@@ -542,7 +559,7 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   L.store_scale = store_scale;
   L.slot_rows = plan.slot_rows;
   // 128-row boxes along K
-  if (!make_map(&L.a[0], x, c.dtype, c.N, c.H, c.H, 128) || !make_map(&L.b[0], w, c.dtype, c.V, c.H, c.H, 128))
+  if (!make_map(&L.a[0], xp, c.dtype, c.N, c.H, ldx, 128) || !make_map(&L.b[0], w, c.dtype, c.V, c.H, c.H, 128))
     return SPEC_ERR_CUDA;
   constexpr bool kWide = std::is_same<E, __half>::value;
   using S = typename std::conditional<kWide, float, __half>::type;  // of kept probabilities
@@ -578,7 +595,7 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
 
   // the backward products: 64-row boxes along the other dimension
   ssv::HeadLaunch B = L;
-  if (!make_map(&B.b[0], w, c.dtype, c.V, c.H, c.H, 64) || !make_map(&B.b[1], x, c.dtype, c.N, c.H, c.H, 64))
+  if (!make_map(&B.b[0], w, c.dtype, c.V, c.H, c.H, 64) || !make_map(&B.b[1], xp, c.dtype, c.N, c.H, ldx, 64))
     return SPEC_ERR_CUDA;
   if (c.grad_hidden &&
       !make_map(&B.out[0], ws.hidden, SPEC_F32, (long long)plan.splits * plan.slot_rows, c.H, c.H, 32))
