@@ -151,7 +151,7 @@ struct DistillWs {
   float* zi;
   ssv::RowNorm* norm;
   float* row_loss;
-  double* part;
+  float4* part;
   size_t total;
 };
 DistillWs distill_ws(void* base, size_t N, size_t k) {
@@ -164,7 +164,7 @@ DistillWs distill_ws(void* base, size_t N, size_t k) {
   w.zi = c.take<float>(N * k);
   w.norm = c.take<ssv::RowNorm>(N);
   w.row_loss = c.take<float>(N);
-  w.part = c.take<double>(3 * ((N + 7) / 8));
+  w.part = c.take<float4>((N + 7) / 8);
   w.total = c.used;
   return w;
 }
@@ -391,7 +391,7 @@ struct HeadWs {
   float* zi;
   float* row_loss;
   float* lse2;
-  double* sums;
+  float4* sums;
   float2* part;
   float* hidden;
   uint16_t* d;
@@ -409,7 +409,7 @@ HeadWs head_ws(void* base, const HeadPlan& p, size_t N, size_t V, size_t H, size
   w.zi = c.take<float>(N * k);
   w.row_loss = c.take<float>(N);
   w.lse2 = c.take<float>(N);
-  w.sums = c.take<double>(3 * ((N + 7) / 8));
+  w.sums = c.take<float4>((N + 7) / 8);
   w.part = c.take<float2>(N * ((V + 255) / 256));
   w.hidden = gh ? c.take<float>((size_t)p.splits * (size_t)p.slot_rows * H) : nullptr;
   w.d = gh || gw ? c.take<uint16_t>(N * (size_t)p.piece) : nullptr;
@@ -655,15 +655,18 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   if (c.grad_hidden) {
     const long long elems = (long long)c.N * c.H;
     const long long slot = (long long)plan.slot_rows * c.H;
-    const dim3 grid((unsigned)((elems / 4 + 255) / 256));
+    const bool many = slots >= 8;
+    const int per = many ? 64 : 256;
+    const dim3 grid((unsigned)((elems / 4 + per - 1) / per));
     const ssv::LossScalars* sc = ws.scalars;
     const float* part = ws.hidden;
-    const cudaError_t e =
-        c.grad_dtype == SPEC_F32
-            ? launch(ssv::hidden_out_kernel<float>, grid, 256, 0, 0, false, st, part, slots, slot, elems, sc,
-                     static_cast<float*>(c.grad_hidden))
-            : launch(ssv::hidden_out_kernel<E>, grid, 256, 0, 0, false, st, part, slots, slot, elems, sc,
-                     static_cast<E*>(c.grad_hidden));
+    auto out = [&](auto* g) {
+      using O = typename std::remove_pointer<decltype(g)>::type;
+      return many ? launch(ssv::hidden_out_kernel<O, 4>, grid, 256, 0, 0, false, st, part, slots, slot, elems, sc, g)
+                  : launch(ssv::hidden_out_kernel<O, 1>, grid, 256, 0, 0, false, st, part, slots, slot, elems, sc, g);
+    };
+    const cudaError_t e = c.grad_dtype == SPEC_F32 ? out(static_cast<float*>(c.grad_hidden))
+                                                   : out(static_cast<E*>(c.grad_hidden));
     if (e != cudaSuccess) return SPEC_ERR_CUDA;
   }
   return SPEC_OK;

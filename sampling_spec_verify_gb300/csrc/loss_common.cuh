@@ -216,6 +216,14 @@ __device__ __forceinline__ void follow_previous() {
 }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Sum over the lanes of a warp, roundings carried along (in every lane, the same).
+__device__ __forceinline__ F2 warp_sum(F2 v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    v = pair_add(v, F2{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+  return v;
+}
+
 __device__ __forceinline__ void raise(uint32_t* status, uint32_t bits) {
   if (status && bits) atomicOr(status, bits);
 }
@@ -364,7 +372,7 @@ struct FinishParams {
   int mean;
   float grad_scale;     // times 1 / T
   float store_scale;    // of the stored logit gradients (head losses)
-  double* part;         // [CTAs, 3] sums of a CTA's rows
+  float4* part;         // [CTAs] sums of a CTA's rows
   float* loss;          // [1]
   float* row_loss;      // [N]
   LossScalars* scalars;
@@ -414,55 +422,60 @@ __device__ __forceinline__ float row_loss_warp(const FinishParams& P, long long 
 }
 
 // Sums of the CTA's eight rows (warp w's loss in every lane of it), and in the
-// last CTA to arrive the call's, all in fixed orders.  256 threads.
+// last CTA to arrive the call's, all in fixed orders, as pairs of floats (fp64
+// additions here were a third of the kernel's time).  256 threads.
 __device__ __forceinline__ void finish_sums(const FinishParams& P, float loss, bool on, float weight) {
-  __shared__ double red[3][8];
+  __shared__ float4 red[8];  // {sum, its rounding, rows, largest |weight|}
   __shared__ uint32_t last;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto total = [&](float4 v) {  // over the lanes of a warp
+    const F2 t = warp_sum(F2{v.x, v.y});
+    return make_float4(t.hi, t.lo, warp_sum(v.z), redux_max_nan(v.w));
+  };
   if (lane == 0) {
-    red[0][w] = on ? (double)weight * (double)loss : 0.0;
-    red[1][w] = on ? 1.0 : 0.0;
-    red[2][w] = on ? (double)fabsf(weight) : 0.0;
+    const float p = on ? weight * loss : 0.0f;
+    red[w] = make_float4(p, on ? fmaf(weight, loss, -p) : 0.0f, on ? 1.0f : 0.0f, on ? fabsf(weight) : 0.0f);
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double sum = 0.0, cnt = 0.0;
-    float wmax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += red[0][i], cnt += red[1][i], wmax = max_nan(wmax, (float)red[2][i]);
-    double* p = P.part + 3ll * blockIdx.x;
-    p[0] = sum, p[1] = cnt, p[2] = (double)wmax;
-    __threadfence();
-    last = atomicAdd(&P.scalars->ticket, 1u) == gridDim.x - 1;
+  if (w == 0) {
+    const float4 v = total(lane < 8 ? red[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+    if (lane == 0) {
+      if (gridDim.x > 1) {
+        P.part[blockIdx.x] = v;
+        __threadfence();
+        last = atomicAdd(&P.scalars->ticket, 1u) == gridDim.x - 1;
+      } else {
+        last = 1;
+      }
+    }
   }
   __syncthreads();
   if (!last) return;
-  __threadfence();
-  double sum = 0.0, cnt = 0.0;
-  float wmax = 0.0f;
+  if (gridDim.x > 1) {
+    __threadfence();
+    F2 sum{0.0f, 0.0f};
+    float cnt = 0.0f, wmax = 0.0f;
 #pragma unroll 4
-  for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) {
-    const double* p = P.part + 3ll * i;
-    sum += __ldcg(p);
-    cnt += __ldcg(p + 1);
-    wmax = max_nan(wmax, (float)__ldcg(p + 2));
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) {
+      const float4 v = __ldcg(P.part + i);
+      sum = pair_add(sum, F2{v.x, v.y});
+      cnt += v.z;
+      wmax = max_nan(wmax, v.w);
+    }
+    const float4 v = total(make_float4(sum.hi, sum.lo, cnt, wmax));
+    __syncthreads();
+    if (lane == 0) red[w] = v;
+    __syncthreads();
   }
-  sum = warp_sum(sum);
-  cnt = warp_sum(cnt);
-  wmax = redux_max_nan(wmax);
-  if (lane == 0) red[0][w] = sum, red[1][w] = cnt, red[2][w] = (double)wmax;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    sum = cnt = 0.0;
-    wmax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += red[0][i], cnt += red[1][i], wmax = max_nan(wmax, (float)red[2][i]);
-    const float den = P.mean && cnt > 0.0 ? (float)cnt : 1.0f;  // at most 2^20 rows through a head; a
-                                                                // count beyond 2^24 is rounded
-    P.loss[0] = (float)sum / den;
-    P.scalars->count = (uint32_t)cnt;
-    P.scalars->inv_wmax = wmax == 0.0f ? 0.0f : 1.0f / wmax;
-    P.scalars->grad_mul = P.grad_scale * wmax / (den * P.store_scale);
+  if (w == 0) {
+    const float4 v = total(lane < 8 ? red[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+    if (lane == 0) {
+      const float den = P.mean && v.z > 0.0f ? v.z : 1.0f;  // counts are exact up to 2^24 rows
+      P.loss[0] = (v.x + v.y) / den;
+      P.scalars->count = (uint32_t)v.z;
+      P.scalars->inv_wmax = v.w == 0.0f ? 0.0f : 1.0f / v.w;
+      P.scalars->grad_mul = P.grad_scale * v.w / (den * P.store_scale);
+    }
   }
 }
 
