@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kDThreads, NV == 0 ? 1 : 2) distill_kernel(con
   constexpr int PV = T::PV;
   constexpr bool kGrad = !std::is_same<O, NoGrad>::value;
   using OG = typename std::conditional<kGrad, O, float>::type;
+  constexpr int kWide = sizeof(OG) * PV;  // bytes of a vector's gradients
   extern __shared__ __align__(128) unsigned char stage_mem[];
   // {m, s} of the unlisted and {m, s} of the listed tokens, per warp of the
   // cluster, pushed by every CTA into every CTA; two rows in turn
@@ -237,8 +238,12 @@ __global__ void __launch_bounds__(kDThreads, NV == 0 ? 1 : 2) distill_kernel(con
     if (!cur.live) {  // left out: no gradient
       if (kGrad) {
         const f32x2 zero[PV / 2] = {};
-        for (int i = tid; i < nvl; i += kDThreads)
-          store_grads<OG, PV, 0>(out + s.a0 + (s.v0 + i) * PV, zero);
+        for (int i = tid; i < nvl; i += kDThreads) {
+          if (NV > 0 || P.wide)
+            store_grads<OG, PV, kWide>(out + s.a0 + (s.v0 + i) * PV, zero);
+          else
+            store_grads<OG, PV, 0>(out + s.a0 + (s.v0 + i) * PV, zero);
+        }
         if (tid < s.head) out[tid] = Elem<OG>::from_f32(0.0f);
         if (tid >= 8 && tid - 8 < s.tail) out[s.a1 + tid - 8] = Elem<OG>::from_f32(0.0f);
       }
@@ -420,7 +425,6 @@ __global__ void __launch_bounds__(kDThreads, NV == 0 ? 1 : 2) distill_kernel(con
       const float coef = grad_w;
       const f32x2 s2 = f2(P.s, P.s), m2 = f2(-go.x, -go.x), c2 = f2(go.y, go.y);
       OG* dst = out + s.a0 + (s.v0 + tid) * PV;
-      constexpr int kWide = sizeof(OG) * PV;  // bytes of a vector's gradients
       auto grads = [&](const uint4& u, f32x2 (&p)[PV / 2]) {
         T::pairs(u, p);
 #pragma unroll
