@@ -50,16 +50,17 @@ enum HeadOp {
 // One product of a launch.  Rows of A and B run along K, or (mn) along the
 // other dimension.
 struct Product {
-  int M, N;     // rows and columns
-  int tiles_m, tiles_n, splits;
-  int ksteps;   // 64-deep steps
+  int M, N, K;  // rows, columns, depth
+  int splits;
   int b_off;    // the piece's start among the rows of B
 };
 
 struct HeadLaunch {
   CUtensorMap a[2], b[2], out[2];
   Product p[2];
-  int tiles0, tiles;  // of product 0, of the launch
+  int which;          // bit 0: product 0, bit 1: product 1
+  const uint32_t* count;  // rows that count; null: all of them
+  const int32_t* perm;    // [rows] the batch's row at each place; null: the same
   int bf16;
   float s;            // log2(e) / T
   // kHeadNorm, kHeadKeep
@@ -76,6 +77,29 @@ struct HeadLaunch {
   uint32_t* status;
 };
 
+// The launch's tiles.  Only rows that count take part in the backward products
+// (and in a recomputed D): the batch's rows lie in such an order that they come
+// first, and their number is read from device memory.
+struct Tiles {
+  int m[2], n[2], ksteps[2];
+  int first, all;  // tiles of product 0, of the launch
+};
+template <HeadOp OP>
+__device__ __forceinline__ Tiles tiles_of(const HeadLaunch& L) {
+  const int rows = L.count ? max((int)*L.count, 1) : 0x7FFFFFFF;
+  Tiles t;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int M = i == 0 ? min(L.p[i].M, rows) : L.p[i].M, K = i == 1 ? min(L.p[i].K, rows) : L.p[i].K;
+    t.m[i] = (M + kTileM - 1) / kTileM;
+    t.n[i] = (L.p[i].N + kTileN - 1) / kTileN;
+    t.ksteps[i] = (K + kTileK - 1) / kTileK;
+  }
+  t.first = (L.which & 1) ? t.m[0] * t.n[0] * L.p[0].splits : 0;
+  t.all = t.first + (OP == kHeadBack && (L.which & 2) ? t.m[1] * t.n[1] * L.p[1].splits : 0);
+  return t;
+}
+
 // Tile `i` of the launch: bands of eight tile rows, down the rows first, so
 // that the tiles in flight share operands in L2.
 struct TileAt {
@@ -83,22 +107,23 @@ struct TileAt {
   int m, n, split, k0, k1;
 };
 template <HeadOp OP>
-__device__ __forceinline__ TileAt tile_at(const HeadLaunch& L, int i) {
+__device__ __forceinline__ TileAt tile_at(const HeadLaunch& L, const Tiles& T, int i) {
   TileAt t;
-  t.second = OP == kHeadBack && i >= L.tiles0;
-  const Product& p = L.p[t.second];
-  if (t.second) i -= L.tiles0;
-  const int per = p.tiles_m * p.tiles_n;
+  t.second = OP == kHeadBack && i >= T.first;
+  if (t.second) i -= T.first;
+  const int tiles_m = t.second ? T.m[1] : T.m[0], tiles_n = t.second ? T.n[1] : T.n[0];
+  const int ksteps = t.second ? T.ksteps[1] : T.ksteps[0], splits = L.p[t.second].splits;
+  const int per = tiles_m * tiles_n;
   t.split = i / per;
   i -= t.split * per;
   constexpr int kBand = 8;
-  const int band = i / (kBand * p.tiles_n);
-  const int rows = min(kBand, p.tiles_m - band * kBand);
-  i -= band * kBand * p.tiles_n;
+  const int band = i / (kBand * tiles_n);
+  const int rows = min(kBand, tiles_m - band * kBand);
+  i -= band * kBand * tiles_n;
   t.m = band * kBand + i % rows;
   t.n = i / rows;
-  t.k0 = (int)((long long)p.ksteps * t.split / p.splits);
-  t.k1 = (int)((long long)p.ksteps * (t.split + 1) / p.splits);
+  t.k0 = (int)((long long)ksteps * t.split / splits);
+  t.k1 = (int)((long long)ksteps * (t.split + 1) / splits);
   return t;
 }
 
@@ -163,6 +188,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
   follow_previous();
   const uint32_t tmem = tmem_slot;
   const int clusters = gridDim.x / 2, first_tile = blockIdx.x / 2;
+  const Tiles T = tiles_of<OP>(L);
 
   if (wid == 0) {
     // ---- loads: one thread of each CTA ----
@@ -170,8 +196,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
       const uint32_t full0 = map_rank(bar_full, 0);
       uint32_t step = 0;
       bool ok = true;
-      for (int i = first_tile; ok && i < L.tiles; i += clusters) {
-        const TileAt t = tile_at<OP>(L, i);
+      for (int i = first_tile; ok && i < T.all; i += clusters) {
+        const TileAt t = tile_at<OP>(L, T, i);
         const CUtensorMap *map_a = &L.a[t.second], *map_b = &L.b[t.second];
         const int b_off = L.p[t.second].b_off;
         const bool a_mn = t.second, b_mn = OP == kHeadBack;
@@ -216,8 +242,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
       constexpr uint32_t kb = b_mn ? 2048 : 32;  // bytes of 16 K steps
       uint32_t step = 0, it = 0;
       bool ok = true;
-      for (int i = first_tile; ok && i < L.tiles; i += clusters, ++it) {
-        const TileAt t = tile_at<OP>(L, i);
+      for (int i = first_tile; ok && i < T.all; i += clusters, ++it) {
+        const TileAt t = tile_at<OP>(L, T, i);
         const uint32_t idesc = mma_idesc(L.bf16 != 0, t.second, b_mn);
         const uint64_t da = t.second ? desc_mn : desc_k;
         const uint32_t ka = t.second ? 2048 : 32;
@@ -290,8 +316,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
                     __float_as_uint(v[j + 3]));
     };
 
-    for (int i = first_tile; i < L.tiles; i += clusters, ++it) {
-      const TileAt t = tile_at<OP>(L, i);
+    for (int i = first_tile; i < T.all; i += clusters, ++it) {
+      const TileAt t = tile_at<OP>(L, T, i);
       const uint32_t acc = it & 1, use = it >> 1;
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_done + 8 * acc, use & 1u, kWaitNs))) {
         raise(L.status, SPEC_DEV_TIMEOUT);
@@ -349,9 +375,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
         if (row < M) L.part[(long long)t.n * M + row] = make_float2(off, sum);
       } else if constexpr (OP == kHeadGrad) {
         float lse = 0.0f, cf = 0.0f;
-        if (row < M && L.keep[row]) {
+        const int n = row < M ? (L.perm ? L.perm[row] : row) : 0;
+        if (row < M && L.keep[n]) {
           lse = L.lse2[row];
-          cf = (L.weight ? L.weight[row] : 1.0f) * L.scalars->inv_wmax * L.store_scale;
+          cf = (L.weight ? L.weight[n] : 1.0f) * L.scalars->inv_wmax * L.store_scale;
         }
         for (int c = 0; c < kTileN; c += 64) {
           if (col0 + c >= N) break;
@@ -407,14 +434,49 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
   if (wid == 0) tmem_free_pair(tmem, 512);
 }
 
-// Copies rows to a pitch of `ld` elements (16 bytes a thread).
-__global__ void __launch_bounds__(256) repitch_kernel(const uint4* src, uint4* dst, int N, int words, int ld_words) {
+// Puts the rows that count before the others, each group in its order: perm[p] is
+// the row at place p, and x is copied row by row to its place (at a pitch of
+// whole lines where the batch's rows start off a sector).  A warp per row; every
+// CTA counts all of `keep` (N bytes, zero-filled to whole words) for itself.
+__global__ void __launch_bounds__(256) compact_kernel(const uint8_t* keep, int N, int per_cta, const uint4* x,
+                                                      uint4* xp, int words, int ld_words, int32_t* perm,
+                                                      LossScalars* scalars) {
+  __shared__ int red[2][8];
   let_next_start();
   follow_previous();
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (long long)N * words) return;
-  const long long n = i / words;
-  dst[n * ld_words + (i - n * words)] = src[i];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int base = blockIdx.x * per_cta;  // a multiple of eight
+  int all = 0, before = 0;
+  const uint2* words8 = reinterpret_cast<const uint2*>(keep);
+  for (int i = threadIdx.x; i < (N + 7) / 8; i += 256) {
+    const uint2 v = words8[i];
+    const int c = __popc(v.x) + __popc(v.y);
+    all += c;
+    if (i * 8 < base) before += c;
+  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (lane == 0) red[0][w] = all, red[1][w] = before;
+  __syncthreads();
+  all = before = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) all += red[0][i], before += red[1][i];
+  if (blockIdx.x == 0 && threadIdx.x == 0) scalars->count = (uint32_t)all;
+  for (int r = 0; r < per_cta; r += 8) {
+    const int n0 = base + r;
+    if (n0 >= N) break;
+    const uint2 v = words8[n0 / 8];
+    const unsigned long long bits = (unsigned long long)v.y << 32 | v.x;
+    const int n = n0 + w;
+    if (n < N) {
+      const bool on = (bits >> (8 * w)) & 1;
+      const int ahead = before + __popcll(bits & ((1ull << (8 * w)) - 1));  // rows before this one that count
+      const long long p = on ? ahead : all + (n - ahead);
+      if (lane == 0) perm[p] = n;
+      for (int i = lane; i < words; i += 32) xp[p * ld_words + i] = __ldcs(x + (long long)n * words + i);
+    }
+    before += __popcll(bits);
+  }
 }
 
 // ---- the listed tokens -----------------------------------------------------------
@@ -455,6 +517,7 @@ struct ListedParams {
   const float* lse2;
   const float* weight;
   const uint8_t* keep;
+  const int32_t* perm;
   const LossScalars* scalars;
   int N, k, v0, C;
   long long ld;
@@ -465,14 +528,16 @@ template <class E>
 __global__ void __launch_bounds__(256) listed_grads_kernel(const ListedParams P, E* d) {
   let_next_start();
   follow_previous();
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (long long)P.N * P.k) return;
-  const long long n = i / P.k;
+  const long long j = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (j >= (long long)P.N * P.k) return;
+  const long long p = j / P.k;
+  if (p >= (long long)P.scalars->count) return;
+  const long long n = P.perm[p], i = n * P.k + (j - p * P.k);
   const int id = P.ids[i];
-  if (id < P.v0 || id >= P.v0 + P.C || !P.keep[n]) return;
+  if (id < P.v0 || id >= P.v0 + P.C) return;
   const float cf = (P.weight ? P.weight[n] : 1.0f) * P.scalars->inv_wmax * P.store_scale;
-  const float q = exp2f((float)((double)P.zi[i] * P.s - (double)P.lse2[n]));
-  d[n * P.ld + (id - P.v0)] = Elem<E>::from_f32(cf == 0.0f ? 0.0f : (q - P.t[i]) * cf);
+  const float q = exp2f((float)((double)P.zi[i] * P.s - (double)P.lse2[p]));
+  d[p * P.ld + (id - P.v0)] = Elem<E>::from_f32(cf == 0.0f ? 0.0f : (q - P.t[i]) * cf);
 }
 
 // Turns kept probabilities (S; fp16 ones lie where D goes) into D: one CTA per
@@ -483,13 +548,18 @@ __global__ void __launch_bounds__(256) dense_grads_kernel(const ListedParams P, 
                                                           E* d) {
   let_next_start();
   follow_previous();
-  const long long n = blockIdx.x;
+  // place p; places up to the next 64-deep step get zeros, the rest is not read
+  const long long p = blockIdx.x;
+  const int count = (int)P.scalars->count;
+  if (p >= max((count + kTileK - 1) / kTileK, 1) * kTileK) return;
+  const bool on = p < count;
+  const long long n = on ? P.perm[p] : 0;
   const int c0 = blockIdx.y * kDenseCols, c1 = min(P.C, c0 + kDenseCols);
-  const float cf = P.keep[n] ? (P.weight ? P.weight[n] : 1.0f) * P.scalars->inv_wmax * P.store_scale : 0.0f;
-  const float lse = P.lse2[n];
+  const float cf = on ? (P.weight ? P.weight[n] : 1.0f) * P.scalars->inv_wmax * P.store_scale : 0.0f;
+  const float lse = on ? P.lse2[p] : 0.0f;
   constexpr int kWords = sizeof(S) / 2;  // 16-byte words of eight entries
-  const uint4* src = reinterpret_cast<const uint4*>(kept + n * P.ld);
-  uint4* dst = reinterpret_cast<uint4*>(d + n * P.ld);
+  const uint4* src = reinterpret_cast<const uint4*>(kept + p * P.ld);
+  uint4* dst = reinterpret_cast<uint4*>(d + p * P.ld);
   constexpr int kPer = kDenseCols / 8 / 256;
   uint4 v[kPer][kWords];
   float f[kPer];
@@ -499,7 +569,7 @@ __global__ void __launch_bounds__(256) dense_grads_kernel(const ListedParams P, 
     if (c < c1) {
 #pragma unroll
       for (int w = 0; w < kWords; ++w) v[i][w] = __ldcs(src + c / 8 * kWords + w);
-      f[i] = part[(long long)(c >> 8) * P.N + n].x;
+      f[i] = part[(long long)(c >> 8) * P.N + p].x;
     }
   }
 #pragma unroll
@@ -531,7 +601,7 @@ __global__ void __launch_bounds__(256) dense_grads_kernel(const ListedParams P, 
     const int id = P.ids[n * P.k + i];
     if (id >= c0 && id < c1) {
       const float q = exp2f((float)((double)P.zi[n * P.k + i] * P.s - (double)lse));
-      d[n * P.ld + id] = Elem<E>::from_f32((q - P.t[n * P.k + i]) * cf);
+      d[p * P.ld + id] = Elem<E>::from_f32((q - P.t[n * P.k + i]) * cf);
     }
   }
 }
@@ -541,8 +611,14 @@ __global__ void __launch_bounds__(256) dense_grads_kernel(const ListedParams P, 
 // 8 rows per CTA.  The tiles' statistics of a row are joined by 32 threads (64
 // contiguous bytes of every tile), each thread's loads independent of one
 // another; then a warp per row.
+//
+// Rows are taken by place.  Where `spare` is given (the hidden states by place),
+// the rows between the last one that counts and the next 64-deep step are
+// zeroed: the head's gradient multiplies them by zeros, and hidden states of
+// rows that are left out may hold anything.
 __global__ void __launch_bounds__(256) head_finish_kernel(const FinishParams P, const float2* part, int tiles_n,
-                                                          float* lse_out, float* lse2) {
+                                                          const int32_t* perm, float* lse_out, float* lse2,
+                                                          uint4* spare, int ld_words) {
   __shared__ float2 sh[32][9];
   let_next_start();
   follow_previous();
@@ -550,8 +626,10 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const FinishParams P, 
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long base = (long long)blockIdx.x * 8;
   // what the second half needs of row base + w, loaded beside the statistics
-  const long long n = base + w;
-  const bool in = n < P.N, on = in && P.keep[n];
+  const long long p = base + w;
+  const bool in = p < P.N;
+  const long long n = in && perm ? perm[p] : p;
+  const bool on = in && P.keep[n];
   RowTeacher teacher{0.0f, 0.0f, 0.0f, 0.0f};
   float weight = 0.0f;
   if (in) {
@@ -593,11 +671,13 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const FinishParams P, 
     l.lo = fmaf(l2.lo, ln2.hi, l.lo);
     if (lane == 0) {
       if (!fine && on) raise(P.status, SPEC_DEV_BAD_LOGITS);
-      lse2[n] = l2.hi;
+      lse2[p] = l2.hi;
       if (lse_out) lse_out[n] = l.hi + l.lo;
     }
     if (on) loss = row_loss_warp(P, n, lane, RowLog{0.0f, pair_add(l, F2{-teacher.shift, -teacher.shift_lo}), 0.0f});
     if (lane == 0) P.row_loss[n] = loss;
+    if (spare && !on && p < max((P.scalars->count + kTileK - 1) / kTileK, 1u) * (long long)kTileK)
+      for (int i = lane; i < ld_words; i += 32) spare[p * ld_words + i] = make_uint4(0u, 0u, 0u, 0u);
   }
   finish_sums(P, loss, on, weight);
 }
@@ -608,13 +688,17 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const FinishParams P, 
 // against 20).
 template <class O, int Q>
 __global__ void __launch_bounds__(256) hidden_out_kernel(const float* part, int slots, long long slot_elems,
-                                                         long long elems, const LossScalars* scalars, O* out) {
+                                                         long long elems, int H, const int32_t* perm,
+                                                         const LossScalars* scalars, O* out) {
   let_next_start();
   follow_previous();
   const long long i = ((long long)blockIdx.x * (256 / Q) + threadIdx.x / Q) * 4;
   const int q = threadIdx.x % Q;
+  const bool in = i < elems;
+  const long long p = in ? i / H : 0;
+  const bool on = in && p < (long long)scalars->count;
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (i < elems) {
+  if (on) {
 #pragma unroll 4
     for (int s = q; s < slots; s += Q) {
       const float4 v = __ldcs(reinterpret_cast<const float4*>(part + s * slot_elems + i));
@@ -628,15 +712,16 @@ __global__ void __launch_bounds__(256) hidden_out_kernel(const float* part, int 
     a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
     a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
   }
-  if (i >= elems || q != 0) return;
-  const float mul = scalars->grad_mul;
+  if (!in || q != 0) return;
+  const float mul = on ? scalars->grad_mul : 0.0f;
+  O* dst = out + (long long)perm[p] * H + (i - p * H);
   if constexpr (sizeof(O) == 4) {
-    *reinterpret_cast<float4*>(out + i) = make_float4(a.x * mul, a.y * mul, a.z * mul, a.w * mul);
+    *reinterpret_cast<float4*>(dst) = make_float4(a.x * mul, a.y * mul, a.z * mul, a.w * mul);
   } else {
     uint2 v;
     v.x = Elem<O>::pack(a.x * mul, a.y * mul);
     v.y = Elem<O>::pack(a.z * mul, a.w * mul);
-    *reinterpret_cast<uint2*>(out + i) = v;
+    *reinterpret_cast<uint2*>(dst) = v;
   }
 }
 

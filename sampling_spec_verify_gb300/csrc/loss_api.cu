@@ -160,7 +160,7 @@ DistillWs distill_ws(void* base, size_t N, size_t k) {
   w.scalars = c.take<ssv::LossScalars>(1);
   w.t = c.take<float>(N * k);
   w.row = c.take<ssv::RowTeacher>(N);
-  w.keep = c.take<uint8_t>(N);
+  w.keep = c.take<uint8_t>((N + 7) / 8 * 8);
   w.zi = c.take<float>(N * k);
   w.norm = c.take<ssv::RowNorm>(N);
   w.row_loss = c.take<float>(N);
@@ -377,13 +377,13 @@ HeadPlan head_plan(int N, int V, int H, bool bf16) {
 }
 
 // Rows that start off a 32-byte sector cost the products a quarter of their rate
-// (1001 x 50257, bf16: H = 1536 94 us, 1544 125, 1552 103); the hidden states are
-// copied to whole lines for them.  (The head is too large to copy.)
-bool repitched(size_t H) { return H % 16 != 0; }
-size_t pitch_of(size_t H) { return repitched(H) ? (H + 63) / 64 * 64 : H; }
+// (1001 x 50257, bf16: H = 1536 94 us, 1544 125, 1552 103); the copy of the hidden
+// states puts them on whole lines.  (The head is too large to copy.)
+size_t pitch_of(size_t H) { return H % 16 ? (H + 63) / 64 * 64 : H; }
 
 struct HeadWs {
-  uint16_t* x;  // hidden states at pitch_of(H), where they are copied
+  uint16_t* x;    // hidden states by place, at pitch_of(H)
+  int32_t* perm;  // row at each place
   ssv::LossScalars* scalars;
   float* t;
   ssv::RowTeacher* row;
@@ -402,18 +402,20 @@ HeadWs head_ws(void* base, const HeadPlan& p, size_t N, size_t V, size_t H, size
   Carver c{static_cast<char*>(base)};
   HeadWs w;
   w.scalars = c.take<ssv::LossScalars>(1);
-  w.x = repitched(H) ? c.take<uint16_t>(N * pitch_of(H)) : nullptr;
+  const bool grads = gh || gw;
+  w.x = grads ? c.take<uint16_t>(N * pitch_of(H)) : nullptr;
+  w.perm = grads ? c.take<int32_t>(N) : nullptr;
   w.t = c.take<float>(N * k);
   w.row = c.take<ssv::RowTeacher>(N);
-  w.keep = c.take<uint8_t>(N);
+  w.keep = c.take<uint8_t>((N + 7) / 8 * 8);
   w.zi = c.take<float>(N * k);
   w.row_loss = c.take<float>(N);
   w.lse2 = c.take<float>(N);
   w.sums = c.take<float4>((N + 7) / 8);
   w.part = c.take<float2>(N * ((V + 255) / 256));
   w.hidden = gh ? c.take<float>((size_t)p.splits * (size_t)p.slot_rows * H) : nullptr;
-  w.d = gh || gw ? c.take<uint16_t>(N * (size_t)p.piece) : nullptr;
-  w.e = (gh || gw) && p.kept && p.kept32 ? c.take<float>(N * (size_t)p.piece) : nullptr;
+  w.d = grads ? c.take<uint16_t>(N * (size_t)p.piece) : nullptr;
+  w.e = grads && p.kept && p.kept32 ? c.take<float>(N * (size_t)p.piece) : nullptr;
   w.total = c.used;
   return w;
 }
@@ -454,19 +456,14 @@ bool make_map(CUtensorMap* m, const void* base, spec_dtype_t dt, long long rows,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Sizes of a product of M x N results, K deep.
+// A product of M x N results, K deep.
 ssv::Product product(int M, int N, int K, int splits, int b_off) {
-  ssv::Product p;
-  p.M = M;
-  p.N = N;
-  p.tiles_m = (M + ssv::kTileM - 1) / ssv::kTileM;
-  p.tiles_n = (N + ssv::kTileN - 1) / ssv::kTileN;
-  p.ksteps = (K + ssv::kTileK - 1) / ssv::kTileK;
-  p.splits = splits < p.ksteps ? splits : p.ksteps;
-  p.b_off = b_off;
-  return p;
+  const int ksteps = (K + ssv::kTileK - 1) / ssv::kTileK;
+  return {M, N, K, splits < ksteps ? splits : ksteps, b_off};
 }
-long long tiles_of(const ssv::Product& p) { return (long long)p.tiles_m * p.tiles_n * p.splits; }
+long long tiles_of(const ssv::Product& p) {
+  return (long long)((p.M + ssv::kTileM - 1) / ssv::kTileM) * ((p.N + ssv::kTileN - 1) / ssv::kTileN) * p.splits;
+}
 
 // Launches the first (which & 1) and the second (which & 2) product of L.
 template <ssv::HeadOp OP, bool OUT32>
@@ -478,11 +475,10 @@ spec_status_t launch_head(ssv::HeadLaunch& L, int which, cudaStream_t st) {
   if (!device(&d, &dev)) return SPEC_ERR_CUDA;
   const int fit = resident_clusters(res, fn, 2, ssv::kHeadSmem, ssv::kHeadThreads, dev, d.smem_optin);
   if (fit <= 0) return SPEC_ERR_CUDA;
-  const long long t0 = (which & 1) ? tiles_of(L.p[0]) : 0, t1 = (which & 2) ? tiles_of(L.p[1]) : 0;
-  if (t0 + t1 > 0x7FFFFFF) return SPEC_ERR_UNSUPPORTED;
-  L.tiles0 = (int)t0;
-  L.tiles = (int)(t0 + t1);
-  const int G = L.tiles < fit ? L.tiles : fit;
+  const long long tiles = ((which & 1) ? tiles_of(L.p[0]) : 0) + ((which & 2) ? tiles_of(L.p[1]) : 0);
+  if (tiles > 0x7FFFFFF) return SPEC_ERR_UNSUPPORTED;
+  L.which = which;
+  const int G = tiles < fit ? (int)tiles : fit;  // pairs without a tile leave at once
   return from_cuda(launch(ssv::head_kernel<OP, OUT32>, dim3((unsigned)(2 * G)), ssv::kHeadThreads, ssv::kHeadSmem, 0,
                           false, st, L));
 }
@@ -535,16 +531,17 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
              (const uint8_t*)ws.keep, c.N, c.H, c.k, ws.zi) != cudaSuccess)
     return SPEC_ERR_CUDA;
 
-  const int ldx = (int)pitch_of((size_t)c.H);
+  const bool grads = c.grad_hidden || c.grad_weight;
+  const int ldx = grads ? (int)pitch_of((size_t)c.H) : c.H;
   const void* xp = x;
-  if (ws.x) {
-    const long long words = (long long)c.N * (c.H / 8);
-    if (launch(ssv::repitch_kernel, dim3((unsigned)((words + 255) / 256)), 256, 0, 0, false, st,
-               reinterpret_cast<const uint4*>(x), reinterpret_cast<uint4*>(ws.x), c.N, c.H / 8, ldx / 8) != cudaSuccess)
+  if (grads) {
+    const int per = 8 * ((c.N + 8191) / 8192);  // rows per CTA
+    if (launch(ssv::compact_kernel, dim3((unsigned)((c.N + per - 1) / per)), 256, 0, 0, false, st,
+               (const uint8_t*)ws.keep, c.N, per, reinterpret_cast<const uint4*>(x), reinterpret_cast<uint4*>(ws.x),
+               c.H / 8, ldx / 8, ws.perm, ws.scalars) != cudaSuccess)
       return SPEC_ERR_CUDA;
     xp = ws.x;
   }
-  const bool grads = c.grad_hidden || c.grad_weight;
   const bool kept = grads && plan.kept;
   ssv::HeadLaunch L;
   std::memset(&L, 0, sizeof(L));
@@ -556,6 +553,7 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   L.lse2 = ws.lse2;
   L.weight = c.row_weight;
   L.keep = ws.keep;
+  L.perm = ws.perm;
   L.store_scale = store_scale;
   L.slot_rows = plan.slot_rows;
   // 128-row boxes along K
@@ -589,10 +587,12 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   F.scalars = ws.scalars;
   F.status = c.status;
   if (launch(ssv::head_finish_kernel, dim3((unsigned)((c.N + 7) / 8)), 256, 0, 0, false, st, F,
-             (const float2*)ws.part, (c.V + 255) / 256, c.lse, ws.lse2) != cudaSuccess)
+             (const float2*)ws.part, (c.V + 255) / 256, (const int32_t*)ws.perm, c.lse, ws.lse2,
+             reinterpret_cast<uint4*>(ws.x), ldx / 8) != cudaSuccess)
     return SPEC_ERR_CUDA;
   if (!grads) return SPEC_OK;
 
+  L.count = &ws.scalars->count;  // from here on, only rows that count
   // the backward products: 64-row boxes along the other dimension
   ssv::HeadLaunch B = L;
   if (!make_map(&B.b[0], w, c.dtype, c.V, c.H, c.H, 64) || !make_map(&B.b[1], xp, c.dtype, c.N, c.H, ldx, 64))
@@ -607,6 +607,7 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   Q.lse2 = ws.lse2;
   Q.weight = c.row_weight;
   Q.keep = ws.keep;
+  Q.perm = ws.perm;
   Q.scalars = ws.scalars;
   Q.N = c.N;
   Q.k = c.k;
@@ -660,10 +661,11 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
     const dim3 grid((unsigned)((elems / 4 + per - 1) / per));
     const ssv::LossScalars* sc = ws.scalars;
     const float* part = ws.hidden;
+    const int32_t* perm = ws.perm;
     auto out = [&](auto* g) {
       using O = typename std::remove_pointer<decltype(g)>::type;
-      return many ? launch(ssv::hidden_out_kernel<O, 4>, grid, 256, 0, 0, false, st, part, slots, slot, elems, sc, g)
-                  : launch(ssv::hidden_out_kernel<O, 1>, grid, 256, 0, 0, false, st, part, slots, slot, elems, sc, g);
+      return many ? launch(ssv::hidden_out_kernel<O, 4>, grid, 256, 0, 0, false, st, part, slots, slot, elems, c.H, perm, sc, g)
+                  : launch(ssv::hidden_out_kernel<O, 1>, grid, 256, 0, 0, false, st, part, slots, slot, elems, c.H, perm, sc, g);
     };
     const cudaError_t e = c.grad_dtype == SPEC_F32 ? out(static_cast<float*>(c.grad_hidden))
                                                    : out(static_cast<E*>(c.grad_hidden));

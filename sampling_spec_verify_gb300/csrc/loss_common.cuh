@@ -239,7 +239,7 @@ struct TargetParams {
   F2 inv_t;
   float* t;              // [N, k] out: teacher probabilities, 0 in unused slots
   RowTeacher* row;       // [N] out
-  uint8_t* keep;         // [N] out: the row counts
+  uint8_t* keep;         // [N, up to a multiple of eight] out: the row counts
   LossScalars* scalars;
   uint32_t* status;
 };
@@ -257,7 +257,10 @@ __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const Target
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0) P.scalars->ticket = 0;
   const long long n = (long long)blockIdx.x * kTargetWarps + w;
-  if (n >= P.N) return;
+  if (n >= P.N) {
+    if (lane == 0) P.keep[n] = 0;  // the flags' last word is whole
+    return;
+  }
 
   if (!P.logits) {  // cross entropy: the label with probability 1
     if (lane == 0) {

@@ -430,6 +430,27 @@ def test_head_rows_left_out_and_bad_rows(ssv):
     assert float(o.loss) == 0 and (o.grad_weight == 0).all() and o.grad_hidden.shape == (0, H)
 
 
+@pytest.mark.parametrize("N,kept", [(20, 3), (300, 64), (700, 129), (700, 0), (700, 700)])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_head_left_out_rows_may_hold_anything(ssv, N, kept, dt):
+    """Hidden states of rows that are left out reach no result but their own lse."""
+    V, H = 900, 72
+    x, w, y, rw = head_inputs(N, V, H, dt, N + kept)
+    order = torch.randperm(N, generator=torch.Generator().manual_seed(3))
+    y[order[kept:]] = -100
+    clean = x.clone()
+    clean[y < 0] = 0
+    x[y < 0] = torch.tensor([float("nan"), float("inf"), -float("inf"), 7.0], dtype=dt).repeat(H // 4)
+    kw = dict(row_weight=rw.to(DEV), reduction="sum", grad_dtype=F32)
+    o = ssv.linear_cross_entropy_fwd_bwd(x.to(DEV), w.to(DEV), y.to(DEV), 1.0, 64.0, **kw)
+    c = ssv.linear_cross_entropy_fwd_bwd(clean.to(DEV), w.to(DEV), y.to(DEV), 1.0, 64.0, **kw)
+    torch.cuda.synchronize()
+    assert int(o.status) == 0
+    assert torch.equal(o.loss, c.loss) and torch.equal(o.row_loss, c.row_loss)
+    assert torch.equal(o.grad_hidden, c.grad_hidden) and torch.equal(o.grad_weight, c.grad_weight)
+    check_head(c, clean, w, dense_labels(y.numpy(), V, -100), 1.0, rw.numpy(), "sum", 64.0, F32)
+
+
 def test_head_weights_of_either_sign(ssv):
     x, w, y, _ = head_inputs(40, 700, 128, BF16, 8)
     rw = torch.linspace(-2, 1, 40)
