@@ -428,7 +428,7 @@ spec_status_t spec_schedule_lengths(const float* survival, int R, int L,
  *    row_weight[n], or 1 where row_weight is NULL.  Gradients are those of
  *    grad_scale * loss.
  *  - A row that is left out has row_loss 0 and no part in loss, count or any
- *    gradient.
+ *    gradient, whatever its logits or hidden states hold (also NaN).
  *  - A row that counts and whose logits hold NaN or +inf, or no finite value,
  *    sets SPEC_DEV_BAD_LOGITS; its results are NaN.
  *  - Results do not depend on timing: the same inputs give the same bits.

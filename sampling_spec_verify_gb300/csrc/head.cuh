@@ -23,7 +23,10 @@
 // a product).  A CTA pair owns a 256 x 256 tile: each CTA stages 128 rows of A
 // and 128 of B per 64-deep step (32 KB, six stages), one thread of the even
 // CTA issues tcgen05.mma for both, accumulators take half of tensor memory so
-// that the epilogue of a tile overlaps the products of the next.
+// that the epilogue of a tile overlaps the products of the next.  Measured at
+// 1792 x 151936 x 2048, bf16: pass 1 574 us (1.94 PFLOP/s on a cold GPU, 1.65 under
+// its power limit), both backward products 1140 us; at 60 rows, where the head's
+// bytes count, pass 1 5.7 TB/s, dX 6.3 TB/s, dW 4.1 TB/s (a plain fill: 4.0).
 #pragma once
 
 #include "loss_common.cuh"
@@ -482,7 +485,8 @@ __global__ void __launch_bounds__(256) compact_kernel(const uint8_t* keep, int N
 // ---- the listed tokens -----------------------------------------------------------
 
 // Raw logits of the listed tokens, zi[n, i] = X_n . W_id: one warp each, fp32
-// sums of exact products.
+// sums of exact products.  Bound: reading rows of the head through L2 (1792 rows of
+// up to 64 tokens, H = 2048: 38 us).
 template <class E>
 __global__ void __launch_bounds__(256) listed_logits_kernel(const E* x, const E* w, const int32_t* ids,
                                                             const uint8_t* keep, int N, int H, int k, float* zi) {
@@ -542,6 +546,7 @@ __global__ void __launch_bounds__(256) listed_grads_kernel(const ListedParams P,
 
 // Turns kept probabilities (S; fp16 ones lie where D goes) into D: one CTA per
 // row and kDenseCols tokens (one read and one write, the listed tokens after).
+// Bound: HBM (1613 x 151936: 167 us for 0.98 GB, 5.9 TB/s).
 constexpr int kDenseCols = 8192;
 template <class E, class S>
 __global__ void __launch_bounds__(256) dense_grads_kernel(const ListedParams P, const float2* part, const S* kept,
