@@ -403,7 +403,6 @@ HeadWs head_ws(void* base, const HeadPlan& p, size_t N, size_t V, size_t H, size
   HeadWs w;
   w.scalars = c.take<ssv::LossScalars>(1);
   const bool grads = gh || gw;
-  w.x = grads ? c.take<uint16_t>(N * pitch_of(H)) : nullptr;
   w.perm = grads ? c.take<int32_t>(N) : nullptr;
   w.t = c.take<float>(N * k);
   w.row = c.take<ssv::RowTeacher>(N);
@@ -416,6 +415,7 @@ HeadWs head_ws(void* base, const HeadPlan& p, size_t N, size_t V, size_t H, size
   w.hidden = gh ? c.take<float>((size_t)p.splits * (size_t)p.slot_rows * H) : nullptr;
   w.d = grads ? c.take<uint16_t>(N * (size_t)p.piece) : nullptr;
   w.e = grads && p.kept && p.kept32 ? c.take<float>(N * (size_t)p.piece) : nullptr;
+  w.x = grads ? c.take<uint16_t>(N * pitch_of(H)) : nullptr;
   w.total = c.used;
   return w;
 }
