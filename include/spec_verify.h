@@ -452,7 +452,9 @@ typedef enum { SPEC_MEAN = 0, SPEC_SUM = 1 } spec_reduction_t;
  * hidden     [N, H], weight [V, H]: dtype SPEC_BF16 or SPEC_F16, contiguous,
  *            16-byte aligned, H a multiple of 8.  Products are exact and summed
  *            in fp32 by the tensor cores, 16 at a time: a logit is within about
- *            2.5e-6 of its size at H = 2048.
+ *            2.5e-6 of its size at H = 2048 (the label's and the listed tokens'
+ *            logits come from the same sums, so that confident rows keep
+ *            their digits).
  * labels     [N] int32; a row whose label is ignore_index is left out, and so
  *            is one whose label is otherwise outside [0, V), which also sets
  *            SPEC_DEV_BAD_TOKEN.

@@ -68,6 +68,11 @@ struct HeadLaunch {
   float s;            // log2(e) / T
   // kHeadNorm, kHeadKeep
   float2* part;       // [tiles_n, M]
+  float* zi;          // [rows, k] logits of the listed tokens, by row and slot
+  const int32_t* labels;   // cross entropy
+  const uint32_t* keys;    // else: the listed tokens, sorted (see TargetParams)
+  const uint16_t* starts;
+  int k;
   // kHeadGrad
   const float* lse2;  // [M] log2 of the normaliser
   const float* weight;
@@ -322,6 +327,23 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
     for (int i = first_tile; i < T.all; i += clusters, ++it) {
       const TileAt t = tile_at<OP>(L, T, i);
       const uint32_t acc = it & 1, use = it >> 1;
+      // pass 1: the listed tokens of this thread's row in this tile, looked up
+      // while the products run
+      long long n_row = 0;
+      int from = 0, to = 0, col = -1;
+      if constexpr (OP == kHeadNorm || OP == kHeadKeep) {
+        const int r = t.m * kTileM + (int)rank * 128 + quad * 32 + lane;
+        if (r < L.p[0].M) {
+          n_row = L.perm ? L.perm[r] : r;
+          if (L.labels) {
+            col = L.labels[n_row] - t.n * kTileN;
+            to = col >= 0 && col < min(kTileN, L.p[0].N - t.n * kTileN) && L.keep[n_row] ? 1 : 0;
+          } else {
+            const uint16_t* s = L.starts + n_row * (T.n[0] + 1) + t.n;
+            from = s[0], to = s[1];
+          }
+        }
+      }
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar_done + 8 * acc, use & 1u, kWaitNs))) {
         raise(L.status, SPEC_DEV_TIMEOUT);
         break;
@@ -376,6 +398,24 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
           if constexpr (OP == kHeadKeep) send(&L.out[0], dst, col0 + c, row0, row0 < M, false);
         }
         if (row < M) L.part[(long long)t.n * M + row] = make_float2(off, sum);
+        // The listed tokens' logits are those of the same products that make the
+        // normaliser: the tensor cores' sums are short of the exact ones by up to
+        // 2.5e-6 of a logit, which would stand alone in the loss of a confident
+        // row (0.6 +- 2e-5) but cancels between the two.
+        for (uint32_t left; (left = __ballot_sync(0xffffffffu, from < to)) != 0;) {
+          const int l = __ffs(left) - 1;
+          uint32_t slot = 0;
+          if (lane == l && !L.labels) {
+            const uint32_t key = L.keys[n_row * L.k + from];
+            slot = key & 255u;
+            col = (int)(key >> 8) - t.n * kTileN;
+          }
+          const float z = tmem_load1(src + (uint32_t)__shfl_sync(0xffffffffu, col, l));
+          if (lane == l) {
+            L.zi[n_row * L.k + slot] = z;
+            ++from;
+          }
+        }
       } else if constexpr (OP == kHeadGrad) {
         float lse = 0.0f, cf = 0.0f;
         const int n = row < M ? (L.perm ? L.perm[row] : row) : 0;
@@ -483,35 +523,6 @@ __global__ void __launch_bounds__(256) compact_kernel(const uint8_t* keep, int N
 }
 
 // ---- the listed tokens -----------------------------------------------------------
-
-// Raw logits of the listed tokens, zi[n, i] = X_n . W_id: one warp each, fp32
-// sums of exact products.  Bound: reading rows of the head through L2 (1792 rows of
-// up to 64 tokens, H = 2048: 38 us).
-template <class E>
-__global__ void __launch_bounds__(256) listed_logits_kernel(const E* x, const E* w, const int32_t* ids,
-                                                            const uint8_t* keep, int N, int H, int k, float* zi) {
-  let_next_start();
-  follow_previous();
-  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (i >= (long long)N * k) return;
-  const long long n = i / k;
-  const int id = ids[i];
-  float acc = 0.0f;
-  if (keep[n] && id >= 0) {
-    const uint4* a = reinterpret_cast<const uint4*>(x + n * H);
-    const uint4* b = reinterpret_cast<const uint4*>(w + (long long)id * H);
-    for (int j = lane; j < H / 8; j += 32) {
-      float fa[8], fb[8];
-      Elem<E>::unpack(a[j], fa);
-      Elem<E>::unpack(b[j], fb);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc = fmaf(fa[e], fb[e], acc);
-    }
-    acc = warp_sum(acc);
-  }
-  if (lane == 0) zi[i] = acc;
-}
 
 // Puts the listed tokens' entries into a piece of D (tokens [v0, v0 + C)).
 struct ListedParams {

@@ -384,6 +384,8 @@ size_t pitch_of(size_t H) { return H % 16 ? (H + 63) / 64 * 64 : H; }
 struct HeadWs {
   uint16_t* x;    // hidden states by place, at pitch_of(H)
   int32_t* perm;  // row at each place
+  uint32_t* keys;   // listed tokens in order, and where each tile of tokens begins
+  uint16_t* starts; // (not for cross entropy)
   ssv::LossScalars* scalars;
   float* t;
   ssv::RowTeacher* row;
@@ -398,7 +400,7 @@ struct HeadWs {
   float* e;  // fp32 probabilities
   size_t total;
 };
-HeadWs head_ws(void* base, const HeadPlan& p, size_t N, size_t V, size_t H, size_t k, bool gh, bool gw) {
+HeadWs head_ws(void* base, const HeadPlan& p, size_t N, size_t V, size_t H, size_t k, bool listed, bool gh, bool gw) {
   Carver c{static_cast<char*>(base)};
   HeadWs w;
   w.scalars = c.take<ssv::LossScalars>(1);
@@ -411,6 +413,8 @@ HeadWs head_ws(void* base, const HeadPlan& p, size_t N, size_t V, size_t H, size
   w.row_loss = c.take<float>(N);
   w.lse2 = c.take<float>(N);
   w.sums = c.take<float4>((N + 7) / 8);
+  w.keys = listed ? c.take<uint32_t>(N * k) : nullptr;
+  w.starts = listed ? c.take<uint16_t>(N * ((V + 255) / 256 + 1)) : nullptr;
   w.part = c.take<float2>(N * ((V + 255) / 256));
   w.hidden = gh ? c.take<float>((size_t)p.splits * (size_t)p.slot_rows * H) : nullptr;
   w.d = grads ? c.take<uint16_t>(N * (size_t)p.piece) : nullptr;
@@ -524,13 +528,13 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   tp.keep = ws.keep;
   tp.scalars = ws.scalars;
   tp.status = c.status;
+  tp.tile = ssv::kTileN;
+  tp.tiles = (c.V + ssv::kTileN - 1) / ssv::kTileN;
+  tp.keys = ws.keys;
+  tp.starts = ws.starts;
   if (launch(ssv::targets_kernel, dim3((unsigned)((c.N + ssv::kTargetWarps - 1) / ssv::kTargetWarps)),
              ssv::kTargetWarps * 32, 0, 0, true, st, tp) != cudaSuccess)
     return SPEC_ERR_CUDA;
-  if (launch(ssv::listed_logits_kernel<E>, dim3((unsigned)((entries + 7) / 8)), 256, 0, 0, false, st, x, w, c.ids,
-             (const uint8_t*)ws.keep, c.N, c.H, c.k, ws.zi) != cudaSuccess)
-    return SPEC_ERR_CUDA;
-
   const bool grads = c.grad_hidden || c.grad_weight;
   const int ldx = grads ? (int)pitch_of((size_t)c.H) : c.H;
   const void* xp = x;
@@ -548,6 +552,11 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   L.bf16 = c.dtype == SPEC_BF16;
   L.s = (float)s;
   L.part = ws.part;
+  L.zi = ws.zi;
+  L.labels = c.logits ? nullptr : c.ids;
+  L.keys = ws.keys;
+  L.starts = ws.starts;
+  L.k = c.k;
   L.status = c.status;
   L.scalars = ws.scalars;
   L.lse2 = ws.lse2;
@@ -698,7 +707,8 @@ spec_status_t head_loss(const HeadCall& c, bool grads) {
   }
   if (!c.hidden || !c.weight || !c.ids || !aligned(c.hidden, 16) || !aligned(c.weight, 16)) return SPEC_ERR_INVALID_ARG;
   const HeadPlan plan = head_plan(c.N, c.V, c.H, c.dtype == SPEC_BF16);
-  const HeadWs ws = head_ws(c.workspace, plan, (size_t)c.N, (size_t)c.V, (size_t)c.H, (size_t)c.k, c.grad_hidden != nullptr,
+  const HeadWs ws = head_ws(c.workspace, plan, (size_t)c.N, (size_t)c.V, (size_t)c.H, (size_t)c.k, c.logits != nullptr,
+                            c.grad_hidden != nullptr,
                             c.grad_weight != nullptr);
   if (!c.workspace || c.bytes < ws.total || !aligned(c.workspace, 256)) return SPEC_ERR_INVALID_ARG;
   return c.dtype == SPEC_BF16 ? head_run<__nv_bfloat16>(c, plan, ws) : head_run<__half>(c, plan, ws);
@@ -739,7 +749,7 @@ size_t spec_linear_loss_workspace_bytes(int N, int V, int H, int k, int want_gra
   size_t most = 0;
   for (int keep = 0; keep < 2; ++keep) {
     const HeadPlan plan = head_plan(N, V, H, keep != 0);
-    const size_t n = head_ws(nullptr, plan, (size_t)N, (size_t)V, (size_t)H, (size_t)k, want_grad_hidden != 0,
+    const size_t n = head_ws(nullptr, plan, (size_t)N, (size_t)V, (size_t)H, (size_t)k, true, want_grad_hidden != 0,
                              want_grad_weight != 0)
                          .total;
     if (n > most) most = n;

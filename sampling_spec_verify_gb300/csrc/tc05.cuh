@@ -98,6 +98,18 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// One column: every thread of the warp gets its lane's value.
+__device__ __forceinline__ float tmem_load1(uint32_t addr) {
+  uint32_t r;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r)
+      : "r"(addr)
+      : "memory");
+  return __uint_as_float(r);
+}
+
 // Shared-memory operand descriptor, 128-byte swizzle.  lbo and sbo in bytes:
 // rows along K: sbo between groups of eight rows (lbo unused); rows along the
 // other dimension: lbo between chunks of 64 elements, sbo between groups of
