@@ -262,7 +262,7 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
   tp.scalars = ws.scalars;
   tp.status = status;
   const unsigned row_grid = (unsigned)((N + ssv::kTargetWarps - 1) / ssv::kTargetWarps);
-  if (launch(ssv::targets_kernel, dim3(row_grid), ssv::kTargetWarps * 32, 0, 0, true, st, tp) != cudaSuccess)
+  if (launch(ssv::targets_kernel<false>, dim3(row_grid), ssv::kTargetWarps * 32, 0, 0, true, st, tp) != cudaSuccess)
     return SPEC_ERR_CUDA;
 
   ssv::DistillParams P = {};
@@ -532,7 +532,7 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   tp.tiles = (c.V + ssv::kTileN - 1) / ssv::kTileN;
   tp.keys = ws.keys;
   tp.starts = ws.starts;
-  if (launch(ssv::targets_kernel, dim3((unsigned)((c.N + ssv::kTargetWarps - 1) / ssv::kTargetWarps)),
+  if (launch(ssv::targets_kernel<true>, dim3((unsigned)((c.N + ssv::kTargetWarps - 1) / ssv::kTargetWarps)),
              ssv::kTargetWarps * 32, 0, 0, true, st, tp) != cudaSuccess)
     return SPEC_ERR_CUDA;
   const bool grads = c.grad_hidden || c.grad_weight;
@@ -685,7 +685,7 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
 
 bool head_dims_ok(int N, int V, int H, int k) { return N >= 0 && V >= 1 && H >= 8 && H % 8 == 0 && k >= 1; }
 bool head_dims_fit(int N, int V, int H, int k) {
-  return N <= (1 << 20) && V <= (1 << 24) && H <= (1 << 16) && k <= ssv::kMaxEntries;
+  return N <= (1 << 20) && V < (1 << 24) && H <= (1 << 16) && k <= ssv::kMaxEntries;
 }
 
 spec_status_t head_loss(const HeadCall& c, bool grads) {

@@ -19,6 +19,7 @@ namespace ssv {
 
 constexpr int kMaxEntries = 256;  // listed teacher tokens per row
 constexpr int kTargetWarps = 8;   // rows per CTA of the kernels with a warp per row
+constexpr int kHashSlots = 512;   // per row, twice kMaxEntries
 
 struct __align__(16) RowTeacher {
   float shift, shift_lo;  // log of the teacher's normaliser: log t_i = x_i / T - (shift + shift_lo)
@@ -240,7 +241,7 @@ struct TargetParams {
   RowTeacher* row;       // [N] out
   uint8_t* keep;         // [N, up to a multiple of eight] out: the row counts
   // through a head: the listed tokens in order, for each tile of tokens
-  uint32_t* keys;        // [N, k] out: id << 8 | slot, ascending; null: not wanted
+  uint32_t* keys;        // [N, k] out: id << 8 | slot, ascending
   uint16_t* starts;      // [N, tiles + 1] out: first key of each tile (all 0 where the row is left out)
   int tiles, tile;       // tokens per tile
   LossScalars* scalars;
@@ -249,15 +250,17 @@ struct TargetParams {
 
 // One warp per row.  Slots with id -1 are unused; an id outside [-1, V), an id
 // listed twice, or a teacher row without a usable normaliser leaves the row out
-// and is reported.  The ids are sorted in shared memory (key: id and slot, V is at
-// most 2^24 through a head): duplicates are neighbours, and the order serves the
-// head's epilogue.
+// and is reported.  Through a head (SORT) the ids are sorted in shared memory
+// (key: id and slot; V is below 2^24) for the epilogue that looks them up, and
+// duplicates are neighbours; otherwise a hash set finds them (1792 rows of 128: 5
+// us against 9).
 //
 // log t_i is formed with its rounding carried along, because the loss is a
 // small difference of such logarithms.  (In fp64 the kernel took 16 us for 1792
 // rows of 128 entries, now 5: an SM does two fp64 operations a clock.)
+template <bool SORT>
 __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const TargetParams P) {
-  __shared__ unsigned long long sorted[kTargetWarps][kMaxEntries];
+  __shared__ uint32_t room[kTargetWarps][SORT ? kMaxEntries : kHashSlots];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0) P.scalars->ticket = 0;
   const long long n = (long long)blockIdx.x * kTargetWarps + w;
@@ -288,37 +291,58 @@ __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const Target
     id[j] = i < P.k ? P.ids[n * P.k + i] : -1;
     x[j] = i < P.k ? P.logits[n * P.k + i] : -INFINITY;
   }
+  uint32_t* key = room[w];
   int size = 32;  // keys to sort
   while (size < P.k) size *= 2;
-  unsigned long long* key = sorted[w];
+  if constexpr (!SORT) {
+    for (int i = lane; i < kHashSlots; i += 32) key[i] = ~0u;
+    __syncwarp();
+  }
   bool bad = false, any = false;
   float m = -INFINITY;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = lane + 32 * j;
     const bool used = id[j] >= 0 && id[j] < P.V;
-    if (i < size) key[i] = used ? (unsigned long long)(uint32_t)id[j] << 8 | (uint32_t)i : ~0ull;
+    if constexpr (SORT) {
+      if (i < size) key[i] = used ? (uint32_t)id[j] << 8 | (uint32_t)i : ~0u;
+    }
     if (used) {
       any = true;
       m = max_nan(m, x[j]);
+      if constexpr (!SORT) {
+        uint32_t s = ((uint32_t)id[j] * 2654435761u) >> 23;  // 9 bits
+        for (int probe = 0; probe < kHashSlots; ++probe) {
+          const uint32_t old = atomicCAS(&key[s], ~0u, (uint32_t)id[j]);
+          if (old == ~0u) break;
+          if (old == (uint32_t)id[j]) {
+            bad = true;
+            break;
+          }
+          s = (s + 1) & (kHashSlots - 1);
+        }
+      }
     } else {
       bad |= id[j] != -1;
       x[j] = -INFINITY;
     }
   }
-  __syncwarp();
-  for (int span = 2; span <= size; span *= 2) {
-    for (int step = span / 2; step; step /= 2) {
-      for (int i = lane; i < size / 2; i += 32) {
-        const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
-        const unsigned long long a = key[lo], b = key[hi];
-        if ((a > b) == ((lo & span) == 0)) key[lo] = b, key[hi] = a;
+  if constexpr (SORT) {
+    __syncwarp();
+    for (int span = 2; span <= size; span *= 2) {
+      for (int step = span / 2; step; step /= 2) {
+        for (int i = lane; i < size / 2; i += 32) {
+          const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
+          const uint32_t a = key[lo], b = key[hi];
+          const bool up = (lo & span) == 0;
+          key[lo] = up ? min(a, b) : max(a, b);
+          key[hi] = up ? max(a, b) : min(a, b);
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
+    for (int i = lane; i + 1 < size; i += 32) bad |= key[i + 1] != ~0u && key[i] >> 8 == key[i + 1] >> 8;
   }
-  for (int i = lane; i + 1 < size; i += 32)
-    bad |= key[i + 1] != ~0ull && key[i] >> 8 == key[i + 1] >> 8;
   bad = __any_sync(0xffffffffu, bad);
   any = __any_sync(0xffffffffu, any);
   m = redux_max_nan(m);
@@ -356,12 +380,12 @@ __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const Target
     const int i = lane + 32 * j;
     if (i < P.k) P.t[n * P.k + i] = ok ? x[j] : 0.0f;
   }
-  if (P.keys) {
-    for (int i = lane; i < P.k; i += 32) P.keys[n * P.k + i] = (uint32_t)key[i];
+  if constexpr (SORT) {
+    for (int i = lane; i < P.k; i += 32) P.keys[n * P.k + i] = key[i];
     for (int b = lane; b <= P.tiles; b += 32) {
       int lo = 0;
       if (ok) {
-        const unsigned long long first = (unsigned long long)b * (unsigned)P.tile << 8;
+        const uint32_t first = (uint32_t)min((long long)b * P.tile, (long long)P.V) << 8;
         int len = P.k;
         while (len > 0) {  // first key that is not below
           const int half = len / 2;
