@@ -532,19 +532,24 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   tp.tiles = (c.V + ssv::kTileN - 1) / ssv::kTileN;
   tp.keys = ws.keys;
   tp.starts = ws.starts;
-  if (launch(ssv::targets_kernel<true>, dim3((unsigned)((c.N + ssv::kTargetWarps - 1) / ssv::kTargetWarps)),
-             ssv::kTargetWarps * 32, 0, 0, true, st, tp) != cudaSuccess)
-    return SPEC_ERR_CUDA;
   const bool grads = c.grad_hidden || c.grad_weight;
   const int ldx = grads ? (int)pitch_of((size_t)c.H) : c.H;
-  const void* xp = x;
-  if (grads) {
-    const int per = 8 * ((c.N + 8191) / 8192);  // rows per CTA
-    if (launch(ssv::compact_kernel, dim3((unsigned)((c.N + per - 1) / per)), 256, 0, 0, false, st,
-               (const uint8_t*)ws.keep, c.N, per, reinterpret_cast<const uint4*>(x), reinterpret_cast<uint4*>(ws.x),
-               c.H / 8, ldx / 8, ws.perm, ws.scalars) != cudaSuccess)
+  const void* xp = grads ? (const void*)ws.x : (const void*)x;
+  const int per = 8 * ((c.N + 8191) / 8192);  // rows per CTA of the kernels that look at all rows
+  const dim3 per_grid((unsigned)((c.N + per - 1) / per));
+  const uint4* x16 = reinterpret_cast<const uint4*>(x);
+  uint4* xp16 = reinterpret_cast<uint4*>(ws.x);
+  if (!c.logits) {
+    if (launch(ssv::label_rows_kernel, per_grid, 256, 0, 0, true, st, tp, per, x16, xp16, c.H / 8, ldx / 8, ws.perm) !=
+        cudaSuccess)
       return SPEC_ERR_CUDA;
-    xp = ws.x;
+  } else {
+    if (launch(ssv::targets_kernel<true>, dim3((unsigned)((c.N + ssv::kTargetWarps - 1) / ssv::kTargetWarps)),
+               ssv::kTargetWarps * 32, 0, 0, true, st, tp) != cudaSuccess)
+      return SPEC_ERR_CUDA;
+    if (grads && launch(ssv::compact_kernel, per_grid, 256, 0, 0, false, st, (const uint8_t*)ws.keep, c.N, per, x16,
+                        xp16, c.H / 8, ldx / 8, ws.perm, ws.scalars) != cudaSuccess)
+      return SPEC_ERR_CUDA;
   }
   const bool kept = grads && plan.kept;
   ssv::HeadLaunch L;

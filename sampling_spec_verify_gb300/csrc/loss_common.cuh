@@ -231,8 +231,8 @@ __device__ __forceinline__ void raise(uint32_t* status, uint32_t bits) {
 // ---- the teacher side ---------------------------------------------------------
 
 struct TargetParams {
-  const int32_t* ids;    // [N, k]; one label per row when `logits` is null
-  const float* logits;   // [N, k] teacher logits, or null
+  const int32_t* ids;    // [N, k] listed tokens (of cross entropy: the labels)
+  const float* logits;   // [N, k] teacher logits (of cross entropy: null)
   const float* lse;      // [N] teacher normaliser, or null
   int N, V, k;
   int ignore;            // label of rows that are left out
@@ -266,19 +266,6 @@ __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const Target
   const long long n = (long long)blockIdx.x * kTargetWarps + w;
   if (n >= P.N) {
     if (lane == 0) P.keep[n] = 0;  // the flags' last word is whole
-    return;
-  }
-
-  if (!P.logits) {  // cross entropy: the label with probability 1
-    if (lane == 0) {
-      const int id = P.ids[n];
-      const bool ok = id >= 0 && id < P.V && id != P.ignore;
-      if (!ok && id != P.ignore) raise(P.status, SPEC_DEV_BAD_TOKEN);
-      P.keep[n] = ok;
-      P.t[n] = ok ? 1.0f : 0.0f;
-      P.row[n] = RowTeacher{0.0f, 0.0f, ok ? 1.0f : 0.0f, 0.0f};
-    }
-    let_next_start();
     return;
   }
 
