@@ -594,9 +594,9 @@ def _loss_buffers(device, stream, given, nbytes, workspace, empties):
     so they are not the ones of the other calls.  Inside a stream capture
     nothing is cached: the memory belongs to the graph."""
     key = (device.index, stream.cuda_stream)
-    capturing = torch.cuda.is_current_stream_capturing()
     current = given is None
     with _Nothing() if current else torch.cuda.stream(stream):
+        capturing = torch.cuda.is_current_stream_capturing()  # of the call's own stream
         made = [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in empties]
         status = None
         if made:

@@ -484,6 +484,45 @@ def test_head_repeats_streams_and_graphs(ssv):
         assert torch.equal(a.grad_hidden, o.grad_hidden) and torch.equal(a.grad_weight, o.grad_weight)
 
 
+@pytest.mark.parametrize("side", [False, True])
+def test_captured_calls_own_their_memory(ssv, side):
+    """Outputs and workspace of a captured call belong to the graph: eager calls
+    of other sizes between the replays change nothing, also where the call runs
+    on a stream that joined the capture."""
+    x, w, y, rw = (t.to(DEV) for t in head_inputs(70, 3001, 136, BF16, 10))
+    z, ids, tx, lse, kw = (t.to(DEV) for t in kd_inputs(20, 3001, 12, BF16, 14, 1.0, padded=True))
+
+    def calls(stream=None):
+        return (ssv.linear_cross_entropy_fwd_bwd(x, w, y, 1.0, row_weight=rw, stream=stream),
+                ssv.topk_distill_fwd_bwd(z, ids, tx, 1.0, teacher_lse=lse, row_weight=kw, stream=stream))
+
+    def values(pair):
+        a, b = pair
+        return [a.loss, a.row_loss, a.lse, a.grad_hidden, a.grad_weight, b.loss, b.row_loss, b.grad]
+
+    want = values(calls())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        if side:
+            s.wait_stream(torch.cuda.current_stream())
+            pair = calls(s)
+            torch.cuda.current_stream().wait_stream(s)
+        else:
+            pair = calls()
+    bx, bw, by, _ = (t.to(DEV) for t in head_inputs(300, 5003, 200, BF16, 9))
+    for _ in range(2):
+        for t in values(pair):
+            t.zero_()
+        ssv.linear_cross_entropy_fwd_bwd(bx, bw, by, 1.0)
+        g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, values(pair)):
+        assert torch.equal(a, b)
+    assert int(pair[0].status.item()) == 0 and int(pair[1].status.item()) == 0
+
+
 def test_python_refusals(ssv):
     x, w, y, rw = (t.to(DEV) for t in head_inputs(4, 64, 16, BF16, 9))
     ce = ssv.linear_cross_entropy_fwd_bwd
