@@ -465,14 +465,15 @@ typedef enum { SPEC_MEAN = 0, SPEC_SUM = 1 } spec_reduction_t;
  *            grad_dtype = dtype or SPEC_F32, 16-byte aligned.  The gradient of
  *            the logits is rounded once to dtype on its way into the products.
  *
- * The workspace size covers the gradients that are asked for, for either dtype.
+ * The workspace size covers the gradients that are asked for.
  * A gradient call holds 16-bit gradients of the logits for a piece of the
  * vocabulary at a time (256 MB, or 4 KB a row where that is more) and
- * recomputes the logits piece by piece; a batch whose entries all fit 1.25 GB
+ * recomputes the logits piece by piece; a batch whose entries all fit 4 GB
  * (2 bytes an entry for SPEC_BF16, 6 for SPEC_F16) takes one piece and keeps the
  * unnormalised probabilities of the forward pass in it instead.
  */
-size_t spec_linear_loss_workspace_bytes(int N, int V, int H, int k, int want_grad_hidden, int want_grad_weight);
+size_t spec_linear_loss_workspace_bytes(spec_dtype_t dtype, int N, int V, int H, int k, int want_grad_hidden,
+                                        int want_grad_weight);
 
 spec_status_t spec_linear_cross_entropy(const void* hidden, const void* weight, spec_dtype_t dtype, int N, int V,
                                         int H, float temperature, const int32_t* labels, int ignore_index,

@@ -131,7 +131,7 @@ def lib():
     head = [vp, vp, i32, i32, i32, i32]                 # hidden, weight, dtype, N, V, H
     tail = [vp, vp, sz, vp]                             # status, workspace, bytes, stream
     L.spec_linear_loss_workspace_bytes.restype = sz
-    L.spec_linear_loss_workspace_bytes.argtypes = [i32] * 6
+    L.spec_linear_loss_workspace_bytes.argtypes = [i32] * 7
     L.spec_linear_cross_entropy.restype = i32
     L.spec_linear_cross_entropy.argtypes = head + [f32, vp, i32, vp, i32, vp, vp, vp] + tail
     L.spec_linear_cross_entropy_fwd_bwd.restype = i32
@@ -711,7 +711,8 @@ def _linear_loss(what, hidden, weight, ids, logits, ignore_index, temperature, g
             _need_out(out.grad_hidden, "grad_hidden", gdt, (N, H), dev)
             _need_out(out.grad_weight, "grad_weight", gdt, (V, H), dev)
     sh, s = _stream_handle(stream, dev)
-    need = L.spec_linear_loss_workspace_bytes(N, V, H, k, int(want_hidden), int(want_weight))
+    need = L.spec_linear_loss_workspace_bytes(_LOSS_DTYPES[hidden.dtype], N, V, H, k, int(want_hidden),
+                                              int(want_weight))
     status, ws, made = _loss_buffers(dev, s, stream, need, workspace, empties)
     if out is None:
         out = LinearLossOutput(made[0], made[1], made[2], made[3] if want_hidden else None,

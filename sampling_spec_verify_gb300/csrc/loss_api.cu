@@ -330,11 +330,13 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
 // ---- losses through the head --------------------------------------------------------
 
 constexpr int kPairs = 76;                       // CTA pairs in flight, for the split rule
-// A batch whose probabilities fit kKeepBytes (2 bytes an entry for bf16; 6 for
-// fp16, which keeps them in fp32 beside D) keeps them between the passes (1792 x
-// 151936 x 2048, both gradients: 2.3 ms against 2.8); the others go in pieces of
-// kPieceBytes.
-constexpr size_t kKeepBytes = (size_t)1280 << 20;
+// A batch whose probabilities fit kKeepBytes, a 64th of this GPU's memory (2 bytes
+// an entry for bf16; 6 for fp16, which keeps them in fp32 beside D), keeps them
+// between the passes; the others go in pieces of kPieceBytes and compute the logits
+// twice.  Both gradients, kept against in pieces: bf16 1792 x 151936 x 2048 2.3 ms
+// against 2.8, 8192 x 151936 x 2048 10.3 against 12.2; fp16 4096 x 129280 x 2048 4.7
+// against 5.6.
+constexpr size_t kKeepBytes = (size_t)4096 << 20;
 constexpr size_t kPieceBytes = (size_t)256 << 20;
 
 // How a call is cut: pieces of the vocabulary and splits of a piece's depth in
@@ -747,19 +749,14 @@ spec_status_t spec_topk_distill_fwd_bwd(const void* student, spec_dtype_t dtype,
                  workspace_bytes, stream);
 }
 
-size_t spec_linear_loss_workspace_bytes(int N, int V, int H, int k, int want_grad_hidden, int want_grad_weight) {
+size_t spec_linear_loss_workspace_bytes(spec_dtype_t dtype, int N, int V, int H, int k, int want_grad_hidden,
+                                        int want_grad_weight) {
+  if (dtype != SPEC_BF16 && dtype != SPEC_F16) return 0;
   if (!head_dims_ok(N, V, H, k) || !head_dims_fit(N, V, H, k)) return 0;
   if (N == 0) return 256;
-  // for either dtype: the larger of the two plans
-  size_t most = 0;
-  for (int keep = 0; keep < 2; ++keep) {
-    const HeadPlan plan = head_plan(N, V, H, keep != 0);
-    const size_t n = head_ws(nullptr, plan, (size_t)N, (size_t)V, (size_t)H, (size_t)k, true, want_grad_hidden != 0,
-                             want_grad_weight != 0)
-                         .total;
-    if (n > most) most = n;
-  }
-  return most;
+  return head_ws(nullptr, head_plan(N, V, H, dtype == SPEC_BF16), (size_t)N, (size_t)V, (size_t)H, (size_t)k, true,
+                 want_grad_hidden != 0, want_grad_weight != 0)
+      .total;
 }
 
 spec_status_t spec_linear_cross_entropy_fwd_bwd(const void* hidden, const void* weight, spec_dtype_t dtype, int N,

@@ -363,9 +363,9 @@ def test_head(ssv, N, V, H, dt, gdt, T, k, red, weighted):
     assert int(o.status) == 0
 
 
-@pytest.mark.parametrize("N", [70000, 170000])
+@pytest.mark.parametrize("N", [70000, 170000, 520000])
 def test_head_in_pieces(ssv, N):
-    """Long batches, the second one long enough that its vocabulary is cut:
+    """Long batches, the last one long enough that its vocabulary is cut:
     against fp64 products on the GPU."""
     V, H = 4100, 64
     x, w, y, _ = head_inputs(N, V, H, BF16, 5)
@@ -467,7 +467,7 @@ def test_head_repeats_streams_and_graphs(ssv):
     s.wait_stream(torch.cuda.current_stream())
     b = ssv.linear_cross_entropy_fwd_bwd(x, w, y, 1.0, row_weight=rw, stream=s)
     torch.cuda.synchronize()
-    ws = torch.full((ssv.lib().spec_linear_loss_workspace_bytes(N, V, H, 1, 1, 1),), 255, dtype=torch.uint8, device=DEV)
+    ws = torch.full((ssv.lib().spec_linear_loss_workspace_bytes(ssv.SPEC_BF16, N, V, H, 1, 1, 1),), 255, dtype=torch.uint8, device=DEV)
     e = lambda *sh, dt=F32: torch.empty(sh, dtype=dt, device=DEV)  # noqa: E731
     out = ssv.LinearLossOutput(e(1), e(N), e(N), e(N, H, dt=BF16), e(V, H, dt=BF16),
                                torch.zeros(1, dtype=torch.int32, device=DEV))

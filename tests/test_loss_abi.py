@@ -93,9 +93,12 @@ def test_workspace_sizes(L):
     f = L.spec_topk_distill_workspace_bytes
     assert f(-1, 10, 1) == f(1, 0, 1) == f(1, 10, 0) == f(1, 10, 257) == 0
     assert f(8, 1000, 16) >= 2 * 8 * 16 * 4
-    g = L.spec_linear_loss_workspace_bytes
+    def g(*dims, dt=BF16):
+        return L.spec_linear_loss_workspace_bytes(dt, *dims)
+    assert g(1, 10, 8, 1, 0, 0, dt=F32) == g(1, 10, 8, 1, 0, 0, dt=3) == 0
     assert g(1, 10, 12, 1, 0, 0) == g(1, 10, 0, 1, 0, 0) == g(-1, 10, 8, 1, 0, 0) == g(1, 10, 8, 257, 1, 1) == 0
     a, b, c = g(100, 5000, 256, 1, 0, 0), g(100, 5000, 256, 1, 1, 0), g(100, 5000, 256, 1, 1, 1)
     assert a > 100 * 20 * 8 and b > a + 100 * 5000 * 2 and c == b
+    assert g(100, 5000, 256, 1, 1, 0, dt=F16) > b + 100 * 5000 * 4  # fp32 probabilities beside the gradient
     # the logits are never kept: at 65536 rows of 151936 tokens they would be 19.9 GB in 16 bits
     assert g(65536, 151936, 4096, 1, 1, 1) < 3 << 30
