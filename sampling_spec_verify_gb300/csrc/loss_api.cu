@@ -383,8 +383,24 @@ HeadPlan head_plan(int N, int V, int H, bool bf16) {
 // states puts them on whole lines.  (The head is too large to copy.)
 size_t pitch_of(size_t H) { return H % 16 ? (H + 63) / 64 * 64 : H; }
 
+// A tensor map over less than 128 KB is read slowly (measured; the order of the reads
+// makes no difference, the rows outside of the batch may hold anything).  Pass 1 of
+// eight rows, by the bytes that the map of the hidden states covers, 32 KB / 64 / 128 /
+// 256: 151936 x 2048 183 / 179 / 141 / 141 us, 151936 x 1024 109 / 107 / 94 / 92.  So
+// calls with gradients extend their copy of the hidden states by rows that nothing
+// looks at, and calls without copy them too where the head is longer than the L2
+// (32000 x 1024: no difference).
+constexpr size_t kMapBytes = (size_t)128 << 10;
+size_t copy_rows(size_t N, size_t H) {
+  const size_t least = (kMapBytes / 2 + pitch_of(H) - 1) / pitch_of(H);
+  return N > least ? N : least;
+}
+bool copies(size_t N, size_t V, size_t H, bool grads) {
+  return grads || (N * H * 2 < kMapBytes && V * H * 2 >= (size_t)128 << 20);
+}
+
 struct HeadWs {
-  uint16_t* x;    // hidden states by place, at pitch_of(H)
+  uint16_t* x;    // hidden states by place, at pitch_of(H), or null: as they lie
   int32_t* perm;  // row at each place
   uint32_t* keys;   // listed tokens in order, and where each tile of tokens begins
   uint16_t* starts; // (not for cross entropy)
@@ -407,7 +423,8 @@ HeadWs head_ws(void* base, const HeadPlan& p, size_t N, size_t V, size_t H, size
   HeadWs w;
   w.scalars = c.take<ssv::LossScalars>(1);
   const bool grads = gh || gw;
-  w.perm = grads ? c.take<int32_t>(N) : nullptr;
+  const bool copy = copies(N, V, H, grads);
+  w.perm = copy ? c.take<int32_t>(N) : nullptr;
   w.t = c.take<float>(N * k);
   w.row = c.take<ssv::RowTeacher>(N);
   w.keep = c.take<uint8_t>((N + 7) / 8 * 8);
@@ -421,7 +438,7 @@ HeadWs head_ws(void* base, const HeadPlan& p, size_t N, size_t V, size_t H, size
   w.hidden = gh ? c.take<float>((size_t)p.splits * (size_t)p.slot_rows * H) : nullptr;
   w.d = grads ? c.take<uint16_t>(N * (size_t)p.piece) : nullptr;
   w.e = grads && p.kept && p.kept32 ? c.take<float>(N * (size_t)p.piece) : nullptr;
-  w.x = grads ? c.take<uint16_t>(N * pitch_of(H)) : nullptr;
+  w.x = copy ? c.take<uint16_t>(copy_rows(N, H) * pitch_of(H)) : nullptr;
   w.total = c.used;
   return w;
 }
@@ -535,8 +552,8 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   tp.keys = ws.keys;
   tp.starts = ws.starts;
   const bool grads = c.grad_hidden || c.grad_weight;
-  const int ldx = grads ? (int)pitch_of((size_t)c.H) : c.H;
-  const void* xp = grads ? (const void*)ws.x : (const void*)x;
+  const int ldx = ws.x ? (int)pitch_of((size_t)c.H) : c.H;
+  const void* xp = ws.x ? (const void*)ws.x : (const void*)x;
   const int per = 8 * ((c.N + 8191) / 8192);  // rows per CTA of the kernels that look at all rows
   const dim3 per_grid((unsigned)((c.N + per - 1) / per));
   const uint4* x16 = reinterpret_cast<const uint4*>(x);
@@ -549,7 +566,7 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
     if (launch(ssv::targets_kernel<true>, dim3((unsigned)((c.N + ssv::kTargetWarps - 1) / ssv::kTargetWarps)),
                ssv::kTargetWarps * 32, 0, 0, true, st, tp) != cudaSuccess)
       return SPEC_ERR_CUDA;
-    if (grads && launch(ssv::compact_kernel, per_grid, 256, 0, 0, false, st, (const uint8_t*)ws.keep, c.N, per, x16,
+    if (ws.x && launch(ssv::compact_kernel, per_grid, 256, 0, 0, false, st, (const uint8_t*)ws.keep, c.N, per, x16,
                         xp16, c.H / 8, ldx / 8, ws.perm, ws.scalars) != cudaSuccess)
       return SPEC_ERR_CUDA;
   }
@@ -573,7 +590,8 @@ spec_status_t head_run(const HeadCall& c, const HeadPlan& plan, const HeadWs& ws
   L.store_scale = store_scale;
   L.slot_rows = plan.slot_rows;
   // 128-row boxes along K
-  if (!make_map(&L.a[0], xp, c.dtype, c.N, c.H, ldx, 128) || !make_map(&L.b[0], w, c.dtype, c.V, c.H, c.H, 128))
+  const long long map_rows = ws.x ? (long long)copy_rows((size_t)c.N, (size_t)c.H) : c.N;
+  if (!make_map(&L.a[0], xp, c.dtype, map_rows, c.H, ldx, 128) || !make_map(&L.b[0], w, c.dtype, c.V, c.H, c.H, 128))
     return SPEC_ERR_CUDA;
   constexpr bool kWide = std::is_same<E, __half>::value;
   using S = typename std::conditional<kWide, float, __half>::type;  // of kept probabilities

@@ -324,6 +324,8 @@ HEAD_CASES = [
     (300, 5003, 712, BF16, BF16, 0.8, 20, "mean", True),
     (1000, 3001, 520, BF16, BF16, 1.0, 0, "mean", True),
     (33, 20011, 1024, BF16, F32, 1.0, 64, "mean", False),
+    (9, 66001, 1024, BF16, BF16, 1.0, 0, "mean", True),   # a few rows, heads longer than the L2
+    (5, 33001, 2056, F16, F16, 0.7, 7, "sum", True),
 ]
 
 
