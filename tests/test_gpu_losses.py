@@ -326,6 +326,7 @@ HEAD_CASES = [
     (33, 20011, 1024, BF16, F32, 1.0, 64, "mean", False),
     (9, 66001, 1024, BF16, BF16, 1.0, 0, "mean", True),   # a few rows, heads longer than the L2
     (5, 33001, 2056, F16, F16, 0.7, 7, "sum", True),
+    (260, 60001, 1128, BF16, BF16, 1.0, 0, "mean", True),  # rows off a sector, two tiles of them
 ]
 
 
