@@ -585,17 +585,24 @@ def schedule_lengths(survival: torch.Tensor, sps: torch.Tensor, *, status: Optio
 _SCRATCH = {}
 _STATUS = {}
 _STATUS_WORDS = 1024
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _loss_buffers(device, stream, given, nbytes, workspace, empties):
+def _loss_stream(given, device):
+    """Handle of a training-loss call's stream.  (A call of few rows takes as long
+    as its host side; the stream object alone would be 2 us of 29.)"""
+    return _raw_stream(device.index) if given is None else given.cuda_stream
+
+
+def _loss_buffers(device, handle, given, nbytes, workspace, empties):
     """(status word, workspace, empty tensors) of a training-loss call, on its
     stream.  Status words come zeroed from a block per (device, stream), one
     for each call; workspaces are cached per (device, stream) and never zeroed,
     so they are not the ones of the other calls.  Inside a stream capture
     nothing is cached: the memory belongs to the graph."""
-    key = (device.index, stream.cuda_stream)
-    current = given is None
-    with _Nothing() if current else torch.cuda.stream(stream):
+    key = (device.index, handle)
+    with _Nothing() if given is None else torch.cuda.stream(given):
         capturing = torch.cuda.is_current_stream_capturing()  # of the call's own stream
         made = [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in empties]
         status = None
@@ -619,6 +626,10 @@ def _loss_buffers(device, stream, given, nbytes, workspace, empties):
                     workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
                     _SCRATCH[key] = workspace
     return status, workspace, made
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 class _Nothing:
@@ -710,28 +721,28 @@ def _linear_loss(what, hidden, weight, ids, logits, ignore_index, temperature, g
                 raise ValueError("out must hold exactly the gradients that are asked for")
             _need_out(out.grad_hidden, "grad_hidden", gdt, (N, H), dev)
             _need_out(out.grad_weight, "grad_weight", gdt, (V, H), dev)
-    sh, s = _stream_handle(stream, dev)
+    handle = _loss_stream(stream, dev)
     need = L.spec_linear_loss_workspace_bytes(_LOSS_DTYPES[hidden.dtype], N, V, H, k, int(want_hidden),
                                               int(want_weight))
-    status, ws, made = _loss_buffers(dev, s, stream, need, workspace, empties)
+    status, ws, made = _loss_buffers(dev, handle, stream, need, workspace, empties)
     if out is None:
         out = LinearLossOutput(made[0], made[1], made[2], made[3] if want_hidden else None,
                                made[-1] if want_weight else None, status)
-    dims = (_ptr(hidden), _ptr(weight), _LOSS_DTYPES[hidden.dtype], N, V, H)
-    rows = (_ptr(row_weight), red, _ptr(out.loss), _ptr(out.row_loss), _ptr(out.lse))
-    end = (_ptr(out.status), _ptr(ws), ws.numel() * ws.element_size(), sh)
+    dims = (_at(hidden), _at(weight), _LOSS_DTYPES[hidden.dtype], N, V, H)
+    rows = (_at(row_weight), red, _at(out.loss), _at(out.row_loss), _at(out.lse))
+    end = (_at(out.status), _at(ws), ws.nbytes, handle)
     t, gs = float(temperature), float(grad_scale)
     if logits is None:
         if grads:
-            st = L.spec_linear_cross_entropy_fwd_bwd(*dims, t, gs, _ptr(ids), int(ignore_index), *rows,
-                                                     _ptr(out.grad_hidden), _ptr(out.grad_weight), gcode, *end)
+            st = L.spec_linear_cross_entropy_fwd_bwd(*dims, t, gs, _at(ids), int(ignore_index), *rows,
+                                                     _at(out.grad_hidden), _at(out.grad_weight), gcode, *end)
         else:
-            st = L.spec_linear_cross_entropy(*dims, t, _ptr(ids), int(ignore_index), *rows, *end)
+            st = L.spec_linear_cross_entropy(*dims, t, _at(ids), int(ignore_index), *rows, *end)
     elif grads:
-        st = L.spec_linear_topk_distill_fwd_bwd(*dims, k, t, gs, _ptr(ids), _ptr(logits), *rows,
-                                                _ptr(out.grad_hidden), _ptr(out.grad_weight), gcode, *end)
+        st = L.spec_linear_topk_distill_fwd_bwd(*dims, k, t, gs, _at(ids), _at(logits), *rows,
+                                                _at(out.grad_hidden), _at(out.grad_weight), gcode, *end)
     else:
-        st = L.spec_linear_topk_distill(*dims, k, t, _ptr(ids), _ptr(logits), *rows, *end)
+        st = L.spec_linear_topk_distill(*dims, k, t, _at(ids), _at(logits), *rows, *end)
     _check(st, what)
     return out
 
@@ -833,16 +844,16 @@ def _distill(what, student, ids, logits, lse, temperature, grad_scale, row_weigh
         _need_out(out.status, "status", torch.int32, (1,), dev)
         if want_grad:
             _need(out.grad, "out.grad", dtype=gdt, shape=(N, V), device=dev)
-    sh, s = _stream_handle(stream, dev)
+    handle = _loss_stream(stream, dev)
     need = L.spec_topk_distill_workspace_bytes(N, V, k)
-    status, ws, made = _loss_buffers(dev, s, stream, need, workspace, empties)
+    status, ws, made = _loss_buffers(dev, handle, stream, need, workspace, empties)
     if out is None:
         out = DistillOutput(made[0], made[1], made[2] if want_grad else None, status)
-    end = (_ptr(out.status), _ptr(ws), ws.numel() * ws.element_size(), sh)
-    common = (_ptr(ids), _ptr(logits), _ptr(lse), _ptr(row_weight), red, _ptr(out.loss), _ptr(out.row_loss))
-    dims = (_ptr(student), _LOSS_DTYPES[student.dtype], N, V, k, float(temperature))
+    end = (_at(out.status), _at(ws), ws.nbytes, handle)
+    common = (_at(ids), _at(logits), _at(lse), _at(row_weight), red, _at(out.loss), _at(out.row_loss))
+    dims = (_at(student), _LOSS_DTYPES[student.dtype], N, V, k, float(temperature))
     if want_grad:
-        st = L.spec_topk_distill_fwd_bwd(*dims, float(grad_scale), *common, _ptr(out.grad), gcode, *end)
+        st = L.spec_topk_distill_fwd_bwd(*dims, float(grad_scale), *common, _at(out.grad), gcode, *end)
     else:
         st = L.spec_topk_distill(*dims, *common, *end)
     _check(st, what)
