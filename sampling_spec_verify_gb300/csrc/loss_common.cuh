@@ -216,11 +216,19 @@ __device__ __forceinline__ void follow_previous() {
 }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// A pair's rounding, 0 where the value is not finite: the rounding of an infinite
+// sum or product comes out as inf - inf and would turn it into NaN.
+__device__ __forceinline__ F2 pair_of(float hi, float lo) { return {hi, fabsf(hi) < INFINITY ? lo : 0.0f}; }
+// pair_add where infinite terms are ordinary.
+__device__ __forceinline__ F2 sum_add(F2 a, F2 b) {
+  const F2 s = pair_add(a, b);
+  return pair_of(s.hi, s.lo);
+}
 // Sum over the lanes of a warp, roundings carried along (in every lane, the same).
 __device__ __forceinline__ F2 warp_sum(F2 v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1)
-    v = pair_add(v, F2{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+    v = sum_add(v, F2{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
   return v;
 }
 
@@ -466,7 +474,8 @@ __device__ __forceinline__ float row_loss_warp(const FinishParams& P, long long 
 
 // Sums of the CTA's eight rows (warp w's loss in every lane of it), and in the
 // last CTA to arrive the call's, all in fixed orders, as pairs of floats (fp64
-// additions here were a third of the kernel's time).  256 threads.
+// additions here were a third of the kernel's time).  256 threads.  A row loss may
+// be +inf (a listed token that the student gives no mass): so is the sum then.
 __device__ __forceinline__ void finish_sums(const FinishParams& P, float loss, bool on, float weight) {
   __shared__ float4 red[8];  // {sum, its rounding, rows, largest |weight|}
   __shared__ uint32_t last;
@@ -477,7 +486,8 @@ __device__ __forceinline__ void finish_sums(const FinishParams& P, float loss, b
   };
   if (lane == 0) {
     const float p = on ? weight * loss : 0.0f;
-    red[w] = make_float4(p, on ? fmaf(weight, loss, -p) : 0.0f, on ? 1.0f : 0.0f, on ? fabsf(weight) : 0.0f);
+    const F2 v = pair_of(p, on ? fmaf(weight, loss, -p) : 0.0f);
+    red[w] = make_float4(v.hi, v.lo, on ? 1.0f : 0.0f, on ? fabsf(weight) : 0.0f);
   }
   __syncthreads();
   if (w == 0) {
@@ -501,7 +511,7 @@ __device__ __forceinline__ void finish_sums(const FinishParams& P, float loss, b
 #pragma unroll 4
     for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) {
       const float4 v = __ldcg(P.part + i);
-      sum = pair_add(sum, F2{v.x, v.y});
+      sum = sum_add(sum, F2{v.x, v.y});
       cnt += v.z;
       wmax = max_nan(wmax, v.w);
     }

@@ -1,0 +1,47 @@
+"""Edges of the drafter-training losses: infinite losses, masked tiles, weights at the
+end of the range, batches that reuse every buffer of a kernel.  Oracle and tolerances
+are those of test_gpu_losses.py."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import dense_teacher, listed_loss
+from test_gpu_losses import BF16, DEV, E, F16, F32, f64, kd_inputs, ssv  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("N", [3, 8, 9, 40, 5000])
+@pytest.mark.parametrize("red", ["mean", "sum"])
+def test_infinite_row_losses_make_the_loss_infinite(ssv, N, red):  # noqa: F811
+    """A student that gives a listed token no mass has an infinite loss, and so has
+    its batch; only opposite infinities make NaN."""
+    V, k = 64, 3
+    z, ids, x, lse, w = kd_inputs(N, V, k, F32, N, 1.0)
+    z[1, ids[1, 0].long()] = float("-inf")
+    w[2] = -0.5
+    d = [t.to(DEV) for t in (z, ids, x, w)]
+    o = ssv.topk_distill_fwd_bwd(*d[:3], 1.0, row_weight=d[3], reduction=red)
+    r = listed_loss(f64(z), dense_teacher(ids.numpy(), x.numpy(), 1.0, V), 1.0, row_weight=w.numpy(), reduction=red)
+    assert np.isposinf(r.loss) and float(o.loss) == float("inf") and int(o.status) == 0
+    z[2, ids[2, 1].long()] = float("-inf")
+    o = ssv.topk_distill(z.to(DEV), *d[1:3], 1.0, row_weight=d[3], reduction=red)
+    assert np.isnan(float(o.loss)) and np.isposinf(f64(o.row_loss)[1:3]).all()
+    w[1] = -1.0
+    o = ssv.topk_distill(z.to(DEV), *d[1:3], 1.0, row_weight=w.to(DEV), reduction=red)
+    assert float(o.loss) == float("-inf")
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("N", [4, 30])
+def test_rows_masked_with_the_lowest_value_keep_their_loss(ssv, dt, N):  # noqa: F811
+    """One token left that the teacher does not list: a large and finite loss."""
+    V, k = 500, 3
+    z, ids, x, lse, w = kd_inputs(N, V, k, dt, 11, 1.0)
+    z[1, torch.arange(V) != 17] = torch.finfo(dt).min
+    ids[1] = torch.tensor([3, 4, 5])
+    o = ssv.topk_distill_fwd_bwd(*(t.to(DEV) for t in (z, ids, x)), 1.0, reduction="sum")
+    r = listed_loss(f64(z), dense_teacher(ids.numpy(), x.numpy(), 1.0, V), 1.0, reduction="sum")
+    assert (np.abs(f64(o.row_loss) - r.row_loss) <= E + 2e-6 * np.abs(r.row_loss)).all()
+    assert abs(float(o.loss) - r.loss) <= E * N + 4e-6 * abs(r.loss)
