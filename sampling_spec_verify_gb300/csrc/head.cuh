@@ -370,7 +370,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
           }
         }
         m *= L.s;
-        const float off = m - kKeepShift;
+        // A tile of nothing but -inf adds nothing: its terms are 2^(-inf - 0), and its
+        // offset stays -inf, so that kept terms are rescaled by 0.
+        const bool none = m == -INFINITY;
+        const float off = none ? 0.0f : m - kKeepShift;
         constexpr int kCols = OP == kHeadKeep && OUT32 ? 32 : 64;
         for (int c = 0; c < kTileN; c += kCols) {
           if (c >= cols) break;
@@ -397,7 +400,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) __cluster_dims__(2, 1, 1)
           }
           if constexpr (OP == kHeadKeep) send(&L.out[0], dst, col0 + c, row0, row0 < M, false);
         }
-        if (row < M) L.part[(long long)t.n * M + row] = make_float2(off, sum);
+        if (row < M) L.part[(long long)t.n * M + row] = make_float2(none ? -INFINITY : off, sum);
         // The listed tokens' logits are those of the same products that make the
         // normaliser: the tensor cores' sums are short of the exact ones by up to
         // 2.5e-6 of a logit, which would stand alone in the loss of a confident

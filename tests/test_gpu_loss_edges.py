@@ -6,8 +6,9 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import dense_teacher, listed_loss
-from test_gpu_losses import BF16, DEV, E, F16, F32, f64, kd_inputs, ssv  # noqa: F401
+from oracle import dense_labels, dense_teacher, listed_loss
+from test_gpu_losses import (BAD_LOGITS, BF16, DEV, E, F16, F32, check_head, f64, head_inputs,
+                             kd_inputs, ssv)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +46,34 @@ def test_rows_masked_with_the_lowest_value_keep_their_loss(ssv, dt, N):  # noqa:
     r = listed_loss(f64(z), dense_teacher(ids.numpy(), x.numpy(), 1.0, V), 1.0, reduction="sum")
     assert (np.abs(f64(o.row_loss) - r.row_loss) <= E + 2e-6 * np.abs(r.row_loss)).all()
     assert abs(float(o.loss) - r.loss) <= E * N + 4e-6 * abs(r.loss)
+
+
+@pytest.mark.parametrize("cut", [slice(0, 256), slice(256, 512), slice(512, 513), slice(256, 513)])
+def test_head_tiles_without_a_finite_logit(ssv, cut):  # noqa: F811
+    """Tokens whose logits are -inf have no part in a row's results, also where
+    they fill a tile of the product (here 256, 256 and 1 tokens)."""
+    N, V, H = 40, 513, 64
+    x, w, y, rw = head_inputs(N, V, H, BF16, 7)
+    gone = torch.zeros(V, dtype=torch.bool)
+    gone[cut] = True
+    x[:, 0], w[:, 0] = 1e20, 0.0
+    w[gone, 0] = -1e20                      # logits of -1e40
+    left = torch.nonzero(~gone)[:, 0]
+    pick = torch.randint(0, len(left), (N,), generator=torch.Generator().manual_seed(1))
+    y = left[pick].to(torch.int32)
+    a = [t.to(DEV) for t in (x, w, y)]
+    o = ssv.linear_cross_entropy_fwd_bwd(*a, 1.0, row_weight=rw.to(DEV), reduction="sum", grad_dtype=F32)
+    f = ssv.linear_cross_entropy(*a, 1.0, row_weight=rw.to(DEV), reduction="sum")
+    assert int(o.status) == 0 and torch.equal(f.loss, o.loss) and torch.equal(f.row_loss, o.row_loss)
+    assert (f64(o.grad_weight)[gone.numpy()] == 0).all()
+    o.grad_weight = o.grad_weight[left.to(DEV)]
+    check_head(o, x, w[left], dense_labels(pick.numpy(), len(left), -100), 1.0, rw.numpy(), "sum", 1.0, F32)
+    # a label among them: an infinite loss (or the least logit's), no NaN
+    y[5] = int(torch.nonzero(gone)[0])
+    o = ssv.linear_cross_entropy_fwd_bwd(a[0], a[1], y.to(DEV), 1.0, reduction="sum", grad_dtype=F32)
+    assert float(o.row_loss[5]) > 3e38 and float(o.loss) > 3e38
+    assert not o.grad_hidden.isnan().any() and not o.grad_weight.isnan().any()
+    # nothing but such tokens is a row that cannot be normalised
+    w[:, 0] = -1e20
+    o = ssv.linear_cross_entropy(a[0], w.to(DEV), a[2], 1.0)
+    assert o.row_loss.isnan().all() and int(o.status) == BAD_LOGITS
