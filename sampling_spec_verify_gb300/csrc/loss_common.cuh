@@ -37,7 +37,7 @@ struct RowNorm {  // of the student: sums of 2^((z - m) s), s = log2(e) / T
 struct LossScalars {
   uint32_t ticket;
   uint32_t count;  // rows that count
-  float inv_wmax;  // 1 / largest |row weight| of those (0 if there is none)
+  float inv_wmax;  // 1 / largest |row weight| of those (0 if there is none; one below 2^-126 counts as 2^-126)
   float grad_mul;  // factor of the stored logit gradients in the results
 };
 
@@ -526,8 +526,10 @@ __device__ __forceinline__ void finish_sums(const FinishParams& P, float loss, b
       const float den = P.mean && v.z > 0.0f ? v.z : 1.0f;  // counts are exact up to 2^24 rows
       P.loss[0] = (v.x + v.y) / den;
       P.scalars->count = (uint32_t)v.z;
-      P.scalars->inv_wmax = v.w == 0.0f ? 0.0f : 1.0f / v.w;
-      P.scalars->grad_mul = P.grad_scale * v.w / (den * P.store_scale);
+      // the inverse of a smaller one would be infinite; (NaN passes on)
+      const float wmax = v.w < 0x1p-126f ? 0x1p-126f : v.w;
+      P.scalars->inv_wmax = v.w == 0.0f ? 0.0f : 1.0f / wmax;
+      P.scalars->grad_mul = P.grad_scale * wmax / (den * P.store_scale);
     }
   }
 }

@@ -77,3 +77,15 @@ def test_head_tiles_without_a_finite_logit(ssv, cut):  # noqa: F811
     w[:, 0] = -1e20
     o = ssv.linear_cross_entropy(a[0], w.to(DEV), a[2], 1.0)
     assert o.row_loss.isnan().all() and int(o.status) == BAD_LOGITS
+
+
+@pytest.mark.parametrize("N", [1, 20])
+def test_head_weights_below_the_normal_range(ssv, N):  # noqa: F811
+    """Row weights that have decayed to subnormal numbers still give the gradient's value."""
+    V, H = 300, 64
+    x, w, y, _ = head_inputs(N, V, H, BF16, 21)
+    rw = torch.full((N,), 1e-39) * torch.linspace(1, 2, N)
+    o = ssv.linear_cross_entropy_fwd_bwd(x.to(DEV), w.to(DEV), y.to(DEV), 1.0, 2.0 ** 126, row_weight=rw.to(DEV),
+                                         reduction="sum", grad_dtype=F32)
+    check_head(o, x, w, dense_labels(y.numpy(), V, -100), 1.0, rw.numpy(), "sum", 2.0 ** 126, F32)
+    assert (f64(o.grad_hidden) != 0).any()
