@@ -37,6 +37,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -189,6 +190,16 @@ def _stream_handle(stream: Optional[torch.cuda.Stream], device):
 
 
 _WS = {}
+_LOCKS = {}
+
+
+def _held(device, handle: int):
+    """Lock of the buffers cached for a stream.  A call is several launches that use
+    one workspace, and ctypes lets other threads run meanwhile: a call holds the lock
+    from the look-up of its buffers to its last launch, so that two threads on one
+    stream (the default one, say) cannot mix their launches over it."""
+    key = (device.index, handle)
+    return _LOCKS.get(key) or _LOCKS.setdefault(key, threading.Lock())
 
 
 def _workspace(nbytes: int, device, stream) -> torch.Tensor:
@@ -274,11 +285,12 @@ def verify(target: torch.Tensor, draft: Optional[torch.Tensor], draft_tokens: to
             torch.zeros((1,), dtype=torch.int32, device=dev))
     sh, s = _stream_handle(stream, dev)
     need = L.spec_verify_workspace_bytes(B, K, V)
-    ws = workspace if workspace is not None else _workspace(need, dev, s)
-    st = L.spec_verify(_ptr(target), _ptr(draft), _dtype_code(target), B, K, V, float(temperature),
-                       _ptr(draft_tokens), _ptr(u_accept), _ptr(u_final), _ptr(out.tokens),
-                       _ptr(out.n_accepted), _ptr(out.alpha), _ptr(out.status), _ptr(ws),
-                       ws.numel() * ws.element_size(), sh)
+    with _held(dev, s.cuda_stream):
+        ws = workspace if workspace is not None else _workspace(need, dev, s)
+        st = L.spec_verify(_ptr(target), _ptr(draft), _dtype_code(target), B, K, V, float(temperature),
+                           _ptr(draft_tokens), _ptr(u_accept), _ptr(u_final), _ptr(out.tokens),
+                           _ptr(out.n_accepted), _ptr(out.alpha), _ptr(out.status), _ptr(ws),
+                           ws.numel() * ws.element_size(), sh)
     _check(st, "spec_verify")
     return out
 
@@ -311,11 +323,12 @@ def verify_ragged(target: torch.Tensor, draft: Optional[torch.Tensor], row_offse
                        torch.zeros((1,), dtype=torch.int32, device=dev))
     sh, s = _stream_handle(stream, dev)
     need = L.spec_verify_ragged_workspace_bytes(B, units, V)
-    ws = workspace if workspace is not None else _workspace(need, dev, s)
-    st = L.spec_verify_ragged(_ptr(target), _ptr(draft), _dtype_code(target), B, _ptr(row_offsets), units, V,
-                              float(temperature), _ptr(draft_tokens), _ptr(u_accept), _ptr(u_final),
-                              _ptr(out.tokens), _ptr(out.n_accepted), _ptr(out.alpha), _ptr(out.status), _ptr(ws),
-                              ws.numel() * ws.element_size(), sh)
+    with _held(dev, s.cuda_stream):
+        ws = workspace if workspace is not None else _workspace(need, dev, s)
+        st = L.spec_verify_ragged(_ptr(target), _ptr(draft), _dtype_code(target), B, _ptr(row_offsets), units, V,
+                                  float(temperature), _ptr(draft_tokens), _ptr(u_accept), _ptr(u_final),
+                                  _ptr(out.tokens), _ptr(out.n_accepted), _ptr(out.alpha), _ptr(out.status), _ptr(ws),
+                                  ws.numel() * ws.element_size(), sh)
     _check(st, "spec_verify_ragged")
     return out
 
@@ -344,11 +357,12 @@ def verify_relaxed(target: torch.Tensor, draft: torch.Tensor, draft_tokens: torc
                        torch.zeros((1,), dtype=torch.int32, device=dev))
     sh, s = _stream_handle(stream, dev)
     need = L.spec_verify_workspace_bytes(B, K, V)
-    ws = workspace if workspace is not None else _workspace(need, dev, s)
-    st = L.spec_verify_relaxed(_ptr(target), _ptr(draft), _dtype_code(target), B, K, V, float(temperature),
-                               int(top_k), float(delta), _ptr(draft_tokens), _ptr(u_final), _ptr(out.tokens),
-                               _ptr(out.n_accepted), _ptr(out.alpha), _ptr(out.status), _ptr(ws),
-                               ws.numel() * ws.element_size(), sh)
+    with _held(dev, s.cuda_stream):
+        ws = workspace if workspace is not None else _workspace(need, dev, s)
+        st = L.spec_verify_relaxed(_ptr(target), _ptr(draft), _dtype_code(target), B, K, V, float(temperature),
+                                   int(top_k), float(delta), _ptr(draft_tokens), _ptr(u_final), _ptr(out.tokens),
+                                   _ptr(out.n_accepted), _ptr(out.alpha), _ptr(out.status), _ptr(ws),
+                                   ws.numel() * ws.element_size(), sh)
     _check(st, "spec_verify_relaxed")
     return out
 
@@ -394,10 +408,11 @@ def tree_verify_greedy(target: torch.Tensor, parent: torch.Tensor, node_tokens: 
                      torch.zeros((1,), dtype=torch.int32, device=dev))
     sh, s = _stream_handle(stream, dev)
     need = L.spec_tree_verify_workspace_bytes(B, N, V)
-    ws = workspace if workspace is not None else _workspace(need, dev, s)
-    st = L.spec_tree_verify_greedy(_ptr(target), _dtype_code(target), B, N, V, _ptr(parent), _ptr(node_tokens),
-                                   _ptr(out.path), _ptr(out.tokens), _ptr(out.n_accepted), _ptr(out.status),
-                                   _ptr(ws), ws.numel() * ws.element_size(), sh)
+    with _held(dev, s.cuda_stream):
+        ws = workspace if workspace is not None else _workspace(need, dev, s)
+        st = L.spec_tree_verify_greedy(_ptr(target), _dtype_code(target), B, N, V, _ptr(parent), _ptr(node_tokens),
+                                       _ptr(out.path), _ptr(out.tokens), _ptr(out.n_accepted), _ptr(out.status),
+                                       _ptr(ws), ws.numel() * ws.element_size(), sh)
     _check(st, "spec_tree_verify_greedy")
     return out
 
@@ -435,11 +450,12 @@ def overlap(target: torch.Tensor, draft: torch.Tensor, temperature: float, *, K:
                             f(B) if want_survival else None, torch.zeros((1,), dtype=torch.int32, device=dev))
     sh, s = _stream_handle(stream, dev)
     need = L.spec_overlap_workspace_bytes(B, K, V)
-    ws = workspace if workspace is not None else _workspace(need, dev, s)
-    st = L.spec_overlap(_ptr(target), _ptr(draft), _dtype_code(target), B, K, KT, V, float(temperature),
-                        _ptr(out.alpha), _ptr(out.tv), _ptr(out.prefix_survival),
-                        _ptr(out.expected_accepted), _ptr(out.status), _ptr(ws),
-                        ws.numel() * ws.element_size(), sh)
+    with _held(dev, s.cuda_stream):
+        ws = workspace if workspace is not None else _workspace(need, dev, s)
+        st = L.spec_overlap(_ptr(target), _ptr(draft), _dtype_code(target), B, K, KT, V, float(temperature),
+                            _ptr(out.alpha), _ptr(out.tv), _ptr(out.prefix_survival),
+                            _ptr(out.expected_accepted), _ptr(out.status), _ptr(ws),
+                            ws.numel() * ws.element_size(), sh)
     _check(st, "spec_overlap")
     return out
 
@@ -477,10 +493,11 @@ def e2e_tv_fwd_bwd(target: torch.Tensor, draft: torch.Tensor, temperature: float
                         torch.zeros((1,), dtype=torch.int32, device=dev))
     sh, s = _stream_handle(stream, dev)
     need = L.spec_e2e_tv_workspace_bytes(B, K, V)
-    ws = workspace if workspace is not None else _workspace(need, dev, s)
-    st = L.spec_e2e_tv_fwd_bwd(_ptr(target), _ptr(draft), _dtype_code(target), B, K, KT, V, float(temperature),
-                               float(grad_scale), _ptr(out.loss), _ptr(out.alpha), _ptr(out.grad),
-                               _ptr(out.status), _ptr(ws), ws.numel() * ws.element_size(), sh)
+    with _held(dev, s.cuda_stream):
+        ws = workspace if workspace is not None else _workspace(need, dev, s)
+        st = L.spec_e2e_tv_fwd_bwd(_ptr(target), _ptr(draft), _dtype_code(target), B, K, KT, V, float(temperature),
+                                   float(grad_scale), _ptr(out.loss), _ptr(out.alpha), _ptr(out.grad),
+                                   _ptr(out.status), _ptr(ws), ws.numel() * ws.element_size(), sh)
     _check(st, "spec_e2e_tv_fwd_bwd")
     return out
 
@@ -519,11 +536,12 @@ def diagnostics(target: torch.Tensor, draft: torch.Tensor, temperature: float, *
         out = DiagOutput(f(), f(), f(), f(), f(), torch.zeros((1,), dtype=torch.int32, device=dev))
     sh, s = _stream_handle(stream, dev)
     need = L.spec_diagnostics_workspace_bytes(B, K, V)
-    ws = workspace if workspace is not None else _workspace(need, dev, s)
-    st = L.spec_diagnostics(_ptr(target), _ptr(draft), _dtype_code(target), B, K, KT, V, float(temperature),
-                            _ptr(out.alpha), _ptr(out.entropy), _ptr(out.cross_entropy), _ptr(out.kl),
-                            _ptr(out.alpha_target_only), _ptr(out.status), _ptr(ws),
-                            ws.numel() * ws.element_size(), sh)
+    with _held(dev, s.cuda_stream):
+        ws = workspace if workspace is not None else _workspace(need, dev, s)
+        st = L.spec_diagnostics(_ptr(target), _ptr(draft), _dtype_code(target), B, K, KT, V, float(temperature),
+                                _ptr(out.alpha), _ptr(out.entropy), _ptr(out.cross_entropy), _ptr(out.kl),
+                                _ptr(out.alpha_target_only), _ptr(out.status), _ptr(ws),
+                                ws.numel() * ws.element_size(), sh)
     _check(st, "spec_diagnostics")
     return out
 
@@ -597,10 +615,11 @@ def _loss_stream(given, device):
 
 def _loss_buffers(device, handle, given, nbytes, workspace, empties):
     """(status word, workspace, empty tensors) of a training-loss call, on its
-    stream.  Status words come zeroed from a block per (device, stream), one
-    for each call; workspaces are cached per (device, stream) and never zeroed,
-    so they are not the ones of the other calls.  Inside a stream capture
-    nothing is cached: the memory belongs to the graph."""
+    stream; the caller holds the stream's lock (``_held``).  Status words come
+    zeroed from a block per (device, stream), one for each call; workspaces are
+    cached per (device, stream) and never zeroed, so they are not the ones of
+    the other calls.  Inside a stream capture nothing is cached: the memory
+    belongs to the graph."""
     key = (device.index, handle)
     with _Nothing() if given is None else torch.cuda.stream(given):
         capturing = torch.cuda.is_current_stream_capturing()  # of the call's own stream
@@ -724,25 +743,26 @@ def _linear_loss(what, hidden, weight, ids, logits, ignore_index, temperature, g
     handle = _loss_stream(stream, dev)
     need = L.spec_linear_loss_workspace_bytes(_LOSS_DTYPES[hidden.dtype], N, V, H, k, int(want_hidden),
                                               int(want_weight))
-    status, ws, made = _loss_buffers(dev, handle, stream, need, workspace, empties)
-    if out is None:
-        out = LinearLossOutput(made[0], made[1], made[2], made[3] if want_hidden else None,
-                               made[-1] if want_weight else None, status)
-    dims = (_at(hidden), _at(weight), _LOSS_DTYPES[hidden.dtype], N, V, H)
-    rows = (_at(row_weight), red, _at(out.loss), _at(out.row_loss), _at(out.lse))
-    end = (_at(out.status), _at(ws), ws.nbytes, handle)
-    t, gs = float(temperature), float(grad_scale)
-    if logits is None:
-        if grads:
-            st = L.spec_linear_cross_entropy_fwd_bwd(*dims, t, gs, _at(ids), int(ignore_index), *rows,
-                                                     _at(out.grad_hidden), _at(out.grad_weight), gcode, *end)
+    with _held(dev, handle):
+        status, ws, made = _loss_buffers(dev, handle, stream, need, workspace, empties)
+        if out is None:
+            out = LinearLossOutput(made[0], made[1], made[2], made[3] if want_hidden else None,
+                                   made[-1] if want_weight else None, status)
+        dims = (_at(hidden), _at(weight), _LOSS_DTYPES[hidden.dtype], N, V, H)
+        rows = (_at(row_weight), red, _at(out.loss), _at(out.row_loss), _at(out.lse))
+        end = (_at(out.status), _at(ws), ws.nbytes, handle)
+        t, gs = float(temperature), float(grad_scale)
+        if logits is None:
+            if grads:
+                st = L.spec_linear_cross_entropy_fwd_bwd(*dims, t, gs, _at(ids), int(ignore_index), *rows,
+                                                         _at(out.grad_hidden), _at(out.grad_weight), gcode, *end)
+            else:
+                st = L.spec_linear_cross_entropy(*dims, t, _at(ids), int(ignore_index), *rows, *end)
+        elif grads:
+            st = L.spec_linear_topk_distill_fwd_bwd(*dims, k, t, gs, _at(ids), _at(logits), *rows,
+                                                    _at(out.grad_hidden), _at(out.grad_weight), gcode, *end)
         else:
-            st = L.spec_linear_cross_entropy(*dims, t, _at(ids), int(ignore_index), *rows, *end)
-    elif grads:
-        st = L.spec_linear_topk_distill_fwd_bwd(*dims, k, t, gs, _at(ids), _at(logits), *rows,
-                                                _at(out.grad_hidden), _at(out.grad_weight), gcode, *end)
-    else:
-        st = L.spec_linear_topk_distill(*dims, k, t, _at(ids), _at(logits), *rows, *end)
+            st = L.spec_linear_topk_distill(*dims, k, t, _at(ids), _at(logits), *rows, *end)
     _check(st, what)
     return out
 
@@ -846,16 +866,17 @@ def _distill(what, student, ids, logits, lse, temperature, grad_scale, row_weigh
             _need(out.grad, "out.grad", dtype=gdt, shape=(N, V), device=dev)
     handle = _loss_stream(stream, dev)
     need = L.spec_topk_distill_workspace_bytes(N, V, k)
-    status, ws, made = _loss_buffers(dev, handle, stream, need, workspace, empties)
-    if out is None:
-        out = DistillOutput(made[0], made[1], made[2] if want_grad else None, status)
-    end = (_at(out.status), _at(ws), ws.nbytes, handle)
-    common = (_at(ids), _at(logits), _at(lse), _at(row_weight), red, _at(out.loss), _at(out.row_loss))
-    dims = (_at(student), _LOSS_DTYPES[student.dtype], N, V, k, float(temperature))
-    if want_grad:
-        st = L.spec_topk_distill_fwd_bwd(*dims, float(grad_scale), *common, _at(out.grad), gcode, *end)
-    else:
-        st = L.spec_topk_distill(*dims, *common, *end)
+    with _held(dev, handle):
+        status, ws, made = _loss_buffers(dev, handle, stream, need, workspace, empties)
+        if out is None:
+            out = DistillOutput(made[0], made[1], made[2] if want_grad else None, status)
+        end = (_at(out.status), _at(ws), ws.nbytes, handle)
+        common = (_at(ids), _at(logits), _at(lse), _at(row_weight), red, _at(out.loss), _at(out.row_loss))
+        dims = (_at(student), _LOSS_DTYPES[student.dtype], N, V, k, float(temperature))
+        if want_grad:
+            st = L.spec_topk_distill_fwd_bwd(*dims, float(grad_scale), *common, _at(out.grad), gcode, *end)
+        else:
+            st = L.spec_topk_distill(*dims, *common, *end)
     _check(st, what)
     return out
 

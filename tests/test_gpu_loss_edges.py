@@ -2,6 +2,8 @@
 end of the range, batches that reuse every buffer of a kernel.  Oracle and tolerances
 are those of test_gpu_losses.py."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -89,3 +91,41 @@ def test_head_weights_below_the_normal_range(ssv, N):  # noqa: F811
                                          reduction="sum", grad_dtype=F32)
     check_head(o, x, w, dense_labels(y.numpy(), V, -100), 1.0, rw.numpy(), "sum", 2.0 ** 126, F32)
     assert (f64(o.grad_hidden) != 0).any()
+
+
+def test_two_host_threads_on_one_stream(ssv):  # noqa: F811
+    """Calls of different sizes from two threads: each gets what it gets alone."""
+    def job(N, V, H, k, seed):
+        x, w, y, rw = (t.to(DEV) for t in head_inputs(N, V, H, BF16, seed))
+        z, ids, tx, lse, kw = (t.to(DEV) for t in kd_inputs(N, V, k, BF16, seed, 1.0, padded=True))
+
+        def call():
+            a = ssv.linear_cross_entropy_fwd_bwd(x, w, y, 1.0, row_weight=rw)
+            b = ssv.linear_topk_distill_fwd_bwd(x, w, ids, tx, 1.0, row_weight=rw)
+            c = ssv.topk_distill_fwd_bwd(z, ids, tx, 1.0, teacher_lse=lse, row_weight=kw)
+            return [a.loss, a.row_loss, a.grad_hidden, a.grad_weight, b.loss, b.grad_hidden, b.grad_weight, c.loss,
+                    c.row_loss, c.grad, a.status, b.status, c.status]
+        return call
+
+    jobs = [job(70, 3001, 136, 12, 1), job(300, 5003, 200, 40, 2)]
+    want = [j() for j in jobs]
+    torch.cuda.synchronize()
+    got, failed = [[], []], []
+
+    def work(i):
+        try:
+            for _ in range(40):
+                got[i].append(jobs[i]())
+        except Exception as e:  # noqa: BLE001
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for i in (0, 1):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(want[i], g))
