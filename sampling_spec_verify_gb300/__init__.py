@@ -184,7 +184,18 @@ def _need(t: torch.Tensor, name: str, dtype=None, shape=None, device=None):
         raise ValueError(f"{name} must be on {device}")
 
 
+def _need_current(device, stream: Optional[torch.cuda.Stream]):
+    """The library launches on the current device: tensors and stream have to be there."""
+    current = torch.cuda.current_device()
+    if device.index != current:
+        raise ValueError(f"tensors are on {device}, but cuda:{current} is the current device: "
+                         f"call under torch.cuda.device({device.index})")
+    if stream is not None and stream.device_index != current:
+        raise ValueError(f"stream belongs to cuda:{stream.device_index}, the tensors are on {device}")
+
+
 def _stream_handle(stream: Optional[torch.cuda.Stream], device):
+    _need_current(device, stream)
     s = torch.cuda.current_stream(device) if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream), s
 
@@ -610,6 +621,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 def _loss_stream(given, device):
     """Handle of a training-loss call's stream.  (A call of few rows takes as long
     as its host side; the stream object alone would be 2 us of 29.)"""
+    _need_current(device, given)
     return _raw_stream(device.index) if given is None else given.cuda_stream
 
 
