@@ -752,6 +752,8 @@ def _linear_loss(what, hidden, weight, ids, logits, ignore_index, temperature, g
                 raise ValueError("out must hold exactly the gradients that are asked for")
             _need_out(out.grad_hidden, "grad_hidden", gdt, (N, H), dev)
             _need_out(out.grad_weight, "grad_weight", gdt, (V, H), dev)
+    if workspace is not None:
+        _need(workspace, "workspace", device=dev)
     handle = _loss_stream(stream, dev)
     need = L.spec_linear_loss_workspace_bytes(_LOSS_DTYPES[hidden.dtype], N, V, H, k, int(want_hidden),
                                               int(want_weight))
@@ -876,6 +878,8 @@ def _distill(what, student, ids, logits, lse, temperature, grad_scale, row_weigh
         _need_out(out.status, "status", torch.int32, (1,), dev)
         if want_grad:
             _need(out.grad, "out.grad", dtype=gdt, shape=(N, V), device=dev)
+    if workspace is not None:
+        _need(workspace, "workspace", device=dev)
     handle = _loss_stream(stream, dev)
     need = L.spec_topk_distill_workspace_bytes(N, V, k)
     with _held(dev, handle):
