@@ -524,7 +524,7 @@ spec_status_t spec_linear_topk_distill_fwd_bwd(const void* hidden, const void* w
  * tokens and q_v (M - t_r / q_r) / T on the others.
  * loss_out [1], row_loss [N] or NULL: float32.  grad [N, V] of grad_dtype =
  * dtype or SPEC_F32.
- * Limit: V * elem_size up to about 3.5 MB (16 CTAs' shared memory).
+ * Limits: N <= 2^30; V * elem_size up to about 3.5 MB (16 CTAs' shared memory).
  */
 size_t spec_topk_distill_workspace_bytes(int N, int V, int k);
 

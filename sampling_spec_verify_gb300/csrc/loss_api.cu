@@ -169,6 +169,9 @@ DistillWs distill_ws(void* base, size_t N, size_t k) {
   return w;
 }
 
+// Rows of a call: the kernels count them in steps of 8 and 256 with 32-bit integers.
+constexpr int kMaxRows = 1 << 30;
+
 // Slices of a row: what a CTA's threads hold in registers (one stage: it is free
 // again as soon as they do); rows too long for 16 such slices stay in shared memory, with
 // two stages or one.  Short batches spread a row over more CTAs.
@@ -239,7 +242,8 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
   if (!temperature_ok(temperature) || !std::isfinite(grad_scale)) return SPEC_ERR_INVALID_ARG;
   if (want_grad && grad_dtype != dtype && grad_dtype != SPEC_F32) return SPEC_ERR_INVALID_ARG;
   if (!loss) return SPEC_ERR_INVALID_ARG;
-  if (k > ssv::kMaxEntries || !distill_shape((long long)V * elem_size(dtype), N, 1, false).S) return SPEC_ERR_UNSUPPORTED;
+  if (N > kMaxRows || k > ssv::kMaxEntries || !distill_shape((long long)V * elem_size(dtype), N, 1, false).S)
+    return SPEC_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (N == 0) return from_cuda(cudaMemsetAsync(loss, 0, sizeof(float), st));
   if (!student || !ids || !logits || (want_grad && !grad)) return SPEC_ERR_INVALID_ARG;
@@ -750,7 +754,7 @@ spec_status_t head_loss(const HeadCall& c, bool grads) {
 extern "C" {
 
 size_t spec_topk_distill_workspace_bytes(int N, int V, int k) {
-  if (N < 0 || V < 1 || k < 1 || k > ssv::kMaxEntries) return 0;
+  if (N < 0 || N > kMaxRows || V < 1 || k < 1 || k > ssv::kMaxEntries) return 0;
   return distill_ws(nullptr, (size_t)N, (size_t)k).total;
 }
 
