@@ -445,8 +445,9 @@ spec_status_t spec_schedule_lengths(const float* survival, int R, int L,
  */
 typedef enum { SPEC_MEAN = 0, SPEC_SUM = 1 } spec_reduction_t;
 
-/* Cross entropy of a vocabulary head, without the logits z_n = hidden_n .
- * weight^T / T ever standing in memory:
+/* Cross entropy of a vocabulary head from its hidden states, z_n = hidden_n .
+ * weight^T / T, without storing the logits (of a call with gradients see
+ * the workspace):
  *   L_n = logsumexp(z_n) - z_n[label_n]
  *
  * hidden     [N, H], weight [V, H]: dtype SPEC_BF16 or SPEC_F16, contiguous,
@@ -465,14 +466,28 @@ typedef enum { SPEC_MEAN = 0, SPEC_SUM = 1 } spec_reduction_t;
  *            grad_dtype = dtype or SPEC_F32, 16-byte aligned.  The gradient of
  *            the logits is rounded once to dtype on its way into the products.
  *
- * The workspace size covers the gradients that are asked for.
- * A gradient call holds 16-bit gradients of the logits for a piece of the
- * vocabulary at a time (256 MB, or 4 KB a row where that is more) and
- * recomputes the logits piece by piece; a batch whose entries all fit 4 GB
- * (2 bytes an entry for SPEC_BF16, 6 for SPEC_F16) takes one piece and keeps the
- * unnormalised probabilities of the forward pass in it instead.
+ * Workspace: spec_linear_loss_workspace_bytes gives the preferred size,
+ * spec_linear_loss_workspace_least the least; a call takes what it is given,
+ * in between too.  Both cover the gradients that are asked for:
+ *  - a call of any kind holds the rows' statistics of every 256 tokens (8 bytes
+ *    each), its lists, and up to one copy of the hidden states;
+ *  - one with grad_hidden adds fp32 partials of it (4 N H bytes each, up to 32 where
+ *    few rows would leave the GPU idle);
+ *  - one with a gradient adds N values for each token of the vocabulary, or of a
+ *    piece of it.  A batch whose N V values fit 4 GB prefers the whole
+ *    vocabulary, and the normaliser's pass then leaves its unnormalised
+ *    probabilities there: 2 bytes a value for SPEC_BF16 and 6 for SPEC_F16, so
+ *    up to as much as the logits in 16 bits, or three times that.  Longer
+ *    batches, and calls with less room, go in pieces of 2 bytes a value
+ *    (preferred 256 MB, least 4 KB a row) and compute the logits a second
+ *    time: one product more than the three with both gradients, or the two
+ *    with one.
+ * The same workspace size gives the same bits; another one may cut the sums
+ * elsewhere and agrees within rounding.
  */
 size_t spec_linear_loss_workspace_bytes(spec_dtype_t dtype, int N, int V, int H, int k, int want_grad_hidden,
+                                        int want_grad_weight);
+size_t spec_linear_loss_workspace_least(spec_dtype_t dtype, int N, int V, int H, int k, int want_grad_hidden,
                                         int want_grad_weight);
 
 spec_status_t spec_linear_cross_entropy(const void* hidden, const void* weight, spec_dtype_t dtype, int N, int V,

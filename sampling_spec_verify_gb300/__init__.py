@@ -26,7 +26,8 @@ Entry points (same names as the C ABI, see include/spec_verify.h):
                          survivals and a throughput table;
 * ``linear_cross_entropy``, ``linear_cross_entropy_fwd_bwd`` -- cross entropy
                          of a vocabulary head from hidden states, without
-                         keeping its logits, and its gradients;
+                         storing its logits, and its gradients (their
+                         memory: ``linear_loss_workspace_bytes``);
 * ``topk_distill``, ``topk_distill_fwd_bwd`` -- distillation of draft logits
                          from a teacher's top logits, and its gradient;
 * ``linear_topk_distill``, ``linear_topk_distill_fwd_bwd`` -- the same from
@@ -45,6 +46,7 @@ import torch
 
 __all__ = [
     "SpecError", "lib", "verify", "verify_ragged", "verify_relaxed", "tree_mask", "tree_verify_greedy", "overlap", "e2e_tv_fwd_bwd", "diagnostics", "truncate_logits", "schedule_lengths", "linear_cross_entropy",
+    "linear_loss_workspace_bytes",
     "linear_cross_entropy_fwd_bwd", "topk_distill", "topk_distill_fwd_bwd", "linear_topk_distill",
     "linear_topk_distill_fwd_bwd", "selftest_bounded_wait", "launch_shape", "kernel_launches", "set_kernel_override",
     "set_launch_override", "VerifyOutput", "OverlapOutput", "E2EOutput", "DiagOutput", "TreeOutput", "HostVerifier",
@@ -133,6 +135,8 @@ def lib():
     tail = [vp, vp, sz, vp]                             # status, workspace, bytes, stream
     L.spec_linear_loss_workspace_bytes.restype = sz
     L.spec_linear_loss_workspace_bytes.argtypes = [i32] * 7
+    L.spec_linear_loss_workspace_least.restype = sz
+    L.spec_linear_loss_workspace_least.argtypes = [i32] * 7
     L.spec_linear_cross_entropy.restype = i32
     L.spec_linear_cross_entropy.argtypes = head + [f32, vp, i32, vp, i32, vp, vp, vp] + tail
     L.spec_linear_cross_entropy_fwd_bwd.restype = i32
@@ -781,13 +785,28 @@ def _linear_loss(what, hidden, weight, ids, logits, ignore_index, temperature, g
     return out
 
 
+def linear_loss_workspace_bytes(N: int, V: int, H: int, dtype: torch.dtype = torch.bfloat16, k: int = 1, *,
+                                want_grad_hidden: bool = True, want_grad_weight: bool = True,
+                                least: bool = False) -> int:
+    """Workspace of a loss through the head (k = 1: cross entropy), in bytes: the
+    size that a call takes by itself, or the least one that it works with.  A
+    call with gradients prefers to keep the probabilities of batches up to 4 GB
+    between its passes; given a smaller ``workspace`` it goes through the vocabulary in
+    pieces that fit, and computes the logits twice."""
+    f = lib().spec_linear_loss_workspace_least if least else lib().spec_linear_loss_workspace_bytes
+    size = f(_LOSS_DTYPES.get(dtype, -1), N, V, H, k, int(want_grad_hidden), int(want_grad_weight))
+    if size == 0:
+        raise ValueError("sizes or dtype beyond what the losses through the head take")
+    return size
+
+
 def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor, temperature: float = 1.0, *,
                          row_weight: Optional[torch.Tensor] = None, ignore_index: int = -100,
                          reduction: str = "mean", out: Optional[LinearLossOutput] = None,
                          workspace: Optional[torch.Tensor] = None,
                          stream: Optional[torch.cuda.Stream] = None) -> LinearLossOutput:
     """Cross entropy of softmax(hidden weight^T / temperature) against labels
-    without keeping the logits (see spec_linear_cross_entropy in the C
+    without storing the logits (see spec_linear_cross_entropy in the C
     header).  hidden [N, H] and weight [V, H] (bf16 or fp16, H a multiple of
     8), labels int32 [N], row_weight float32 [N].  ``row_loss`` is unweighted
     (minus the label's log-probability); ``loss`` is the weighted sum, over
@@ -821,7 +840,7 @@ def linear_topk_distill(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids:
                         out: Optional[LinearLossOutput] = None, workspace: Optional[torch.Tensor] = None,
                         stream: Optional[torch.cuda.Stream] = None) -> LinearLossOutput:
     """KL(t || q) of the teacher's renormalised top logits against
-    q = softmax(hidden weight^T / temperature), without keeping the logits (see
+    q = softmax(hidden weight^T / temperature), without storing the logits (see
     spec_linear_topk_distill in the C header).  teacher_ids int32 [N, k] (-1:
     unused slot) and teacher_logits float32 [N, k], k <= 256."""
     if teacher_logits is None:

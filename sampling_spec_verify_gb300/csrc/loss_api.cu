@@ -342,6 +342,7 @@ constexpr int kPairs = 76;                       // CTA pairs in flight, for the
 // against 5.6.
 constexpr size_t kKeepBytes = (size_t)4096 << 20;
 constexpr size_t kPieceBytes = (size_t)256 << 20;
+constexpr long long kLeastTiles = 8;
 
 // How a call is cut: pieces of the vocabulary and splits of a piece's depth in
 // the product that gives the hidden states' gradient.
@@ -353,14 +354,17 @@ struct HeadPlan {
   int splits;
   int slot_rows;
 };
-HeadPlan head_plan(int N, int V, int H, bool bf16) {
+// `most`: tiles of 256 tokens a piece has at most, for a caller whose workspace is
+// smaller than the preferred one (head_fit); 0: the rule above.
+HeadPlan head_plan(int N, int V, int H, bool bf16, long long most = 0) {
   HeadPlan p;
   const long long vt = ((long long)V + 255) / 256;
   long long cap = (long long)(kPieceBytes / 2 / (size_t)N) / 256;  // tiles of tokens
-  if (cap < 8) cap = 8;
+  if (cap < kLeastTiles) cap = kLeastTiles;
   p.kept32 = !bf16;
-  p.kept = (size_t)N * (size_t)vt * (bf16 ? 512 : 1536) <= kKeepBytes;
+  p.kept = !most && (size_t)N * (size_t)vt * (bf16 ? 512 : 1536) <= kKeepBytes;
   if (p.kept) cap = vt;
+  if (most && most < cap) cap = most;
   p.pieces = (int)((vt + cap - 1) / cap);
   p.piece = (int)((vt + p.pieces - 1) / p.pieces) * 256;
   p.pieces = (int)(((long long)V + p.piece - 1) / p.piece);
@@ -447,6 +451,21 @@ HeadWs head_ws(void* base, const HeadPlan& p, size_t N, size_t V, size_t H, size
   w.x = copy ? c.take<uint16_t>(copy_rows(N, H) * pitch_of(H)) : nullptr;
   w.total = c.used;
   return w;
+}
+
+// The plan for a workspace of `bytes`: the preferred one where it fits, else without
+// kept probabilities, in pieces of the vocabulary as long as they fit, down to kLeastTiles.
+HeadPlan head_fit(int N, int V, int H, int k, bool bf16, bool listed, bool gh, bool gw, size_t bytes) {
+  auto total = [&](const HeadPlan& p) {
+    return head_ws(nullptr, p, (size_t)N, (size_t)V, (size_t)H, (size_t)k, listed, gh, gw).total;
+  };
+  HeadPlan p = head_plan(N, V, H, bf16);
+  long long tiles = p.piece / 256;
+  while (total(p) > bytes && (p.kept || tiles > kLeastTiles)) {
+    if (!p.kept) tiles -= tiles / 8 > 1 ? tiles / 8 : 1;
+    p = head_plan(N, V, H, bf16, tiles);
+  }
+  return p;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -741,12 +760,22 @@ spec_status_t head_loss(const HeadCall& c, bool grads) {
     return from_cuda(e);
   }
   if (!c.hidden || !c.weight || !c.ids || !aligned(c.hidden, 16) || !aligned(c.weight, 16)) return SPEC_ERR_INVALID_ARG;
-  const HeadPlan plan = head_plan(c.N, c.V, c.H, c.dtype == SPEC_BF16);
+  const HeadPlan plan = head_fit(c.N, c.V, c.H, c.k, c.dtype == SPEC_BF16, c.logits != nullptr,
+                                 c.grad_hidden != nullptr, c.grad_weight != nullptr, c.bytes);
   const HeadWs ws = head_ws(c.workspace, plan, (size_t)c.N, (size_t)c.V, (size_t)c.H, (size_t)c.k, c.logits != nullptr,
                             c.grad_hidden != nullptr,
                             c.grad_weight != nullptr);
   if (!c.workspace || c.bytes < ws.total || !aligned(c.workspace, 256)) return SPEC_ERR_INVALID_ARG;
   return c.dtype == SPEC_BF16 ? head_run<__nv_bfloat16>(c, plan, ws) : head_run<__half>(c, plan, ws);
+}
+
+// Bytes of the workspace of a call that has room for `bytes`.
+size_t head_workspace(spec_dtype_t dtype, int N, int V, int H, int k, bool gh, bool gw, size_t bytes) {
+  if (dtype != SPEC_BF16 && dtype != SPEC_F16) return 0;
+  if (!head_dims_ok(N, V, H, k) || !head_dims_fit(N, V, H, k)) return 0;
+  if (N == 0) return 256;
+  const HeadPlan p = head_fit(N, V, H, k, dtype == SPEC_BF16, true, gh, gw, bytes);
+  return head_ws(nullptr, p, (size_t)N, (size_t)V, (size_t)H, (size_t)k, true, gh, gw).total;
 }
 
 }  // namespace
@@ -779,12 +808,12 @@ spec_status_t spec_topk_distill_fwd_bwd(const void* student, spec_dtype_t dtype,
 
 size_t spec_linear_loss_workspace_bytes(spec_dtype_t dtype, int N, int V, int H, int k, int want_grad_hidden,
                                         int want_grad_weight) {
-  if (dtype != SPEC_BF16 && dtype != SPEC_F16) return 0;
-  if (!head_dims_ok(N, V, H, k) || !head_dims_fit(N, V, H, k)) return 0;
-  if (N == 0) return 256;
-  return head_ws(nullptr, head_plan(N, V, H, dtype == SPEC_BF16), (size_t)N, (size_t)V, (size_t)H, (size_t)k, true,
-                 want_grad_hidden != 0, want_grad_weight != 0)
-      .total;
+  return head_workspace(dtype, N, V, H, k, want_grad_hidden != 0, want_grad_weight != 0, SIZE_MAX);
+}
+
+size_t spec_linear_loss_workspace_least(spec_dtype_t dtype, int N, int V, int H, int k, int want_grad_hidden,
+                                        int want_grad_weight) {
+  return head_workspace(dtype, N, V, H, k, want_grad_hidden != 0, want_grad_weight != 0, 0);
 }
 
 spec_status_t spec_linear_cross_entropy_fwd_bwd(const void* hidden, const void* weight, spec_dtype_t dtype, int N,
