@@ -46,7 +46,7 @@ import torch
 
 __all__ = [
     "SpecError", "lib", "verify", "verify_ragged", "verify_relaxed", "tree_mask", "tree_verify_greedy", "overlap", "e2e_tv_fwd_bwd", "diagnostics", "truncate_logits", "schedule_lengths", "linear_cross_entropy",
-    "linear_loss_workspace_bytes",
+    "linear_loss_workspace_bytes", "release_workspaces",
     "linear_cross_entropy_fwd_bwd", "topk_distill", "topk_distill_fwd_bwd", "linear_topk_distill",
     "linear_topk_distill_fwd_bwd", "selftest_bounded_wait", "launch_shape", "kernel_launches", "set_kernel_override",
     "set_launch_override", "VerifyOutput", "OverlapOutput", "E2EOutput", "DiagOutput", "TreeOutput", "HostVerifier",
@@ -661,6 +661,16 @@ def _loss_buffers(device, handle, given, nbytes, workspace, empties):
                     workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
                     _SCRATCH[key] = workspace
     return status, workspace, made
+
+
+def release_workspaces() -> None:
+    """Gives up the workspaces that the training losses have cached, one a stream
+    and as large as its largest call's (up to 4 GB and more).  Later calls
+    allocate anew.  (The other calls' zero-filled ones are small and stay: a
+    captured graph may hold their addresses.)"""
+    for key in list(_SCRATCH):
+        with _LOCKS[key]:
+            _SCRATCH.pop(key, None)
 
 
 def _at(t: Optional[torch.Tensor]):

@@ -92,3 +92,21 @@ def test_a_refused_call_releases_its_stream(slow, monkeypatch):
     with pytest.raises(ZeroDivisionError):
         ssv.linear_cross_entropy(x, x, zeros(4, dtype=torch.int32))
     assert not ssv._held(x.device, 0).locked()
+
+
+def test_cached_workspaces_can_be_released(slow):
+    loss = calls()[0]
+    loss()
+    assert [w.numel() for w in ssv._SCRATCH.values()] == [4096]
+    held = ssv._held(torch.device("cpu"), 0)
+    held.acquire()  # a call is between its look-up and its last launch
+    t = threading.Thread(target=ssv.release_workspaces)
+    t.start()
+    time.sleep(0.05)
+    assert len(ssv._SCRATCH) == 1 and t.is_alive()
+    held.release()
+    t.join()
+    assert not ssv._SCRATCH
+    loss()
+    assert len(ssv._SCRATCH) == 1 and slow.calls == 2
+    ssv.release_workspaces()
