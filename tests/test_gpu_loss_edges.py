@@ -9,8 +9,8 @@ import pytest
 import torch
 
 from oracle import dense_labels, dense_teacher, listed_loss
-from test_gpu_losses import (BAD_LOGITS, BF16, DEV, E, F16, F32, check_head, f64, head_inputs,
-                             kd_inputs, ssv)  # noqa: F401
+from test_gpu_losses import (BAD_LOGITS, BF16, DEV, E, F16, F32, check_head, check_kd, f64, head_inputs, kd_inputs,
+                             ssv)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -129,3 +129,66 @@ def test_two_host_threads_on_one_stream(ssv):  # noqa: F811
     for i in (0, 1):
         for g in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(want[i], g))
+
+
+# ---------------------------------------------------------------------------
+# every buffer used again: several live rows a cluster, at every cluster size
+# ---------------------------------------------------------------------------
+
+REUSE_CASES = [
+    # N, V, k, dtype, grad dtype, tail, padded, masked, gradients off a vector's boundary
+    (400, 40003, 40, BF16, BF16, True, True, True, False),    # two CTAs a row
+    (330, 60008, 64, F16, F32, False, False, False, False),
+    (190, 120001, 33, BF16, F32, True, True, False, False),   # four
+    (150, 70001, 100, F32, F32, True, False, False, False),
+    (100, 129280, 64, F32, F32, True, True, False, False),    # eight
+    (60, 160001, 20, F32, F32, True, False, True, False),     # sixteen
+    (40, 300000, 256, F32, F32, False, True, False, False),
+    (200, 80003, 16, BF16, BF16, True, True, False, True),    # from shared memory, two stages
+    (100, 100000, 30, F32, F32, True, False, False, True),
+    (30, 800001, 9, F32, F32, True, False, False, False),     # one stage
+]
+
+
+@pytest.mark.parametrize("N,V,k,dt,gdt,tail,padded,masked,off", REUSE_CASES)
+def test_distill_many_rows_a_cluster(ssv, N, V, k, dt, gdt, tail, padded, masked, off):  # noqa: F811
+    z, ids, x, lse, w = kd_inputs(N, V, k, dt, N + V, 1.0, padded, masked)
+    scale = 3.0 if gdt != F16 else 3.0 * 4096
+    grad = torch.empty(N * V + 1, dtype=gdt, device=DEV)[1 if off else 0:][:N * V].view(N, V)
+    out = ssv.DistillOutput(torch.empty(1, device=DEV), torch.empty(N, device=DEV), grad,
+                            torch.zeros(1, dtype=torch.int32, device=DEV))
+    d = [t.to(DEV) for t in (z, ids, x, lse, w)]
+    kw = dict(teacher_lse=d[3] if tail else None, row_weight=d[4])
+    o = ssv.topk_distill_fwd_bwd(d[0], d[1], d[2], 1.0, scale, grad_dtype=gdt, out=out, **kw)
+    f = ssv.topk_distill(d[0], d[1], d[2], 1.0, **kw)
+    torch.cuda.synchronize()
+    assert int(o.status) == 0
+    for n0 in range(0, N, 50):  # the oracle's arrays are long
+        rows = slice(n0, n0 + 50)
+        r = listed_loss(f64(z[rows]), dense_teacher(ids[rows].numpy(), x[rows].numpy(), 1.0, V,
+                                                    f64(lse[rows]) if tail else None), 1.0,
+                        row_weight=w[rows].numpy(), reduction="sum", grad_scale=scale / int((ids >= 0).any(1).sum()))
+        check_kd(o, r, 1.0, gdt, rows=rows)
+        check_kd(f, r, 1.0, rows=rows)
+
+
+def test_head_lists_of_many_rows(ssv):  # noqa: F811
+    """More than 8192 rows: a CTA of the kernels that look at every row takes several blocks of them."""
+    N, V, H, k = 9001, 520, 64, 5
+    x, w, y, rw = head_inputs(N, V, H, BF16, 31)
+    full = f64(x) @ f64(w).T
+    ids = np.argsort(-full, axis=1)[:, :k].astype(np.int32)
+    tx = np.take_along_axis(full, ids, axis=1).astype(np.float32)
+    ids[::3] = -1
+    ids[1::5, 2:] = -1
+    for target, call in ((dense_teacher(ids, tx, 1.0, V),
+                          lambda **kw: ssv.linear_topk_distill_fwd_bwd(x.to(DEV), w.to(DEV), torch.from_numpy(ids).to(DEV),
+                                                                       torch.from_numpy(tx).to(DEV), 1.0, **kw)),
+                         (dense_labels(np.where(np.arange(N) % 4 == 0, -100, y.numpy()), V, -100),
+                          lambda **kw: ssv.linear_cross_entropy_fwd_bwd(
+                              x.to(DEV), w.to(DEV), torch.where(torch.arange(N) % 4 == 0, -100, y).int().to(DEV), 1.0,
+                              **kw))):
+        o = call(row_weight=rw.to(DEV), reduction="sum", grad_dtype=F32)
+        torch.cuda.synchronize()
+        assert int(o.status) == 0
+        check_head(o, x, w, target, 1.0, rw.numpy(), "sum", 1.0, F32)
