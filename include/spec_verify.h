@@ -539,7 +539,8 @@ spec_status_t spec_linear_topk_distill_fwd_bwd(const void* hidden, const void* w
  * tokens and q_v (M - t_r / q_r) / T on the others.
  * loss_out [1], row_loss [N] or NULL: float32.  grad [N, V] of grad_dtype =
  * dtype or SPEC_F32.
- * Limits: N <= 2^30; V * elem_size up to about 3.5 MB (16 CTAs' shared memory).
+ * Limits: N <= 2^30; a row of at most 16 x 208 KiB (what 16 CTAs hold): V up to
+ * 1703936 16-bit or 851968 fp32 logits.
  */
 size_t spec_topk_distill_workspace_bytes(int N, int V, int k);
 

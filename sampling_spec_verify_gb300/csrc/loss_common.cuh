@@ -60,14 +60,6 @@ struct Elem;
 template <>
 struct Elem<__nv_bfloat16> {
   static constexpr int PV = 8;  // elements per 16-byte vector
-  __device__ static __forceinline__ void unpack(const uint4& w, float (&x)[8]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(u[i] << 16);
-      x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
-  }
   // The 8 values as 4 packed pairs in element order (exact widening).
   __device__ static __forceinline__ void pairs(const uint4& w, f32x2 (&p)[4]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -140,10 +132,6 @@ struct Elem<__half> {
 template <>
 struct Elem<float> {
   static constexpr int PV = 4;
-  __device__ static __forceinline__ void unpack(const uint4& w, float (&x)[4]) {
-    x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y);
-    x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
-  }
   __device__ static __forceinline__ void pairs(const uint4& w, f32x2 (&p)[2]) {
     p[0] = f2(__uint_as_float(w.x), __uint_as_float(w.y));
     p[1] = f2(__uint_as_float(w.z), __uint_as_float(w.w));
@@ -198,11 +186,6 @@ __device__ __forceinline__ F2 pair_add(F2 a, F2 b) {
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-__device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;

@@ -45,3 +45,11 @@ def test_least_sizes_refuse_what_the_calls_refuse(L):  # noqa: F811
     for V in (1, 255, 2048, 2049):  # a vocabulary of a piece or less has little to save
         for dt in (BF16, F16):
             assert f(dt, 5, V, 64, 1, 1, 1) <= L.spec_linear_loss_workspace_bytes(dt, 5, V, 64, 1, 1, 1)
+
+
+@pytest.mark.parametrize("bwd", [True, False])
+def test_longest_rows(L, bwd):  # noqa: F811
+    """The header's limit, on both sides: a row of 16 times 208 KiB and one vector more."""
+    for dt, V in ((BF16, 1703936), (F16, 1703936), (F32, 851968)):
+        assert kd(L, bwd=bwd, dt=dt, gdt=dt, V=V, ws=None) == INVALID  # only the workspace is missing
+        assert kd(L, bwd=bwd, dt=dt, gdt=dt, V=V + 8, ws=None) == UNSUPPORTED
