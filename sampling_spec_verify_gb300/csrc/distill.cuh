@@ -36,8 +36,12 @@ constexpr int kDMaxCluster = 16;
 // (us, 896 x 129280 bf16 with gradient; 1024 x 151936 loss alone): 10 vectors,
 // three and four CTAs an SM 104; 66.  19 vectors, two CTAs 91; 70.  The loss
 // alone takes the same slices as with its gradient, so that both give the same
-// bits.  Kernels exist for 4, 8, 13, 16 and 19: places beyond a slice hold -inf and are
-// worked on without a test (a branch per vector cost 10%).
+// bits.  Kernels exist for every third length, 4, 7, ... 19: places beyond a slice hold
+// -inf and are worked on without a test (a branch per vector cost 10%).  Against
+// kernels for every length (us, rows of 2e8 bf16 logits in all with gradient; loss
+// alone): slices of 17 vectors 149 in the kernel for 19, 149 in their own; 97, 95.
+// 14: 152, 149; 106, 103.  11: 162, 156; 114, 111.  8: 192, 186; 138, 133.  5: 258,
+// 245; 195, 182.  Rows of 2 vectors a thread (3300 tokens): 604, 555; 472, 333.
 constexpr int kDVecs = 19;
 
 struct DistillParams {

@@ -225,11 +225,14 @@ spec_status_t launch_distill(const ssv::DistillParams& P, cudaStream_t st) {
   if (!sh.S) return SPEC_ERR_UNSUPPORTED;
   if (!sh.regs) return launch_distill_nv<E, O, 0>(P, sh, d, dev, st);
   const int vecs = (int)(sh.cap / 16 + ssv::kDThreads - 1) / ssv::kDThreads;
-  if (vecs <= 4) return launch_distill_nv<E, O, 4>(P, sh, d, dev, st);
-  if (vecs <= 8) return launch_distill_nv<E, O, 8>(P, sh, d, dev, st);
-  if (vecs <= 13) return launch_distill_nv<E, O, 13>(P, sh, d, dev, st);
-  if (vecs <= 16) return launch_distill_nv<E, O, 16>(P, sh, d, dev, st);
-  return launch_distill_nv<E, O, ssv::kDVecs>(P, sh, d, dev, st);
+  switch (vecs <= 4 ? 0 : (vecs - 2) / 3) {  // the next of 4, 7, 10, ...
+    case 0: return launch_distill_nv<E, O, 4>(P, sh, d, dev, st);
+    case 1: return launch_distill_nv<E, O, 7>(P, sh, d, dev, st);
+    case 2: return launch_distill_nv<E, O, 10>(P, sh, d, dev, st);
+    case 3: return launch_distill_nv<E, O, 13>(P, sh, d, dev, st);
+    case 4: return launch_distill_nv<E, O, 16>(P, sh, d, dev, st);
+    default: return launch_distill_nv<E, O, ssv::kDVecs>(P, sh, d, dev, st);
+  }
 }
 
 spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int k, float temperature,

@@ -192,3 +192,21 @@ def test_head_lists_of_many_rows(ssv):  # noqa: F811
         torch.cuda.synchronize()
         assert int(o.status) == 0
         check_head(o, x, w, target, 1.0, rw.numpy(), "sum", 1.0, F32)
+
+
+@pytest.mark.parametrize("vecs", [1, 3, 4, 5, 7, 8, 10, 11, 13, 14, 16, 17, 19])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_distill_every_slice_length(ssv, vecs, dt):  # noqa: F811
+    """Rows of one CTA each whose threads hold 1 to 19 vectors, not all of them full."""
+    V = (vecs * 256 - 37) * (8 if dt == BF16 else 4) + 3
+    N, k = 160, 24
+    z, ids, x, lse, w = kd_inputs(N, V, k, dt, vecs, 1.0)
+    d = [t.to(DEV) for t in (z, ids, x, lse)]
+    o = ssv.topk_distill_fwd_bwd(*d[:3], 1.0, 3.0, teacher_lse=d[3], reduction="sum")
+    f = ssv.topk_distill(*d[:3], 1.0, teacher_lse=d[3], reduction="sum")
+    torch.cuda.synchronize()
+    assert torch.equal(o.row_loss, f.row_loss) and int(o.status) == 0
+    for rows in (slice(0, 20), slice(N - 20, N)):
+        r = listed_loss(f64(z[rows]), dense_teacher(ids[rows].numpy(), x[rows].numpy(), 1.0, V, f64(lse[rows])), 1.0,
+                        reduction="sum", grad_scale=3.0)
+        check_kd(o, r, 1.0, dt, rows=rows)
