@@ -741,6 +741,9 @@ def _linear_loss(what, hidden, weight, ids, logits, ignore_index, temperature, g
     if logits is None:
         k = 1
         _need(ids, "labels", dtype=torch.int32, shape=(N,), device=dev)
+        ignore_index = int(ignore_index)
+        if not -2 ** 31 <= ignore_index < 2 ** 31:
+            raise ValueError(f"ignore_index must be an int32 value, as the labels are, got {ignore_index}")
     else:
         _need(ids, "teacher_ids", dtype=torch.int32, device=dev)
         if ids.dim() != 2 or ids.shape[0] != N:
@@ -782,10 +785,10 @@ def _linear_loss(what, hidden, weight, ids, logits, ignore_index, temperature, g
         t, gs = float(temperature), float(grad_scale)
         if logits is None:
             if grads:
-                st = L.spec_linear_cross_entropy_fwd_bwd(*dims, t, gs, _at(ids), int(ignore_index), *rows,
+                st = L.spec_linear_cross_entropy_fwd_bwd(*dims, t, gs, _at(ids), ignore_index, *rows,
                                                          _at(out.grad_hidden), _at(out.grad_weight), gcode, *end)
             else:
-                st = L.spec_linear_cross_entropy(*dims, t, _at(ids), int(ignore_index), *rows, *end)
+                st = L.spec_linear_cross_entropy(*dims, t, _at(ids), ignore_index, *rows, *end)
         elif grads:
             st = L.spec_linear_topk_distill_fwd_bwd(*dims, k, t, gs, _at(ids), _at(logits), *rows,
                                                     _at(out.grad_hidden), _at(out.grad_weight), gcode, *end)

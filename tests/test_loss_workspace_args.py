@@ -1,5 +1,6 @@
-"""Workspaces that a training-loss call is given: what the kernels cannot write to is
-refused before the library is called (CPU; the tensors only claim to be on a GPU)."""
+"""Arguments of the training losses that the binding looks at before the library is
+called: workspaces that the kernels cannot write to, values that an int32 cannot hold
+(CPU; the tensors only claim to be on a GPU)."""
 
 import pytest
 import torch
@@ -23,12 +24,17 @@ def gpu(*shape, dtype=torch.float32):
 
 class Library:
     def __init__(self):
-        self.sizes = []
+        self.sizes, self.args = [], None
 
     def __getattr__(self, name):
         if name.endswith("workspace_bytes"):
             return lambda *a: 4096
-        return lambda *a: self.sizes.append(a[-2]) or 0
+
+        def call(*a):
+            self.sizes.append(a[-2])
+            self.args = a
+            return 0
+        return call
 
 
 @pytest.fixture
@@ -69,3 +75,18 @@ def test_workspaces(library, which):
     with pytest.raises(TypeError):
         calls(12345678)[which]()
     assert library.sizes == [5000, 8400]
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+def test_ignore_index(library, bwd):
+    """An index that 32 bits would cut to another label is refused."""
+    x, w, y = gpu(4, 8, dtype=torch.bfloat16), gpu(9, 8, dtype=torch.bfloat16), gpu(4, dtype=torch.int32)
+    out = ssv.LinearLossOutput(gpu(1), gpu(4), gpu(4), gpu(4, 8, dtype=torch.bfloat16) if bwd else None,
+                               gpu(9, 8, dtype=torch.bfloat16) if bwd else None, gpu(1, dtype=torch.int32))
+    call = ssv.linear_cross_entropy_fwd_bwd if bwd else ssv.linear_cross_entropy
+    for i in (-100, 0, 2 ** 31 - 1, -2 ** 31, torch.tensor(-7)):
+        call(x, w, y, ignore_index=i, out=out, workspace=gpu(5000))
+        assert int(i) in library.args
+    for i in (2 ** 31, -2 ** 31 - 1, 2 ** 32, 3 * 2 ** 40):
+        with pytest.raises(ValueError, match="ignore_index"):
+            call(x, w, y, ignore_index=i, out=out, workspace=gpu(5000))
