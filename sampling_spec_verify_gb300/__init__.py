@@ -647,7 +647,8 @@ def _loss_buffers(device, handle, given, nbytes, workspace, empties):
             else:
                 block = _STATUS.get(key)
                 if not block:
-                    block = list(torch.zeros((_STATUS_WORDS, 1), dtype=torch.int32, device=device).unbind())
+                    with torch.inference_mode(False):  # later calls may not be in it, and own their words too
+                        block = list(torch.zeros((_STATUS_WORDS, 1), dtype=torch.int32, device=device).unbind())
                     _STATUS[key] = block
                 status = block.pop()
         if workspace is None:

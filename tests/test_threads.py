@@ -1,4 +1,5 @@
-"""Host threads that call on one stream: no two calls share a cached workspace (CPU).
+"""What the binding caches for a stream: host threads that call on it do not share a
+workspace, workspaces can be given up, status words outlive inference mode (CPU).
 
 The library is replaced by one that takes its time, as the launches of a call do, and
 notes which workspaces are in use; the tensors are never looked at."""
@@ -110,3 +111,13 @@ def test_cached_workspaces_can_be_released(slow):
     loss()
     assert len(ssv._SCRATCH) == 1 and slow.calls == 2
     ssv.release_workspaces()
+
+
+def test_status_words_of_a_block_made_in_inference_mode(slow):
+    """An evaluation call makes the block of status words, a training call's may be written to."""
+    with torch.inference_mode():
+        calls()[3]()
+    o = calls()[2]()
+    o.status.zero_()
+    o.status |= 1
+    assert not o.status.is_inference()
