@@ -454,7 +454,7 @@ typedef enum { SPEC_MEAN = 0, SPEC_SUM = 1 } spec_reduction_t;
  *            16-byte aligned, H a multiple of 8 (N <= 2^20, V < 2^24, H <= 2^16;
  *            SPEC_ERR_UNSUPPORTED beyond).  Products are exact and summed
  *            in fp32 by the tensor cores, 16 at a time: a logit is within about
- *            2.5e-6 of its size at H = 2048 (the label's and the listed tokens'
+ *            2.5e-6 of its size at H = 2048, growing with H (the label's and the listed tokens'
  *            logits come from the same sums, so that confident rows keep
  *            their digits).
  * labels     [N] int32; a row whose label is ignore_index is left out, and so

@@ -336,7 +336,9 @@ spec_status_t distill(const void* student, spec_dtype_t dtype, int N, int V, int
 
 // ---- losses through the head --------------------------------------------------------
 
-constexpr int kPairs = 76;                       // CTA pairs in flight, for the split rule
+// CTA pairs in flight on this GPU's 152 SMs, for the split rule.  A constant: the size
+// of a workspace, which the splits enter, is asked for without a device at hand.
+constexpr int kPairs = 76;
 // A batch whose probabilities fit kKeepBytes, a 64th of this GPU's memory (2 bytes
 // an entry for bf16; 6 for fp16, which keeps them in fp32 beside D), keeps them
 // between the passes; the others go in pieces of kPieceBytes and compute the logits

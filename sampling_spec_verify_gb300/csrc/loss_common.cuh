@@ -381,8 +381,11 @@ __global__ void __launch_bounds__(kTargetWarps * 32) targets_kernel(const Target
     RowTeacher r{shift.hi, shift.lo, 0.0f, 0.0f};
     if (ok) {
       r.sum = P.lse ? sum : 1.0f;
+      // The remainder is as exact as the sum of 32-bit terms, about 1e-7 absolute: two
+      // digits of one of 1e-5.  The inputs say no more: half a step of a float32
+      // normaliser near 15 moves it by 5e-7.  (64-bit exponentials cost 16 us a
+      // launch instead of 5.)  Below 1e-6 it is the rounding of the sum, not mass.
       const float rest = 1.0f - sum;
-      // a remainder below 1e-6 is the rounding of the sum, not mass
       if (P.lse && rest > 1e-6f) r.rest = rest;
     }
     P.row[n] = r;
@@ -422,7 +425,8 @@ struct RowLog {
 };
 
 // log z of a normal z > 0 within 2^-25: the exponent's part is exact in the high word,
-// the mantissa's logarithm is below 0.41.
+// the mantissa's logarithm is below 0.41.  (The exponent's ln 2 is split in two words, the
+// first short enough that its product is exact: the reduction of Cody and Waite.)
 __device__ __forceinline__ F2 log_pair(float z) {
   int e;
   float f = frexpf(z, &e);  // [0.5, 1)
