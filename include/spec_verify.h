@@ -53,7 +53,7 @@ typedef enum {
   SPEC_ERR_CUDA = 3         /* the CUDA runtime reported an error */
 } spec_status_t;
 
-/* SPEC_F16: the drafter-training losses only. */
+/* SPEC_F16: the drafter-training losses, and keys and values. */
 typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype_t;
 
 /* Bits OR-ed into *dev_status by the kernels. */
@@ -63,6 +63,8 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype_t;
 #define SPEC_DEV_TIMEOUT 8u        /* a bounded wait inside a kernel gave up */
 #define SPEC_DEV_EMPTY_RESIDUAL 16u /* rejection with zero residual mass: drawn from p */
 #define SPEC_DEV_BAD_OFFSETS 32u   /* ragged row offsets rejected (nothing computed), or a tree parent outside [-1, i) */
+#define SPEC_DEV_BAD_PAGE 64u      /* a page or slot outside the cache */
+#define SPEC_DEV_NO_PAGES 128u     /* too few free pages for the tokens that a step commits */
 
 /* Version of this ABI (bumped on any signature change). */
 int spec_abi_version(void);
@@ -555,6 +557,171 @@ spec_status_t spec_topk_distill_fwd_bwd(const void* student, spec_dtype_t dtype,
                                         const float* row_weight, spec_reduction_t reduction, float* loss_out,
                                         float* row_loss, void* grad, spec_dtype_t grad_dtype, uint32_t* dev_status,
                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* One decoding step around the verify: attention over a paged cache, the
+ * cache's tables, and the sampling rules on the logits.
+ *
+ * A pass holds, for every request b, T_b rows: row 0 is the last committed
+ * token, the others are drafted tokens (a chain, or a tree's nodes), as the
+ * target slots of spec_verify, spec_verify_ragged and spec_tree_verify_greedy
+ * follow them.  Rows are laid out [B, T, ...] (row_offsets NULL, T_b = T) or
+ * flattened with row_offsets [B + 1] int32 (request b owns the rows
+ * [row_offsets[b], row_offsets[b + 1]), at most T of them).  A request whose
+ * offsets decrease, leave [0, rows] or hold more than T rows is left out
+ * (nothing of it is written) and sets SPEC_DEV_BAD_OFFSETS.  Rows that no
+ * request owns are left as they were.
+ * mask [B, T, T] uint8: row i sees row j of its pass iff mask[b][i][j] != 0
+ * (spec_tree_mask of the rows' parent map); NULL: a chain, i sees 0 .. i.
+ *
+ * The cache holds, page by page, the keys and values of committed tokens:
+ * token n of request b lies at place n % page_size of the page
+ * block_table[b][n / page_size]. */
+
+typedef struct {
+  const void* q;       /* [rows, Hq, D] dtype, strides below */
+  const void* k_new;   /* [rows, Hkv, D]: keys of the pass's own rows */
+  const void* v_new;   /* [rows, Hkv, D] */
+  const void* k_cache; /* [pages, page_size, Hkv, D] */
+  const void* v_cache; /* [pages, page_size, Hkv, D] */
+  void* out;           /* [rows, Hq, D] dtype, contiguous (written) */
+  float* lse;          /* [rows, Hq] contiguous (written) or NULL */
+  const int32_t* block_table;  /* [B, table_width], rows table_stride apart */
+  const int32_t* context_lens; /* [B]: cached tokens of each request */
+  const int32_t* row_offsets;  /* [B + 1] or NULL */
+  const uint8_t* mask;         /* [B, T, T] or NULL */
+  long long q_stride[2];       /* elements between rows, heads */
+  long long k_new_stride[2], v_new_stride[2];
+  long long k_stride[3], v_stride[3]; /* elements between pages, tokens, heads */
+  long long table_stride;
+  int B, T, rows, Hq, Hkv, D, pages, page_size, table_width;
+  spec_dtype_t dtype;  /* SPEC_BF16 or SPEC_F16 */
+  float scale;         /* of the scores, finite */
+} spec_attention_t;
+
+/* Attention of a pass's rows over the cache and the pass itself.
+ *
+ * "SpecOPD", section "树注意力(Tree Attention)": a node sees the committed
+ * prefix, itself and its ancestors, so that one target pass scores every node;
+ * "Speculative Decoding 与 MTP", section 2 (a chain); T = 1 is plain decoding.
+ * For row i of request b and head h, over the cached tokens n <
+ * context_lens[b] and the rows j that row i sees:
+ *   s = scale q . k,  out = sum exp(s) v / sum exp(s),  lse = log sum exp(s)
+ * with the keys and values of head h / (Hq / Hkv).  A row that sees nothing,
+ * or only scores of -inf, gets out = 0 and lse = -inf.  Keys and values that a
+ * row does not see do not enter it, whatever they hold.  Scores and sums are
+ * fp32; the weights exp(s - max) are rounded once to dtype for the product
+ * with v.
+ *
+ * Limits: D a multiple of 8, at most 256; Hq a multiple of Hkv; page_size a
+ * multiple of 8; T <= 1024; strides multiples of 8 and below 2^39; tensors on
+ * 16-byte boundaries.
+ * A context length outside [0, table_width * page_size] counts as the nearer
+ * bound and sets SPEC_DEV_BAD_OFFSETS.  A page outside [0, pages) reads as
+ * zeros and sets SPEC_DEV_BAD_PAGE.
+ * The workspace need not be zeroed, and is not left zero. */
+size_t spec_tree_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
+
+spec_status_t spec_tree_attention(const spec_attention_t* args, uint32_t* dev_status, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Tables of the cache for the tokens that a step commits.
+ *
+ * Request b holds ceil(context_lens[b] / page_size) pages, the first entries
+ * of its row of the block table.  new_lens[b] >= 0 tokens are appended to it,
+ * or its last -new_lens[b] are taken back (-context_lens[b]: the request is
+ * done).  free_pages[0 .. free_count) is a stack of unused pages.  First all
+ * pages that are given back are pushed, in the order of the requests and, in
+ * each, of its table; then the pages that are needed are popped in the same
+ * order.  From the first request on that finds too few pages left, requests
+ * that need pages are left as they were (their slots -1, their length
+ * unchanged) and SPEC_DEV_NO_PAGES is set.
+ *
+ * context_lens, new_lens [B] int32; block_table [B, table_width] int32;
+ * free_pages [capacity] int32; free_count [1] int32.
+ * out_table, out_free: as block_table and free_pages, and may be them (in
+ *   place); they may not overlap them otherwise.  Entries of the table behind
+ *   a request's pages, and of the stack above its new count, keep what they
+ *   held: the pages given back were pushed before any was popped.
+ * out_count [1], out_lens [B] int32 (written): the new count and lengths; not
+ *   the inputs.
+ * slots [B, T] int32 (written): page * page_size + place of the appended
+ *   tokens, then -1.
+ * A request with context_lens or the new length outside [0, table_width *
+ * page_size], or with new_lens > T, is left as it was and sets
+ * SPEC_DEV_BAD_OFFSETS.  A free_count outside [0, capacity], or pages given
+ * back beyond the capacity, leave every request as it was and set that bit. */
+spec_status_t spec_plan_cache(const int32_t* context_lens, const int32_t* new_lens, const int32_t* block_table,
+                              const int32_t* free_pages, const int32_t* free_count, int B, int T, int table_width,
+                              int capacity, int page_size, int32_t* out_table, int32_t* out_free, int32_t* out_count,
+                              int32_t* out_lens, int32_t* slots, uint32_t* dev_status, void* stream);
+
+typedef struct {
+  const void* k_new;    /* [layers, rows, Hkv, D], strides below */
+  const void* v_new;
+  void* k_cache;        /* [layers, pages, page_size, Hkv, D] (written) */
+  void* v_cache;
+  const int32_t* slots; /* [B, S]: spec_plan_cache's; -1: none */
+  const int32_t* path;  /* [B, S - 1], rows path_stride apart: accepted nodes, or NULL */
+  const int32_t* row_offsets;                   /* [B + 1] or NULL */
+  long long k_new_stride[3], v_new_stride[3];   /* elements between layers, rows, heads */
+  long long k_stride[4], v_stride[4];           /* elements between layers, pages, tokens, heads */
+  long long path_stride;
+  int layers, B, T, rows, S, Hkv, D, pages, page_size;
+  spec_dtype_t dtype;   /* SPEC_BF16 or SPEC_F16 */
+} spec_commit_t;
+
+/* Copies the keys and values of the committed rows of a pass into the cache,
+ * all layers at once ("Speculative Decoding 与 MTP", section 11: a tree commits
+ * a single path).  Place i of request b takes row 0 for i = 0, then row i
+ * (path NULL) or path[b][i - 1] + 1 (spec_tree_verify_greedy's path, whose
+ * node n is the pass's row n + 1).  Slots below 0 take nothing.  A slot beyond
+ * the cache sets SPEC_DEV_BAD_PAGE, a node below 0 or a row that the request does
+ * not have SPEC_DEV_BAD_OFFSETS; neither writes anything.  Slots have to be distinct:
+ * of one that occurs twice, what its token holds afterwards may come from
+ * either row.
+ * Limits: D a multiple of 8; strides multiples of 8; tensors on 16-byte boundaries;
+ * pages * page_size below 2^31. */
+spec_status_t spec_commit_cache(const spec_commit_t* args, uint32_t* dev_status, void* stream);
+
+typedef struct {
+  const void* logits;          /* [rows, V] dtype, contiguous */
+  void* out;                   /* as logits (written); may be logits */
+  const int32_t* tokens;       /* [rows]: the pass's row tokens; -1: not counted */
+  const int32_t* history;      /* [B, history_width]: tokens before the pass */
+  const int32_t* history_lens; /* [B] */
+  const int32_t* prompt_lens;  /* [B] or NULL (0): the history's first tokens that were given, not generated */
+  const float* repetition;     /* [B] or NULL (1) */
+  const float* frequency;      /* [B] or NULL (0) */
+  const float* presence;       /* [B] or NULL (0) */
+  const int32_t* bias_ids;     /* [B, biases]; -1: none */
+  const float* bias;           /* [B, biases] */
+  const uint32_t* allowed;     /* [rows, ceil(V / 32)] or NULL: bit v % 32 of word v / 32 */
+  const int32_t* row_offsets;  /* [B + 1] or NULL */
+  const uint8_t* mask;         /* [B, T, T] or NULL */
+  int B, T, rows, V, history_width, biases;
+  spec_dtype_t dtype;          /* SPEC_F32 or SPEC_BF16 */
+} spec_adjust_t;
+
+/* Sampling rules on the logits of a pass, before spec_truncate_logits and the
+ * verify; apply them to the target and the draft logits alike
+ * ("Speculative Decoding 与 MTP", sections 4 and 23: p and q after the same
+ * transforms, and a mask that only one side applies breaks correctness).
+ *
+ * For token v at row i of request b, c(v) counts v in the history behind the
+ * prompt and among the tokens of the rows that row i sees (itself included):
+ *   z  = z > 0 ? z / repetition : z * repetition   where c(v) > 0 or the prompt holds v
+ *   z -= frequency * c(v) + presence               where c(v) > 0 (two subtractions, in this order)
+ *   z += the sum of the biases listed for v, added up in their order
+ *   z  = -inf                                      where v is not allowed
+ * in fp32, rounded once to dtype.  Untouched logits are copied bit by bit.
+ * Tokens, history and bias ids outside [0, V) count for nothing and set
+ * SPEC_DEV_BAD_TOKEN (-1 as a row's token or a bias id does not); history or
+ * prompt lengths beyond the history count as the nearer bound and set
+ * SPEC_DEV_BAD_OFFSETS.  Rows that nothing is allowed for become -inf
+ * throughout.
+ * Limits: T <= 1024, biases <= 1024, history_width <= 1000000, V <= 2^24. */
+spec_status_t spec_adjust_logits(const spec_adjust_t* args, uint32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Failure-path self-test of the bounded wait.

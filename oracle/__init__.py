@@ -8,3 +8,4 @@ it has no CPU fallback.
 from .spec_oracle import *  # noqa: F401,F403
 from .spec_oracle import NEAR_TIE  # noqa: F401
 from .loss_oracle import dense_labels, dense_teacher, head_loss, listed_loss  # noqa: F401
+from . import decode_oracle as decode  # noqa: F401

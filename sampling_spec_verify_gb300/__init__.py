@@ -31,7 +31,12 @@ Entry points (same names as the C ABI, see include/spec_verify.h):
 * ``topk_distill``, ``topk_distill_fwd_bwd`` -- distillation of draft logits
                          from a teacher's top logits, and its gradient;
 * ``linear_topk_distill``, ``linear_topk_distill_fwd_bwd`` -- the same from
-                         hidden states, through the head.
+                         hidden states, through the head;
+* ``tree_attention``  -- attention of a pass's rows (a chain, a tree, one token)
+                         over a paged cache and the pass's own keys;
+* ``plan_cache``      -- block tables, free pages and slots from request lengths;
+* ``commit_cache``    -- keys and values of committed rows into their slots;
+* ``adjust_logits``   -- penalties for repeated tokens, biases and grammar masks.
 """
 
 from __future__ import annotations
@@ -51,7 +56,9 @@ __all__ = [
     "linear_topk_distill_fwd_bwd", "selftest_bounded_wait", "launch_shape", "kernel_launches", "set_kernel_override",
     "set_launch_override", "VerifyOutput", "OverlapOutput", "E2EOutput", "DiagOutput", "TreeOutput", "HostVerifier",
     "LinearLossOutput", "DistillOutput",
+    "tree_attention", "plan_cache", "commit_cache", "adjust_logits", "AttentionOutput", "CachePlan",
     "DEV_BAD_TOKEN", "DEV_BAD_LOGITS", "DEV_BAD_UNIFORM", "DEV_TIMEOUT", "DEV_EMPTY_RESIDUAL", "DEV_BAD_OFFSETS",
+    "DEV_BAD_PAGE", "DEV_NO_PAGES",
     "SPEC_OK", "SPEC_ERR_INVALID_ARG", "SPEC_ERR_UNSUPPORTED", "SPEC_ERR_CUDA",
 ]
 
@@ -62,7 +69,7 @@ SPEC_OK, SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA = 0, 1, 2, 3
 SPEC_F32, SPEC_BF16, SPEC_F16 = 0, 1, 2
 SPEC_MEAN, SPEC_SUM = 0, 1
 DEV_BAD_TOKEN, DEV_BAD_LOGITS, DEV_BAD_UNIFORM, DEV_TIMEOUT, DEV_EMPTY_RESIDUAL = 1, 2, 4, 8, 16
-DEV_BAD_OFFSETS = 32
+DEV_BAD_OFFSETS, DEV_BAD_PAGE, DEV_NO_PAGES = 32, 64, 128
 
 _lib = None
 
@@ -153,6 +160,16 @@ def lib():
     L.spec_topk_distill_fwd_bwd.restype = i32
     L.spec_topk_distill_fwd_bwd.argtypes = [vp, i32, i32, i32, i32, f32, f32, vp, vp, vp, vp, i32, vp, vp, vp,
                                             i32] + tail
+    L.spec_tree_attention_workspace_bytes.restype = sz
+    L.spec_tree_attention_workspace_bytes.argtypes = [i32] * 5
+    L.spec_tree_attention.restype = i32
+    L.spec_tree_attention.argtypes = [vp, vp, vp, sz, vp]
+    L.spec_plan_cache.restype = i32
+    L.spec_plan_cache.argtypes = [vp] * 5 + [i32] * 5 + [vp] * 7
+    L.spec_commit_cache.restype = i32
+    L.spec_commit_cache.argtypes = [vp, vp, vp]
+    L.spec_adjust_logits.restype = i32
+    L.spec_adjust_logits.argtypes = [vp, vp, vp]
     _lib = L
     return L
 
@@ -957,6 +974,342 @@ def topk_distill_fwd_bwd(student: torch.Tensor, teacher_ids: torch.Tensor, teach
     dtype)."""
     return _distill("spec_topk_distill_fwd_bwd", student, teacher_ids, teacher_logits, teacher_lse, temperature,
                     grad_scale, row_weight, reduction, True, grad_dtype, out, workspace, stream)
+
+
+# ---------------------------------------------------------------------------
+# a decoding step around the verify: attention, cache, sampling rules
+# ---------------------------------------------------------------------------
+
+def _need_strided(t: torch.Tensor, name: str, dtype=None, dims=None, device=None):
+    """Like ``_need`` for tensors whose rows may lie apart: the last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if dims is not None and t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def _strides(t: torch.Tensor):
+    """Strides of all dimensions but the last; one of size 1 is never stepped along."""
+    return [s if n > 1 else t.shape[-1] for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+
+
+def _need_pass(t: torch.Tensor, name: str, dtype, shape, ragged: bool, lead: int, device):
+    """Strides of a pass's rows [*, B, T, heads, D] (``lead`` dimensions before them) or,
+    ragged, [*, rows, heads, D]: (lead..., row, head)."""
+    _need_strided(t, name, dtype=dtype, dims=len(shape), device=device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    s = _strides(t)
+    if ragged:
+        return s
+    B, T = t.shape[lead:lead + 2]
+    if B > 1 and T > 1 and s[lead] != T * s[lead + 1]:
+        raise ValueError(f"the rows of {name} must be evenly spaced over requests")
+    return s[:lead] + [s[lead + 1] if T > 1 else s[lead]] + s[lead + 2:]
+
+
+def _pass_shape(B_offsets: Optional[torch.Tensor], max_rows: Optional[int], lead_shape, name: str, device):
+    """(B, T, rows) of a pass, from [B, T] or from row offsets and the most rows of a request."""
+    if B_offsets is None:
+        if max_rows is not None:
+            raise ValueError("max_rows goes with row_offsets")
+        B, T = lead_shape
+        return (B, T, B * T) if B * T else (0, max(T, 1), 0)
+    _need(B_offsets, "row_offsets", dtype=torch.int32, device=device)
+    if B_offsets.dim() != 1 or B_offsets.numel() < 1:
+        raise ValueError("row_offsets must be [B + 1]")
+    if max_rows is None or int(max_rows) < 1:
+        raise ValueError(f"row_offsets of {name} need max_rows >= 1, the most rows of a request")
+    return B_offsets.numel() - 1, int(max_rows), lead_shape[0]
+
+
+def _need_mask(mask: Optional[torch.Tensor], B: int, T: int, device):
+    if mask is not None:
+        _need(mask, "mask", dtype=torch.uint8, device=device)
+        if mask.numel() != B * T * T or (B and tuple(mask.shape) != (B, T, T)):
+            raise ValueError(f"mask must be [{B}, {T}, {T}], got {tuple(mask.shape)}")
+
+
+class _Attention(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k_new", "v_new", "k_cache", "v_cache", "out", "lse", "block_table",
+                                                "context_lens", "row_offsets", "mask")]
+                + [(n, ctypes.c_longlong * k) for n, k in (("q_stride", 2), ("k_new_stride", 2), ("v_new_stride", 2),
+                                                           ("k_stride", 3), ("v_stride", 3))]
+                + [("table_stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_int) for n in ("B", "T", "rows", "Hq", "Hkv", "D", "pages", "page_size", "table_width",
+                                               "dtype")]
+                + [("scale", ctypes.c_float)])
+
+
+class _Commit(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_new", "v_new", "k_cache", "v_cache", "slots", "path", "row_offsets")]
+                + [(n, ctypes.c_longlong * k) for n, k in (("k_new_stride", 3), ("v_new_stride", 3), ("k_stride", 4),
+                                                           ("v_stride", 4))]
+                + [("path_stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_int) for n in ("layers", "B", "T", "rows", "S", "Hkv", "D", "pages", "page_size",
+                                               "dtype")])
+
+
+class _Adjust(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("logits", "out", "tokens", "history", "history_lens", "prompt_lens",
+                                                "repetition", "frequency", "presence", "bias_ids", "bias", "allowed",
+                                                "row_offsets", "mask")]
+                + [(n, ctypes.c_int) for n in ("B", "T", "rows", "V", "history_width", "biases", "dtype")])
+
+
+def _longs(values):
+    return (ctypes.c_longlong * len(values))(*values)
+
+
+_KV_DTYPES = {torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+
+
+@dataclass
+class AttentionOutput:
+    out: torch.Tensor             # as q, contiguous
+    lse: Optional[torch.Tensor]   # float32, q's shape without the last dimension
+    status: torch.Tensor          # int32 [1] device status word
+
+
+def tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, block_table: torch.Tensor, context_lens: torch.Tensor, *,
+                   mask: Optional[torch.Tensor] = None, row_offsets: Optional[torch.Tensor] = None,
+                   max_rows: Optional[int] = None, scale: Optional[float] = None, want_lse: bool = False,
+                   out: Optional[AttentionOutput] = None, workspace: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> AttentionOutput:
+    """Attention of a pass's rows (a chain, a tree, or one token a request) over
+    a paged cache and the pass's own keys and values (see spec_tree_attention in
+    the C header).  q [B, T, Hq, D], k_new and v_new [B, T, Hkv, D] (bf16 or
+    fp16), or [rows, heads, D] with ``row_offsets`` int32 [B + 1] and
+    ``max_rows``; k_cache and v_cache [pages, page_size, Hkv, D]; block_table
+    int32 [B, width]; context_lens int32 [B]; mask uint8 [B, T, T] (``tree_mask``
+    of the rows' parent map; None: a chain).  ``scale`` is 1 / sqrt(D) unless
+    given.  Only the last dimension has to be contiguous; the others lie
+    multiples of 8 elements apart."""
+    L = lib()
+    ragged = row_offsets is not None
+    _need_strided(q, "q", dims=3 if ragged else 4)
+    if q.dtype not in _KV_DTYPES:
+        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
+    dev, dt = q.device, q.dtype
+    Hq, D = q.shape[-2:]
+    B, T, rows = _pass_shape(row_offsets, max_rows, q.shape[:-2], "q", dev)
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need_strided(t, name, dtype=dt, dims=4, device=dev)
+    pages, page, Hkv, _ = k_cache.shape
+    if k_cache.shape[3] != D or v_cache.shape != k_cache.shape:
+        raise ValueError(f"k_cache and v_cache must be [pages, page_size, Hkv, {D}], got {tuple(k_cache.shape)} "
+                         f"and {tuple(v_cache.shape)}")
+    q_stride = _need_pass(q, "q", dt, q.shape, ragged, 0, dev)
+    shape = (*q.shape[:-2], Hkv, D)
+    kn_stride = _need_pass(k_new, "k_new", dt, shape, ragged, 0, dev)
+    vn_stride = _need_pass(v_new, "v_new", dt, shape, ragged, 0, dev)
+    _need(context_lens, "context_lens", dtype=torch.int32, device=dev)
+    _need_strided(block_table, "block_table", dtype=torch.int32, dims=2, device=dev)
+    if (rows or ragged) and (tuple(context_lens.shape) != (B,) or block_table.shape[0] != B):
+        raise ValueError(f"context_lens and block_table must have {B} rows")
+    _need_mask(mask, B, T, dev)
+    empties = []
+    if out is None:
+        empties = [(tuple(q.shape), dt)] + [(tuple(q.shape[:-1]), torch.float32)] * want_lse
+    else:
+        _need(out.out, "out.out", dtype=dt, shape=q.shape, device=dev)
+        _need_out(out.lse, "lse", torch.float32, q.shape[:-1], dev)
+        _need_out(out.status, "status", torch.int32, (1,), dev)
+    if workspace is not None:
+        _need(workspace, "workspace", device=dev)
+    handle = _loss_stream(stream, dev)
+    need = L.spec_tree_attention_workspace_bytes(B, T, Hq, Hkv, D)
+    with _held(dev, handle):
+        status, ws, made = _loss_buffers(dev, handle, stream, need, workspace, empties)
+        if out is None:
+            out = AttentionOutput(made[0], made[1] if want_lse else None, status)
+        a = _Attention(_at(q), _at(k_new), _at(v_new), _at(k_cache), _at(v_cache), _at(out.out), _at(out.lse),
+                       _at(block_table), _at(context_lens), _at(row_offsets), _at(mask), _longs(q_stride),
+                       _longs(kn_stride), _longs(vn_stride), _longs(_strides(k_cache)), _longs(_strides(v_cache)),
+                       block_table.stride(0) if B > 1 else block_table.shape[1], B, T, rows, Hq, Hkv, D, pages, page,
+                       block_table.shape[1], _KV_DTYPES[dt], D ** -0.5 if scale is None else float(scale))
+        st = L.spec_tree_attention(ctypes.byref(a), _at(out.status), _at(ws), ws.nbytes, handle)
+    _check(st, "spec_tree_attention")
+    return out
+
+
+@dataclass
+class CachePlan:
+    block_table: torch.Tensor   # int32 [B, width]
+    free_pages: torch.Tensor    # int32 [capacity]
+    free_count: torch.Tensor    # int32 [1]
+    context_lens: torch.Tensor  # int32 [B]: lengths after the step
+    slots: torch.Tensor         # int32 [B, max_new]: places of the appended tokens, then -1
+    status: torch.Tensor        # int32 [1] device status word
+
+
+def plan_cache(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+               free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int, max_new: int, *,
+               out: Optional[CachePlan] = None, stream: Optional[torch.cuda.Stream] = None) -> CachePlan:
+    """Block tables, free pages and slots of the tokens that a step appends
+    (``new_lens`` int32 [B], e.g. n_accepted + 1; at most ``max_new``) or takes back
+    (negative; -context_lens: the request is done), from lengths alone and without
+    the host (see spec_plan_cache in the C header).  context_lens int32 [B],
+    block_table int32 [B, width], free_pages int32 [capacity] a stack of
+    free_count int32 [1] pages.  ``out.block_table`` and ``out.free_pages`` may
+    be the inputs (in place)."""
+    L = lib()
+    _need(block_table, "block_table", dtype=torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, width]")
+    B, width = block_table.shape
+    dev = block_table.device
+    T = int(max_new)
+    if T < 0:
+        raise ValueError(f"max_new must not be negative, got {T}")
+    _need(context_lens, "context_lens", dtype=torch.int32, shape=(B,), device=dev)
+    _need(new_lens, "new_lens", dtype=torch.int32, shape=(B,), device=dev)
+    _need(free_pages, "free_pages", dtype=torch.int32, device=dev)
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be [capacity]")
+    _need(free_count, "free_count", dtype=torch.int32, shape=(1,), device=dev)
+    shapes = [(B, width), tuple(free_pages.shape), (1,), (B,), (B, T)]
+    if out is not None:
+        for t, name, shape in zip((out.block_table, out.free_pages, out.free_count, out.context_lens, out.slots),
+                                  ("block_table", "free_pages", "free_count", "context_lens", "slots"), shapes):
+            _need(t, f"out.{name}", dtype=torch.int32, shape=shape, device=dev)
+        _need_out(out.status, "status", torch.int32, (1,), dev)
+    handle = _loss_stream(stream, dev)
+    with _held(dev, handle):
+        if out is None:
+            status, _, made = _loss_buffers(dev, handle, stream, 0, block_table, [(s, torch.int32) for s in shapes])
+            out = CachePlan(*made, status)
+        st = L.spec_plan_cache(_at(context_lens), _at(new_lens), _at(block_table), _at(free_pages), _at(free_count), B,
+                               T, width, free_pages.numel(), int(page_size), _at(out.block_table), _at(out.free_pages),
+                               _at(out.free_count), _at(out.context_lens), _at(out.slots), _at(out.status), handle)
+    _check(st, "spec_plan_cache")
+    return out
+
+
+def commit_cache(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 slots: torch.Tensor, *, path: Optional[torch.Tensor] = None,
+                 row_offsets: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Copies the keys and values of a pass's committed rows into the cache (see
+    spec_commit_cache in the C header): place i of a request, at ``slots`` int32
+    [B, S] (``plan_cache``'s), takes row i or, with ``path`` int32 [B, >= S - 1]
+    (``tree_verify_greedy``'s), row 0 and then the rows of the accepted nodes.
+    k_new and v_new [B, T, Hkv, D] or, with ``row_offsets`` int32 [B + 1], [rows,
+    Hkv, D]; k_cache and v_cache [pages, page_size, Hkv, D].  All of them may have
+    one more dimension in front, the model's layers.  ``status`` is an optional
+    int32 [1] device word."""
+    L = lib()
+    ragged = row_offsets is not None
+    _need_strided(k_cache, "k_cache")
+    dt, dev = k_cache.dtype, k_cache.device
+    if dt not in _KV_DTYPES:
+        raise TypeError(f"k_cache must be bfloat16 or float16, got {dt}")
+    if k_cache.dim() not in (4, 5):
+        raise ValueError("k_cache must be [pages, page_size, Hkv, D], or [layers, pages, page_size, Hkv, D]")
+    lead = k_cache.dim() - 4
+    _need_strided(v_cache, "v_cache", dtype=dt, dims=4 + lead, device=dev)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError(f"v_cache must have shape {tuple(k_cache.shape)}, got {tuple(v_cache.shape)}")
+    layers = k_cache.shape[0] if lead else 1
+    pages, page, Hkv, D = k_cache.shape[lead:]
+    _need_strided(k_new, "k_new", dtype=dt, dims=lead + (3 if ragged else 4), device=dev)
+    rows_shape = tuple(k_new.shape[lead:-2])
+    shape = (*k_cache.shape[:lead], *rows_shape, Hkv, D)
+    kn_stride = _need_pass(k_new, "k_new", dt, shape, ragged, lead, dev)
+    vn_stride = _need_pass(v_new, "v_new", dt, shape, ragged, lead, dev)
+    B, T, rows = _pass_shape(row_offsets, max(rows_shape[0], 1) if ragged else None, rows_shape, "k_new", dev)
+    _need(slots, "slots", dtype=torch.int32, device=dev)
+    if slots.dim() != 2 or ((rows or ragged) and slots.shape[0] != B):
+        raise ValueError(f"slots must be [{B}, S], got {tuple(slots.shape)}")
+    S = slots.shape[1]
+    if path is not None:
+        _need_strided(path, "path", dtype=torch.int32, dims=2, device=dev)
+        if path.shape[0] != slots.shape[0] or path.shape[1] < S - 1:
+            raise ValueError(f"path must be [{slots.shape[0]}, {max(S - 1, 0)}] or wider, got {tuple(path.shape)}")
+    if status is not None:
+        _need(status, "status", dtype=torch.int32, shape=(1,), device=dev)
+    handle = _loss_stream(stream, dev)
+    one = [] if lead else [D]  # the single layer's stride
+    a = _Commit(_at(k_new), _at(v_new), _at(k_cache), _at(v_cache), _at(slots), _at(path) if S > 1 else None,
+                _at(row_offsets), _longs(one + kn_stride), _longs(one + vn_stride), _longs(one + _strides(k_cache)),
+                _longs(one + _strides(v_cache)),
+                0 if path is None else path.stride(0) if path.shape[0] > 1 else path.shape[1],
+                layers, B, T, rows, S, Hkv, D, pages, page, _KV_DTYPES[dt])
+    _check(L.spec_commit_cache(ctypes.byref(a), _at(status), handle), "spec_commit_cache")
+
+
+def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor, history: torch.Tensor, history_lens: torch.Tensor, *,
+                  prompt_lens: Optional[torch.Tensor] = None, repetition: Optional[torch.Tensor] = None,
+                  frequency: Optional[torch.Tensor] = None, presence: Optional[torch.Tensor] = None,
+                  bias_ids: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  allowed: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                  row_offsets: Optional[torch.Tensor] = None, max_rows: Optional[int] = None,
+                  out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Penalties for repeated tokens, biases and grammar masks on a pass's logits
+    (see spec_adjust_logits in the C header), before ``truncate_logits`` and the
+    verify.  logits [B, T, V] (bf16 or fp32) follow the pass's rows, whose tokens
+    are ``tokens`` int32 [B, T]; or [rows, V] and [rows] with ``row_offsets`` int32
+    [B + 1] and ``max_rows``.  history int32 [B, width] holds history_lens int32
+    [B] tokens, the first prompt_lens of them the prompt's; repetition, frequency
+    and presence float32 [B]; bias_ids int32 [B, n] and bias float32 [B, n];
+    allowed int32 [B, T, ceil(V / 32)] bits; mask uint8 [B, T, T] (a tree; None: a
+    chain).  ``out`` may be ``logits`` (in place); ``status`` is an optional int32
+    [1] device word."""
+    L = lib()
+    ragged = row_offsets is not None
+    _need(logits, "logits")
+    if logits.dim() != (2 if ragged else 3):
+        raise ValueError("logits must be [B, T, V], or [rows, V] with row_offsets")
+    code = _dtype_code(logits)
+    dev, V = logits.device, logits.shape[-1]
+    at = tuple(logits.shape[:-1])
+    B, T, rows = _pass_shape(row_offsets, max_rows, at, "logits", dev)
+    n = B if rows or ragged else at[0]
+    _need(tokens, "tokens", dtype=torch.int32, shape=at, device=dev)
+    _need(history, "history", dtype=torch.int32, device=dev)
+    if history.dim() != 2 or history.shape[0] != n:
+        raise ValueError(f"history must be [{n}, width], got {tuple(history.shape)}")
+    _need(history_lens, "history_lens", dtype=torch.int32, shape=(n,), device=dev)
+    if prompt_lens is not None:
+        _need(prompt_lens, "prompt_lens", dtype=torch.int32, shape=(n,), device=dev)
+    for t, name in ((repetition, "repetition"), (frequency, "frequency"), (presence, "presence")):
+        if t is not None:
+            _need(t, name, dtype=torch.float32, shape=(n,), device=dev)
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias go together")
+    biases = 0
+    if bias is not None:
+        _need(bias_ids, "bias_ids", dtype=torch.int32, device=dev)
+        if bias_ids.dim() != 2 or bias_ids.shape[0] != n:
+            raise ValueError(f"bias_ids must be [{n}, entries], got {tuple(bias_ids.shape)}")
+        biases = bias_ids.shape[1]
+        _need(bias, "bias", dtype=torch.float32, shape=(n, biases), device=dev)
+    if allowed is not None:
+        _need(allowed, "allowed", dtype=torch.int32, shape=(*at, (V + 31) // 32), device=dev)
+    _need_mask(mask, B, T, dev)
+    if out is None:
+        with _Nothing() if stream is None else torch.cuda.stream(stream):
+            out = torch.empty_like(logits)
+    else:
+        _need(out, "out", dtype=logits.dtype, shape=logits.shape, device=dev)
+    if status is not None:
+        _need(status, "status", dtype=torch.int32, shape=(1,), device=dev)
+    handle = _loss_stream(stream, dev)
+    a = _Adjust(_at(logits), _at(out), _at(tokens), _at(history), _at(history_lens), _at(prompt_lens), _at(repetition),
+                _at(frequency), _at(presence), _at(bias_ids), _at(bias), _at(allowed), _at(row_offsets), _at(mask),
+                B, T, rows, V, history.shape[1], biases, code)
+    _check(L.spec_adjust_logits(ctypes.byref(a), _at(status), handle), "spec_adjust_logits")
+    return out
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,165 @@
+"""Rules on a pass's logits against the fp64 oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+from decode_cases import tree_masks
+from oracle import decode
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def ssv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import sampling_spec_verify_gb300 as m
+    m.lib()
+    return m
+
+
+def case(seed, rows, V, H, dtype, biases=0, grammar=False, tree=False, prompts=True, T=None, spare=0):
+    rng = np.random.default_rng(seed)
+    B, T, R = len(rows), T or max(rows), sum(rows) + spare
+    few = max(1, min(V, 40))  # repeats
+    tok = lambda *s: np.where(rng.uniform(size=s) < 0.5, rng.integers(0, few, size=s), rng.integers(0, V, size=s))  # noqa: E731
+    lens = rng.integers(0, H + 1, size=B)
+    c = dict(z=torch.from_numpy((2.5 * rng.normal(size=(R, V))).astype(np.float32)).to(dtype), tokens=tok(R),
+             history=tok(B, H), lens=lens, prompts=rng.integers(0, lens + 1) if prompts else None,
+             repetition=rng.uniform(0.8, 1.6, size=B).astype(np.float32),
+             frequency=rng.uniform(-0.1, 0.5, size=B).astype(np.float32),
+             presence=rng.uniform(-0.5, 1.0, size=B).astype(np.float32), bias_ids=None, bias=None, allowed=None,
+             mask=tree_masks(rng, B, T) if tree else None, offsets=np.concatenate([[0], np.cumsum(rows)]), T=T)
+    if biases:
+        c["bias_ids"] = np.where(rng.uniform(size=(B, biases)) < 0.2, -1, tok(B, biases))
+        c["bias"] = (3 * rng.normal(size=(B, biases))).astype(np.float32)
+    if grammar:
+        c["allowed"] = rng.integers(0, 2 ** 32, size=(R, -(-V // 32)), dtype=np.uint32)
+        c["allowed"][0] = 0  # nothing is allowed
+    return c
+
+
+def call(ssv, c, ragged, z=None, **kw):
+    B, T = len(c["lens"]), c["T"]
+    i32 = lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a).astype(np.int64).astype(np.uint32).view(np.int32) if a.dtype == np.uint32 else np.ascontiguousarray(a, dtype=np.int32)).to(DEV)  # noqa: E731
+    f32 = lambda a: None if a is None else torch.from_numpy(a).to(DEV)  # noqa: E731
+    z = c["z"].to(DEV) if z is None else z
+    fit = (lambda t: t) if ragged else (lambda t: None if t is None else t.view(B, T, *t.shape[1:]))
+    if ragged:
+        kw.update(row_offsets=i32(c["offsets"]), max_rows=T)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = ssv.adjust_logits(fit(z), fit(i32(c["tokens"])), i32(c["history"]), i32(c["lens"]),
+                            prompt_lens=i32(c["prompts"]), repetition=f32(c["repetition"]),
+                            frequency=f32(c["frequency"]), presence=f32(c["presence"]), bias_ids=i32(c["bias_ids"]),
+                            bias=f32(c["bias"]), allowed=fit(i32(c["allowed"])),
+                            mask=None if c["mask"] is None else torch.from_numpy(c["mask"]).to(DEV), status=st, **kw)
+    torch.cuda.synchronize()
+    return out.reshape(-1, out.shape[-1]), int(st.item())
+
+
+def want_of(c):
+    return decode.adjust_logits(c["z"].double().numpy(), c["tokens"], c["offsets"], c["mask"], c["history"], c["lens"],
+                                c["prompts"], c["repetition"], c["frequency"], c["presence"], c["bias_ids"], c["bias"],
+                                c["allowed"])
+
+
+def agree(c, got, dtype):
+    """At most eight fp32 roundings of values no larger than the sum of what enters, then one to dtype."""
+    want = want_of(c)
+    n = c["offsets"][-1]
+    got, want = got.double().cpu().numpy()[:n], want[:n]
+    scale = np.abs(c["z"].double().numpy()[:n]) * 2 + 2.0
+    if c["frequency"] is not None:
+        scale = scale + 0.5 * (c["history"].shape[1] + c["T"])
+    if c["bias"] is not None:
+        scale = scale + np.abs(c["bias"]).sum(axis=1).max()
+    fin = np.isfinite(want)
+    assert (got[~fin] == want[~fin]).all()
+    u = torch.finfo(dtype).eps / 2 if dtype != F else 0.0
+    assert (np.abs(got - want)[fin] <= (u * np.abs(want) + 8 * 2.0 ** -24 * scale)[fin]).all()
+
+
+@pytest.mark.parametrize("rows,V,H,dtype,biases,grammar,tree,ragged", [
+    ([1], 1, 1, F, 0, False, False, False), ([3], 31, 5, F, 4, True, False, False),
+    ([5], 1000, 700, BF, 0, False, False, False), ([2, 2], 4097, 300, BF, 20, True, True, False),
+    ([7, 1, 0, 4], 5003, 100, F, 8, True, True, True), ([9] * 3, 50257, 2000, BF, 64, True, True, False),
+    ([17] * 2, 50257, 2000, F, 64, True, True, False), ([8] * 20, 32000, 900, BF, 300, True, False, False),
+    ([4, 3], 151936, 4000, BF, 1024, True, False, True), ([2], 129280, 3, F, 0, True, False, False),
+    ([40], 777, 0, BF, 3, False, True, False)])
+def test_against_oracle(ssv, rows, V, H, dtype, biases, grammar, tree, ragged):
+    c = case(V + len(rows), rows, V, H, dtype, biases, grammar, tree, spare=2 if ragged else 0)
+    got, st = call(ssv, c, ragged)
+    agree(c, got, dtype)
+    assert st == 0
+    z = c["z"].to(DEV)  # in place
+    there, _ = call(ssv, c, ragged, z=z, out=z if ragged else z.view(len(rows), c["T"], V))
+    n = c["offsets"][-1]
+    assert torch.equal(there[:n], got[:n]) and there.data_ptr() == z.data_ptr()
+    assert torch.equal(z[n:].cpu(), c["z"][n:])  # rows of nobody
+
+
+def test_untouched_rows_are_copied_bit_by_bit(ssv):
+    c = case(1, [2], 4099, 0, BF, prompts=False)
+    c.update(tokens=np.array([-1, -1]), repetition=None, frequency=None, presence=None)
+    bits = torch.randint(-2 ** 15, 2 ** 15, (2, 4099), dtype=torch.int16, generator=torch.Generator().manual_seed(2))
+    got, st = call(ssv, c, False, z=bits.view(BF).to(DEV))
+    assert torch.equal(got.view(torch.int16).cpu(), bits) and st == 0
+
+
+def test_special_values(ssv):
+    low, inf, nan = torch.finfo(BF).min, float("inf"), float("nan")
+    c = case(3, [1], 64, 8, BF, prompts=False)
+    c["z"][0, :8] = torch.tensor([low, inf, -inf, nan, 0.0, -0.0, 1.0, low])
+    c.update(history=np.arange(8)[None], lens=np.array([7]), tokens=np.array([-1]))
+    c.update(repetition=np.array([2.0], dtype=np.float32), frequency=None, presence=None)
+    got, st = call(ssv, c, False)
+    assert st == 0
+    assert got[0, :8].tolist()[:3] == [-inf, inf, -inf] and bool(torch.isnan(got[0, 3]))
+    assert got[0, 4:8].tolist() == [0.0, 0.0, 0.5, torch.tensor(low).to(BF).item()]
+
+
+def test_what_is_outside_counts_for_nothing(ssv):
+    base = case(4, [3, 3], 500, 20, F, biases=6, prompts=True)
+    good, st = call(ssv, base, False)
+    assert st == 0
+    c = dict(base, history=np.concatenate([base["history"], np.full((2, 1), 3)], axis=1))
+    for key, at, value in (("history", (0, 0), 500), ("history", (0, 0), -1), ("tokens", (1,), 500),
+                           ("tokens", (1,), -2), ("bias_ids", (1, 2), 2 ** 31 - 1), ("bias_ids", (1, 2), -3)):
+        c = {k: v.copy() if isinstance(v, np.ndarray) else v for k, v in base.items()}
+        c["lens"][0], c["prompts"][0] = 20, 1
+        c[key][at] = value
+        got, st = call(ssv, c, False)
+        assert st == ssv.DEV_BAD_TOKEN
+        agree(c, got, F)
+    for lens, prompts in (([21, 4], [1, 2]), ([-1, 4], [0, 2]), ([5, 4], [6, 2]), ([5, 4], [-1, 2])):
+        c = dict(base, lens=np.array(lens), prompts=np.array(prompts))
+        got, st = call(ssv, c, False)
+        assert st == ssv.DEV_BAD_OFFSETS
+        agree(c, got, F)
+    c = dict(base, offsets=np.array([0, 4, 3]))
+    got, st = call(ssv, c, True, out=base["z"].to(DEV).clone().zero_())
+    assert st == ssv.DEV_BAD_OFFSETS and not got.any()
+
+
+def test_same_bits_in_a_graph_and_on_a_stream(ssv):
+    c = case(6, [4] * 8, 32000, 500, BF, 30, True, True)
+    want, _ = call(ssv, c, False)
+    s = torch.cuda.Stream()
+    got, _ = call(ssv, c, False, stream=s)
+    assert torch.equal(got, want)
+    z = c["z"].to(DEV).view(8, 4, 32000)
+    t = torch.from_numpy(c["tokens"].astype(np.int32)).to(DEV).view(8, 4)
+    h = torch.from_numpy(c["history"].astype(np.int32)).to(DEV)
+    n = torch.from_numpy(c["lens"].astype(np.int32)).to(DEV)
+    r = torch.from_numpy(c["repetition"]).to(DEV)
+    eager = ssv.adjust_logits(z, t, h, n, repetition=r)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o = ssv.adjust_logits(z, t, h, n, repetition=r)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, eager)

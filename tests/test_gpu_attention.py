@@ -1,0 +1,235 @@
+"""Attention over the paged cache against the fp64 oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+from decode_cases import attention_bounds, attention_case, attention_oracle, on_gpu
+
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def ssv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import sampling_spec_verify_gb300 as m
+    m.lib()
+    return m
+
+
+def check(ssv, c, dtype, **kw):
+    args, more = on_gpu(c)
+    o = ssv.tree_attention(*args, want_lse=True, **more, **kw)
+    torch.cuda.synchronize()
+    r = attention_oracle(c)
+    n = c["offsets"][-1]
+    got = o.out.reshape(-1, *o.out.shape[-2:]).double().cpu().numpy()[:n]
+    lse = o.lse.reshape(-1, o.lse.shape[-1]).double().cpu().numpy()[:n]
+    tol, tol_lse = attention_bounds(c, r, dtype)
+    off = np.abs(got - r.out[:n]) / tol[:n]
+    assert np.isfinite(got).all() and off.max(initial=0.0) <= 1.0, off.max()
+    same = np.where(np.isinf(r.lse[:n]), lse == r.lse[:n], np.abs(lse - r.lse[:n]) <= tol_lse[:n])
+    assert same.all()
+    assert int(o.status.item()) == 0
+    return o
+
+
+CASES = [
+    # rows, contexts, Hq, Hkv, D, page, dtype, options
+    ([1], [0], 1, 1, 64, 16, BF, {}),
+    ([1], [1], 4, 2, 128, 16, BF, {}),
+    ([1, 1, 1], [7, 128, 129], 8, 1, 128, 16, HF, {}),
+    ([5], [1000], 32, 8, 128, 16, BF, {}),
+    ([5, 5], [127, 300], 10, 2, 80, 24, HF, dict(tree=True)),
+    ([3, 3, 3], [64, 0, 63], 4, 4, 8, 8, BF, dict(tree=True)),
+    ([2, 2], [511, 1100], 6, 2, 256, 32, BF, dict(tree=True)),
+    ([2], [90], 2, 2, 248, 8, HF, {}),
+    ([33, 33], [700, 90], 8, 2, 128, 64, BF, dict(tree=True)),
+    ([65], [257], 8, 1, 64, 128, HF, dict(tree=True)),
+    ([40], [130], 16, 2, 128, 16, BF, {}),
+    ([150], [40], 2, 1, 64, 16, BF, dict(tree=True)),
+    ([300], [0], 3, 1, 72, 40, HF, {}),
+    ([1, 7, 3, 0, 5], [100, 0, 333, 50, 16], 6, 2, 128, 16, BF, dict(ragged=True, tree=True, spare_rows=3)),
+    ([0, 4, 0], [9, 700, 9], 4, 2, 96, 48, HF, dict(ragged=True, T=9, spare_rows=130)),
+    ([4, 4], [200, 500], 8, 2, 128, 16, BF, dict(layout="hnd")),
+    ([4, 4], [200, 500], 8, 2, 64, 16, HF, dict(layout="joint", strided=True, tree=True)),
+    ([9] * 40, list(range(0, 400, 10)), 4, 2, 64, 8, BF, dict(tree=True)),
+    ([2], [6000], 4, 1, 128, 160, BF, {}),
+    ([20, 20], [300, 170], 30, 2, 192, 16, BF, dict(tree=True)),
+    ([6], [400], 8, 2, 128, 16, HF, dict(spread=40.0)),  # one key takes nearly all of the weight
+]
+
+
+@pytest.mark.parametrize("rows,ctx,Hq,Hkv,D,page,dtype,more", CASES)
+def test_against_oracle(ssv, rows, ctx, Hq, Hkv, D, page, dtype, more):
+    check(ssv, attention_case(len(rows) * 1000 + ctx[0] + D, rows, ctx, Hq, Hkv, D, page, dtype, **more), dtype)
+
+
+def test_rows_that_see_nothing(ssv):
+    c = attention_case(3, [4, 4], [0, 20], 4, 2, 64, 16, BF, tree=True)
+    c["mask"][0, 1] = 0
+    c["mask"][1, 2] = 0  # sees the cache alone
+    o = check(ssv, c, BF)
+    assert not o.out[0, 1].any() and bool((o.lse[0, 1] == float("-inf")).all())
+
+
+def test_garbage_that_is_not_seen_does_not_enter(ssv):
+    c = attention_case(4, [6, 6], [40, 130], 4, 2, 128, 16, BF, tree=True)
+    c["mask"][:] = 0
+    for i in range(6):
+        c["mask"][:, i, 0] = 1
+        c["mask"][:, i, i] = 1
+    clean = {k: c[k].clone() for k in ("k_new", "v_new")}
+    want = check(ssv, c, BF)
+    for bad in (float("nan"), float("inf"), float("-inf"), torch.finfo(BF).min):
+        for k in ("k_new", "v_new"):
+            c[k] = clean[k].clone()
+            c[k].view(2, 6, 2, 128)[:, 3, :, 5:9] = bad
+        args, kw = on_gpu(c)
+        o = ssv.tree_attention(*args, want_lse=True, **kw)
+        torch.cuda.synchronize()
+        keep = [0, 1, 2, 4, 5]
+        assert torch.equal(o.out[:, keep], want.out[:, keep]) and torch.equal(o.lse[:, keep], want.lse[:, keep])
+    c["k_new"] = clean["k_new"]  # a value that is seen passes on
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        c["v_new"] = clean["v_new"].clone()
+        c["v_new"].view(2, 6, 2, 128)[:, 3, :, 5:9] = bad
+        args, kw = on_gpu(c)
+        o = ssv.tree_attention(*args, **kw)
+        torch.cuda.synchronize()
+        got = o.out[:, 3, :, 5:9].float()
+        assert bool(torch.isnan(got).all()) if bad != bad else bool((got == bad).all())
+        assert torch.equal(o.out[:, 3, :, 9:], want.out[:, 3, :, 9:])
+        assert torch.equal(o.out[:, keep], want.out[:, keep])
+
+
+def test_nan_query_stays_in_its_row(ssv):
+    c = attention_case(5, [3, 3], [50, 60], 4, 2, 64, 16, HF)
+    want = check(ssv, c, HF)
+    c["q"][4, 1, 7] = float("nan")
+    args, kw = on_gpu(c)
+    o = ssv.tree_attention(*args, **kw)
+    torch.cuda.synchronize()
+    nan = torch.isnan(o.out)
+    assert bool(nan[1, 1, 1].all()) and int(nan.sum()) == 64
+    assert torch.equal(o.out[~nan], want.out[~nan])
+
+
+def test_rows_of_nobody_stay(ssv):
+    c = attention_case(6, [2, 3], [30, 9], 4, 2, 64, 16, BF, ragged=True, T=4, spare_rows=5)
+    args, kw = on_gpu(c)
+    out = ssv.AttentionOutput(torch.full_like(args[0], 7.0), torch.full(args[0].shape[:2], 7.0, device="cuda"),
+                              torch.zeros(1, dtype=torch.int32, device="cuda"))
+    ssv.tree_attention(*args, out=out, want_lse=True, **kw)
+    torch.cuda.synchronize()
+    assert bool((out.out[5:] == 7).all()) and bool((out.lse[5:] == 7).all()) and not bool((out.out[:5] == 7).all())
+
+
+def test_bad_lengths_offsets_and_pages(ssv):
+    c = attention_case(7, [2, 2, 2], [30, 9, 40], 4, 2, 64, 16, BF, ragged=True, T=3)
+    good = check(ssv, c, BF)
+    args, kw = on_gpu(c)
+
+    def run(ctx=None, offsets=None, table=None):
+        a, k = list(args), dict(kw)
+        if ctx is not None:
+            a[6] = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+        if offsets is not None:
+            k["row_offsets"] = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+        if table is not None:
+            a[5] = torch.from_numpy(table).cuda()
+        out = ssv.AttentionOutput(torch.full_like(args[0], 7.0), None, torch.zeros(1, dtype=torch.int32, device="cuda"))
+        ssv.tree_attention(*a, out=out, **k)
+        torch.cuda.synchronize()
+        return out.out, int(out.status.item())
+
+    o, st = run(ctx=[30, -4, 40])  # counts as 0
+    o0, st0 = run(ctx=[30, 0, 40])
+    assert st == ssv.DEV_BAD_OFFSETS and st0 == 0 and torch.equal(o, o0)
+    _, st = run(ctx=[30, 10 ** 6, 40])
+    assert st & ssv.DEV_BAD_OFFSETS
+    for offsets in ([0, 2, 4, 7], [0, 2, 1, 6], [-1, 2, 4, 6], [0, 2, 6, 6]):
+        o, st = run(offsets=offsets)
+        assert st == ssv.DEV_BAD_OFFSETS
+        assert torch.equal(o[:2], good.out[:2]) or offsets[0] == -1
+    assert bool((run(offsets=[0, 2, 6, 6])[0][2:] == 7).all())
+    # pages outside the cache read as zeros
+    for page in (-1, -2 ** 31, 10 ** 9, int(args[3].shape[0])):
+        t = c["table"].copy()
+        t[2, 1] = page
+        o, st = run(table=t)
+        assert st == ssv.DEV_BAD_PAGE and torch.equal(o[:4], good.out[:4])
+        d = dict(c, table=t)
+        r = attention_oracle(d)
+        assert (np.abs(o[4:6].double().cpu().numpy() - r.out[4:6]) <= attention_bounds(d, r, BF)[0][4:6]).all()
+
+
+def test_no_cache_at_all(ssv):
+    c = attention_case(8, [3], [0], 2, 1, 64, 16, BF)
+    args, kw = on_gpu(c)
+    want = ssv.tree_attention(*args, **kw).out
+    args[3] = args[4] = torch.empty(0, 16, 1, 64, dtype=BF, device="cuda")
+    args[5] = torch.empty(1, 0, dtype=torch.int32, device="cuda")
+    assert torch.equal(ssv.tree_attention(*args, **kw).out, want)
+    e = ssv.tree_attention(args[0][:0], args[1][:0], args[2][:0], args[3], args[4], args[5][:0], args[6][:0])
+    assert e.out.shape[0] == 0
+
+
+def test_same_bits_again_on_a_stream_and_in_a_graph(ssv):
+    c = attention_case(9, [8, 8], [3000, 500], 8, 2, 128, 16, BF, tree=True)
+    args, kw = on_gpu(c)
+    first = ssv.tree_attention(*args, want_lse=True, **kw)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = ssv.tree_attention(*args, want_lse=True, stream=s, **kw)
+    s.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(ssv.tree_attention(*args, want_lse=True, **kw))
+        graphs.append(g)
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    for o in (other, *outs):
+        assert torch.equal(o.out, first.out) and torch.equal(o.lse, first.lse)
+    # other lengths in the same graph
+    args[6].copy_(torch.tensor([17, 2900], dtype=torch.int32))
+    args[5].copy_(args[5].flip(0))
+    want = ssv.tree_attention(*args, want_lse=True, **kw)
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0].out, want.out)
+
+
+def test_cache_beyond_32_bits(ssv):
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    page, Hkv, D = 64, 8, 128
+    pages = (5 << 30) // (page * Hkv * D)  # 5 Gi elements
+    c = attention_case(10, [4], [190], 8, Hkv, D, page, BF, poison=False)
+    args, kw = on_gpu(c)
+    want = ssv.tree_attention(*args, **kw)
+    kc, vc = (torch.empty(pages, page, Hkv, D, dtype=BF, device="cuda") for _ in range(2))
+    t = args[5].clone()
+    n = t[0, :3].long()
+    far = torch.tensor([pages - 1, pages // 2 + 1, pages - 7], device="cuda")
+    kc[far], vc[far] = args[3][n], args[4][n]
+    t[0, :3] = far.int()
+    o = ssv.tree_attention(*args[:3], kc, vc, t, args[6], **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(o.out, want.out)
+
+
+def test_given_scale(ssv):
+    c = attention_case(11, [3, 3], [100, 20], 4, 2, 64, 16, BF)
+    c["scale"] = 0.37
+    check(ssv, c, BF, scale=0.37)
+    c["scale"] = 0.0  # the mean of what is seen
+    check(ssv, c, BF, scale=0.0)
+    c["scale"] = -0.2
+    check(ssv, c, BF, scale=-0.2)
