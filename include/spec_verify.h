@@ -613,9 +613,10 @@ typedef struct {
  * fp32; the weights exp(s - max) are rounded once to dtype for the product
  * with v.
  *
- * Limits: D a multiple of 8, at most 256; Hq a multiple of Hkv; page_size a
- * multiple of 8; T <= 1024; strides multiples of 8 and below 2^39; tensors on
- * 16-byte boundaries.
+ * Limits: D a multiple of 8, at most 256; Hq a multiple of Hkv, at most 128
+ * times it; page_size a multiple of 8; T <= 1024; table_width * page_size below
+ * 2^31; strides multiples of 8 and below 2^39; tensors on 16-byte boundaries,
+ * the workspace on a 256-byte one.
  * A context length outside [0, table_width * page_size] counts as the nearer
  * bound and sets SPEC_DEV_BAD_OFFSETS.  A page outside [0, pages) reads as
  * zeros and sets SPEC_DEV_BAD_PAGE.

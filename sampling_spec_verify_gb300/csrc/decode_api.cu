@@ -5,9 +5,11 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "adjust.cuh"
 #include "attend.cuh"
@@ -51,13 +53,146 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// ---- attention ---------------------------------------------------------------------
+
+constexpr int kMaxPassRows = 1024;
+constexpr int kMaxCtas = 152;  // of the attention, one an SM
+
+struct AttendPlan {
+  int dp, mt, tok, slot_rows;
+  float* part;
+  float4* stat;
+  ssv::AttendSplit* split;
+  size_t bytes;
+};
+// Rows of 128 query rows and two such tiles a CTA where a request's pass may have
+// more of them (one tile: the cache would be read again for the second).  A head
+// beyond 128 fills the tensor memory with one tile.
+AttendPlan attend_plan(int T, int group, int D, void* base) {
+  AttendPlan p = {};
+  p.dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
+  p.tok = 128 / group;
+  p.mt = p.dp <= 128 && T > p.tok ? 2 : 1;
+  p.slot_rows = p.mt == 2 ? 256 : (T < p.tok ? T : p.tok) * group;
+  char* at = static_cast<char*>(base);
+  auto take = [&](size_t n) {
+    char* x = base ? at + p.bytes : nullptr;
+    p.bytes += (n + 255) & ~size_t(255);
+    return x;
+  };
+  const size_t slots = (size_t)2 * kMaxCtas * p.slot_rows;
+  p.part = reinterpret_cast<float*>(take(slots * p.dp * sizeof(float)));
+  p.stat = reinterpret_cast<float4*>(take(slots * sizeof(float4)));
+  p.split = reinterpret_cast<ssv::AttendSplit*>(take(kMaxCtas * sizeof(ssv::AttendSplit)));
+  return p;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static std::atomic<EncodeTiled> fn{nullptr};
+  EncodeTiled f = fn.load(std::memory_order_acquire);
+  if (f) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  f = reinterpret_cast<EncodeTiled>(p);
+  fn.store(f, std::memory_order_release);
+  return f;
+}
+
+// Boxes of 128 bytes (64 elements) along the first dimension, 128-byte swizzle; strides in elements.
+template <int N>
+bool make_map(CUtensorMap* m, const void* base, bool bf16, const long long (&size)[N], const long long (&stride)[N - 1],
+              const int (&box)[N - 1]) {
+  EncodeTiled enc = encode_tiled();
+  if (!enc) return false;
+  cuuint64_t dims[N], strides[N - 1];
+  cuuint32_t boxes[N], step[N];
+  for (int i = 0; i < N; ++i) {
+    dims[i] = (cuuint64_t)size[i];
+    boxes[i] = i ? (cuuint32_t)box[i - 1] : 64;
+    step[i] = 1;
+    if (i) strides[i - 1] = (cuuint64_t)stride[i - 1] * 2;
+  }
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, N, const_cast<void*>(base),
+             dims, strides, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class E, int DP, int MT>
+spec_status_t run_attend(const spec_attention_t& A, const AttendPlan& p, uint32_t* status, cudaStream_t st) {
+  using Sh = ssv::AttendShape<DP, MT>;
+  constexpr bool bf = std::is_same<E, __nv_bfloat16>::value;
+  int dev = 0;
+  const int sms = device_sms(&dev);
+  if (!sms) return SPEC_ERR_CUDA;
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t made[kMaxDevices];
+  std::call_once(once[dev], [dev]() {
+    made[dev] = cudaFuncSetAttribute(ssv::attend_kernel<E, DP, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  });
+  if (made[dev] != cudaSuccess) return SPEC_ERR_CUDA;
+  ssv::AttendLaunch L = {};
+  L.a = A;
+  L.status = status;
+  L.part = p.part;
+  L.stat = p.stat;
+  L.split = p.split;
+  L.c = A.scale == 0.0f ? 1.0f : (float)(1.4426950408889634 * std::fabs((double)A.scale));
+  L.flip = A.scale > 0.0f ? 1.0f : A.scale < 0.0f ? -1.0f : 0.0f;
+  L.group = A.Hq / A.Hkv;
+  L.tok = p.tok;
+  L.q_rows = A.T < p.tok ? A.T : p.tok;
+  L.slot_rows = p.slot_rows;
+  L.box = Sh::NK;
+  while (A.page_size % L.box) L.box /= 2;
+  if (!make_map<3>(&L.q, A.q, bf, {A.D, A.Hq, A.rows}, {A.q_stride[1], A.q_stride[0]}, {L.group, L.q_rows}) ||
+      !make_map<3>(&L.k_new, A.k_new, bf, {A.D, A.Hkv, A.rows}, {A.k_new_stride[1], A.k_new_stride[0]}, {1, 8}) ||
+      !make_map<3>(&L.v_new, A.v_new, bf, {A.D, A.Hkv, A.rows}, {A.v_new_stride[1], A.v_new_stride[0]}, {1, 8}))
+    return SPEC_ERR_CUDA;
+  // Without a cache no context has a page to read: the maps then cover the pass's own keys.
+  const bool cache = A.pages > 0;
+  const void *kc = cache ? A.k_cache : A.k_new, *vc = cache ? A.v_cache : A.v_new;
+  const long long pages = cache ? A.pages : 1, page = cache ? A.page_size : 1, heads = A.Hkv;
+  for (int i = 0; i < 2; ++i) {
+    const long long* s = i ? A.v_stride : A.k_stride;
+    const long long same[3] = {A.D, A.D, A.D};
+    if (!cache) s = same;
+    for (int small = 0; small < 2; ++small) {
+      CUtensorMap* m = i ? (small ? &L.v8 : &L.v) : (small ? &L.k8 : &L.k);
+      if (!make_map<4>(m, i ? vc : kc, bf, {A.D, page, heads, pages}, {s[1], s[2], s[0]}, {small ? 8 : L.box, 1, 1}))
+        return SPEC_ERR_CUDA;
+    }
+  }
+  const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+  ssv::attend_kernel<E, DP, MT><<<grid, Sh::kThreads, Sh::kSmem, st>>>(L);
+  if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)((MT * L.q_rows * L.group + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return from_cuda(count_launch(cudaLaunchKernelEx(&cfg, ssv::attend_join_kernel<E, DP, MT>, L)));
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t spec_tree_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
-  if (B < 0 || T < 1 || T > 1024 || Hkv < 1 || Hq < 1 || Hq % Hkv || D < 8 || D > 256 || D % 8) return 0;
-  return 256;
+  if (B < 0 || T < 1 || T > kMaxPassRows || Hkv < 1 || Hq < 1 || Hq % Hkv || D < 8 || D > 256 || D % 8 ||
+      Hq / Hkv > ssv::kAttendMaxGroup)
+    return 0;
+  return attend_plan(T, Hq / Hkv, D, nullptr).bytes;
 }
 
 spec_status_t spec_tree_attention(const spec_attention_t* args, uint32_t* dev_status, void* workspace,
@@ -68,7 +203,9 @@ spec_status_t spec_tree_attention(const spec_attention_t* args, uint32_t* dev_st
       A.page_size < 1 || A.table_width < 0 || (A.dtype != SPEC_BF16 && A.dtype != SPEC_F16) || !std::isfinite(A.scale))
     return SPEC_ERR_INVALID_ARG;
   if (!A.row_offsets && (long long)A.B * A.T != A.rows) return SPEC_ERR_INVALID_ARG;
-  if (A.D > 256 || A.D % 8 || A.page_size % 8 || A.T > 1024) return SPEC_ERR_UNSUPPORTED;
+  if (A.D > 256 || A.D % 8 || A.page_size % 8 || A.T > kMaxPassRows || A.Hq / A.Hkv > ssv::kAttendMaxGroup ||
+      (long long)A.table_width * A.page_size > 0x7FFFFFFFll)
+    return SPEC_ERR_UNSUPPORTED;
   if (A.B == 0 || A.rows == 0) return SPEC_OK;
   if (!A.q || !A.k_new || !A.v_new || !A.out || !A.context_lens) return SPEC_ERR_INVALID_ARG;
   if (A.table_width > 0 && (!A.block_table || A.table_stride < A.table_width)) return SPEC_ERR_INVALID_ARG;
@@ -80,15 +217,22 @@ spec_status_t spec_tree_attention(const spec_attention_t* args, uint32_t* dev_st
     return SPEC_ERR_INVALID_ARG;
   if (workspace_bytes < spec_tree_attention_workspace_bytes(A.B, A.T, A.Hq, A.Hkv, A.D) || !workspace)
     return SPEC_ERR_INVALID_ARG;
-  if (A.B > 65535 || A.Hq > 65535) return SPEC_ERR_UNSUPPORTED;
-  ssv::AttendParams P = {A, dev_status};
-  const dim3 grid((unsigned)((A.T + 3) / 4), (unsigned)A.B, (unsigned)A.Hq);
+  if (!aligned(workspace, 256)) return SPEC_ERR_INVALID_ARG;
+  const AttendPlan p = attend_plan(A.T, A.Hq / A.Hkv, A.D, workspace);
+  const bool bf = A.dtype == SPEC_BF16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (A.dtype == SPEC_BF16)
-    ssv::attend_plain_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(P);
-  else
-    ssv::attend_plain_kernel<__half><<<grid, 128, 0, st>>>(P);
-  return from_cuda(count_launch(cudaGetLastError()));
+#define SSV_ATTEND(DP, MT) \
+  return bf ? run_attend<__nv_bfloat16, DP, MT>(A, p, dev_status, st) : run_attend<__half, DP, MT>(A, p, dev_status, st)
+  if (p.dp == 64) {
+    if (p.mt == 1) SSV_ATTEND(64, 1);
+    SSV_ATTEND(64, 2);
+  }
+  if (p.dp == 128) {
+    if (p.mt == 1) SSV_ATTEND(128, 1);
+    SSV_ATTEND(128, 2);
+  }
+  SSV_ATTEND(256, 1);
+#undef SSV_ATTEND
 }
 
 spec_status_t spec_plan_cache(const int32_t* context_lens, const int32_t* new_lens, const int32_t* block_table,
