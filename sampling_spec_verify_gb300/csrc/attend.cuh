@@ -26,8 +26,8 @@
 // A CTA: warp 0 loads (keys and values through a ring of shared-memory tiles by
 // TMA, page by page; a page's part of a tile is a box of the tensor map),
 // warp 1 issues the products (scores into tensor memory, weights times values
-// with the weights read from tensor memory), four warps per 128 rows do the
-// softmax, a thread per row.
+// with the weights read from tensor memory), two warpgroups do the softmax, a
+// thread per row.
 #pragma once
 
 #include "loss_common.cuh"
@@ -38,22 +38,27 @@ namespace ssv {
 constexpr uint64_t kAttendWaitNs = 2000000000ull;
 constexpr int kAttendMaxGroup = 128;
 
-// DP: head size in shared memory.  MT: tiles of 128 rows that a CTA works on.
+// DP: head size in shared memory.  MT: tiles of 128 query rows that a CTA works
+// on.  GROUPS: warpgroups of the softmax.  Two groups take a row tile each, or
+// take turns over the tiles of keys of one row tile, with a result, maximum and sum
+// of their own that are joined at the end; a head beyond 128 leaves tensor
+// memory for one result only.
 template <int DP, int MT>
 struct AttendShape {
   static constexpr int NK = DP > 128 ? 64 : 128;      // keys a tile
+  static constexpr int GROUPS = DP > 128 ? 1 : 2;
+  static constexpr bool kTurns = MT == 1 && GROUPS == 2;
   static constexpr int CH = DP / 64;                  // 128-byte columns of a row
   static constexpr int kChunk = NK * 128;             // bytes of one column of a tile
   static constexpr int kTile = CH * kChunk;           // keys or values of a tile
   static constexpr int kQChunk = 128 * 128;
   static constexpr int kQ = MT * CH * kQChunk;
-  static constexpr int kRoom = 226 * 1024;
+  static constexpr int kRoom = 217 * 1024;
   static constexpr int kRing = (kRoom - kQ) / kTile > 12 ? 12 : (kRoom - kQ) / kTile;
   static constexpr int kSmem = kQ + kRing * kTile + 1024;
-  static constexpr int kThreads = 64 + 128 * MT;
-  static constexpr int kScores = 2;                   // buffers of scores: two of one row tile, or one each of two
+  static constexpr int kThreads = 64 + 128 * GROUPS;
   static constexpr int kOut = 256;                    // tensor-memory column of the results
-  static_assert(kScores * NK <= kOut && kOut + MT * DP <= 512, "tensor memory");
+  static_assert(2 * NK <= kOut && kOut + GROUPS * DP <= 512, "tensor memory");
   static_assert(kRing >= 4, "keys and values of two tiles");
 };
 
@@ -175,14 +180,31 @@ __device__ __forceinline__ bool not_finite16(uint32_t x) {  // one element
 
 // ---- the kernel --------------------------------------------------------------------
 
+// A value that is the same in all lanes, in a form that the compiler knows to be.
+__device__ __forceinline__ int same_in_warp(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool one_lane() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 template <class E, int DP, int MT>
-__global__ void __launch_bounds__(64 + 128 * MT, 1) attend_kernel(const __grid_constant__ AttendLaunch L) {
+__global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
+    attend_kernel(const __grid_constant__ AttendLaunch L) {
   using El = Elem<E>;
   using Sh = AttendShape<DP, MT>;
-  constexpr int NK = Sh::NK, CH = Sh::CH, R = Sh::kRing, kThreads = Sh::kThreads;
+  constexpr int NK = Sh::NK, CH = Sh::CH, R = Sh::kRing, kThreads = Sh::kThreads, GROUPS = Sh::GROUPS;
+  constexpr bool kTurns = Sh::kTurns;
   constexpr bool kBf16 = El::kLow == 0xFF80FF80u;
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t bars[2 * R + 16];
+  __shared__ float4 row_stat[2][GROUPS][128];  // kTurns: maximum and sums of a group's rows, two segments in turn
   __shared__ uint32_t tmem_slot;
   __shared__ long long warp_sum_of[kThreads / 32];
   __shared__ long long start_off;
@@ -190,16 +212,17 @@ __global__ void __launch_bounds__(64 + 128 * MT, 1) attend_kernel(const __grid_c
   __shared__ int not_finite[2];  // a value of the pass that is not finite was met: 1 + number of the segment
 
   const spec_attention_t& A = L.a;
-  const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, wid = same_in_warp(tid >> 5), lane = tid & 31;
   const uint32_t q0 = (smem_addr(raw) + 1023u) & ~1023u, ring0 = q0 + Sh::kQ;
   const uint32_t bar_full = smem_addr(bars), bar_empty = bar_full + 8 * R;
   const uint32_t bar_q = bar_empty + 8 * R, bar_q_free = bar_q + 8;
   const uint32_t bar_s = bar_q_free + 8;      // scores written, two buffers
   const uint32_t bar_p = bar_s + 16;          // weights written, two
-  const uint32_t bar_o = bar_p + 16;          // a product with the values done, per row tile
-  const uint32_t bar_o_free = bar_o + 16;     // the result read, per row tile
+  const uint32_t bar_o = bar_p + 16;          // a product with the values done, per result
+  const uint32_t bar_o_free = bar_o + 16;     // the result read, per result
   const uint32_t bar_fix = bar_o_free + 16;   // values of a last tile looked over, two in turn
-  const uint32_t bar_drain = bar_fix + 16;
+  const uint32_t bar_join = bar_fix + 16;     // kTurns: both groups' maxima and sums are there
+  const uint32_t bar_drain = bar_join + 8;
   const int tok_unit = L.tok * MT;
 
   if (tid == 0) {
@@ -213,10 +236,11 @@ __global__ void __launch_bounds__(64 + 128 * MT, 1) attend_kernel(const __grid_c
       mbar_init(bar_s + 8 * i, 1);
       mbar_init(bar_p + 8 * i, 4);
       mbar_init(bar_o + 8 * i, 1);
-      mbar_init(bar_o_free + 8 * i, 4);
+      mbar_init(bar_o_free + 8 * i, kTurns ? 8 : 4);
       mbar_init(bar_fix + 8 * i, 4);
       not_finite[i] = 0;
     }
+    mbar_init(bar_join, 8);
     mbar_init(bar_drain, 1);
     fence_mbar_init();
     prefetch_map(&L.q);
@@ -283,26 +307,28 @@ __global__ void __launch_bounds__(64 + 128 * MT, 1) attend_kernel(const __grid_c
   auto place_v = [](int i, int n) { return MT == 2 ? 2 * i + 1 : i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
 
   if (wid == 0) {
-    // ---- loads ----
+    // ---- loads: the warp as a whole, each copy by one lane ----
     uint32_t step = 0, seg = 0;
     uint32_t bad = 0;
     bool ok = true;
     for (; ok && w.next(A); ++seg) {
-      const int n = w.t1 - w.t0, kh = w.unit % A.Hkv, mg = w.unit / A.Hkv;
-      const int first_row = w.s.r0 + mg * tok_unit;  // of the pass
-      const int tiles_m = min(MT, (w.s.rows - mg * tok_unit + L.tok - 1) / L.tok);
+      const int t0 = same_in_warp(w.t0), n = same_in_warp(w.t1) - t0, unit = same_in_warp(w.unit);
+      const int kh = unit % A.Hkv, mg = unit / A.Hkv, full_tiles = same_in_warp(w.s.full);
+      const int first_row = same_in_warp(w.s.r0) + mg * tok_unit;  // of the pass
+      const int tiles_m = min(MT, (same_in_warp(w.s.rows) - mg * tok_unit + L.tok - 1) / L.tok);
       const int32_t* table = A.block_table + w.b * A.table_stride;
       for (int x = 0; ok && x < 2 * n; ++x, ++step) {
         if (x == (MT == 1 && n > 1 ? 2 : 1)) {  // q behind the first keys, which do not wait for the last segment
           if (seg > 0) ok = mbar_wait_bounded(bar_q_free, (seg - 1) & 1u, kAttendWaitNs);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (lane == 0) {
+          if (one_lane()) {
             mbar_arrive_expect_tx(bar_q, (uint32_t)(tiles_m * chunks * L.q_rows * L.group * 128));
             for (int m = 0; m < tiles_m; ++m)
               for (int ch = 0; ch < chunks; ++ch)
                 tma_load_3d(q0 + (m * CH + ch) * Sh::kQChunk, &L.q, ch * 64, kh * L.group, first_row + m * L.tok, bar_q);
           }
+          __syncwarp();
         }
         bool values;
         int i;
@@ -313,40 +339,59 @@ __global__ void __launch_bounds__(64 + 128 * MT, 1) attend_kernel(const __grid_c
           values = x == 2 * n - 1 || (x > 0 && !(x & 1));
           i = x == 2 * n - 1 ? n - 1 : values ? (x - 2) >> 1 : (x + 1) >> 1;
         }
-        const int t = w.t0 + i;
+        const int t = t0 + i;
         const uint32_t s = step % R, use = step / R, full = bar_full + 8 * s, dst = ring0 + s * Sh::kTile;
+        // a lane's box of the tile: its page and place
+        int cached = NK, at = 0, j0 = 0, fresh = 0, size = L.box;
+        if (t >= full_tiles) {
+          w.s.tail(t, cached, at, j0, fresh);
+          size = 8;
+        }
+        const int old = same_in_warp((cached + size - 1) / size), boxes = old + same_in_warp((fresh + 7) / 8);
+        int page = 0, place = 0;
+        if (lane < old) {
+          const int pos = t * NK + lane * size, p = pos / A.page_size;
+          page = __ldg(table + p);
+          place = pos - p * A.page_size;
+          if (page < 0 || page >= A.pages) page = A.pages, bad = SPEC_DEV_BAD_PAGE;  // behind the end: zeros
+        }
         if (use > 0) ok = mbar_wait_bounded(bar_empty + 8 * s, (use - 1) & 1u, kAttendWaitNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (t < w.s.full) {
-          if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(chunks * NK * 128));
+        if (t < full_tiles) {
+          if (one_lane()) mbar_arrive_expect_tx(full, (uint32_t)(chunks * NK * 128));
           __syncwarp();
           const CUtensorMap* map = values ? &L.v : &L.k;
-          const int copies = NK / L.box * chunks;
-          for (int y = lane; y < copies; y += 32) {
-            const int bx = y / chunks, ch = y - bx * chunks, pos = t * NK + bx * L.box, p = pos / A.page_size;
-            int page = __ldg(table + p);
-            if (page < 0 || page >= A.pages) page = A.pages, bad = SPEC_DEV_BAD_PAGE;  // behind the end: zeros
-            tma_load_4d(dst + ch * Sh::kChunk + bx * L.box * 128, map, ch * 64, pos - p * A.page_size, kh, page, full);
+#pragma unroll 1
+          for (int bx = 0; bx < old; ++bx) {
+            const int pg = __shfl_sync(0xffffffffu, page, bx), pl = __shfl_sync(0xffffffffu, place, bx);
+            if (one_lane()) {
+#pragma unroll
+              for (int ch = 0; ch < CH; ++ch)
+                if (ch < chunks) tma_load_4d(dst + ch * Sh::kChunk + bx * L.box * 128, map, ch * 64, pl, kh, pg, full);
+            }
+            __syncwarp();
           }
         } else {
-          int cached, at, j0, fresh;
-          w.s.tail(t, cached, at, j0, fresh);
-          const int old = (cached + 7) / 8, boxes = old + (fresh + 7) / 8;
-          if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(chunks * boxes * 8 * 128));
+          if (one_lane()) mbar_arrive_expect_tx(full, (uint32_t)(chunks * boxes * 8 * 128));
           __syncwarp();
-          for (int y = lane; y < boxes * chunks; y += 32) {
-            const int bx = y / chunks, ch = y - bx * chunks;
-            const uint32_t to = dst + ch * Sh::kChunk;
-            if (bx < old) {
-              const int pos = t * NK + bx * 8, p = pos / A.page_size;
-              int page = __ldg(table + p);
-              if (page < 0 || page >= A.pages) page = A.pages, bad = SPEC_DEV_BAD_PAGE;
-              tma_load_4d(to + bx * 1024, values ? &L.v8 : &L.k8, ch * 64, pos - p * A.page_size, kh, page, full);
-            } else {
-              const int j = (bx - old) * 8;
-              tma_load_3d(to + (at + j) * 128, values ? &L.v_new : &L.k_new, ch * 64, kh, w.s.r0 + j0 + j, full);
+          const CUtensorMap *map = values ? &L.v8 : &L.k8, *map_new = values ? &L.v_new : &L.k_new;
+          const int row_at = same_in_warp(w.s.r0 + j0), at_u = same_in_warp(at);
+#pragma unroll 1
+          for (int bx = 0; bx < boxes; ++bx) {
+            const int pg = __shfl_sync(0xffffffffu, page, bx & 31), pl = __shfl_sync(0xffffffffu, place, bx & 31);
+            if (one_lane()) {
+#pragma unroll
+              for (int ch = 0; ch < CH; ++ch) {
+                if (ch >= chunks) continue;
+                const uint32_t to = dst + ch * Sh::kChunk;
+                if (bx < old)
+                  tma_load_4d(to + bx * 1024, map, ch * 64, pl, kh, pg, full);
+                else
+                  tma_load_3d(to + at_u * 128 + (bx - old) * 1024, map_new, ch * 64, kh, row_at + (bx - old) * 8, full);
+              }
             }
+            __syncwarp();
           }
         }
       }
@@ -362,114 +407,130 @@ __global__ void __launch_bounds__(64 + 128 * MT, 1) attend_kernel(const __grid_c
       __syncwarp();
     }
   } else if (wid == 1) {
-    // ---- products: one thread ----
-    if (lane == 0) {
-      constexpr uint64_t desc_k = smem_desc_base(16, 1024), desc_v = smem_desc_base(Sh::kChunk, 1024);
-      const uint32_t idesc_s = mma_idesc_128(kBf16, NK, false);
-      const uint32_t idesc_o = mma_idesc_128(kBf16, (A.D + 15) & ~15, true);
-      const int ksteps = (A.D + 15) / 16;
-      uint32_t base = 0, seg = 0, fixes = 0, cnt[2] = {0, 0}, done[2] = {0, 0}, segs[2] = {0, 0};
-      bool ok = true;
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok) ok = mbar_wait_bounded(bar, parity & 1u, kAttendWaitNs);
-        return ok;
-      };
-      // All products with the values of row tile m are done, none of them skipped: the buffer
-      // of scores that held their weights may be written (only products into one accumulator
-      // keep their order by themselves).
-      auto settle = [&](int m) {
-        while (done[m] != cnt[m]) {
-          if (!wait(bar_o + 8 * m, done[m])) return false;
-          ++done[m];
-        }
-        return true;
-      };
-      // scores of a tile against row tile m, into buffer sb
-      auto scores = [&](uint32_t at, int m, int sb) {
-        const uint32_t k0 = ring0 + at % R * Sh::kTile;
-        for (int j = 0; j < ksteps; ++j)
-          mma_smem(tmem + sb * NK, smem_desc(desc_k, q0 + (m * CH + j / 4) * Sh::kQChunk + j % 4 * 32),
-                   smem_desc(desc_k, k0 + j / 4 * Sh::kChunk + j % 4 * 32), idesc_s, j > 0 ? 1u : 0u);
-        mma_commit(bar_s + 8 * sb);
-      };
-      auto weigh = [&](uint32_t at, int m, int sb, int keys, bool more) {
-        const uint32_t v0 = ring0 + at % R * Sh::kTile;
-        for (int j = 0; j * 16 < keys; ++j)
-          mma_tmem(tmem + Sh::kOut + m * DP, tmem + sb * NK + j * 8, smem_desc(desc_v, v0 + j * 2048), idesc_o,
-                   more || j > 0 ? 1u : 0u);
-        mma_commit(bar_o + 8 * m);
-      };
-      for (; ok && w.next(A); ++seg) {
-        const int n = w.t1 - w.t0, mg = w.unit / A.Hkv;
-        const int tiles_m = MT == 1 ? 1 : min(MT, (w.s.rows - mg * tok_unit + L.tok - 1) / L.tok);
-        auto full_at = [&](int place) { return wait(bar_full + 8 * ((base + place) % R), (base + place) / R); };
-        if (!full_at(place_k(0, n)) || !wait(bar_q, seg)) break;
-        for (int m = 0; ok && m < tiles_m; ++m) settle(m);
-        if (!ok) break;
-        tc_fence_after();
-        for (int m = 0; m < tiles_m; ++m) scores(base, m, MT == 1 ? cnt[0] & 1 : m);
-        mma_commit(bar_empty + 8 * (base % R));
-        if (n == 1) mma_commit(bar_q_free);
-        for (int i = 0; ok && i < n; ++i) {
-          const int t = w.t0 + i;
-          int keys = NK;
-          if (t >= w.s.full) {
-            int cached, at, j0, fresh;
-            w.s.tail(t, cached, at, j0, fresh);
-            keys = fresh > 0 ? at + fresh : cached;
-          }
-          const uint32_t next_k = base + (i + 1 < n ? place_k(i + 1, n) : 0), this_v = base + place_v(i, n);
-          if (MT == 1 && !settle(0)) break;
-          if (MT == 1 && i + 1 < n) {
-            if (!full_at(place_k(i + 1, n))) break;
-            tc_fence_after();
-            scores(next_k, 0, (cnt[0] + 1) & 1);
-            mma_commit(bar_empty + 8 * (next_k % R));
-            if (i + 2 == n) mma_commit(bar_q_free);
-          }
-          if (t >= w.s.full) {
-            if (!wait(bar_fix + 8 * (fixes & 1), fixes >> 1)) break;
-            ++fixes;
-          }
-          if (!full_at(place_v(i, n))) break;
+    // ---- products: the warp as a whole, each product by one lane ----
+    constexpr uint64_t desc_k = smem_desc_base(16, 1024), desc_v = smem_desc_base(Sh::kChunk, 1024);
+    const uint32_t idesc_s = mma_idesc_128(kBf16, NK, false);
+    const uint32_t idesc_o = mma_idesc_128(kBf16, (A.D + 15) & ~15, true);
+    const int ksteps = (A.D + 15) / 16;
+    // per result: products with the values issued, known to be done; segments
+    uint32_t base = 0, seg = 0, fixes[2] = {0, 0}, tiles = 0, cnt[2] = {0, 0}, done[2] = {0, 0}, segs[2] = {0, 0};
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, kAttendWaitNs));
+      return ok;
+    };
+    // All products of result g with the values are done, none of them skipped: the buffer of
+    // scores that held their weights may be written (only products into one accumulator
+    // keep their order by themselves).
+    auto settle = [&](int g) {
+      while (done[g] != cnt[g]) {
+        if (!wait(bar_o + 8 * g, done[g])) return false;
+        ++done[g];
+      }
+      return true;
+    };
+    // scores of a tile against row tile m, into buffer sb
+    auto scores = [&](uint32_t at, int m, int sb) {
+      const uint32_t k0 = ring0 + at % R * Sh::kTile, qm = q0 + m * CH * Sh::kQChunk, d = tmem + sb * NK;
+      if (one_lane()) {
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            if (m >= tiles_m) break;
-            const int sb = MT == 1 ? cnt[0] & 1 : m;
-            if (!wait(bar_p + 8 * sb, MT == 1 ? cnt[0] >> 1 : cnt[m])) break;
-            if (i == 0 && segs[m] > 0 && !wait(bar_o_free + 8 * m, segs[m] - 1)) break;
-            tc_fence_after();
-            weigh(this_v, m, sb, keys, i > 0);
-            ++cnt[m];
-            if (MT == 2 && i + 1 < n) {
-              if ((m == 0 && !full_at(place_k(i + 1, n))) || !settle(m)) break;
-              tc_fence_after();
-              scores(next_k, m, m);
-            }
-          }
-          if (!ok) break;
-          mma_commit(bar_empty + 8 * (this_v % R));
+        for (int j = 0; j < DP / 16; ++j)
+          if (j < ksteps)
+            mma_smem(d, smem_desc(desc_k, qm + j / 4 * Sh::kQChunk + j % 4 * 32),
+                     smem_desc(desc_k, k0 + j / 4 * Sh::kChunk + j % 4 * 32), idesc_s, j > 0 ? 1u : 0u);
+        mma_commit(bar_s + 8 * sb);
+      }
+      __syncwarp();
+    };
+    auto weigh = [&](uint32_t at, int g, int sb, int keys, bool more) {
+      const uint32_t v0 = ring0 + at % R * Sh::kTile, d = tmem + Sh::kOut + g * DP, p = tmem + sb * NK;
+      if (one_lane()) {
+#pragma unroll
+        for (int j = 0; j < NK / 16; ++j)
+          if (j * 16 < keys) mma_tmem(d, p + j * 8, smem_desc(desc_v, v0 + j * 2048), idesc_o, more || j > 0 ? 1u : 0u);
+        mma_commit(bar_o + 8 * g);
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint32_t bar) {
+      if (one_lane()) mma_commit(bar);
+      __syncwarp();
+    };
+    for (; ok && w.next(A); ++seg) {
+      const int t0 = same_in_warp(w.t0), n = same_in_warp(w.t1) - t0, mg = same_in_warp(w.unit) / A.Hkv;
+      const int full_tiles = same_in_warp(w.s.full);
+      const int tiles_m = MT == 1 ? 1 : min(MT, (same_in_warp(w.s.rows) - mg * tok_unit + L.tok - 1) / L.tok);
+      auto full_at = [&](int place) { return wait(bar_full + 8 * ((base + place) % R), (base + place) / R); };
+      if (!full_at(place_k(0, n)) || !wait(bar_q, seg)) break;
+      for (int g = 0; ok && g < GROUPS; ++g) settle(g);
+      if (!ok) break;
+      tc_fence_after();
+      // tiles counts those before this segment: buffers take turns where one group has two
+      for (int m = 0; m < tiles_m; ++m) scores(base, m, MT == 2 ? m : kTurns ? 0 : tiles & 1);
+      commit(bar_empty + 8 * (base % R));
+      if (n == 1) commit(bar_q_free);
+      for (int i = 0; ok && i < n; ++i, ++tiles) {
+        const int t = t0 + i;
+        int keys = NK;
+        if (t >= full_tiles) {
+          int cached, at, j0, fresh;
+          w.s.tail(t, cached, at, j0, fresh);
+          keys = same_in_warp(fresh > 0 ? at + fresh : cached);
+        }
+        const uint32_t next_k = base + (i + 1 < n ? place_k(i + 1, n) : 0), this_v = base + place_v(i, n);
+        const int fixer = kTurns ? i & 1 : 0;
+        if (MT == 1 && !settle(kTurns ? (i + 1) & 1 : 0)) break;
+        if (MT == 1 && i + 1 < n) {
+          if (!full_at(place_k(i + 1, n))) break;
+          tc_fence_after();
+          scores(next_k, 0, kTurns ? (i + 1) & 1 : (tiles + 1) & 1);
+          commit(bar_empty + 8 * (next_k % R));
+          if (i + 2 == n) commit(bar_q_free);
+        }
+        if (t >= full_tiles) {
+          const int fb = GROUPS == 1 ? fixes[0] & 1 : fixer;  // one group: two barriers in turn
+          if (!wait(bar_fix + 8 * fb, GROUPS == 1 ? fixes[0] >> 1 : fixes[fixer])) break;
+          ++fixes[fixer];
+        }
+        if (!full_at(place_v(i, n))) break;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (m >= tiles_m) break;
+          const int g = kTurns ? i & 1 : m, sb = GROUPS == 1 ? tiles & 1 : g;
+          if (!wait(bar_p + 8 * sb, GROUPS == 1 ? tiles >> 1 : cnt[g])) break;
+          if (i == 0 && segs[m] > 0 && !wait(bar_o_free + 8 * m, segs[m] - 1)) break;
+          tc_fence_after();
+          weigh(this_v, g, sb, keys, kTurns ? i > 1 : i > 0);
+          ++cnt[g];
           if (MT == 2 && i + 1 < n) {
-            mma_commit(bar_empty + 8 * (next_k % R));
-            if (i + 2 == n) mma_commit(bar_q_free);
+            if ((m == 0 && !full_at(place_k(i + 1, n))) || !settle(m)) break;
+            tc_fence_after();
+            scores(next_k, m, m);
           }
         }
-        base += 2 * n;
-        for (int m = 0; m < tiles_m; ++m) ++segs[m];
+        if (!ok) break;
+        commit(bar_empty + 8 * (this_v % R));
+        if (MT == 2 && i + 1 < n) {
+          commit(bar_empty + 8 * (next_k % R));
+          if (i + 2 == n) commit(bar_q_free);
+        }
       }
-      if (!ok) {
-        raise(L.status, SPEC_DEV_TIMEOUT);
-        mma_commit(bar_drain);
-        mbar_wait_bounded(bar_drain, 0, 10000000ull);
-      }
+      base += 2 * n;
+      for (int m = 0; m < tiles_m; ++m) ++segs[m];
+    }
+    if (!ok) {
+      if (lane == 0) raise(L.status, SPEC_DEV_TIMEOUT);
+      commit(bar_drain);
+      mbar_wait_bounded(bar_drain, 0, 10000000ull);
     }
     __syncwarp();
   } else {
     // ---- softmax: a thread per row ----
-    const int m = MT == 1 ? 0 : (wid - 2) >> 2, quad = wid & 3;  // the tensor-memory lanes that this warp may use
-    const int r = quad * 32 + lane, tid_m = tid - 64 - m * 128;
+    const int g = GROUPS == 1 ? 0 : (wid - 2) >> 2, m = MT == 2 ? g : 0;
+    const int quad = wid & 3;  // the tensor-memory lanes that this warp may use
+    const int r = quad * 32 + lane, tid_g = tid - 64 - g * 128;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t out_at = tmem + Sh::kOut + m * DP + lanes;
+    const uint32_t out_at = tmem + Sh::kOut + lanes;  // result 0
     uint32_t base = 0, cnt = 0, seg = 0, fixes = 0;
     bool ok = true, left_open = false;
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -485,12 +546,13 @@ __global__ void __launch_bounds__(64 + 128 * MT, 1) attend_kernel(const __grid_c
         base += 2 * n;
         continue;
       }
-      const bool live = tok < rows && tok < L.tok;
+      const bool live = tok < rows;
       const bool warp_live = quad * 32 < rows * L.group;
       const int i_row = row0 + tok;
       float top = -INFINITY, total_w = 0.0f, exact_w = 0.0f;  // m / c; sums of the rounded weights and of the weights
-      for (int i = 0; i < n; ++i, ++cnt) {
-        const int t = w.t0 + i, sb = MT == 1 ? cnt & 1 : m;
+      for (int i = kTurns ? g : 0; i < n; i += kTurns ? 2 : 1, ++cnt) {
+        const bool opening = kTurns ? i < 2 : i == 0;
+        const int t = w.t0 + i, sb = GROUPS == 1 ? cnt & 1 : g;
         const bool last = t >= w.s.full;
         int cached = 0, at = 0, j0 = 0, fresh = 0, keys = NK;
         uint32_t sees[NK / 32];
@@ -510,77 +572,76 @@ __global__ void __launch_bounds__(64 + 128 * MT, 1) attend_kernel(const __grid_c
                 if (see ? see[k - at] != 0 : j0 + k - at <= i_row) sees[u] |= 1u << (k - 32 * u);
           }
         }
-        if (!wait(bar_s + 8 * sb, MT == 1 ? cnt >> 1 : cnt)) break;
-        // Every product with the values is waited for, the last one before this tile's
-        // here: a wait that skips one could take it for the one two before.
-        if (i > 0 && !wait(bar_o + 8 * m, cnt - 1)) break;
+        if (!wait(bar_s + 8 * sb, GROUPS == 1 ? cnt >> 1 : cnt)) break;
         tc_fence_after();
+        float fix = 1.0f;  // of the result so far
         if (warp_live) {
           const uint32_t score_at = tmem + sb * NK + lanes;
-          uint32_t v[NK / 32][32];
-#pragma unroll
-          for (int u = 0; u < NK / 32; ++u)
-            if (!last || 32 * u < keys) tmem_start32(score_at + 32 * u, v[u]);
-          float mx = -INFINITY;
-#pragma unroll
-          for (int u = 0; u < NK / 32; ++u) {
-            if (last && 32 * u >= keys) continue;
-            tmem_wait32(v[u]);
+          uint32_t v[2][32];  // 64 columns at a time, in two passes: 168 registers a thread is all there are
+          auto fetch = [&](int h) {
+            tmem_start32(score_at + 64 * h, v[0]);
+            tmem_start32(score_at + 64 * h + 32, v[1]);
+            tmem_wait32(v[0]);
+            tmem_wait32(v[1]);
             if (L.flip != 1.0f) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[u][j] = __float_as_uint(__uint_as_float(v[u][j]) * L.flip);
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[u][j] = __float_as_uint(__uint_as_float(v[u][j]) * L.flip);
             }
             if (last) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!((sees[u] >> j) & 1u)) v[u][j] = 0xFF800000u;
-            }
+              for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(v[u][j]));
+                for (int j = 0; j < 32; ++j)
+                  if (!((sees[2 * h + u] >> j) & 1u)) v[u][j] = 0xFF800000u;
+            }
+          };
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int h = NK / 64 - 1; h >= 0; --h) {  // the first half stays in registers
+            if (64 * h >= keys) continue;
+            fetch(h);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int j = 0; j < 32; j += 8)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  mx[c] = fmaxf(mx[c], fmaxf(__uint_as_float(v[u][j + c]), __uint_as_float(v[u][j + c + 4])));
           }
           // a larger maximum: the sums so far shrink, unless by less than 2^8
-          const float grown = fmaxf(top, mx);
+          const float grown = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
           const bool grow = live && grown > top && !((grown - top) * L.c <= 8.0f);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float fix = !grow ? 1.0f : top == -INFINITY ? 0.0f : ex2((top - grown) * L.c);
-            if (grow) top = grown;
+          if (grow) {
+            fix = top == -INFINITY ? 0.0f : ex2((top - grown) * L.c);
+            top = grown;
             total_w *= fix;
             exact_w *= fix;
-            if (i > 0) {
-              for (int d = 0; d < A.D; d += 32) {
-                uint32_t o[32];
-                tmem_start32(out_at + d, o);
-                tmem_wait32(o);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fix);
-                tmem_store32(out_at + d, o);
-              }
-            }
           }
           const float off = top == -INFINITY ? 0.0f : top * L.c;
           const f32x2 c2 = f2(L.c, L.c), off2 = f2(-off, -off);
           f32x2 s0 = 0, s1 = 0, e0 = 0, e1 = 0;
 #pragma unroll
-          for (int u = 0; u < NK / 32; u += 2) {
-            if (last && 32 * u >= keys) continue;
+          for (int h = 0; h < NK / 64; ++h) {
+            if (64 * h >= keys) continue;
+            if (h > 0) fetch(h);
             uint32_t p[32];
 #pragma unroll
             for (int j = 0; j < 64; j += 2) {
-              const int uu = u + j / 32;
-              float a = 0.0f, b = 0.0f;
-              if (!last || 32 * uu < keys) {
-                f2_split(f2_fma(f2(__uint_as_float(v[uu][j % 32]), __uint_as_float(v[uu][j % 32 + 1])), c2, off2), a, b);
-                a = ex2(a);
-                b = ex2(b);
-              }
-              const uint32_t h = El::pack(a, b);
-              p[j / 2] = h;
+              const int u = j / 32;
+              float a, b;
+              f2_split(f2_fma(f2(__uint_as_float(v[u][j % 32]), __uint_as_float(v[u][j % 32 + 1])), c2, off2), a, b);
+              a = ex2(a);
+              b = ex2(b);
+              const uint32_t pair = El::pack(a, b);
+              p[j / 2] = pair;
               float ra, rb;  // as the product takes them
               if constexpr (kBf16) {
-                ra = __uint_as_float(h << 16);
-                rb = __uint_as_float(h & 0xFFFF0000u);
+                ra = __uint_as_float(pair << 16);
+                rb = __uint_as_float(pair & 0xFFFF0000u);
               } else {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&pair));
                 ra = f.x;
                 rb = f.y;
               }
@@ -592,16 +653,33 @@ __global__ void __launch_bounds__(64 + 128 * MT, 1) attend_kernel(const __grid_c
                 e0 = f2_add(e0, f2(a, b));
               }
             }
-            tmem_store32(score_at + 16 * u, p);
+            tmem_store32(score_at + 32 * h, p);
           }
           total_w += f2_hsum(f2_add(s0, s1));
           exact_w += f2_hsum(f2_add(e0, e1));
-          tmem_wait_stores();
-          tc_fence_before();
         }
+        if (!opening) {
+          // Two groups: the scores of this tile came behind the last product into the result.
+          // One group: every product is waited for, the last one before this tile's here (a
+          // wait that skips one could take it for the one two before).
+          if (GROUPS == 1 && !wait(bar_o, cnt - 1)) break;
+          if (__any_sync(0xffffffffu, fix != 1.0f)) {
+            tc_fence_after();
+            for (int d = 0; d < A.D; d += 32) {
+              uint32_t o[32];
+              tmem_start32(out_at + g * DP + d, o);
+              tmem_wait32(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fix);
+              tmem_store32(out_at + g * DP + d, o);
+            }
+          }
+        }
+        tmem_wait_stores();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p + 8 * sb);
-        if (last && m == 0) {
+        if (last && (MT == 1 || m == 0)) {
           // Values that no row may take in: the gaps become zeros; what is not finite among the
           // pass's values becomes zero here and is added to the rows that see it at the end.
           const uint32_t vs = base + place_v(i, n);
@@ -609,13 +687,13 @@ __global__ void __launch_bounds__(64 + 128 * MT, 1) attend_kernel(const __grid_c
           const uint32_t v0 = ring0 + vs % R * Sh::kTile;
           const int upto_k = (keys + 15) & ~15, gap = (fresh > 0 ? at : upto_k) - cached;
           const int zero_rows = gap + (fresh > 0 ? upto_k - keys : 0), per = 8 * chunks;
-          for (int x = tid_m; x < zero_rows * per; x += 128) {
+          for (int x = tid_g; x < zero_rows * per; x += 128) {
             const int z = x / per, y = x - z * per, row = z < gap ? cached + z : keys + z - gap;
             const uint32_t to = v0 + (y >> 3) * Sh::kChunk + row * 128 + (y & 7) * 16;
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
           }
           bool met = false;
-          for (int x = tid_m; x < fresh * per; x += 128) {
+          for (int x = tid_g; x < fresh * per; x += 128) {
             const int z = x / per, y = x - z * per;
             const uint32_t from = v0 + (y >> 3) * Sh::kChunk + (at + z) * 128 + (y & 7) * 16;
             uint32_t e[4];
@@ -639,38 +717,63 @@ __global__ void __launch_bounds__(64 + 128 * MT, 1) attend_kernel(const __grid_c
           if (met) *(volatile int*)&not_finite[seg & 1] = (int)seg + 1;
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_fix + 8 * (fixes++ & 1));
-          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_fix + 8 * (GROUPS == 1 ? fixes & 1 : kTurns ? g : 0));
+          ++fixes;
         }
       }
       if (!ok) break;
       // ---- the segment's result ----
-      if (!wait(bar_o + 8 * m, cnt - 1)) break;
+      const bool mine_too = !kTurns || g == 0 || n > 1;  // this group had a tile
+      if (mine_too && !wait(bar_o + 8 * g, cnt - 1)) break;
+      float f0 = 1.0f, f1 = 0.0f;  // factors of the two groups' results
+      if constexpr (kTurns) {
+        row_stat[seg & 1][g][r] = make_float4(top, total_w, exact_w, 0.0f);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_join);
+        if (!wait(bar_join, seg)) break;
+        const float4 other = row_stat[seg & 1][g ^ 1][r];
+        const float both = fmaxf(top, other.x), off = both == -INFINITY ? 0.0f : both;
+        const float f = ex2((top - off) * L.c), fo = ex2((other.x - off) * L.c);
+        total_w = total_w * f + other.y * fo;
+        exact_w = exact_w * f + other.z * fo;
+        top = both;
+        f0 = g == 0 ? f : fo;
+        f1 = g == 0 ? fo : f;
+      }
       tc_fence_after();
       const bool whole = w.t0 == 0 && w.t1 == w.s.tiles, opens = w.t0 == 0;
       const float inv = whole ? (total_w == 0.0f ? 0.0f : 1.0f / total_w) : 1.0f;
+      f0 *= inv;
+      f1 *= inv;
       const bool odd = w.t1 > w.s.full && *(volatile int*)&not_finite[seg & 1] == (int)seg + 1;
       const long long row = w.s.r0 + i_row, out_row = row * A.Hq + kh * L.group + head;
       const size_t slot = ((size_t)cta * 2 + (opens ? 1 : 0)) * L.slot_rows + m * 128 + r;
       if (warp_live) {
-        for (int d = 0; d < A.D; d += 32) {
+        for (int d = kTurns ? 32 * g : 0; d < A.D; d += kTurns ? 64 : 32) {  // the groups share the columns
           uint32_t o[32];
-          tmem_start32(out_at + d, o);
+          tmem_start32(out_at + (MT == 2 ? g * DP : 0) + d, o);
           tmem_wait32(o);
+          float x[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(o[j]) * f0;
+          if (kTurns && n > 1) {
+            tmem_start32(out_at + DP + d, o);
+            tmem_wait32(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = fmaf(__uint_as_float(o[j]), f1, x[j]);
+          }
           if (live) {
-            float x[32];
-  #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(o[j]) * inv;
             if (odd) {
-              int j_from, j_to, cached, at, j0, fresh;
+              int j_from, cached, at, j0, fresh;
               w.s.tail(max(w.t0, w.s.full), cached, at, j_from, fresh);
               w.s.tail(w.t1 - 1, cached, at, j0, fresh);
-              j_to = j0 + max(fresh, 0);
+              const int j_to = j0 + max(fresh, 0);
               for (int j = j_from; j < j_to; ++j) {
                 const bool seen = A.mask ? A.mask[((long long)w.b * A.T + i_row) * A.T + j] != 0 : j <= i_row;
                 if (!seen) continue;
                 const E* val = (const E*)A.v_new + (w.s.r0 + j) * A.v_new_stride[0] + kh * A.v_new_stride[1] + d;
-  #pragma unroll
+#pragma unroll
                 for (int e = 0; e < 32; ++e) {
                   if (d + e >= A.D) break;
                   const float f = El::to_f32(val[e]);
@@ -680,21 +783,21 @@ __global__ void __launch_bounds__(64 + 128 * MT, 1) attend_kernel(const __grid_c
             }
             if (whole) {
               E* to = (E*)A.out + out_row * A.D + d;
-  #pragma unroll
+#pragma unroll
               for (int j = 0; j < 32; j += 8)
                 if (d + j < A.D)
                   *(uint4*)(to + j) = make_uint4(El::pack(x[j], x[j + 1]), El::pack(x[j + 2], x[j + 3]),
                                                  El::pack(x[j + 4], x[j + 5]), El::pack(x[j + 6], x[j + 7]));
             } else {
               float* to = L.part + slot * DP + d;
-  #pragma unroll
+#pragma unroll
               for (int j = 0; j < 32; j += 4)
                 if (d + j < A.D) *(float4*)(to + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
             }
           }
           __syncwarp();  // the loads are the whole warp's
         }
-        if (live) {
+        if (live && (!kTurns || g == 0)) {
           const float top2 = top == -INFINITY ? -INFINITY : top * L.c;
           if (!whole)
             L.stat[slot] = make_float4(top2, total_w, exact_w, 0.0f);
@@ -704,8 +807,8 @@ __global__ void __launch_bounds__(64 + 128 * MT, 1) attend_kernel(const __grid_c
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_o_free + 8 * m);
-      if (opens && !whole && m == 0 && tid_m == 0) {
+      if (lane == 0) mbar_arrive(bar_o_free + 8 * (MT == 2 ? g : 0));
+      if (opens && !whole && g == 0 && tid_g == 0) {
         const long long last_tile = w.from + w.s.tiles - 1;
         L.split[cta] = {w.b, w.unit, (int)(((last_tile + 1) * ctas - 1) / total)};
         left_open = true;
@@ -713,7 +816,7 @@ __global__ void __launch_bounds__(64 + 128 * MT, 1) attend_kernel(const __grid_c
       base += 2 * n;
     }
     if (!ok) raise(L.status, SPEC_DEV_TIMEOUT);
-    if (m == 0 && tid_m == 0 && !left_open) L.split[cta] = {0, 0, -1};
+    if (g == 0 && tid_g == 0 && !left_open) L.split[cta] = {0, 0, -1};
   }
   tc_fence_before();
   __syncthreads();
