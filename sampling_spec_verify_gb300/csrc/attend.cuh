@@ -23,9 +23,9 @@
 // device: nothing of the launch depends on them, and the order of the sums
 // follows from the lengths alone.
 //
-// A CTA: warp 0 loads (keys and values through a ring of shared-memory tiles by
-// TMA, page by page; a page's part of a tile is a box of the tensor map),
-// warp 1 issues the products (scores into tensor memory, weights times values
+// A CTA: two warps load, one the keys and q, one the values (through a ring of
+// shared-memory tiles by TMA; a page's part of a tile is a box of the tensor map),
+// one issues the products (scores into tensor memory, weights times values
 // with the weights read from tensor memory), two warpgroups do the softmax, a
 // thread per row.
 #pragma once
@@ -56,7 +56,7 @@ struct AttendShape {
   static constexpr int kRoom = 217 * 1024;
   static constexpr int kRing = (kRoom - kQ) / kTile > 12 ? 12 : (kRoom - kQ) / kTile;
   static constexpr int kSmem = kQ + kRing * kTile + 1024;
-  static constexpr int kThreads = 64 + 128 * GROUPS;
+  static constexpr int kThreads = 96 + 128 * GROUPS;  // two loading warps and one of the products around the groups
   static constexpr int kOut = 256;                    // tensor-memory column of the results
   static_assert(2 * NK <= kOut && kOut + GROUPS * DP <= 512, "tensor memory");
   static_assert(kRing >= 4, "keys and values of two tiles");
@@ -306,40 +306,19 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
   auto place_k = [](int i, int) { return MT == 2 ? 2 * i : i == 0 ? 0 : 2 * i - 1; };
   auto place_v = [](int i, int n) { return MT == 2 ? 2 * i + 1 : i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
 
-  if (wid == 0) {
-    // ---- loads: the warp as a whole, each copy by one lane ----
-    uint32_t step = 0, seg = 0;
+  if (wid == 0 || wid == kThreads / 32 - 1) {
+    // ---- loads: a warp for q and the keys, one for the values; each copy by one lane ----
+    const bool values = wid != 0;
+    uint32_t base = 0, step = 0, seg = 0;
     uint32_t bad = 0;
-    bool ok = true;
+    bool ok = true, any = false;
     for (; ok && w.next(A); ++seg) {
       const int t0 = same_in_warp(w.t0), n = same_in_warp(w.t1) - t0, unit = same_in_warp(w.unit);
       const int kh = unit % A.Hkv, mg = unit / A.Hkv, full_tiles = same_in_warp(w.s.full);
-      const int first_row = same_in_warp(w.s.r0) + mg * tok_unit;  // of the pass
-      const int tiles_m = min(MT, (same_in_warp(w.s.rows) - mg * tok_unit + L.tok - 1) / L.tok);
       const int32_t* table = A.block_table + w.b * A.table_stride;
-      for (int x = 0; ok && x < 2 * n; ++x, ++step) {
-        if (x == (MT == 1 && n > 1 ? 2 : 1)) {  // q behind the first keys, which do not wait for the last segment
-          if (seg > 0) ok = mbar_wait_bounded(bar_q_free, (seg - 1) & 1u, kAttendWaitNs);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (one_lane()) {
-            mbar_arrive_expect_tx(bar_q, (uint32_t)(tiles_m * chunks * L.q_rows * L.group * 128));
-            for (int m = 0; m < tiles_m; ++m)
-              for (int ch = 0; ch < chunks; ++ch)
-                tma_load_3d(q0 + (m * CH + ch) * Sh::kQChunk, &L.q, ch * 64, kh * L.group, first_row + m * L.tok, bar_q);
-          }
-          __syncwarp();
-        }
-        bool values;
-        int i;
-        if constexpr (MT == 2) {
-          values = x & 1;
-          i = x >> 1;
-        } else {
-          values = x == 2 * n - 1 || (x > 0 && !(x & 1));
-          i = x == 2 * n - 1 ? n - 1 : values ? (x - 2) >> 1 : (x + 1) >> 1;
-        }
+      for (int i = 0; ok && i < n; ++i) {
         const int t = t0 + i;
+        step = base + (values ? place_v(i, n) : place_k(i, n));
         const uint32_t s = step % R, use = step / R, full = bar_full + 8 * s, dst = ring0 + s * Sh::kTile;
         // a lane's box of the tile: its page and place
         int cached = NK, at = 0, j0 = 0, fresh = 0, size = L.box;
@@ -348,33 +327,38 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           size = 8;
         }
         const int old = same_in_warp((cached + size - 1) / size), boxes = old + same_in_warp((fresh + 7) / 8);
-        int page = 0, place = 0;
-        if (lane < old) {
-          const int pos = t * NK + lane * size, p = pos / A.page_size;
-          page = __ldg(table + p);
-          place = pos - p * A.page_size;
-          if (page < 0 || page >= A.pages) page = A.pages, bad = SPEC_DEV_BAD_PAGE;  // behind the end: zeros
-        }
+        const int pos = t * NK + lane * size, p = pos / A.page_size, place = pos - p * A.page_size;
+        int page = lane < old ? __ldg(table + p) : 0;
         if (use > 0) ok = mbar_wait_bounded(bar_empty + 8 * s, (use - 1) & 1u, kAttendWaitNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        any = true;
+        if (page < 0 || page >= A.pages) page = A.pages, bad = SPEC_DEV_BAD_PAGE;  // behind the end: zeros
         if (t < full_tiles) {
           if (one_lane()) mbar_arrive_expect_tx(full, (uint32_t)(chunks * NK * 128));
-          __syncwarp();
           const CUtensorMap* map = values ? &L.v : &L.k;
-#pragma unroll 1
-          for (int bx = 0; bx < old; ++bx) {
-            const int pg = __shfl_sync(0xffffffffu, page, bx), pl = __shfl_sync(0xffffffffu, place, bx);
+          constexpr int kBatch = 8;
+          for (int b8 = 0; b8 < old; b8 += kBatch) {
+            int pg[kBatch], pl[kBatch];
+#pragma unroll
+            for (int y = 0; y < kBatch; ++y) {
+              pg[y] = __shfl_sync(0xffffffffu, page, b8 + y);
+              pl[y] = __shfl_sync(0xffffffffu, place, b8 + y);
+            }
             if (one_lane()) {
 #pragma unroll
-              for (int ch = 0; ch < CH; ++ch)
-                if (ch < chunks) tma_load_4d(dst + ch * Sh::kChunk + bx * L.box * 128, map, ch * 64, pl, kh, pg, full);
+              for (int y = 0; y < kBatch; ++y) {
+                if (b8 + y >= old) break;
+                const uint32_t to = dst + (b8 + y) * L.box * 128;
+#pragma unroll
+                for (int ch = 0; ch < CH; ++ch)
+                  if (ch < chunks) tma_load_4d(to + ch * Sh::kChunk, map, ch * 64, pl[y], kh, pg[y], full);
+              }
             }
             __syncwarp();
           }
         } else {
           if (one_lane()) mbar_arrive_expect_tx(full, (uint32_t)(chunks * boxes * 8 * 128));
-          __syncwarp();
           const CUtensorMap *map = values ? &L.v8 : &L.k8, *map_new = values ? &L.v_new : &L.k_new;
           const int row_at = same_in_warp(w.s.r0 + j0), at_u = same_in_warp(at);
 #pragma unroll 1
@@ -394,15 +378,31 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
             __syncwarp();
           }
         }
+        if (!values && i == (MT == 1 && n > 1 ? 1 : 0)) {  // q behind the first keys, which do not wait for the last segment
+          const int first_row = same_in_warp(w.s.r0) + mg * tok_unit;  // of the pass
+          const int tiles_m = min(MT, (same_in_warp(w.s.rows) - mg * tok_unit + L.tok - 1) / L.tok);
+          if (seg > 0) ok = mbar_wait_bounded(bar_q_free, (seg - 1) & 1u, kAttendWaitNs);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (one_lane()) {
+            mbar_arrive_expect_tx(bar_q, (uint32_t)(tiles_m * chunks * L.q_rows * L.group * 128));
+            for (int m = 0; m < tiles_m; ++m)
+              for (int ch = 0; ch < chunks; ++ch)
+                tma_load_3d(q0 + (m * CH + ch) * Sh::kQChunk, &L.q, ch * 64, kh * L.group, first_row + m * L.tok, bar_q);
+          }
+          __syncwarp();
+        }
       }
+      base += 2 * n;
     }
     raise(L.status, bad);
     if (!ok) {
       if (lane == 0) {
         raise(L.status, SPEC_DEV_TIMEOUT);
-        for (int i = 0; i < R && step > 0; ++i, --step)  // the copies in flight
-          mbar_wait_bounded(bar_full + 8 * ((step - 1) % R), ((step - 1) / R) & 1u, 10000000ull);
-        mbar_wait_bounded(bar_q, seg & 1u, 10000000ull);
+        // the copies in flight, of either warp: what the ring's last uses are filled with
+        for (int i = 0; any && i < R && (uint32_t)i <= step; ++i)
+          mbar_wait_bounded(bar_full + 8 * ((step - i) % R), ((step - i) / R) & 1u, 10000000ull);
+        if (!values) mbar_wait_bounded(bar_q, seg & 1u, 10000000ull);
       }
       __syncwarp();
     }
@@ -577,30 +577,28 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
         float fix = 1.0f;  // of the result so far
         if (warp_live) {
           const uint32_t score_at = tmem + sb * NK + lanes;
-          uint32_t v[2][32];  // 64 columns at a time, in two passes: 168 registers a thread is all there are
+          // 64 columns at a time, in two passes and in loops that are not unrolled: the
+          // registers hold no more, and a longer body waits for its instructions.
+          uint32_t v[2][32];
           auto fetch = [&](int h) {
             tmem_start32(score_at + 64 * h, v[0]);
             tmem_start32(score_at + 64 * h + 32, v[1]);
             tmem_wait32(v[0]);
             tmem_wait32(v[1]);
-            if (L.flip != 1.0f) {
+            if (last | (L.flip != 1.0f)) {
+              const uint32_t s0 = last ? h == 0 ? sees[0] : sees[NK / 32 - 2] : ~0u;
+              const uint32_t s1 = last ? h == 0 ? sees[1] : sees[NK / 32 - 1] : ~0u;
 #pragma unroll
-              for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[u][j] = __float_as_uint(__uint_as_float(v[u][j]) * L.flip);
-            }
-            if (last) {
-#pragma unroll
-              for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (!((sees[2 * h + u] >> j) & 1u)) v[u][j] = 0xFF800000u;
+              for (int j = 0; j < 32; ++j) {
+                v[0][j] = (s0 >> j) & 1u ? __float_as_uint(__uint_as_float(v[0][j]) * L.flip) : 0xFF800000u;
+                v[1][j] = (s1 >> j) & 1u ? __float_as_uint(__uint_as_float(v[1][j]) * L.flip) : 0xFF800000u;
+              }
             }
           };
+          const int halves = keys > 64 ? 2 : 1;
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int h = NK / 64 - 1; h >= 0; --h) {  // the first half stays in registers
-            if (64 * h >= keys) continue;
+#pragma unroll 1
+          for (int h = 0; h < halves; ++h) {
             fetch(h);
 #pragma unroll
             for (int u = 0; u < 2; ++u)
@@ -622,10 +620,9 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           const float off = top == -INFINITY ? 0.0f : top * L.c;
           const f32x2 c2 = f2(L.c, L.c), off2 = f2(-off, -off);
           f32x2 s0 = 0, s1 = 0, e0 = 0, e1 = 0;
-#pragma unroll
-          for (int h = 0; h < NK / 64; ++h) {
-            if (64 * h >= keys) continue;
-            if (h > 0) fetch(h);
+#pragma unroll 1
+          for (int h = 0; h < halves; ++h) {  // a half's weights take the place of scores that are read
+            fetch(h);
             uint32_t p[32];
 #pragma unroll
             for (int j = 0; j < 64; j += 2) {
