@@ -115,17 +115,19 @@ __device__ __forceinline__ AttendRequest attend_request(const spec_attention_t& 
 
 // A request's tiles of keys: `full` of the context alone, then the context's
 // last `rest` tokens, a gap up to a multiple of 8, and the pass's rows.
+constexpr int kAttendUnitCost = 3;
+
 template <int NK>
 struct AttendSpan {
   int r0, rows, full, rest, tiles;
-  long long cost;  // tiles of all units
+  long long cost;  // of all units: their tiles and kAttendUnitCost each
   __device__ __forceinline__ void load(const spec_attention_t& A, int b, int tok_unit) {
     const AttendRequest r = attend_request(A, b);
     r0 = r.r0, rows = r.rows;
     full = r.context / NK;
     rest = r.context % NK;
     tiles = full + (((rest + 7) & ~7) + rows + NK - 1) / NK;
-    cost = rows ? (long long)tiles * A.Hkv * ((rows + tok_unit - 1) / tok_unit) : 0;
+    cost = rows ? (long long)(tiles + kAttendUnitCost) * A.Hkv * ((rows + tok_unit - 1) / tok_unit) : 0;
   }
   // Tile t >= full: its cached tokens lie at [0, cached), the pass's rows [j0, j0 + fresh) from place `at` on.
   __device__ __forceinline__ void tail(int t, int& cached, int& at, int& j0, int& fresh) const {
@@ -137,36 +139,43 @@ struct AttendSpan {
   }
 };
 
-// The CTA's share of all tiles, unit by unit.  Every warp walks it by itself.
+// The CTA's share, unit by unit.  Every warp walks it by itself.  Shares are cut
+// where costs are equal: a unit costs as much as its tiles and kAttendUnitCost more
+// (its query rows, last tile and result), which come before its first tile.
 template <int NK>
 struct AttendWalk {
-  long long at, end;  // tiles of the batch
+  long long at, end;  // costs of the batch
   long long off;      // of request b
   int b, tok_unit;
   AttendSpan<NK> s;
   // the segment
   int unit, t0, t1;
-  long long from;     // its first tile in the batch's order
+  long long unit_end; // of the unit, in the batch's costs
   __device__ __forceinline__ bool next(const spec_attention_t& A) {
-    if (at >= end) return false;
-    while (off >= s.cost) {  // below the total there is another request
-      if (b + 1 >= A.B) return false;  // the lengths changed under the call
-      off = 0;
-      s.load(A, ++b, tok_unit);
+    while (at < end) {
+      while (off >= s.cost) {  // below the total there is another request
+        if (b + 1 >= A.B) return false;  // the lengths changed under the call
+        off = 0;
+        s.load(A, ++b, tok_unit);
+      }
+      const int each = s.tiles + kAttendUnitCost;
+      int from;
+      if (s.cost <= 0x7FFFFFFF) {
+        unit = (int)off / each;
+        from = (int)off - unit * each;
+      } else {
+        unit = (int)(off / each);
+        from = (int)(off - (long long)unit * each);
+      }
+      const int n = (int)min((long long)(each - from), end - at);
+      unit_end = at + each - from;
+      t0 = max(from - kAttendUnitCost, 0);
+      t1 = from + n - kAttendUnitCost;
+      at += n;
+      off += n;
+      if (t1 > t0) return true;
     }
-    if (s.cost <= 0x7FFFFFFF) {
-      unit = (int)off / s.tiles;
-      t0 = (int)off - unit * s.tiles;
-    } else {
-      unit = (int)(off / s.tiles);
-      t0 = (int)(off - (long long)unit * s.tiles);
-    }
-    from = at;
-    const int n = (int)min((long long)(s.tiles - t0), end - at);
-    t1 = t0 + n;
-    at += n;
-    off += n;
-    return true;
+    return false;
   }
 };
 
@@ -337,25 +346,22 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
         if (t < full_tiles) {
           if (one_lane()) mbar_arrive_expect_tx(full, (uint32_t)(chunks * NK * 128));
           const CUtensorMap* map = values ? &L.v : &L.k;
-          constexpr int kBatch = 8;
-          for (int b8 = 0; b8 < old; b8 += kBatch) {
-            int pg[kBatch], pl[kBatch];
-#pragma unroll
-            for (int y = 0; y < kBatch; ++y) {
-              pg[y] = __shfl_sync(0xffffffffu, page, b8 + y);
-              pl[y] = __shfl_sync(0xffffffffu, place, b8 + y);
-            }
+          // box by box; the place within the page is stepped along, the page comes from its lane
+          int pl = same_in_warp(place), pg = __shfl_sync(0xffffffffu, page, 0);
+          uint32_t to = dst;
+#pragma unroll 1
+          for (int bx = 0; bx < old; ++bx) {
+            const int next = __shfl_sync(0xffffffffu, page, bx + 1);
             if (one_lane()) {
 #pragma unroll
-              for (int y = 0; y < kBatch; ++y) {
-                if (b8 + y >= old) break;
-                const uint32_t to = dst + (b8 + y) * L.box * 128;
-#pragma unroll
-                for (int ch = 0; ch < CH; ++ch)
-                  if (ch < chunks) tma_load_4d(to + ch * Sh::kChunk, map, ch * 64, pl[y], kh, pg[y], full);
-              }
+              for (int ch = 0; ch < CH; ++ch)
+                if (ch < chunks) tma_load_4d(to + ch * Sh::kChunk, map, ch * 64, pl, kh, pg, full);
             }
             __syncwarp();
+            pg = next;
+            pl += L.box;
+            if (pl == A.page_size) pl = 0;
+            to += L.box * 128;
           }
         } else {
           if (one_lane()) mbar_arrive_expect_tx(full, (uint32_t)(chunks * boxes * 8 * 128));
@@ -806,8 +812,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_o_free + 8 * (MT == 2 ? g : 0));
       if (opens && !whole && g == 0 && tid_g == 0) {
-        const long long last_tile = w.from + w.s.tiles - 1;
-        L.split[cta] = {w.b, w.unit, (int)(((last_tile + 1) * ctas - 1) / total)};
+        L.split[cta] = {w.b, w.unit, (int)((w.unit_end * ctas - 1) / total)};
         left_open = true;
       }
       base += 2 * n;
