@@ -68,7 +68,7 @@ struct AttendSplit {  // a unit that goes on in the next CTAs
 
 struct AttendLaunch {
   CUtensorMap q, k_new, v_new;
-  CUtensorMap k, v;    // boxes of `box` tokens of a page
+  CUtensorMap k, v;    // boxes of `box` tokens of a page (see `fold`)
   CUtensorMap k8, v8;  // boxes of 8: the last tokens
   spec_attention_t a;
   uint32_t* status;
@@ -81,6 +81,11 @@ struct AttendLaunch {
   int box;             // tokens of a page that one copy takes
   int q_rows;          // rows of the pass that one copy of q takes
   int slot_rows;       // query rows of a partial result
+  // One copy takes all 64-element columns of a box where a head's columns continue an
+  // even dimension of the cache: 1, its heads (one behind the other in a token), 2, its
+  // pages (heads of pages evenly spaced); 0: a copy for each column.
+  int fold_k, fold_v;
+  int row8, col;       // bytes between groups of eight rows, 64-element columns of a tile in shared memory
 };
 
 // ---- requests, units and tiles ---------------------------------------------------
@@ -349,6 +354,20 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           // box by box; the place within the page is stepped along, the page comes from its lane
           int pl = same_in_warp(place), pg = __shfl_sync(0xffffffffu, page, 0);
           uint32_t to = dst;
+          const int fold = values ? L.fold_v : L.fold_k;
+          if (fold) {
+            const int col0 = fold == 1 ? kh * chunks : 0, heads = fold == 1 ? 1 : A.Hkv, head0 = fold == 1 ? 0 : kh;
+#pragma unroll 1
+            for (int bx = 0; bx < old; ++bx) {
+              const int next = __shfl_sync(0xffffffffu, page, bx + 1);
+              if (one_lane()) tma_load_5d(to, map, 0, 0, col0, pl >> 3, pg * heads + head0, full);
+              __syncwarp();
+              pg = next;
+              pl += L.box;
+              if (pl == A.page_size) pl = 0;
+              to += L.box * chunks * 128;
+            }
+          } else {
 #pragma unroll 1
           for (int bx = 0; bx < old; ++bx) {
             const int next = __shfl_sync(0xffffffffu, page, bx + 1);
@@ -363,6 +382,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
             if (pl == A.page_size) pl = 0;
             to += L.box * 128;
           }
+          }
         } else {
           if (one_lane()) mbar_arrive_expect_tx(full, (uint32_t)(chunks * boxes * 8 * 128));
           const CUtensorMap *map = values ? &L.v8 : &L.k8, *map_new = values ? &L.v_new : &L.k_new;
@@ -374,11 +394,11 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
 #pragma unroll
               for (int ch = 0; ch < CH; ++ch) {
                 if (ch >= chunks) continue;
-                const uint32_t to = dst + ch * Sh::kChunk;
+                const uint32_t to = dst + ch * L.col;
                 if (bx < old)
-                  tma_load_4d(to + bx * 1024, map, ch * 64, pl, kh, pg, full);
+                  tma_load_4d(to + bx * L.row8, map, ch * 64, pl, kh, pg, full);
                 else
-                  tma_load_3d(to + at_u * 128 + (bx - old) * 1024, map_new, ch * 64, kh, row_at + (bx - old) * 8, full);
+                  tma_load_3d(to + (at_u / 8 + bx - old) * L.row8, map_new, ch * 64, kh, row_at + (bx - old) * 8, full);
               }
             }
             __syncwarp();
@@ -414,7 +434,8 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
     }
   } else if (wid == 1) {
     // ---- products: the warp as a whole, each product by one lane ----
-    constexpr uint64_t desc_k = smem_desc_base(16, 1024), desc_v = smem_desc_base(Sh::kChunk, 1024);
+    constexpr uint64_t desc_q = smem_desc_base(16, 1024);
+    const uint64_t desc_k = smem_desc_base(16, (uint32_t)L.row8), desc_v = smem_desc_base((uint32_t)L.col, (uint32_t)L.row8);
     const uint32_t idesc_s = mma_idesc_128(kBf16, NK, false);
     const uint32_t idesc_o = mma_idesc_128(kBf16, (A.D + 15) & ~15, true);
     const int ksteps = (A.D + 15) / 16;
@@ -442,8 +463,8 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
 #pragma unroll
         for (int j = 0; j < DP / 16; ++j)
           if (j < ksteps)
-            mma_smem(d, smem_desc(desc_k, qm + j / 4 * Sh::kQChunk + j % 4 * 32),
-                     smem_desc(desc_k, k0 + j / 4 * Sh::kChunk + j % 4 * 32), idesc_s, j > 0 ? 1u : 0u);
+            mma_smem(d, smem_desc(desc_q, qm + j / 4 * Sh::kQChunk + j % 4 * 32),
+                     smem_desc(desc_k, k0 + j / 4 * L.col + j % 4 * 32), idesc_s, j > 0 ? 1u : 0u);
         mma_commit(bar_s + 8 * sb);
       }
       __syncwarp();
@@ -453,7 +474,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
       if (one_lane()) {
 #pragma unroll
         for (int j = 0; j < NK / 16; ++j)
-          if (j * 16 < keys) mma_tmem(d, p + j * 8, smem_desc(desc_v, v0 + j * 2048), idesc_o, more || j > 0 ? 1u : 0u);
+          if (j * 16 < keys) mma_tmem(d, p + j * 8, smem_desc(desc_v, v0 + j * 2 * L.row8), idesc_o, more || j > 0 ? 1u : 0u);
         mma_commit(bar_o + 8 * g);
       }
       __syncwarp();
@@ -692,13 +713,13 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           const int zero_rows = gap + (fresh > 0 ? upto_k - keys : 0), per = 8 * chunks;
           for (int x = tid_g; x < zero_rows * per; x += 128) {
             const int z = x / per, y = x - z * per, row = z < gap ? cached + z : keys + z - gap;
-            const uint32_t to = v0 + (y >> 3) * Sh::kChunk + row * 128 + (y & 7) * 16;
+            const uint32_t to = v0 + (y >> 3) * L.col + (row >> 3) * L.row8 + (row & 7) * 128 + (y & 7) * 16;
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
           }
           bool met = false;
           for (int x = tid_g; x < fresh * per; x += 128) {
-            const int z = x / per, y = x - z * per;
-            const uint32_t from = v0 + (y >> 3) * Sh::kChunk + (at + z) * 128 + (y & 7) * 16;
+            const int z = x / per, y = x - z * per, row = at + z;
+            const uint32_t from = v0 + (y >> 3) * L.col + (row >> 3) * L.row8 + (row & 7) * 128 + (y & 7) * 16;
             uint32_t e[4];
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3])

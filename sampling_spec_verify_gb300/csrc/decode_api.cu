@@ -159,12 +159,30 @@ spec_status_t run_attend(const spec_attention_t& A, const AttendPlan& p, uint32_
   const bool cache = A.pages > 0;
   const void *kc = cache ? A.k_cache : A.k_new, *vc = cache ? A.v_cache : A.v_new;
   const long long pages = cache ? A.pages : 1, page = cache ? A.page_size : 1, heads = A.Hkv;
+  const int chunks = (A.D + 63) / 64;
+  auto fold_of = [&](const long long* s) {
+    if (!cache || A.D % 64 || chunks == 1) return 0;
+    return s[2] == A.D ? 1 : s[0] == heads * s[2] && pages * heads <= 0x7FFFFFFFll ? 2 : 0;
+  };
+  L.fold_k = fold_of(A.k_stride);
+  L.fold_v = fold_of(A.v_stride);
+  if (!L.fold_k || !L.fold_v) L.fold_k = L.fold_v = 0;  // both tiles lie alike
+  L.row8 = L.fold_k ? chunks * 1024 : 1024;
+  L.col = L.fold_k ? 1024 : Sh::kChunk;
   for (int i = 0; i < 2; ++i) {
     const long long* s = i ? A.v_stride : A.k_stride;
     const long long same[3] = {A.D, A.D, A.D};
     if (!cache) s = same;
     for (int small = 0; small < 2; ++small) {
       CUtensorMap* m = i ? (small ? &L.v8 : &L.v) : (small ? &L.k8 : &L.k);
+      const int fold = i ? L.fold_v : L.fold_k;
+      if (fold && !small) {
+        const long long cols = fold == 1 ? heads * chunks : chunks, last = fold == 1 ? pages : pages * heads;
+        if (!make_map<5>(m, i ? vc : kc, bf, {64, 8, cols, page / 8, last}, {s[1], 64, 8 * s[1], s[fold == 1 ? 0 : 2]},
+                         {8, chunks, L.box / 8, 1}))
+          return SPEC_ERR_CUDA;
+        continue;
+      }
       if (!make_map<4>(m, i ? vc : kc, bf, {A.D, page, heads, pages}, {s[1], s[2], s[0]}, {small ? 8 : L.box, 1, 1}))
         return SPEC_ERR_CUDA;
     }
