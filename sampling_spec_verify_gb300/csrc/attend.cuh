@@ -194,20 +194,6 @@ __device__ __forceinline__ bool not_finite16(uint32_t x) {  // one element
 
 // ---- the kernel --------------------------------------------------------------------
 
-// A value that is the same in all lanes, in a form that the compiler knows to be.
-__device__ __forceinline__ int same_in_warp(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool one_lane() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
 template <class E, int DP, int MT>
 __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
     attend_kernel(const __grid_constant__ AttendLaunch L) {
@@ -307,7 +293,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
     start_off = off;
   }
   __syncthreads();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = (uint32_t)same_in_warp((int)tmem_slot);
   AttendWalk<NK> w;
   w.at = first, w.end = end, w.tok_unit = tok_unit;
   if (first < end) {
@@ -321,12 +307,12 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
   auto place_v = [](int i, int n) { return MT == 2 ? 2 * i + 1 : i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
 
   if (wid == 0 || wid == kThreads / 32 - 1) {
-    // ---- loads: a warp for q and the keys, one for the values; each copy by one lane ----
+    // ---- loads: a warp for q and the keys, one for the values ----
     const bool values = wid != 0;
     uint32_t base = 0, step = 0, seg = 0;
     uint32_t bad = 0;
     bool ok = true, any = false;
-    for (; ok && w.next(A); ++seg) {
+    for (; ok && __any_sync(0xffffffffu, w.next(A)); ++seg) {
       const int t0 = same_in_warp(w.t0), n = same_in_warp(w.t1) - t0, unit = same_in_warp(w.unit);
       const int kh = unit % A.Hkv, mg = unit / A.Hkv, full_tiles = same_in_warp(w.s.full);
       const int32_t* table = A.block_table + w.b * A.table_stride;
@@ -342,6 +328,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
         }
         const int old = same_in_warp((cached + size - 1) / size), boxes = old + same_in_warp((fresh + 7) / 8);
         const int pos = t * NK + lane * size, p = pos / A.page_size, place = pos - p * A.page_size;
+        const int place0 = t * NK % A.page_size;
         int page = lane < old ? __ldg(table + p) : 0;
         if (use > 0) ok = mbar_wait_bounded(bar_empty + 8 * s, (use - 1) & 1u, kAttendWaitNs);
         ok = __all_sync(0xffffffffu, ok);
@@ -349,19 +336,19 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
         any = true;
         if (page < 0 || page >= A.pages) page = A.pages, bad = SPEC_DEV_BAD_PAGE;  // behind the end: zeros
         if (t < full_tiles) {
-          if (one_lane()) mbar_arrive_expect_tx(full, (uint32_t)(chunks * NK * 128));
+          mbar_expect(full, (uint32_t)(chunks * NK * 128));
           const CUtensorMap* map = values ? &L.v : &L.k;
           // box by box; the place within the page is stepped along, the page comes from its lane
-          int pl = same_in_warp(place), pg = __shfl_sync(0xffffffffu, page, 0);
+          auto page_of = [&](int bx) { return (int)__reduce_or_sync(0xffffffffu, lane == bx ? (uint32_t)page : 0u); };
+          int pl = place0, pg = page_of(0);
           uint32_t to = dst;
           const int fold = values ? L.fold_v : L.fold_k;
           if (fold) {
             const int col0 = fold == 1 ? kh * chunks : 0, heads = fold == 1 ? 1 : A.Hkv, head0 = fold == 1 ? 0 : kh;
 #pragma unroll 1
             for (int bx = 0; bx < old; ++bx) {
-              const int next = __shfl_sync(0xffffffffu, page, bx + 1);
-              if (one_lane()) tma_load_5d(to, map, 0, 0, col0, pl >> 3, pg * heads + head0, full);
-              __syncwarp();
+              const int next = page_of(bx + 1);
+              tma_load_5d(to, map, 0, 0, col0, pl >> 3, pg * heads + head0, full);
               pg = next;
               pl += L.box;
               if (pl == A.page_size) pl = 0;
@@ -370,13 +357,10 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           } else {
 #pragma unroll 1
           for (int bx = 0; bx < old; ++bx) {
-            const int next = __shfl_sync(0xffffffffu, page, bx + 1);
-            if (one_lane()) {
+            const int next = page_of(bx + 1);
 #pragma unroll
-              for (int ch = 0; ch < CH; ++ch)
-                if (ch < chunks) tma_load_4d(to + ch * Sh::kChunk, map, ch * 64, pl, kh, pg, full);
-            }
-            __syncwarp();
+            for (int ch = 0; ch < CH; ++ch)
+              if (ch < chunks) tma_load_4d(to + ch * Sh::kChunk, map, ch * 64, pl, kh, pg, full);
             pg = next;
             pl += L.box;
             if (pl == A.page_size) pl = 0;
@@ -384,24 +368,22 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           }
           }
         } else {
-          if (one_lane()) mbar_arrive_expect_tx(full, (uint32_t)(chunks * boxes * 8 * 128));
+          mbar_expect(full, (uint32_t)(chunks * boxes * 8 * 128));
           const CUtensorMap *map = values ? &L.v8 : &L.k8, *map_new = values ? &L.v_new : &L.k_new;
           const int row_at = same_in_warp(w.s.r0 + j0), at_u = same_in_warp(at);
 #pragma unroll 1
           for (int bx = 0; bx < boxes; ++bx) {
-            const int pg = __shfl_sync(0xffffffffu, page, bx & 31), pl = __shfl_sync(0xffffffffu, place, bx & 31);
-            if (one_lane()) {
+            const int pg = (int)__reduce_or_sync(0xffffffffu, lane == bx ? (uint32_t)page : 0u);
+            const int pl = (int)__reduce_or_sync(0xffffffffu, lane == bx ? (uint32_t)place : 0u);
 #pragma unroll
-              for (int ch = 0; ch < CH; ++ch) {
-                if (ch >= chunks) continue;
-                const uint32_t to = dst + ch * L.col;
-                if (bx < old)
-                  tma_load_4d(to + bx * L.row8, map, ch * 64, pl, kh, pg, full);
-                else
-                  tma_load_3d(to + (at_u / 8 + bx - old) * L.row8, map_new, ch * 64, kh, row_at + (bx - old) * 8, full);
-              }
+            for (int ch = 0; ch < CH; ++ch) {
+              if (ch >= chunks) continue;
+              const uint32_t to = dst + ch * L.col;
+              if (bx < old)
+                tma_load_4d(to + bx * L.row8, map, ch * 64, pl, kh, pg, full);
+              else
+                tma_load_3d(to + (at_u / 8 + bx - old) * L.row8, map_new, ch * 64, kh, row_at + (bx - old) * 8, full);
             }
-            __syncwarp();
           }
         }
         if (!values && i == (MT == 1 && n > 1 ? 1 : 0)) {  // q behind the first keys, which do not wait for the last segment
@@ -410,13 +392,10 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           if (seg > 0) ok = mbar_wait_bounded(bar_q_free, (seg - 1) & 1u, kAttendWaitNs);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (one_lane()) {
-            mbar_arrive_expect_tx(bar_q, (uint32_t)(tiles_m * chunks * L.q_rows * L.group * 128));
-            for (int m = 0; m < tiles_m; ++m)
-              for (int ch = 0; ch < chunks; ++ch)
-                tma_load_3d(q0 + (m * CH + ch) * Sh::kQChunk, &L.q, ch * 64, kh * L.group, first_row + m * L.tok, bar_q);
-          }
-          __syncwarp();
+          mbar_expect(bar_q, (uint32_t)(tiles_m * chunks * L.q_rows * L.group * 128));
+          for (int m = 0; m < tiles_m; ++m)
+            for (int ch = 0; ch < chunks; ++ch)
+              tma_load_3d(q0 + (m * CH + ch) * Sh::kQChunk, &L.q, ch * 64, kh * L.group, first_row + m * L.tok, bar_q);
         }
       }
       base += 2 * n;
@@ -433,7 +412,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
       __syncwarp();
     }
   } else if (wid == 1) {
-    // ---- products: the warp as a whole, each product by one lane ----
+    // ---- products ----
     constexpr uint64_t desc_q = smem_desc_base(16, 1024);
     const uint64_t desc_k = smem_desc_base(16, (uint32_t)L.row8), desc_v = smem_desc_base((uint32_t)L.col, (uint32_t)L.row8);
     const uint32_t idesc_s = mma_idesc_128(kBf16, NK, false);
@@ -459,31 +438,21 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
     // scores of a tile against row tile m, into buffer sb
     auto scores = [&](uint32_t at, int m, int sb) {
       const uint32_t k0 = ring0 + at % R * Sh::kTile, qm = q0 + m * CH * Sh::kQChunk, d = tmem + sb * NK;
-      if (one_lane()) {
 #pragma unroll
-        for (int j = 0; j < DP / 16; ++j)
-          if (j < ksteps)
-            mma_smem(d, smem_desc(desc_q, qm + j / 4 * Sh::kQChunk + j % 4 * 32),
-                     smem_desc(desc_k, k0 + j / 4 * L.col + j % 4 * 32), idesc_s, j > 0 ? 1u : 0u);
-        mma_commit(bar_s + 8 * sb);
-      }
-      __syncwarp();
+      for (int j = 0; j < DP / 16; ++j)
+        if (j < ksteps)
+          mma_smem(d, smem_desc(desc_q, qm + j / 4 * Sh::kQChunk + j % 4 * 32),
+                   smem_desc(desc_k, k0 + j / 4 * L.col + j % 4 * 32), idesc_s, j > 0 ? 1u : 0u);
+      mma_commit(bar_s + 8 * sb);
     };
     auto weigh = [&](uint32_t at, int g, int sb, int keys, bool more) {
       const uint32_t v0 = ring0 + at % R * Sh::kTile, d = tmem + Sh::kOut + g * DP, p = tmem + sb * NK;
-      if (one_lane()) {
 #pragma unroll
-        for (int j = 0; j < NK / 16; ++j)
-          if (j * 16 < keys) mma_tmem(d, p + j * 8, smem_desc(desc_v, v0 + j * 2 * L.row8), idesc_o, more || j > 0 ? 1u : 0u);
-        mma_commit(bar_o + 8 * g);
-      }
-      __syncwarp();
+      for (int j = 0; j < NK / 16; ++j)
+        if (j * 16 < keys) mma_tmem(d, p + j * 8, smem_desc(desc_v, v0 + j * 2 * L.row8), idesc_o, more || j > 0 ? 1u : 0u);
+      mma_commit(bar_o + 8 * g);
     };
-    auto commit = [&](uint32_t bar) {
-      if (one_lane()) mma_commit(bar);
-      __syncwarp();
-    };
-    for (; ok && w.next(A); ++seg) {
+    for (; ok && __any_sync(0xffffffffu, w.next(A)); ++seg) {
       const int t0 = same_in_warp(w.t0), n = same_in_warp(w.t1) - t0, mg = same_in_warp(w.unit) / A.Hkv;
       const int full_tiles = same_in_warp(w.s.full);
       const int tiles_m = MT == 1 ? 1 : min(MT, (same_in_warp(w.s.rows) - mg * tok_unit + L.tok - 1) / L.tok);
@@ -494,8 +463,8 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
       tc_fence_after();
       // tiles counts those before this segment: buffers take turns where one group has two
       for (int m = 0; m < tiles_m; ++m) scores(base, m, MT == 2 ? m : kTurns ? 0 : tiles & 1);
-      commit(bar_empty + 8 * (base % R));
-      if (n == 1) commit(bar_q_free);
+      mma_commit(bar_empty + 8 * (base % R));
+      if (n == 1) mma_commit(bar_q_free);
       for (int i = 0; ok && i < n; ++i, ++tiles) {
         const int t = t0 + i;
         int keys = NK;
@@ -511,8 +480,8 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           if (!full_at(place_k(i + 1, n))) break;
           tc_fence_after();
           scores(next_k, 0, kTurns ? (i + 1) & 1 : (tiles + 1) & 1);
-          commit(bar_empty + 8 * (next_k % R));
-          if (i + 2 == n) commit(bar_q_free);
+          mma_commit(bar_empty + 8 * (next_k % R));
+          if (i + 2 == n) mma_commit(bar_q_free);
         }
         if (t >= full_tiles) {
           const int fb = GROUPS == 1 ? fixes[0] & 1 : fixer;  // one group: two barriers in turn
@@ -536,10 +505,10 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           }
         }
         if (!ok) break;
-        commit(bar_empty + 8 * (this_v % R));
+        mma_commit(bar_empty + 8 * (this_v % R));
         if (MT == 2 && i + 1 < n) {
-          commit(bar_empty + 8 * (next_k % R));
-          if (i + 2 == n) commit(bar_q_free);
+          mma_commit(bar_empty + 8 * (next_k % R));
+          if (i + 2 == n) mma_commit(bar_q_free);
         }
       }
       base += 2 * n;
@@ -547,7 +516,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
     }
     if (!ok) {
       if (lane == 0) raise(L.status, SPEC_DEV_TIMEOUT);
-      commit(bar_drain);
+      mma_commit(bar_drain);
       mbar_wait_bounded(bar_drain, 0, 10000000ull);
     }
     __syncwarp();
