@@ -56,7 +56,10 @@ struct AttendShape {
   static constexpr int kRoom = 217 * 1024;
   static constexpr int kRing = (kRoom - kQ) / kTile > 12 ? 12 : (kRoom - kQ) / kTile;
   static constexpr int kSmem = kQ + kRing * kTile + 1024;
-  static constexpr int kThreads = 96 + 128 * GROUPS;  // two loading warps and one of the products around the groups
+  // The groups' warps come first, then four of which three work: the products' and the keys'
+  // warps share a scheduler (and its instruction cache) with no softmax of the first 64 rows.
+  static constexpr int kValuesWarp = 4 * GROUPS + 1, kProductWarp = kValuesWarp + 1, kKeysWarp = kValuesWarp + 2;
+  static constexpr int kThreads = 32 * (4 * GROUPS + 4);
   static constexpr int kOut = 256;                    // tensor-memory column of the results
   static_assert(2 * NK <= kOut && kOut + GROUPS * DP <= 512, "tensor memory");
   static_assert(kRing >= 4, "keys and values of two tiles");
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
     prefetch_map(&L.k_new);
     prefetch_map(&L.v_new);
   }
-  if (wid == 1) {
+  if (wid == Sh::kProductWarp) {
     tmem_alloc(smem_addr(&tmem_slot), 512);
     tmem_relinquish();
   }
@@ -306,9 +309,9 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
   auto place_k = [](int i, int) { return MT == 2 ? 2 * i : i == 0 ? 0 : 2 * i - 1; };
   auto place_v = [](int i, int n) { return MT == 2 ? 2 * i + 1 : i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
 
-  if (wid == 0 || wid == kThreads / 32 - 1) {
+  if (wid == Sh::kKeysWarp || wid == Sh::kValuesWarp) {
     // ---- loads: a warp for q and the keys, one for the values ----
-    const bool values = wid != 0;
+    const bool values = wid == Sh::kValuesWarp;
     uint32_t base = 0, step = 0, seg = 0;
     uint32_t bad = 0;
     bool ok = true, any = false;
@@ -411,7 +414,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
       }
       __syncwarp();
     }
-  } else if (wid == 1) {
+  } else if (wid == Sh::kProductWarp) {
     // ---- products ----
     constexpr uint64_t desc_q = smem_desc_base(16, 1024);
     const uint64_t desc_k = smem_desc_base(16, (uint32_t)L.row8), desc_v = smem_desc_base((uint32_t)L.col, (uint32_t)L.row8);
@@ -438,18 +441,31 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
     // scores of a tile against row tile m, into buffer sb
     auto scores = [&](uint32_t at, int m, int sb) {
       const uint32_t k0 = ring0 + at % R * Sh::kTile, qm = q0 + m * CH * Sh::kQChunk, d = tmem + sb * NK;
+      // descriptors count in 16 bytes
+      const uint64_t dq = smem_desc(desc_q, qm), dk = smem_desc(desc_k, k0);
+      const uint32_t col = (uint32_t)L.col >> 4;
+      if (ksteps == DP / 16) {
 #pragma unroll
-      for (int j = 0; j < DP / 16; ++j)
-        if (j < ksteps)
-          mma_smem(d, smem_desc(desc_q, qm + j / 4 * Sh::kQChunk + j % 4 * 32),
-                   smem_desc(desc_k, k0 + j / 4 * L.col + j % 4 * 32), idesc_s, j > 0 ? 1u : 0u);
+        for (int j = 0; j < DP / 16; ++j)
+          mma_smem(d, dq + j / 4 * (Sh::kQChunk >> 4) + j % 4 * 2, dk + j / 4 * col + j % 4 * 2, idesc_s, j > 0 ? 1u : 0u);
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < ksteps; ++j)
+          mma_smem(d, dq + j / 4 * (Sh::kQChunk >> 4) + j % 4 * 2, dk + j / 4 * col + j % 4 * 2, idesc_s, j > 0 ? 1u : 0u);
+      }
       mma_commit(bar_s + 8 * sb);
     };
     auto weigh = [&](uint32_t at, int g, int sb, int keys, bool more) {
       const uint32_t v0 = ring0 + at % R * Sh::kTile, d = tmem + Sh::kOut + g * DP, p = tmem + sb * NK;
+      const uint64_t dv = smem_desc(desc_v, v0);
+      const uint32_t step = (uint32_t)L.row8 >> 3;
+      if (keys == NK) {
 #pragma unroll
-      for (int j = 0; j < NK / 16; ++j)
-        if (j * 16 < keys) mma_tmem(d, p + j * 8, smem_desc(desc_v, v0 + j * 2 * L.row8), idesc_o, more || j > 0 ? 1u : 0u);
+        for (int j = 0; j < NK / 16; ++j) mma_tmem(d, p + j * 8, dv + j * step, idesc_o, more || j > 0 ? 1u : 0u);
+      } else {
+#pragma unroll 1
+        for (int j = 0; j * 16 < keys; ++j) mma_tmem(d, p + j * 8, dv + j * step, idesc_o, more || j > 0 ? 1u : 0u);
+      }
       mma_commit(bar_o + 8 * g);
     };
     for (; ok && __any_sync(0xffffffffu, w.next(A)); ++seg) {
@@ -520,11 +536,11 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
       mbar_wait_bounded(bar_drain, 0, 10000000ull);
     }
     __syncwarp();
-  } else {
+  } else if (wid < 4 * GROUPS) {
     // ---- softmax: a thread per row ----
-    const int g = GROUPS == 1 ? 0 : (wid - 2) >> 2, m = MT == 2 ? g : 0;
+    const int g = wid >> 2, m = MT == 2 ? g : 0;
     const int quad = wid & 3;  // the tensor-memory lanes that this warp may use
-    const int r = quad * 32 + lane, tid_g = tid - 64 - g * 128;
+    const int r = quad * 32 + lane, tid_g = tid - g * 128;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t out_at = tmem + Sh::kOut + lanes;  // result 0
     uint32_t base = 0, cnt = 0, seg = 0, fixes = 0;
@@ -813,7 +829,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
   tc_fence_before();
   __syncthreads();
   let_next_start();
-  if (wid == 1) {
+  if (wid == Sh::kProductWarp) {
     tc_fence_after();
     tmem_free(tmem, 512);
   }
