@@ -342,8 +342,14 @@ spec_status_t spec_adjust_logits(const spec_adjust_t* args, uint32_t* dev_status
   int dev = 0;
   const int sms = device_sms(&dev);
   if (!sms) return SPEC_ERR_CUDA;
-  int parts = (A.V + ssv::kAdjustMaxSlice - 1) / ssv::kAdjustMaxSlice;
-  while ((long long)A.B * parts < 2ll * sms && A.V / parts > 4096) ++parts;
+  // Slices of 8192 tokens (several CTAs an SM), unless reading the history for each of them
+  // would come to more than a quarter of the logits' bytes, and shorter ones where
+  // requests are few.
+  long long want = 8192;
+  const long long least = 16ll * A.history_width * A.B / ((long long)A.rows * es);
+  if (want < least) want = least < ssv::kAdjustMaxSlice ? least : ssv::kAdjustMaxSlice;
+  int parts = (int)((A.V + want - 1) / want);
+  while ((long long)A.B * parts < 4ll * sms && A.V / parts > 2048) ++parts;
   ssv::AdjustParams P = {A, dev_status, ((A.V + parts - 1) / parts + 63) / 64 * 64};
   const size_t smem = ssv::adjust_smem(P.slice, A.biases, A.T);
   static std::once_flag once[2][kMaxDevices];

@@ -111,7 +111,7 @@ ADJUST = dict(logits=P, out=P, tokens=P, history=P, history_lens=P, B=2, T=3, ro
 
 @pytest.mark.parametrize("o,want", [
     (dict(B=-1), INVALID), (dict(T=0), INVALID), (dict(rows=5), INVALID), (dict(V=0), INVALID), (dict(V=1 << 25), UNSUPPORTED),
-    (dict(history_width=-1), INVALID), (dict(history_width=1000001), UNSUPPORTED), (dict(biases=-1), INVALID),
+    (dict(history_width=-1), INVALID), (dict(history_width=1 << 19), UNSUPPORTED), (dict(biases=-1), INVALID),
     (dict(biases=1025, bias_ids=P, bias=P), UNSUPPORTED), (dict(biases=3), INVALID), (dict(biases=3, bias=P), INVALID),
     (dict(T=1025, rows=2050), UNSUPPORTED), (dict(dtype=2), INVALID), (dict(logits=None), INVALID),
     (dict(out=None), INVALID), (dict(tokens=None), INVALID), (dict(history=None), INVALID),
