@@ -712,10 +712,9 @@ typedef struct {
  * For token v at row i of request b, c(v) counts v in the history behind the
  * prompt and among the tokens of the rows that row i sees (itself included):
  *   z  = z > 0 ? z / repetition : z * repetition   where c(v) > 0 or the prompt holds v
- *   z -= frequency * c(v) + presence               where c(v) > 0 (two subtractions, in this order)
- *   z += the sum of the biases listed for v, added up in their order
+ *   z += the biases listed for v, less frequency * c(v) + presence where c(v) > 0
  *   z  = -inf                                      where v is not allowed
- * in fp32, rounded once to dtype.  Untouched logits are copied bit by bit.
+ * in fp32 (the biases added up in their order), rounded once to dtype.  Untouched logits are copied bit by bit.
  * Tokens, history and bias ids outside [0, V) count for nothing and set
  * SPEC_DEV_BAD_TOKEN (-1 as a row's token or a bias id does not); history or
  * prompt lengths beyond the history count as the nearer bound and set

@@ -5,21 +5,31 @@
 //   z -= f c(v) + p                 c(v) > 0, occurrences that were generated or drafted
 //   z += biases of v ;  z = -inf    v not allowed
 //
-// A CTA owns a slice of the vocabulary for one request: the slice's
-// occurrences are counted once in shared memory (32-bit counters, exact in any
-// order), then all the request's rows stream through it.  A row's own drafted
-// tokens are compared only where a touched token is one of them, so that nothing
-// has to be counted between the rows.  Bound: memory, the logits in and out; the
-// counters are looked at only where a bitmap of touched tokens says so.
+// A CTA owns a slice of the vocabulary for one request.  The slices of the request's
+// rows pass through a ring of shared-memory stages, in and out by bulk copies.
+// While the first ones come in, the slice's occurrences are counted (32-bit
+// counters, exact in any order), turned into what they add to a logit, and the
+// touched tokens listed; then each row's listed tokens are computed in its stage, a
+// lane per token, and a grammar's bits applied to whole vectors.  Bound: memory, the
+// logits in and out.  (Logits that pass through registers instead: 157 us for 128 x 8 x
+// 129280 in bf16 with every rule, two thirds of the instructions for moving them.)
 #pragma once
 
+#include <type_traits>
+
 #include "loss_common.cuh"
+#include "tc05.cuh"
 
 namespace ssv {
 
-constexpr int kAdjustThreads = 256;
+constexpr int kAdjustThreads = 512;  // at most
+// Threads of a CTA; a word of a row's grammar each.
+inline int adjust_threads(int slice) { return slice > 4096 ? 512 : 256; }
 constexpr int kAdjustMaxRows = 1024, kAdjustMaxBiases = 1024;
-constexpr int kAdjustMaxSlice = 32768;
+constexpr int kAdjustStages = 3, kAdjustNear = 64;
+constexpr uint64_t kAdjustWaitNs = 2000000000ull;
+// Tokens a CTA: 16 KB of logits, or twice that.
+__host__ __device__ constexpr int adjust_slice(int elem) { return 16384 / elem; }
 
 struct AdjustParams {
   spec_adjust_t a;
@@ -31,12 +41,14 @@ struct AdjustParams {
 // less its first place there, bit 19 a row of the pass holds it, bits 0..18 its occurrences in
 // the generated history.
 constexpr uint32_t kSeenPrompt = 1u << 31, kDrafted = 1u << 19, kCountMask = kDrafted - 1;
-constexpr uint32_t kRare = 0x7FF80000u;  // a bias, or a row of the pass
 constexpr int kBiasShift = 20;
 constexpr int kAdjustMaxHistory = (int)kCountMask;
 
-inline size_t adjust_smem(int slice, int biases, int rows) {
-  return (size_t)slice * 4 + (size_t)slice / 8 + 8 + (size_t)biases * 9 + (size_t)rows * 4;
+// Stages first, on 16-byte boundaries; a stage holds a slice and what its first vector is off one.
+__host__ __device__ inline size_t adjust_stage(int slice, int elem) { return (size_t)slice * elem + 16; }
+inline size_t adjust_smem(int slice, int elem, int biases, int rows) {
+  return kAdjustStages * adjust_stage(slice, elem) + (size_t)slice * 6 + (size_t)slice / 2 + 8 + (size_t)biases * 9 +
+         (size_t)rows * 4 + 64;
 }
 
 // Elements of a 16-byte vector to -inf where `no` has their bit.
@@ -55,18 +67,25 @@ __device__ __forceinline__ void drop_elements(uint4& w, uint32_t no) {
 }
 
 template <class E>
-__global__ void __launch_bounds__(kAdjustThreads, 5) adjust_kernel(const __grid_constant__ AdjustParams P) {
+__global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_constant__ AdjustParams P) {
   using El = Elem<E>;
-  constexpr int PV = El::PV, kVecs = 2;  // vectors a thread has in flight
-  extern __shared__ uint32_t sh[];
+  constexpr int PV = El::PV;
+  extern __shared__ __align__(16) unsigned char raw[];
+  __shared__ __align__(8) uint64_t bars[kAdjustStages];
+  __shared__ int in_warp[kAdjustThreads / 32];
+  __shared__ unsigned long long sees[kAdjustNear];  // rows that a row sees, where they are few
   const spec_adjust_t& A = P.a;
-  const int S = P.slice, tid = threadIdx.x;
-  uint32_t* counts = sh;                          // [S]
-  uint32_t* touched = counts + S;                 // [S / 32 + 2]
-  float* bias = reinterpret_cast<float*>(touched + S / 32 + 2);  // [biases]
+  const int S = P.slice, tid = threadIdx.x, threads = blockDim.x;  // 256, or 512 for a long slice
+  const size_t stage = adjust_stage(S, sizeof(E));
+  uint32_t* counts = reinterpret_cast<uint32_t*>(raw + kAdjustStages * stage);  // [S]
+  uint32_t* touched = counts + S;                                               // [S / 32]
+  uint32_t* by_row = touched + S / 32;            // [S / 32] tokens whose count goes by the row
+  uint32_t* grammar[2] = {by_row + S / 32, by_row + S / 16 + 1};  // [S / 32 + 1] a row's bits, two rows in turn
+  float* bias = reinterpret_cast<float*>(by_row + 3 * (S / 32) + 2);            // [biases]
   int32_t* bias_id = reinterpret_cast<int32_t*>(bias + A.biases);
   int32_t* drafted = bias_id + A.biases;          // [T] a row's token in the slice, or -1
-  uint8_t* again = reinterpret_cast<uint8_t*>(drafted + A.T);  // [biases] later places have the token too
+  uint16_t* list = reinterpret_cast<uint16_t*>(drafted + A.T);  // [S] the slice's touched tokens
+  uint8_t* again = reinterpret_cast<uint8_t*>(list + S);        // [biases] later places have the token too
   const int b = blockIdx.y, v0 = blockIdx.x * S, v1 = min(v0 + S, A.V), n = v1 - v0;
 
   int r0 = b * A.T, r1 = r0 + A.T;
@@ -79,21 +98,55 @@ __global__ void __launch_bounds__(kAdjustThreads, 5) adjust_kernel(const __grid_
   }
   const int rows = r1 - r0;
   if (rows == 0) return;
-  {
-    uint4* zero = reinterpret_cast<uint4*>(sh);  // the slice is a multiple of 64 tokens
-    for (int i = tid; i < S / 4; i += kAdjustThreads) zero[i] = make_uint4(0, 0, 0, 0);
-    for (int i = tid; i < S / 32 + 2; i += kAdjustThreads) touched[i] = 0;
-    for (int i = tid; i < A.biases; i += kAdjustThreads) again[i] = 0;
+
+  // A row of the slice: elements before the first 16-byte boundary, whole vectors, the
+  // rest.  What is not in vectors (all of it where input and output lie differently)
+  // never enters a stage.
+  struct Row {
+    const E* in;
+    E* out;
+    int lead, vecs, pad;  // elements, vectors; the stage's bytes before the slice's first element
+  };
+  auto row_at = [&](int i) {
+    Row r;
+    const long long at = (long long)(r0 + i) * A.V + v0;
+    r.in = static_cast<const E*>(A.logits) + at;
+    r.out = static_cast<E*>(A.out) + at;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(r.in), y = reinterpret_cast<uintptr_t>(r.out);
+    r.lead = ((x ^ y) & 15) ? n : min(n, (int)(((16 - (x & 15)) & 15) / sizeof(E)));
+    r.vecs = (n - r.lead) / PV;
+    r.pad = r.vecs > 0 && r.lead > 0 ? 16 - r.lead * (int)sizeof(E) : 0;
+    return r;
+  };
+  const uint32_t stages0 = smem_addr(raw), bar0 = smem_addr(bars);
+  const uint64_t policy = l2_evict_first_policy();
+  auto load = [&](int i) {  // one thread
+    const Row r = row_at(i);
+    const uint32_t bar = bar0 + 8 * (i % kAdjustStages), bytes = (uint32_t)r.vecs * 16;
+    mbar_arrive_expect_tx(bar, bytes);
+    if (bytes)
+      bulk_load(stages0 + (uint32_t)(i % kAdjustStages * stage) + r.pad + r.lead * (uint32_t)sizeof(E), r.in + r.lead,
+                bytes, bar, policy);
+  };
+  if (tid == 0) {
+    for (int s = 0; s < kAdjustStages; ++s) mbar_init(bar0 + 8 * s, 1);
+    fence_mbar_init();
+    for (int i = 0; i < min(rows, kAdjustStages); ++i) load(i);
   }
+  for (int i = tid; i < S + S / 16; i += threads) counts[i] = 0;  // touched and by_row too
+  for (int i = tid; i < A.biases; i += threads) again[i] = 0;
   __syncthreads();
 
   uint32_t bad = 0;
-  auto mark = [&](int v) { atomicOr(&touched[v >> 5], 1u << (v & 31)); };
+  auto mark = [&](int v) {  // most occurrences are of tokens that occurred before
+    const uint32_t bit = 1u << (v & 31);
+    if (!(touched[v >> 5] & bit)) atomicOr(&touched[v >> 5], bit);
+  };
   if (A.biases > 0) {
     // A token's first place in the list keeps its bias; those of later places are added
     // to it in the list's order.
     const float* given = A.bias + (long long)b * A.biases;
-    for (int i = tid; i < A.biases; i += kAdjustThreads) {
+    for (int i = tid; i < A.biases; i += threads) {
       const int t = A.bias_ids[(long long)b * A.biases + i];
       bias_id[i] = t;
       bias[i] = given[i];
@@ -105,12 +158,12 @@ __global__ void __launch_bounds__(kAdjustThreads, 5) adjust_kernel(const __grid_
     }
     __syncthreads();
     auto first_of = [&](int t) { return A.biases - (int)(counts[t - v0] >> kBiasShift); };
-    for (int i = tid; i < A.biases; i += kAdjustThreads) {
+    for (int i = tid; i < A.biases; i += threads) {
       const int t = bias_id[i];
       if (t >= v0 && t < v1 && first_of(t) != i) again[first_of(t)] = 1;
     }
     __syncthreads();
-    for (int i = tid; i < A.biases; i += kAdjustThreads)
+    for (int i = tid; i < A.biases; i += threads)
       if (again[i]) {
         float sum = bias[i];
         for (int j = i + 1; j < A.biases; ++j)
@@ -124,16 +177,16 @@ __global__ void __launch_bounds__(kAdjustThreads, 5) adjust_kernel(const __grid_
     len = min(max(len, 0), A.history_width);
     if (prompt < 0 || prompt > len) bad |= SPEC_DEV_BAD_OFFSETS;
     const int32_t* h = A.history + (long long)b * A.history_width;
-    for (int i0 = tid; i0 < len; i0 += 8 * kAdjustThreads) {
+    for (int i0 = tid; i0 < len; i0 += 8 * threads) {
       int t[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int i = i0 + u * kAdjustThreads;
+        const int i = i0 + u * threads;
         t[u] = i < len ? __ldg(h + i) : v0;
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int i = i0 + u * kAdjustThreads;
+        const int i = i0 + u * threads;
         if (i >= len) break;
         if (t[u] < 0 || t[u] >= A.V) {
           bad |= SPEC_DEV_BAD_TOKEN;
@@ -146,7 +199,7 @@ __global__ void __launch_bounds__(kAdjustThreads, 5) adjust_kernel(const __grid_
         }
       }
     }
-    for (int j = tid; j < rows; j += kAdjustThreads) {
+    for (int j = tid; j < rows; j += threads) {
       const int t = A.tokens[r0 + j];
       if (t < -1 || t >= A.V) bad |= SPEC_DEV_BAD_TOKEN;
       const bool here = t >= v0 && t < v1;
@@ -154,6 +207,7 @@ __global__ void __launch_bounds__(kAdjustThreads, 5) adjust_kernel(const __grid_
       if (here) {
         atomicOr(&counts[t - v0], kDrafted);
         mark(t - v0);
+        atomicOr(&by_row[(t - v0) >> 5], 1u << (t & 31));
       }
     }
   }
@@ -164,107 +218,211 @@ __global__ void __launch_bounds__(kAdjustThreads, 5) adjust_kernel(const __grid_
   const float inv_rep = 1.0f / rep;  // one rounding more than a division, and no code for it
   const float freq = A.frequency ? A.frequency[b] : 0.0f;
   const float pres = A.presence ? A.presence[b] : 0.0f;
-  auto rule = [&](int i, int v, float x) {  // row i, token v of the slice
+  // Counts that are the same for all rows become what they add, the last bit of its fraction
+  // (2^-23 of it) whether the repetition penalty goes before.
+  // The touched tokens in their order, a word of the bitmap a thread.
+  int n_list = 0;
+  {
+    const uint32_t word = tid < S / 32 ? touched[tid] : 0u;
+    const int lane = tid & 31, wid = tid >> 5;
+    int upto = __popc(word);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) in_warp[wid] = upto;
+    __syncthreads();
+    for (int k = 0; k < threads / 32; ++k) {
+      if (k == wid) upto += n_list;
+      n_list += in_warp[k];
+    }
+    int q = upto - __popc(word);
+    for (uint32_t bits = word; bits; bits &= bits - 1) list[q++] = (uint16_t)(tid * 32 + __ffs(bits) - 1);
+  }
+  // Few rows: which of them a row sees as bits, and a drafted token with the rows that have it.
+  const bool near = rows <= kAdjustNear;
+  int own = -1;
+  uint32_t own_word = 0;
+  unsigned long long own_rows = 0;
+  if (near && tid < rows) {
+    unsigned long long see = (2ull << tid) - 1;
+    if (A.mask) {
+      const uint8_t* m = A.mask + ((long long)b * A.T + tid) * A.T;
+      see = 0;
+      for (int j = 0; j < rows; ++j) see |= (unsigned long long)(m[j] != 0) << j;
+    }
+    sees[tid] = see;
+    own = drafted[tid];
+    if (own >= 0) {
+      for (int j = 0; j < rows; ++j) own_rows |= (unsigned long long)(drafted[j] == own) << j;
+      if (own_rows & ((1ull << tid) - 1)) own = -1;  // an earlier row has the token too: its thread's
+    }
+    if (own >= 0) own_word = counts[own];
+  }
+  __syncthreads();
+  for (int q = tid; q < n_list; q += threads) {
+    const int v = list[q];
+    if ((by_row[v >> 5] >> (v & 31)) & 1u) continue;
+    const uint32_t w = counts[v], c = w & kCountMask;
+    const int at = (int)((w & ~kSeenPrompt) >> kBiasShift);
+    float add = at ? bias[A.biases - at] : 0.0f;
+    if (c) add = -freq * (float)c - pres + add;
+    counts[v] = (__float_as_uint(add) & ~1u) | (c || (w & kSeenPrompt) ? 1u : 0u);
+  }
+  __syncthreads();
+  auto short_rule = [&](uint32_t word, float x) {
+    const float y = x * (x > 0.0f ? inv_rep : rep);
+    return (word & 1u ? y : x) + __uint_as_float(word & ~1u);
+  };
+  auto counted = [&](uint32_t w, uint32_t c, float x) {  // the whole rule, of c occurrences
+    if (c || (w & kSeenPrompt)) x *= x > 0.0f ? inv_rep : rep;
+    const int at = (int)((w & ~kSeenPrompt) >> kBiasShift);
+    float add = at ? bias[A.biases - at] : 0.0f;
+    if (c) add = -freq * (float)c - pres + add;
+    return x + add;
+  };
+  auto rule = [&](int i, int v, float x) {  // row i, token v of the slice that goes by the row
     const uint32_t w = counts[v];
     uint32_t c = w & kCountMask;
-    if (w & kDrafted) {
-      const uint8_t* see = A.mask ? A.mask + ((long long)b * A.T + i) * A.T : nullptr;
-      const int upto = see ? rows : i + 1;
-      for (int j = 0; j < upto; ++j)
-        if (drafted[j] == v && (!see || see[j])) ++c;
-    }
-    if (c || (w & kSeenPrompt)) x = x > 0.0f ? x * inv_rep : x * rep;
-    if (c) x = x - freq * (float)c - pres;
-    const int at = (int)((w & ~kSeenPrompt) >> kBiasShift);
-    if (at) x += bias[A.biases - at];
-    return x;
+    const uint8_t* see = A.mask ? A.mask + ((long long)b * A.T + i) * A.T : nullptr;
+    const int upto = see ? rows : i + 1;
+    for (int j = 0; j < upto; ++j)
+      if (drafted[j] == v && (!see || see[j])) ++c;
+    return counted(w, c, x);
+  };
+  auto computed = [&](int i, int v, float x) {
+    return (by_row[v >> 5] >> (v & 31)) & 1u ? rule(i, v, x) : short_rule(counts[v], x);
   };
 
-  const int words = (A.V + 31) / 32;
-  const E* in_all = static_cast<const E*>(A.logits);
-  E* out_all = static_cast<E*>(A.out);
+  // A row's bits of the slice are read while the row before it is at work, a word a thread.
+  const int words = (A.V + 31) / 32, mine = min(S / 32, words - (v0 >> 5));
+  uint32_t bits = 0;
+  auto read_bits = [&](int i) {
+    const uint32_t* from = A.allowed + (long long)(r0 + i) * words + (v0 >> 5);
+    if (tid < mine) bits = __ldg(from + tid);
+  };
+  auto keep_bits = [&](int i) {
+    if (tid < mine) grammar[i & 1][tid] = bits;
+  };
+  if (A.allowed) {
+    read_bits(0);
+    keep_bits(0);
+    __syncthreads();
+  }
+  // A thread's first listed tokens stay in registers over the rows: token, what it adds.
+  constexpr int kHold = 4;
+  int held_at[kHold];
+  uint32_t held[kHold];
+#pragma unroll
+  for (int u = 0; u < kHold; ++u) {
+    const int q = tid + u * threads, v = q < n_list ? list[q] : -1;
+    const bool slow = v >= 0 && ((by_row[v >> 5] >> (v & 31)) & 1u);
+    held_at[u] = slow ? ~(v + 1) : v;  // below -1: goes by the row
+    held[u] = v >= 0 ? counts[v] : 0;
+  }
+  auto read_edge = [&](int i) {
+    const Row r = row_at(i);
+    return tid < n - r.vecs * PV ? r.in[tid < r.lead ? tid : tid + r.vecs * PV] : El::neg_inf();
+  };
+  E edge = read_edge(0);
+  bool ok = true;
   for (int i = 0; i < rows; ++i) {
-    const long long row = (long long)(r0 + i) * A.V + v0;
-    const E *in = in_all + row;
-    E* out = out_all + row;
-    const uint32_t* allow = A.allowed ? A.allowed + (long long)(r0 + i) * words : nullptr;
-    // elements before the first 16-byte boundary, whole vectors, the rest
-    const int lead = min(n, (int)(((16 - (reinterpret_cast<uintptr_t>(in) & 15)) & 15) / sizeof(E)));
-    const int vecs = (n - lead) / PV;
-    const bool same = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-    auto one = [&](int v) {
-      const bool ok = !allow || ((allow[(v0 + v) >> 5] >> ((v0 + v) & 31)) & 1u);
-      const E raw = in[v];
+    const Row r = row_at(i);
+    const uint32_t* allow = A.allowed ? grammar[i & 1] : nullptr;  // by token of the slice
+    if (allow && i + 1 < rows) read_bits(i + 1);
+    // elements outside of the vectors, a thread's first one read a row ahead
+    const int edges = n - r.vecs * PV;
+    const E first = edge;
+    if (i + 1 < rows) edge = read_edge(i + 1);
+    for (int q = tid; q < edges; q += threads) {
+      const int v = q < r.lead ? q : q + r.vecs * PV;
+      const E was = q == tid ? first : r.in[v];
+      const bool keep = !allow || ((allow[v >> 5] >> (v & 31)) & 1u);
       const bool hit = (touched[v >> 5] >> (v & 31)) & 1u;
-      out[v] = !ok ? El::neg_inf() : hit ? El::from_f32(rule(i, v, El::to_f32(raw))) : raw;
-    };
-    if (!same) {
-      for (int v = tid; v < n; v += kAdjustThreads) one(v);
-      continue;
+      r.out[v] = !keep ? El::neg_inf() : hit ? El::from_f32(computed(i, v, El::to_f32(was))) : was;
     }
-    for (int v = tid; v < lead; v += kAdjustThreads) one(v);
-    for (int v = lead + vecs * PV + tid; v < n; v += kAdjustThreads) one(v);
-    const uint4* src = reinterpret_cast<const uint4*>(in + lead);
-    uint4* dst = reinterpret_cast<uint4*>(out + lead);
-    // The whole rule's code is there once a vector, in a loop over the elements that need
-    // it: unrolled over them it waited for its instructions (128 x 8 x 129280: 426 us).
-    // Dense places (a language's frequent tokens) take the short rule side by side.
-    for (int k0 = tid; k0 < vecs; k0 += kVecs * kAdjustThreads) {
-      uint4 w[kVecs];
-      uint32_t ok[kVecs];
+    if (!r.vecs) {
+      ok = ok && mbar_wait_bounded(bar0 + 8 * (i % kAdjustStages), (uint32_t)(i / kAdjustStages) & 1u, kAdjustWaitNs);
+    } else {
+      unsigned char* here = raw + i % kAdjustStages * stage;
+      E* x = reinterpret_cast<E*>(here + r.pad);  // by token of the slice
+      const int from = r.lead, to = r.lead + r.vecs * PV;
+      ok = mbar_wait_bounded(bar0 + 8 * (i % kAdjustStages), (uint32_t)(i / kAdjustStages) & 1u, kAdjustWaitNs);
+      if (ok) {
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u) {
-        const int k = k0 + u * kAdjustThreads;
-        ok[u] = ~0u;
-        if (k < vecs) {
-          w[u] = __ldcs(src + k);
-          if (allow) {
-            const int g = v0 + lead + k * PV, s = g & 31;
-            uint32_t x = __ldg(allow + (g >> 5)) >> s;
-            if (s > 32 - PV) x |= __ldg(allow + (g >> 5) + 1) << (32 - s);
-            ok[u] = x;
+        for (int u = 0; u < kHold; ++u)
+          if (held_at[u] >= from && held_at[u] < to) {
+            E* at = x + held_at[u];
+            *at = El::from_f32(short_rule(held[u], El::to_f32(*at)));
+          }
+        if (own >= from && own < to)
+          x[own] = El::from_f32(counted(own_word, (own_word & kCountMask) + __popcll(sees[i] & own_rows), El::to_f32(x[own])));
+        bool slow = false;
+#pragma unroll
+        for (int u = 0; u < kHold; ++u) slow |= held_at[u] < -1;
+        if (slow && !near) {
+#pragma unroll 1
+          for (int q = tid; q < min(n_list, kHold * threads); q += threads) {
+            const int v = list[q];
+            if (((by_row[v >> 5] >> (v & 31)) & 1u) && v >= from && v < to) x[v] = El::from_f32(rule(i, v, El::to_f32(x[v])));
+          }
+        }
+#pragma unroll 1
+        for (int q = tid + kHold * threads; q < n_list; q += threads) {
+          const int v = list[q];
+          const bool goes = (by_row[v >> 5] >> (v & 31)) & 1u;
+          if (v >= from && v < to && !(goes && near)) x[v] = El::from_f32(computed(i, v, El::to_f32(x[v])));
+        }
+      }
+      if (allow) {
+        __syncthreads();
+        uint4* vec = reinterpret_cast<uint4*>(x + from);
+        if (from == 0) {  // the vectors' bits lie in one byte each
+          const uint8_t* bytes = reinterpret_cast<const uint8_t*>(allow);
+#pragma unroll 4
+          for (int k = tid; k < r.vecs; k += threads) {
+            const uint32_t keep = (uint32_t)bytes[k * PV >> 3] >> (k * PV & 7);
+            uint4 w = vec[k];
+            drop_elements<E>(w, ~keep);
+            vec[k] = w;
+          }
+        } else {
+#pragma unroll 4
+          for (int k = tid; k < r.vecs; k += threads) {
+            const int at = from + k * PV;
+            const uint32_t keep = __funnelshift_r(allow[at >> 5], allow[(at >> 5) + 1], at & 31);
+            uint4 w = vec[k];
+            drop_elements<E>(w, ~keep);
+            vec[k] = w;
           }
         }
       }
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) {
-        const int k = k0 + u * kAdjustThreads;
-        if (k >= vecs) break;
-        const int v = lead + k * PV, s = v & 31;
-        uint32_t hit = __funnelshift_r(touched[v >> 5], touched[(v >> 5) + 1], s) & ((1u << PV) - 1) & ok[u];
-        const uint4 raw = w[u];
-        if (__popc(hit) > 2) {  // tokens that were merely counted, all elements at once
-          E e[PV];
-          *reinterpret_cast<uint4*>(e) = raw;
-#pragma unroll
-          for (int j = 0; j < PV; ++j) {
-            const uint32_t word = (hit >> j) & 1u ? counts[v + j] : kRare;
-            const float x0 = El::to_f32(e[j]);
-            float x = x0 > 0.0f ? x0 * inv_rep : x0 * rep;
-            if (word & kCountMask) x = x - freq * (float)(word & kCountMask) - pres;
-            if (!(word & kRare)) {
-              hit &= ~(1u << j);
-              e[j] = El::from_f32(x);
-            }
-          }
-          w[u] = *reinterpret_cast<uint4*>(e);
-        }
-        if (allow) drop_elements<E>(w[u], ~ok[u]);
-        __stcs(dst + k, w[u]);
-        while (hit) {  // the others, one by one behind the vector
-          const int j = __ffs(hit) - 1;
-          hit &= hit - 1;
-          float x;
-          if constexpr (PV == 4) {
-            x = __uint_as_float(j & 2 ? (j & 1 ? raw.w : raw.z) : (j & 1 ? raw.y : raw.x));
-          } else {
-            const uint32_t pair = j & 4 ? (j & 2 ? raw.w : raw.z) : (j & 2 ? raw.y : raw.x);
-            x = __uint_as_float(j & 1 ? pair & 0xFFFF0000u : pair << 16);
-          }
-          out[v + j] = El::from_f32(rule(i, v + j, x));
-        }
+      fence_proxy_async_smem();
+    }
+    if (allow && i + 1 < rows) keep_bits(i + 1);
+    if (!__syncthreads_and(ok)) break;
+    if (tid == 0) {
+      if (r.vecs) {
+        bulk_store(r.out + r.lead, stages0 + (uint32_t)(i % kAdjustStages * stage) + r.pad + r.lead * (uint32_t)sizeof(E),
+                   (uint32_t)r.vecs * 16);
+      }
+      bulk_commit();
+      // the stage of the row before is free once its store has read it
+      const int next = i - 1 + kAdjustStages;
+      if (i > 0 && next < rows) {
+        bulk_wait_read<1>();
+        load(next);
       }
     }
+  }
+  if (tid == 0) {
+    if (!ok) {
+      raise(P.status, SPEC_DEV_TIMEOUT);
+      for (int i = 0; i < kAdjustStages; ++i)  // copies in flight, either phase of a stage
+        for (uint32_t p = 0; p < 2; ++p) mbar_wait_bounded(bar0 + 8 * i, p, 10000000ull);
+    }
+    bulk_wait_all();
   }
 }
 

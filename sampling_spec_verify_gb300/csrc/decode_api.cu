@@ -342,21 +342,20 @@ spec_status_t spec_adjust_logits(const spec_adjust_t* args, uint32_t* dev_status
   int dev = 0;
   const int sms = device_sms(&dev);
   if (!sms) return SPEC_ERR_CUDA;
-  // Slices of 8192 tokens (several CTAs an SM), unless reading the history for each of them
-  // would come to more than a quarter of the logits' bytes, and shorter ones where
-  // requests are few.
-  long long want = 8192;
-  const long long least = 16ll * A.history_width * A.B / ((long long)A.rows * es);
-  if (want < least) want = least < ssv::kAdjustMaxSlice ? least : ssv::kAdjustMaxSlice;
+  // Slices of 16 KB, twice that where reading the history for each of them would come to
+  // more than a quarter of the logits' bytes, and shorter ones where requests are few.
+  const long long short_slice = ssv::adjust_slice(es), least = 16ll * A.history_width * A.B / ((long long)A.rows * es);
+  const long long want = least > short_slice ? 2 * short_slice : short_slice;
   int parts = (int)((A.V + want - 1) / want);
-  while ((long long)A.B * parts < 4ll * sms && A.V / parts > 2048) ++parts;
+  while ((long long)A.B * (parts + 1) <= 4ll * sms && A.V / parts > 2048) ++parts;
   ssv::AdjustParams P = {A, dev_status, ((A.V + parts - 1) / parts + 63) / 64 * 64};
-  const size_t smem = ssv::adjust_smem(P.slice, A.biases, A.T);
+  const size_t smem = ssv::adjust_smem(P.slice, es, A.biases, A.T);
   static std::once_flag once[2][kMaxDevices];
   static cudaError_t made[2][kMaxDevices];
   const int which = A.dtype == SPEC_BF16;
   std::call_once(once[which][dev], [which, dev]() {
-    const int most = (int)ssv::adjust_smem(ssv::kAdjustMaxSlice, ssv::kAdjustMaxBiases, ssv::kAdjustMaxRows);
+    const int el = which ? 2 : 4;
+    const int most = (int)ssv::adjust_smem(2 * ssv::adjust_slice(el), el, ssv::kAdjustMaxBiases, ssv::kAdjustMaxRows);
     made[which][dev] =
         which ? cudaFuncSetAttribute(ssv::adjust_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)
               : cudaFuncSetAttribute(ssv::adjust_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
@@ -365,9 +364,9 @@ spec_status_t spec_adjust_logits(const spec_adjust_t* args, uint32_t* dev_status
   const dim3 grid((unsigned)((A.V + P.slice - 1) / P.slice), (unsigned)A.B);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (which)
-    ssv::adjust_kernel<__nv_bfloat16><<<grid, ssv::kAdjustThreads, smem, st>>>(P);
+    ssv::adjust_kernel<__nv_bfloat16><<<grid, ssv::adjust_threads(P.slice), smem, st>>>(P);
   else
-    ssv::adjust_kernel<float><<<grid, ssv::kAdjustThreads, smem, st>>>(P);
+    ssv::adjust_kernel<float><<<grid, ssv::adjust_threads(P.slice), smem, st>>>(P);
   return from_cuda(count_launch(cudaGetLastError()));
 }
 

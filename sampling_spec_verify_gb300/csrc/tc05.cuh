@@ -31,6 +31,11 @@ __device__ __forceinline__ void tma_reduce_add(const CUtensorMap* map, uint32_t 
                "r"(src), "r"(x), "r"(y)
                : "memory");
 }
+// Copies shared memory to global memory; both 16-byte aligned, `bytes` a multiple of 16.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Waits until at most N of this thread's committed stores still read shared memory.
 template <int N>
