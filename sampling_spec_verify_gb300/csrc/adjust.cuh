@@ -28,8 +28,8 @@ inline int adjust_threads(int slice) { return slice > 4096 ? 512 : 256; }
 constexpr int kAdjustMaxRows = 1024, kAdjustMaxBiases = 1024;
 constexpr int kAdjustStages = 3, kAdjustNear = 64;
 constexpr uint64_t kAdjustWaitNs = 2000000000ull;
-// Tokens a CTA: 16 KB of logits, or twice that.
-__host__ __device__ constexpr int adjust_slice(int elem) { return 16384 / elem; }
+// Tokens a CTA: 8 KB of logits, or twice that.
+__host__ __device__ constexpr int adjust_slice(int elem) { return 8192 / elem; }
 
 struct AdjustParams {
   spec_adjust_t a;
@@ -133,6 +133,22 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
     fence_mbar_init();
     for (int i = 0; i < min(rows, kAdjustStages); ++i) load(i);
   }
+  // All that the counting reads first is asked for at once, and used after the zeroing.
+  const float* given = A.biases ? A.bias + (long long)b * A.biases : nullptr;
+  const int32_t* given_ids = A.biases ? A.bias_ids + (long long)b * A.biases : nullptr;
+  const int first_id = tid < A.biases ? __ldg(given_ids + tid) : -1;
+  const float first_bias = tid < A.biases ? __ldg(given + tid) : 0.0f;
+  const int first_token = tid < rows ? __ldg(A.tokens + r0 + tid) : -1;
+  const int32_t* h = A.history + (long long)b * A.history_width;
+  constexpr int kBatch = 8;
+  int t[kBatch];
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) t[u] = tid + u * threads < A.history_width ? __ldg(h + tid + u * threads) : 0;
+  int len = A.history_lens[b], prompt = A.prompt_lens ? A.prompt_lens[b] : 0;
+  const float rep = A.repetition ? A.repetition[b] : 1.0f;
+  const float inv_rep = 1.0f / rep;  // one rounding more than a division, and no code for it
+  const float freq = A.frequency ? A.frequency[b] : 0.0f;
+  const float pres = A.presence ? A.presence[b] : 0.0f;
   for (int i = tid; i < S + S / 16; i += threads) counts[i] = 0;  // touched and by_row too
   for (int i = tid; i < A.biases; i += threads) again[i] = 0;
   __syncthreads();
@@ -145,11 +161,10 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
   if (A.biases > 0) {
     // A token's first place in the list keeps its bias; those of later places are added
     // to it in the list's order.
-    const float* given = A.bias + (long long)b * A.biases;
     for (int i = tid; i < A.biases; i += threads) {
-      const int t = A.bias_ids[(long long)b * A.biases + i];
+      const int t = i == tid ? first_id : given_ids[i];
       bias_id[i] = t;
-      bias[i] = given[i];
+      bias[i] = i == tid ? first_bias : given[i];
       if (t < -1 || t >= A.V) bad |= SPEC_DEV_BAD_TOKEN;
       if (t >= v0 && t < v1) {
         atomicMax(&counts[t - v0], (uint32_t)(A.biases - i) << kBiasShift);  // the first place is the largest
@@ -172,20 +187,16 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
       }
   }
   {
-    int len = A.history_lens[b], prompt = A.prompt_lens ? A.prompt_lens[b] : 0;
     if (len < 0 || len > A.history_width) bad |= SPEC_DEV_BAD_OFFSETS;
     len = min(max(len, 0), A.history_width);
     if (prompt < 0 || prompt > len) bad |= SPEC_DEV_BAD_OFFSETS;
-    const int32_t* h = A.history + (long long)b * A.history_width;
-    for (int i0 = tid; i0 < len; i0 += 8 * threads) {
-      int t[8];
+    for (int i0 = tid; i0 < len; i0 += kBatch * threads) {
+      if (i0 != tid) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i = i0 + u * threads;
-        t[u] = i < len ? __ldg(h + i) : v0;
+        for (int u = 0; u < kBatch; ++u) t[u] = i0 + u * threads < len ? __ldg(h + i0 + u * threads) : 0;
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < kBatch; ++u) {
         const int i = i0 + u * threads;
         if (i >= len) break;
         if (t[u] < 0 || t[u] >= A.V) {
@@ -200,7 +211,7 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
       }
     }
     for (int j = tid; j < rows; j += threads) {
-      const int t = A.tokens[r0 + j];
+      const int t = j == tid ? first_token : A.tokens[r0 + j];
       if (t < -1 || t >= A.V) bad |= SPEC_DEV_BAD_TOKEN;
       const bool here = t >= v0 && t < v1;
       drafted[j] = here ? t - v0 : -1;
@@ -214,10 +225,6 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
   if (blockIdx.x == 0) raise(P.status, bad);  // every slice sees the same
   __syncthreads();
 
-  const float rep = A.repetition ? A.repetition[b] : 1.0f;
-  const float inv_rep = 1.0f / rep;  // one rounding more than a division, and no code for it
-  const float freq = A.frequency ? A.frequency[b] : 0.0f;
-  const float pres = A.presence ? A.presence[b] : 0.0f;
   // Counts that are the same for all rows become what they add, the last bit of its fraction
   // (2^-23 of it) whether the repetition penalty goes before.
   // The touched tokens in their order, a word of the bitmap a thread.
