@@ -43,6 +43,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from dataclasses import dataclass
 from typing import Optional
@@ -986,13 +987,13 @@ def _need_strided(t: torch.Tensor, name: str, dtype=None, dims=None, device=None
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if dims is not None and t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
-    if device is not None and t.device != device:
+    if device is not None and t.get_device() != device.index:
         raise ValueError(f"{name} must be on {device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
@@ -1003,17 +1004,24 @@ def _strides(t: torch.Tensor):
 
 def _need_pass(t: torch.Tensor, name: str, dtype, shape, ragged: bool, lead: int, device):
     """Strides of a pass's rows [*, B, T, heads, D] (``lead`` dimensions before them) or,
-    ragged, [*, rows, heads, D]: (lead..., row, head)."""
-    _need_strided(t, name, dtype=dtype, dims=len(shape), device=device)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    s = _strides(t)
+    ragged, [*, rows, heads, D]: (lead..., row, head).  (A call of few rows takes as
+    long as its host side: what is right is looked at once, the reason of a refusal
+    is found afterwards.)"""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != device.index
+            or t.stride(-1) != 1):
+        _need_strided(t, name, dtype=dtype, dims=len(shape), device=device)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    s = t.stride()
     if ragged:
-        return s
-    B, T = t.shape[lead:lead + 2]
-    if B > 1 and T > 1 and s[lead] != T * s[lead + 1]:
-        raise ValueError(f"the rows of {name} must be evenly spaced over requests")
-    return s[:lead] + [s[lead + 1] if T > 1 else s[lead]] + s[lead + 2:]
+        rows, row, head = shape[-3], s[-3], s[-2]
+    else:
+        B, T = shape[-4], shape[-3]
+        if B > 1 and T > 1 and s[-4] != T * s[-3]:
+            raise ValueError(f"the rows of {name} must be evenly spaced over requests")
+        rows, row, head = B * T, s[-3] if T > 1 else s[-4], s[-2]
+    D = shape[-1]  # a dimension of size 1 is never stepped along
+    return (*(x if n > 1 else D for n, x in zip(shape[:lead], s)), row if rows > 1 else D, head if shape[-2] > 1 else D)
 
 
 def _pass_shape(B_offsets: Optional[torch.Tensor], max_rows: Optional[int], lead_shape, name: str, device):
@@ -1038,35 +1046,15 @@ def _need_mask(mask: Optional[torch.Tensor], B: int, T: int, device):
             raise ValueError(f"mask must be [{B}, {T}, {T}], got {tuple(mask.shape)}")
 
 
-class _Attention(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k_new", "v_new", "k_cache", "v_cache", "out", "lse", "block_table",
-                                                "context_lens", "row_offsets", "mask")]
-                + [(n, ctypes.c_longlong * k) for n, k in (("q_stride", 2), ("k_new_stride", 2), ("v_new_stride", 2),
-                                                           ("k_stride", 3), ("v_stride", 3))]
-                + [("table_stride", ctypes.c_longlong)]
-                + [(n, ctypes.c_int) for n in ("B", "T", "rows", "Hq", "Hkv", "D", "pages", "page_size", "table_width",
-                                               "dtype")]
-                + [("scale", ctypes.c_float)])
+# spec_attention_t, spec_commit_t and spec_adjust_t as the C compiler lays them out:
+# pointers, then strides, then sizes (packing costs a tenth of a ctypes.Structure)
+_ATTENTION = struct.Struct("@11P13q10if0q")
+_COMMIT = struct.Struct("@7P15q10i0q")
+_ADJUST = struct.Struct("@14P7i0q")
 
 
-class _Commit(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_new", "v_new", "k_cache", "v_cache", "slots", "path", "row_offsets")]
-                + [(n, ctypes.c_longlong * k) for n, k in (("k_new_stride", 3), ("v_new_stride", 3), ("k_stride", 4),
-                                                           ("v_stride", 4))]
-                + [("path_stride", ctypes.c_longlong)]
-                + [(n, ctypes.c_int) for n in ("layers", "B", "T", "rows", "S", "Hkv", "D", "pages", "page_size",
-                                               "dtype")])
-
-
-class _Adjust(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("logits", "out", "tokens", "history", "history_lens", "prompt_lens",
-                                                "repetition", "frequency", "presence", "bias_ids", "bias", "allowed",
-                                                "row_offsets", "mask")]
-                + [(n, ctypes.c_int) for n in ("B", "T", "rows", "V", "history_width", "biases", "dtype")])
-
-
-def _longs(values):
-    return (ctypes.c_longlong * len(values))(*values)
+def _or0(t: Optional[torch.Tensor]):
+    return 0 if t is None else t.data_ptr()
 
 
 _KV_DTYPES = {torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
@@ -1102,24 +1090,26 @@ def tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_
     dev, dt = q.device, q.dtype
     Hq, D = q.shape[-2:]
     B, T, rows = _pass_shape(row_offsets, max_rows, q.shape[:-2], "q", dev)
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need_strided(t, name, dtype=dt, dims=4, device=dev)
-    pages, page, Hkv, _ = k_cache.shape
-    if k_cache.shape[3] != D or v_cache.shape != k_cache.shape:
+    _need_strided(k_cache, "k_cache", dtype=dt, dims=4, device=dev)
+    _need_strided(v_cache, "v_cache", dtype=dt, dims=4, device=dev)
+    pages, page, Hkv, last = k_cache.shape
+    if last != D or v_cache.shape != k_cache.shape:
         raise ValueError(f"k_cache and v_cache must be [pages, page_size, Hkv, {D}], got {tuple(k_cache.shape)} "
                          f"and {tuple(v_cache.shape)}")
-    q_stride = _need_pass(q, "q", dt, q.shape, ragged, 0, dev)
-    shape = (*q.shape[:-2], Hkv, D)
+    q_shape = q.shape
+    q_stride = _need_pass(q, "q", dt, q_shape, ragged, 0, dev)
+    shape = (*q_shape[:-2], Hkv, D)
     kn_stride = _need_pass(k_new, "k_new", dt, shape, ragged, 0, dev)
     vn_stride = _need_pass(v_new, "v_new", dt, shape, ragged, 0, dev)
     _need(context_lens, "context_lens", dtype=torch.int32, device=dev)
     _need_strided(block_table, "block_table", dtype=torch.int32, dims=2, device=dev)
-    if (rows or ragged) and (tuple(context_lens.shape) != (B,) or block_table.shape[0] != B):
+    width = block_table.shape[1]
+    if (rows or ragged) and (context_lens.shape != (B,) or block_table.shape[0] != B):
         raise ValueError(f"context_lens and block_table must have {B} rows")
     _need_mask(mask, B, T, dev)
     empties = []
     if out is None:
-        empties = [(tuple(q.shape), dt)] + [(tuple(q.shape[:-1]), torch.float32)] * want_lse
+        empties = [(q_shape, dt), (q_shape[:-1], torch.float32)] if want_lse else [(q_shape, dt)]
     else:
         _need(out.out, "out.out", dtype=dt, shape=q.shape, device=dev)
         _need_out(out.lse, "lse", torch.float32, q.shape[:-1], dev)
@@ -1132,12 +1122,12 @@ def tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_
         status, ws, made = _loss_buffers(dev, handle, stream, need, workspace, empties)
         if out is None:
             out = AttentionOutput(made[0], made[1] if want_lse else None, status)
-        a = _Attention(_at(q), _at(k_new), _at(v_new), _at(k_cache), _at(v_cache), _at(out.out), _at(out.lse),
-                       _at(block_table), _at(context_lens), _at(row_offsets), _at(mask), _longs(q_stride),
-                       _longs(kn_stride), _longs(vn_stride), _longs(_strides(k_cache)), _longs(_strides(v_cache)),
-                       block_table.stride(0) if B > 1 else block_table.shape[1], B, T, rows, Hq, Hkv, D, pages, page,
-                       block_table.shape[1], _KV_DTYPES[dt], D ** -0.5 if scale is None else float(scale))
-        st = L.spec_tree_attention(ctypes.byref(a), _at(out.status), _at(ws), ws.nbytes, handle)
+        a = _ATTENTION.pack(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                            out.out.data_ptr(), _or0(out.lse), block_table.data_ptr(), context_lens.data_ptr(),
+                            _or0(row_offsets), _or0(mask), *q_stride, *kn_stride, *vn_stride, *_strides(k_cache),
+                            *_strides(v_cache), block_table.stride(0) if B > 1 else width, B, T, rows, Hq, Hkv, D,
+                            pages, page, width, _KV_DTYPES[dt], D ** -0.5 if scale is None else float(scale))
+        st = L.spec_tree_attention(a, _at(out.status), ws.data_ptr(), ws.nbytes, handle)
     _check(st, "spec_tree_attention")
     return out
 
@@ -1186,6 +1176,7 @@ def plan_cache(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table: 
     handle = _loss_stream(stream, dev)
     with _held(dev, handle):
         if out is None:
+            # no workspace is needed: any tensor stands for it
             status, _, made = _loss_buffers(dev, handle, stream, 0, block_table, [(s, torch.int32) for s in shapes])
             out = CachePlan(*made, status)
         st = L.spec_plan_cache(_at(context_lens), _at(new_lens), _at(block_table), _at(free_pages), _at(free_count), B,
@@ -1238,13 +1229,13 @@ def commit_cache(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor
     if status is not None:
         _need(status, "status", dtype=torch.int32, shape=(1,), device=dev)
     handle = _loss_stream(stream, dev)
-    one = [] if lead else [D]  # the single layer's stride
-    a = _Commit(_at(k_new), _at(v_new), _at(k_cache), _at(v_cache), _at(slots), _at(path) if S > 1 else None,
-                _at(row_offsets), _longs(one + kn_stride), _longs(one + vn_stride), _longs(one + _strides(k_cache)),
-                _longs(one + _strides(v_cache)),
-                0 if path is None else path.stride(0) if path.shape[0] > 1 else path.shape[1],
-                layers, B, T, rows, S, Hkv, D, pages, page, _KV_DTYPES[dt])
-    _check(L.spec_commit_cache(ctypes.byref(a), _at(status), handle), "spec_commit_cache")
+    one = () if lead else (D,)  # the single layer's stride
+    a = _COMMIT.pack(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr(),
+                     _or0(path) if S > 1 else 0, _or0(row_offsets), *one, *kn_stride, *one, *vn_stride, *one,
+                     *_strides(k_cache), *one, *_strides(v_cache),
+                     0 if path is None else path.stride(0) if path.shape[0] > 1 else path.shape[1],
+                     layers, B, T, rows, S, Hkv, D, pages, page, _KV_DTYPES[dt])
+    _check(L.spec_commit_cache(a, _at(status), handle), "spec_commit_cache")
 
 
 def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor, history: torch.Tensor, history_lens: torch.Tensor, *,
@@ -1305,10 +1296,10 @@ def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor, history: torch.Ten
     if status is not None:
         _need(status, "status", dtype=torch.int32, shape=(1,), device=dev)
     handle = _loss_stream(stream, dev)
-    a = _Adjust(_at(logits), _at(out), _at(tokens), _at(history), _at(history_lens), _at(prompt_lens), _at(repetition),
-                _at(frequency), _at(presence), _at(bias_ids), _at(bias), _at(allowed), _at(row_offsets), _at(mask),
-                B, T, rows, V, history.shape[1], biases, code)
-    _check(L.spec_adjust_logits(ctypes.byref(a), _at(status), handle), "spec_adjust_logits")
+    a = _ADJUST.pack(logits.data_ptr(), out.data_ptr(), tokens.data_ptr(), history.data_ptr(), history_lens.data_ptr(),
+                     *map(_or0, (prompt_lens, repetition, frequency, presence, bias_ids, bias, allowed, row_offsets, mask)),
+                     B, T, rows, V, history.shape[1], biases, code)
+    _check(L.spec_adjust_logits(a, _at(status), handle), "spec_adjust_logits")
     return out
 
 

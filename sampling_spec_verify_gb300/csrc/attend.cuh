@@ -323,71 +323,58 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
         const int t = t0 + i;
         step = base + (values ? place_v(i, n) : place_k(i, n));
         const uint32_t s = step % R, use = step / R, full = bar_full + 8 * s, dst = ring0 + s * Sh::kTile;
-        // a lane's box of the tile: its page and place
-        int cached = NK, at = 0, j0 = 0, fresh = 0, size = L.box;
-        if (t >= full_tiles) {
-          w.s.tail(t, cached, at, j0, fresh);
-          size = 8;
-        }
-        const int old = same_in_warp((cached + size - 1) / size), boxes = old + same_in_warp((fresh + 7) / 8);
-        const int pos = t * NK + lane * size, p = pos / A.page_size, place = pos - p * A.page_size;
-        const int place0 = t * NK % A.page_size;
-        int page = lane < old ? __ldg(table + p) : 0;
+        // The tile's cached tokens in whole boxes of the map, then in boxes of 8, and the pass's
+        // rows; a lane looks up the page and place of one box.
+        int cached = NK, at = 0, j0 = 0, fresh = 0;
+        if (t >= full_tiles) w.s.tail(t, cached, at, j0, fresh);
+        cached = same_in_warp(cached);
+        const int big = cached / L.box, small = (cached - big * L.box + 7) / 8, rows_new = same_in_warp((fresh + 7) / 8);
+        const int pos = t * NK + (lane < big ? lane * L.box : big * L.box + (lane - big) * 8), p = pos / A.page_size;
+        const int place = pos - p * A.page_size;
+        int page = lane < big + small ? __ldg(table + p) : 0;
         if (use > 0) ok = mbar_wait_bounded(bar_empty + 8 * s, (use - 1) & 1u, kAttendWaitNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         any = true;
         if (page < 0 || page >= A.pages) page = A.pages, bad = SPEC_DEV_BAD_PAGE;  // behind the end: zeros
-        if (t < full_tiles) {
-          mbar_expect(full, (uint32_t)(chunks * NK * 128));
-          const CUtensorMap* map = values ? &L.v : &L.k;
-          // box by box; the place within the page is stepped along, the page comes from its lane
-          auto page_of = [&](int bx) { return (int)__reduce_or_sync(0xffffffffu, lane == bx ? (uint32_t)page : 0u); };
-          int pl = place0, pg = page_of(0);
-          uint32_t to = dst;
-          const int fold = values ? L.fold_v : L.fold_k;
+        mbar_expect(full, (uint32_t)(chunks * (big * L.box + (small + rows_new) * 8) * 128));
+        auto of_lane = [&](int x, int from) { return (int)__reduce_or_sync(0xffffffffu, lane == from ? (uint32_t)x : 0u); };
+        int pl = t * NK % A.page_size, pg = of_lane(page, 0);  // the place is stepped along
+        uint32_t to = dst;
+        const CUtensorMap* map = values ? &L.v : &L.k;
+        const int fold = values ? L.fold_v : L.fold_k;
+        const int col0 = fold == 1 ? kh * chunks : 0, heads = fold == 1 ? 1 : A.Hkv, head0 = fold == 1 ? 0 : kh;
+#pragma unroll 1
+        for (int bx = 0; bx < big; ++bx) {
+          const int next = of_lane(page, bx + 1);
           if (fold) {
-            const int col0 = fold == 1 ? kh * chunks : 0, heads = fold == 1 ? 1 : A.Hkv, head0 = fold == 1 ? 0 : kh;
-#pragma unroll 1
-            for (int bx = 0; bx < old; ++bx) {
-              const int next = page_of(bx + 1);
-              tma_load_5d(to, map, 0, 0, col0, pl >> 3, pg * heads + head0, full);
-              pg = next;
-              pl += L.box;
-              if (pl == A.page_size) pl = 0;
-              to += L.box * chunks * 128;
-            }
+            tma_load_5d(to, map, 0, 0, col0, pl >> 3, pg * heads + head0, full);
           } else {
-#pragma unroll 1
-          for (int bx = 0; bx < old; ++bx) {
-            const int next = page_of(bx + 1);
 #pragma unroll
             for (int ch = 0; ch < CH; ++ch)
-              if (ch < chunks) tma_load_4d(to + ch * Sh::kChunk, map, ch * 64, pl, kh, pg, full);
-            pg = next;
-            pl += L.box;
-            if (pl == A.page_size) pl = 0;
-            to += L.box * 128;
+              if (ch < chunks) tma_load_4d(to + ch * L.col, map, ch * 64, pl, kh, pg, full);
           }
-          }
-        } else {
-          mbar_expect(full, (uint32_t)(chunks * boxes * 8 * 128));
-          const CUtensorMap *map = values ? &L.v8 : &L.k8, *map_new = values ? &L.v_new : &L.k_new;
-          const int row_at = same_in_warp(w.s.r0 + j0), at_u = same_in_warp(at);
+          pg = next;
+          pl += L.box;
+          if (pl == A.page_size) pl = 0;
+          to += L.box / 8 * L.row8;
+        }
+        map = values ? &L.v8 : &L.k8;
 #pragma unroll 1
-          for (int bx = 0; bx < boxes; ++bx) {
-            const int pg = (int)__reduce_or_sync(0xffffffffu, lane == bx ? (uint32_t)page : 0u);
-            const int pl = (int)__reduce_or_sync(0xffffffffu, lane == bx ? (uint32_t)place : 0u);
+        for (int bx = 0; bx < small; ++bx, to += L.row8) {
+          const int pg8 = of_lane(page, big + bx), pl8 = of_lane(place, big + bx);
 #pragma unroll
-            for (int ch = 0; ch < CH; ++ch) {
-              if (ch >= chunks) continue;
-              const uint32_t to = dst + ch * L.col;
-              if (bx < old)
-                tma_load_4d(to + bx * L.row8, map, ch * 64, pl, kh, pg, full);
-              else
-                tma_load_3d(to + (at_u / 8 + bx - old) * L.row8, map_new, ch * 64, kh, row_at + (bx - old) * 8, full);
-            }
-          }
+          for (int ch = 0; ch < CH; ++ch)
+            if (ch < chunks) tma_load_4d(to + ch * L.col, map, ch * 64, pl8, kh, pg8, full);
+        }
+        map = values ? &L.v_new : &L.k_new;
+        to = dst + same_in_warp(at) / 8 * L.row8;
+        const int row_at = same_in_warp(w.s.r0 + j0);
+#pragma unroll 1
+        for (int bx = 0; bx < rows_new; ++bx, to += L.row8) {
+#pragma unroll
+          for (int ch = 0; ch < CH; ++ch)
+            if (ch < chunks) tma_load_3d(to + ch * L.col, map, ch * 64, kh, row_at + bx * 8, full);
         }
         if (!values && i == (MT == 1 && n > 1 ? 1 : 0)) {  // q behind the first keys, which do not wait for the last segment
           const int first_row = same_in_warp(w.s.r0) + mg * tok_unit;  // of the pass
@@ -425,7 +412,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
     uint32_t base = 0, seg = 0, fixes[2] = {0, 0}, tiles = 0, cnt[2] = {0, 0}, done[2] = {0, 0}, segs[2] = {0, 0};
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, kAttendWaitNs));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_short(bar, parity & 1u, kAttendWaitNs));
       return ok;
     };
     // All products of result g with the values are done, none of them skipped: the buffer of
@@ -481,50 +468,72 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
       for (int m = 0; m < tiles_m; ++m) scores(base, m, MT == 2 ? m : kTurns ? 0 : tiles & 1);
       mma_commit(bar_empty + 8 * (base % R));
       if (n == 1) mma_commit(bar_q_free);
-      for (int i = 0; ok && i < n; ++i, ++tiles) {
-        const int t = t0 + i;
-        int keys = NK;
-        if (t >= full_tiles) {
-          int cached, at, j0, fresh;
-          w.s.tail(t, cached, at, j0, fresh);
-          keys = same_in_warp(fresh > 0 ? at + fresh : cached);
-        }
-        const uint32_t next_k = base + (i + 1 < n ? place_k(i + 1, n) : 0), this_v = base + place_v(i, n);
-        const int fixer = kTurns ? i & 1 : 0;
-        if (MT == 1 && !settle(kTurns ? (i + 1) & 1 : 0)) break;
-        if (MT == 1 && i + 1 < n) {
-          if (!full_at(place_k(i + 1, n))) break;
-          tc_fence_after();
-          scores(next_k, 0, kTurns ? (i + 1) & 1 : (tiles + 1) & 1);
-          mma_commit(bar_empty + 8 * (next_k % R));
-          if (i + 2 == n) mma_commit(bar_q_free);
-        }
-        if (t >= full_tiles) {
-          const int fb = GROUPS == 1 ? fixes[0] & 1 : fixer;  // one group: two barriers in turn
-          if (!wait(bar_fix + 8 * fb, GROUPS == 1 ? fixes[0] >> 1 : fixes[fixer])) break;
-          ++fixes[fixer];
-        }
-        if (!full_at(place_v(i, n))) break;
+      auto keys_of = [&](int t) {
+        if (t < full_tiles) return NK;
+        int cached, at, j0, fresh;
+        w.s.tail(t, cached, at, j0, fresh);
+        return same_in_warp(fresh > 0 ? at + fresh : cached);
+      };
+      if constexpr (MT == 2) {
+        for (int i = 0; ok && i < n; ++i) {
+          const int t = t0 + i;
+          const uint32_t this_v = base + place_v(i, n), next_k = base + place_k(i + 1, n);
+          if (t >= full_tiles && !wait(bar_fix, fixes[0]++)) break;
+          if (!full_at(place_v(i, n))) break;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if (m >= tiles_m) break;
-          const int g = kTurns ? i & 1 : m, sb = GROUPS == 1 ? tiles & 1 : g;
-          if (!wait(bar_p + 8 * sb, GROUPS == 1 ? tiles >> 1 : cnt[g])) break;
-          if (i == 0 && segs[m] > 0 && !wait(bar_o_free + 8 * m, segs[m] - 1)) break;
-          tc_fence_after();
-          weigh(this_v, g, sb, keys, kTurns ? i > 1 : i > 0);
-          ++cnt[g];
-          if (MT == 2 && i + 1 < n) {
-            if ((m == 0 && !full_at(place_k(i + 1, n))) || !settle(m)) break;
+          for (int m = 0; m < 2; ++m) {
+            if (m >= tiles_m || !wait(bar_p + 8 * m, cnt[m])) break;
+            if (i == 0 && segs[m] > 0 && !wait(bar_o_free + 8 * m, segs[m] - 1)) break;
             tc_fence_after();
-            scores(next_k, m, m);
+            weigh(this_v, m, m, keys_of(t), i > 0);
+            ++cnt[m];
+#if 1
+            if (i + 1 < n) {
+              if ((m == 0 && !full_at(place_k(i + 1, n))) || !settle(m)) break;
+              tc_fence_after();
+              scores(next_k, m, m);
+            }
+#endif
+          }
+          if (!ok) break;
+          mma_commit(bar_empty + 8 * (this_v % R));
+          if (i + 1 < n) {
+#if 0
+            if (!full_at(place_k(i + 1, n))) break;
+            for (int m = 0; m < tiles_m; ++m) {
+              if (!settle(m)) break;
+              tc_fence_after();
+              scores(next_k, m, m);
+            }
+            if (!ok) break;
+#endif
+            mma_commit(bar_empty + 8 * (next_k % R));
+            if (i + 2 == n) mma_commit(bar_q_free);
           }
         }
-        if (!ok) break;
-        mma_commit(bar_empty + 8 * (this_v % R));
-        if (MT == 2 && i + 1 < n) {
-          mma_commit(bar_empty + 8 * (next_k % R));
-          if (i + 2 == n) mma_commit(bar_q_free);
+      } else {
+        for (int i = 0; ok && i < n; ++i, ++tiles) {
+          const int t = t0 + i, g = kTurns ? i & 1 : 0, sb = kTurns ? g : tiles & 1;
+          const uint32_t this_v = base + place_v(i, n);
+          if (!settle(kTurns ? g ^ 1 : 0)) break;
+          if (i + 1 < n) {
+            const uint32_t next_k = base + place_k(i + 1, n);
+            if (!full_at(place_k(i + 1, n))) break;
+            tc_fence_after();
+            scores(next_k, 0, sb ^ 1);
+            mma_commit(bar_empty + 8 * (next_k % R));
+            if (i + 2 == n) mma_commit(bar_q_free);
+          }
+          if (t >= full_tiles) {  // one group: two barriers in turn
+            if (!wait(bar_fix + 8 * (kTurns ? g : fixes[0] & 1), kTurns ? fixes[g] : fixes[0] >> 1)) break;
+            ++fixes[g];
+          }
+          if (!full_at(place_v(i, n)) || !wait(bar_p + 8 * sb, kTurns ? cnt[g] : tiles >> 1)) break;
+          if (i == 0 && segs[0] > 0 && !wait(bar_o_free, segs[0] - 1)) break;
+          tc_fence_after();
+          weigh(this_v, g, sb, keys_of(t), kTurns ? i > 1 : i > 0);
+          ++cnt[g];
+          mma_commit(bar_empty + 8 * (this_v % R));
         }
       }
       base += 2 * n;
@@ -546,7 +555,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
     uint32_t base = 0, cnt = 0, seg = 0, fixes = 0;
     bool ok = true, left_open = false;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, kAttendWaitNs));
+      ok = __all_sync(0xffffffffu, mbar_wait_short(bar, parity & 1u, kAttendWaitNs));
       return ok;
     };
     const int tok = r / L.group, head = r - tok * L.group;

@@ -179,6 +179,15 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
       "r"(bytes)
       : "memory");
 }
+// mbar_wait_bounded for waits of a few hundred cycles: it does not sleep between its tries.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+  } while (global_timer_ns() - t0 <= limit_ns);
+  return false;
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }

@@ -23,6 +23,32 @@ def L():
     return ssv.lib()
 
 
+def structure(pointers, longs, ints, floats=()):
+    class C(ctypes.Structure):
+        _fields_ = ([(n, ctypes.c_void_p) for n in pointers.split()]
+                    + [(n, ctypes.c_longlong * k if k > 1 else ctypes.c_longlong) for n, k in longs]
+                    + [(n, ctypes.c_int) for n in ints.split()] + [(n, ctypes.c_float) for n in floats])
+    return C
+
+
+ATTENTION = structure("q k_new v_new k_cache v_cache out lse block_table context_lens row_offsets mask",
+                      (("q_stride", 2), ("k_new_stride", 2), ("v_new_stride", 2), ("k_stride", 3), ("v_stride", 3),
+                       ("table_stride", 1)),
+                      "B T rows Hq Hkv D pages page_size table_width dtype", ("scale",))
+COMMIT_T = structure("k_new v_new k_cache v_cache slots path row_offsets",
+                     (("k_new_stride", 3), ("v_new_stride", 3), ("k_stride", 4), ("v_stride", 4), ("path_stride", 1)),
+                     "layers B T rows S Hkv D pages page_size dtype")
+ADJUST_T = structure("logits out tokens history history_lens prompt_lens repetition frequency presence bias_ids bias "
+                     "allowed row_offsets mask", (), "B T rows V history_width biases dtype")
+
+
+def test_packed_arguments_are_the_structures():
+    for packed, c in ((ssv._ATTENTION, ATTENTION), (ssv._COMMIT, COMMIT_T), (ssv._ADJUST, ADJUST_T)):
+        assert packed.size == ctypes.sizeof(c)
+    a = ATTENTION.from_buffer_copy(ssv._ATTENTION.pack(*range(1, 35), 0.5))
+    assert (a.q, a.mask, list(a.v_stride), a.table_stride, a.B, a.dtype, a.scale) == (1, 11, [21, 22, 23], 24, 25, 34, 0.5)
+
+
 def struct(cls, fields, o):
     a = cls()
     for k, v in dict(fields, **o).items():
@@ -50,12 +76,12 @@ ATTN = dict(q=P, k_new=P, v_new=P, k_cache=P, v_cache=P, out=P, block_table=P, c
     (dict(v_stride=(2 ** 39, 128, 64)), INVALID), (dict(k_new_stride=(-128, 64)), INVALID),
     (dict(B=0, rows=0), OK), (dict(B=2, rows=0, row_offsets=P), OK)])
 def test_attention_refuses(L, o, want):
-    a = struct(ssv._Attention, ATTN, o)
+    a = struct(ATTENTION, ATTN, o)
     assert L.spec_tree_attention(ctypes.byref(a), None, P, 1 << 40, None) == want
 
 
 def test_attention_workspace(L):
-    a = struct(ssv._Attention, ATTN, {})
+    a = struct(ATTENTION, ATTN, {})
     need = L.spec_tree_attention_workspace_bytes(2, 3, 4, 2, 64)
     assert need > 0
     assert L.spec_tree_attention(ctypes.byref(a), None, None, need, None) == INVALID
@@ -100,7 +126,7 @@ COMMIT = dict(k_new=P, v_new=P, k_cache=P, v_cache=P, slots=P, k_new_stride=(512
     (dict(k_cache=ODD), INVALID), (dict(path=P, path_stride=1), INVALID), (dict(k_stride=(1, 2048, 128, 64)), INVALID),
     (dict(v_new_stride=(512, -8, 64)), INVALID), (dict(layers=0), OK), (dict(S=0), OK), (dict(B=0, rows=0), OK)])
 def test_commit_refuses(L, o, want):
-    a = struct(ssv._Commit, COMMIT, o)
+    a = struct(COMMIT_T, COMMIT, o)
     assert L.spec_commit_cache(ctypes.byref(a), None, None) == want
     assert L.spec_commit_cache(None, None, None) == INVALID
 
@@ -118,7 +144,7 @@ ADJUST = dict(logits=P, out=P, tokens=P, history=P, history_lens=P, B=2, T=3, ro
     (dict(history_lens=None), INVALID), (dict(logits=P + 1), INVALID), (dict(out=P + 2), INVALID),
     (dict(out=P + 1198), INVALID), (dict(B=0, rows=0), OK), (dict(rows=0, row_offsets=P), OK)])
 def test_adjust_refuses(L, o, want):
-    a = struct(ssv._Adjust, ADJUST, o)
+    a = struct(ADJUST_T, ADJUST, o)
     assert L.spec_adjust_logits(ctypes.byref(a), None, None) == want
     assert L.spec_adjust_logits(None, None, None) == INVALID
 
@@ -138,6 +164,9 @@ class Fake:
 
     def stride(self, d=None):
         return self._stride if d is None else self._stride[d]
+
+    def get_device(self):
+        return self.device.index
 
     def is_contiguous(self):
         return self._stride == torch.empty(self.shape, device="meta").stride()
