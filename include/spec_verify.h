@@ -688,7 +688,7 @@ spec_status_t spec_commit_cache(const spec_commit_t* args, uint32_t* dev_status,
 typedef struct {
   const void* logits;          /* [rows, V] dtype, contiguous */
   void* out;                   /* as logits (written); may be logits */
-  const int32_t* tokens;       /* [rows]: the pass's row tokens; -1: not counted */
+  const int32_t* tokens;       /* [rows]: the pass's row tokens; -1: not counted (a root that the history holds) */
   const int32_t* history;      /* [B, history_width]: tokens before the pass */
   const int32_t* history_lens; /* [B] */
   const int32_t* prompt_lens;  /* [B] or NULL (0): the history's first tokens that were given, not generated */

@@ -1249,8 +1249,8 @@ def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor, history: torch.Ten
     """Penalties for repeated tokens, biases and grammar masks on a pass's logits
     (see spec_adjust_logits in the C header), before ``truncate_logits`` and the
     verify.  logits [B, T, V] (bf16 or fp32) follow the pass's rows, whose tokens
-    are ``tokens`` int32 [B, T]; or [rows, V] and [rows] with ``row_offsets`` int32
-    [B + 1] and ``max_rows``.  history int32 [B, width] holds history_lens int32
+    are ``tokens`` int32 [B, T] (-1: not counted, such as a first row that the history
+    holds); or [rows, V] and [rows] with ``row_offsets`` int32 [B + 1] and ``max_rows``.  history int32 [B, width] holds history_lens int32
     [B] tokens, the first prompt_lens of them the prompt's; repetition, frequency
     and presence float32 [B]; bias_ids int32 [B, n] and bias float32 [B, n];
     allowed int32 [B, T, ceil(V / 32)] bits; mask uint8 [B, T, T] (a tree; None: a

@@ -83,6 +83,7 @@ struct AttendLaunch {
   int group, tok;      // heads a key head, rows of the pass in 128 query rows
   int box;             // tokens of a page that one copy takes
   int q_rows;          // rows of the pass that one copy of q takes
+  int beyond;          // a page that the maps do not have: reads as zeros
   int slot_rows;       // query rows of a partial result
   // One copy takes all 64-element columns of a box where a head's columns continue an
   // even dimension of the cache: 1, its heads (one behind the other in a token), 2, its
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         any = true;
-        if (page < 0 || page >= A.pages) page = A.pages, bad = SPEC_DEV_BAD_PAGE;  // behind the end: zeros
+        if (page < 0 || page >= A.pages) page = L.beyond, bad = SPEC_DEV_BAD_PAGE;
         mbar_expect(full, (uint32_t)(chunks * (big * L.box + (small + rows_new) * 8) * 128));
         auto of_lane = [&](int x, int from) { return (int)__reduce_or_sync(0xffffffffu, lane == from ? (uint32_t)x : 0u); };
         int pl = t * NK % A.page_size, pg = of_lane(page, 0);  // the place is stepped along
@@ -487,26 +488,15 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
             tc_fence_after();
             weigh(this_v, m, m, keys_of(t), i > 0);
             ++cnt[m];
-#if 1
             if (i + 1 < n) {
               if ((m == 0 && !full_at(place_k(i + 1, n))) || !settle(m)) break;
               tc_fence_after();
               scores(next_k, m, m);
             }
-#endif
           }
           if (!ok) break;
           mma_commit(bar_empty + 8 * (this_v % R));
           if (i + 1 < n) {
-#if 0
-            if (!full_at(place_k(i + 1, n))) break;
-            for (int m = 0; m < tiles_m; ++m) {
-              if (!settle(m)) break;
-              tc_fence_after();
-              scores(next_k, m, m);
-            }
-            if (!ok) break;
-#endif
             mma_commit(bar_empty + 8 * (next_k % R));
             if (i + 2 == n) mma_commit(bar_q_free);
           }

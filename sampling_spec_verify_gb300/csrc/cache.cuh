@@ -175,7 +175,8 @@ struct CommitParams {
 };
 
 // A warp per (layer, request, place): its row's keys and values, all heads, in
-// 16-byte pieces.  Bound: memory, the rows in and out.
+// 16-byte pieces, eight a lane in flight.  Bound: memory, the rows in and out.
+constexpr int kCommitBatch = 4;
 __global__ void __launch_bounds__(256) commit_kernel(const __grid_constant__ CommitParams P) {
   const spec_commit_t& A = P.a;
   const int lane = threadIdx.x & 31;
@@ -210,12 +211,24 @@ __global__ void __launch_bounds__(256) commit_kernel(const __grid_constant__ Com
     const uint16_t* vn = (const uint16_t*)A.v_new + layer * A.v_new_stride[0] + r * A.v_new_stride[1];
     uint16_t* kc = (uint16_t*)A.k_cache + layer * A.k_stride[0] + page * A.k_stride[1] + place * A.k_stride[2];
     uint16_t* vc = (uint16_t*)A.v_cache + layer * A.v_stride[0] + page * A.v_stride[1] + place * A.v_stride[2];
-    for (int p = lane; p < pieces; p += 32) {
-      const int h = p / per_head, d = (p - h * per_head) * 8;
-      const uint4 k = *(const uint4*)(kn + h * A.k_new_stride[2] + d);
-      const uint4 v = *(const uint4*)(vn + h * A.v_new_stride[2] + d);
-      *(uint4*)(kc + h * A.k_stride[3] + d) = k;
-      *(uint4*)(vc + h * A.v_stride[3] + d) = v;
+    for (int p0 = lane; p0 < pieces; p0 += 32 * kCommitBatch) {
+      uint4 k[kCommitBatch], v[kCommitBatch];
+#pragma unroll
+      for (int u = 0; u < kCommitBatch; ++u) {
+        const int p = p0 + 32 * u, h = p / per_head, d = (p - h * per_head) * 8;
+        if (p < pieces) {
+          k[u] = __ldcs((const uint4*)(kn + h * A.k_new_stride[2] + d));
+          v[u] = __ldcs((const uint4*)(vn + h * A.v_new_stride[2] + d));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kCommitBatch; ++u) {
+        const int p = p0 + 32 * u, h = p / per_head, d = (p - h * per_head) * 8;
+        if (p < pieces) {
+          *(uint4*)(kc + h * A.k_stride[3] + d) = k[u];
+          *(uint4*)(vc + h * A.v_stride[3] + d) = v[u];
+        }
+      }
     }
   }
 }

@@ -159,9 +159,10 @@ spec_status_t run_attend(const spec_attention_t& A, const AttendPlan& p, uint32_
   const bool cache = A.pages > 0;
   const void *kc = cache ? A.k_cache : A.k_new, *vc = cache ? A.v_cache : A.v_new;
   const long long pages = cache ? A.pages : 1, page = cache ? A.page_size : 1, heads = A.Hkv;
+  L.beyond = (int)pages;
   const int chunks = (A.D + 63) / 64;
   auto fold_of = [&](const long long* s) {
-    if (!cache || A.D % 64 || chunks == 1) return 0;
+    if (!cache || A.D % 64 || chunks == 1 || s[1] >= kMaxStride / 8) return 0;
     return s[2] == A.D ? 1 : s[0] == heads * s[2] && pages * heads <= 0x7FFFFFFFll ? 2 : 0;
   };
   L.fold_k = fold_of(A.k_stride);
@@ -342,7 +343,7 @@ spec_status_t spec_adjust_logits(const spec_adjust_t* args, uint32_t* dev_status
   int dev = 0;
   const int sms = device_sms(&dev);
   if (!sms) return SPEC_ERR_CUDA;
-  // Slices of 16 KB, twice that where reading the history for each of them would come to
+  // Slices of 8 KB, twice that where reading the history for each of them would come to
   // more than a quarter of the logits' bytes, and shorter ones where requests are few.
   const long long short_slice = ssv::adjust_slice(es), least = 16ll * A.history_width * A.B / ((long long)A.rows * es);
   const long long want = least > short_slice ? 2 * short_slice : short_slice;

@@ -88,7 +88,9 @@ def agree(c, got, dtype):
     ([7, 1, 0, 4], 5003, 100, F, 8, True, True, True), ([9] * 3, 50257, 2000, BF, 64, True, True, False),
     ([17] * 2, 50257, 2000, F, 64, True, True, False), ([8] * 20, 32000, 900, BF, 300, True, False, False),
     ([4, 3], 151936, 4000, BF, 1024, True, False, True), ([2], 129280, 3, F, 0, True, False, False),
-    ([40], 777, 0, BF, 3, False, True, False)])
+    ([40], 777, 0, BF, 3, False, True, False), ([70], 3001, 60, F, 9, True, True, False),
+    ([100, 65], 4096, 500, BF, 0, True, False, True), ([1] * 50, 20000, 9000, BF, 5, True, False, False),
+    ([1] * 50, 9001, 9000, F, 5, False, False, False)])
 def test_against_oracle(ssv, rows, V, H, dtype, biases, grammar, tree, ragged):
     c = case(V + len(rows), rows, V, H, dtype, biases, grammar, tree, spare=2 if ragged else 0)
     got, st = call(ssv, c, ragged)
@@ -107,6 +109,18 @@ def test_untouched_rows_are_copied_bit_by_bit(ssv):
     bits = torch.randint(-2 ** 15, 2 ** 15, (2, 4099), dtype=torch.int16, generator=torch.Generator().manual_seed(2))
     got, st = call(ssv, c, False, z=bits.view(BF).to(DEV))
     assert torch.equal(got.view(torch.int16).cpu(), bits) and st == 0
+
+
+@pytest.mark.parametrize("dtype,V,shift_in,shift_out", [(BF, 4096, 1, 1), (BF, 5001, 0, 3), (F, 4096, 1, 0), (F, 777, 2, 2)])
+def test_memory_off_16_bytes(ssv, dtype, V, shift_in, shift_out):
+    c = case(7, [3, 3], V, 200, dtype, 12, True, True)
+    want, _ = call(ssv, c, False)
+    big = torch.zeros(6 * V + 8, dtype=dtype, device=DEV)
+    z = big[shift_in:shift_in + 6 * V].view(6, V).copy_(c["z"])
+    out = torch.full((6 * V + 16,), 7.0, dtype=dtype, device=DEV)
+    got, st = call(ssv, c, False, z=z, out=out[8 + shift_out:8 + shift_out + 6 * V].view(2, 3, V))
+    assert torch.equal(got, want) and st == 0
+    assert bool((out[:8 + shift_out] == 7).all()) and bool((out[8 + shift_out + 6 * V:] == 7).all())
 
 
 def test_special_values(ssv):

@@ -178,6 +178,48 @@ def test_no_cache_at_all(ssv):
     assert e.out.shape[0] == 0
 
 
+def test_pages_of_an_empty_cache_read_as_zeros(ssv):
+    c = attention_case(12, [3], [20], 2, 1, 64, 16, BF, poison=False)
+    c["table"][:] = 0
+    c["k_cache"], c["v_cache"] = c["k_cache"][:0], c["v_cache"][:0]
+    args, kw = on_gpu(c)
+    o = ssv.tree_attention(*args, **kw)
+    torch.cuda.synchronize()
+    r = attention_oracle(dict(c, k_cache=torch.zeros(1, 16, 1, 64, dtype=BF), v_cache=torch.zeros(1, 16, 1, 64, dtype=BF)))
+    c["v_cache"] = torch.zeros(1, 16, 1, 64, dtype=BF)
+    tol = attention_bounds(c, r, BF)[0]
+    assert int(o.status.item()) == ssv.DEV_BAD_PAGE
+    assert (np.abs(o.out[0].double().cpu().numpy() - r.out) <= tol).all()
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,page,tree", [(128, 1, 16, 4, 128, 16, False), (48, 33, 8, 2, 128, 32, True),
+                                                    (64, 5, 8, 4, 192, 16, True), (96, 9, 4, 4, 64, 64, False)])
+def test_many_units_a_cta_give_the_same_bits(ssv, B, T, Hq, Hkv, D, page, tree):
+    """Units that follow each other in a CTA and go on in the next: their products, results and
+    maxima may not run into each other (a result read before its last product was such a fault)."""
+    ctx = [(37 * i) % 2100 for i in range(B)]
+    c = attention_case(13, [T] * B, ctx, Hq, Hkv, D, page, BF, tree=tree)
+    args, kw = on_gpu(c)
+    first = ssv.tree_attention(*args, want_lse=True, **kw)
+    q, kn, vn, kc, vc, table, lens = args
+    for b in range(0, B, 5):  # against 64 bits
+        n = int(lens[b])
+        ids = table[b, :-(-n // page)].long()
+        old = lambda t: t[ids].flatten(0, 1)[:n].double()  # noqa: E731
+        k, v = torch.cat([old(kc), kn[b].double()]), torch.cat([old(vc), vn[b].double()])
+        sees = torch.ones(T, n + T, dtype=torch.bool, device="cuda")
+        sees[:, n:] = kw["mask"][b] != 0 if tree else torch.ones(T, T, device="cuda").tril() != 0
+        k, v = (t.repeat_interleave(Hq // Hkv, dim=1) for t in (k, v))
+        s = torch.einsum("thd,nhd->htn", q[b].double(), k) * c["scale"]
+        p = torch.softmax(s.masked_fill(~sees, float("-inf")), dim=2)
+        want, mass = torch.einsum("htn,nhd->thd", p, v), torch.einsum("htn,nhd->thd", p, v.abs())
+        # a rounding of every weight and one of the result; scores within 2^-10 of themselves
+        assert bool(((first.out[b].double() - want).abs() <= 2.0 ** -8 * 1.01 * (mass + want.abs()) + 2.0 ** -8 * mass / 8).all())
+    for _ in range(30):
+        o = ssv.tree_attention(*args, want_lse=True, **kw)
+        assert torch.equal(o.out, first.out) and torch.equal(o.lse, first.lse)
+
+
 def test_same_bits_again_on_a_stream_and_in_a_graph(ssv):
     c = attention_case(9, [8, 8], [3000, 500], 8, 2, 128, 16, BF, tree=True)
     args, kw = on_gpu(c)
