@@ -66,7 +66,8 @@ struct AttendShape {
 };
 
 struct AttendSplit {  // a unit that goes on in the next CTAs
-  int b, unit, last;  // last: the CTA that holds its end; -1: none
+  int unit, last;  // last: the CTA that holds its end; -1: none
+  int r0, rows;    // of its request
 };
 
 struct AttendLaunch {
@@ -817,13 +818,13 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_o_free + 8 * (MT == 2 ? g : 0));
       if (opens && !whole && g == 0 && tid_g == 0) {
-        L.split[cta] = {w.b, w.unit, (int)((w.unit_end * ctas - 1) / total)};
+        L.split[cta] = {w.unit, (int)((w.unit_end * ctas - 1) / total), w.s.r0, w.s.rows};
         left_open = true;
       }
       base += 2 * n;
     }
     if (!ok) raise(L.status, SPEC_DEV_TIMEOUT);
-    if (g == 0 && tid_g == 0 && !left_open) L.split[cta] = {0, 0, -1};
+    if (g == 0 && tid_g == 0 && !left_open) L.split[cta] = {0, -1, 0, 0};
   }
   tc_fence_before();
   __syncthreads();
@@ -839,7 +840,6 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
 template <class E, int DP, int MT>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendLaunch L) {
   using El = Elem<E>;
-  constexpr int NK = AttendShape<DP, MT>::NK;
   const spec_attention_t& A = L.a;
   follow_previous();
   const AttendSplit split = L.split[blockIdx.x];
@@ -847,10 +847,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   const int lane = threadIdx.x & 31, x = blockIdx.y * 8 + (threadIdx.x >> 5), per = L.tok * L.group;
   const int m = x / per, r = x - m * per, tok = r / L.group, head = r - tok * L.group;
   if (m >= MT) return;
-  AttendSpan<NK> s;
-  s.load(A, split.b, L.tok * MT);
   const int kh = split.unit % A.Hkv, i_row = split.unit / A.Hkv * L.tok * MT + m * L.tok + tok;
-  if (i_row >= s.rows) return;
+  if (i_row >= split.rows) return;
   const int first = blockIdx.x, n = split.last - first + 1;
   const size_t at = m * 128 + r;
   auto slot = [&](int i) { return ((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * L.slot_rows + at; };
@@ -880,7 +878,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const long long out_row = (long long)(s.r0 + i_row) * A.Hq + kh * L.group + head;
+  const long long out_row = (long long)(split.r0 + i_row) * A.Hq + kh * L.group + head;
   E* to = (E*)A.out + out_row * A.D + lane * PER;
 #pragma unroll
   for (int j = 0; j < PER; j += 2)

@@ -31,8 +31,9 @@ __device__ __forceinline__ PlanRequest plan_request(const PlanParams& P, int len
   const long long room = (long long)P.width * P.page, after = (long long)len + added;
   PlanRequest r;
   r.fits = len >= 0 && len <= room && after >= 0 && after <= room && added <= P.T;
-  r.held = r.fits ? (int)(((long long)len + P.page - 1) / P.page) : 0;
-  r.want = r.fits ? (int)((after + P.page - 1) / P.page) : 0;
+  // below 2^31 each, as width * page is: 32 bits do
+  r.held = r.fits ? (int)(((uint32_t)len + (uint32_t)P.page - 1u) / (uint32_t)P.page) : 0;
+  r.want = r.fits ? (int)(((uint32_t)after + (uint32_t)P.page - 1u) / (uint32_t)P.page) : 0;
   return r;
 }
 
@@ -94,6 +95,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
       nd += r.need();
     }
   };
+  // whole 16-byte pieces where both sides allow, entries at the ends
+  auto copy = [&](const int32_t* from, int32_t* to, long long n, int at, int step) {
+    const bool even = ((reinterpret_cast<uintptr_t>(from) | reinterpret_cast<uintptr_t>(to)) & 15) == 0;
+    const long long pieces = even ? n / 4 : 0;
+    const int4* from4 = reinterpret_cast<const int4*>(from);
+    int4* to4 = reinterpret_cast<int4*>(to);
+#pragma unroll 4
+    for (long long i = at; i < pieces; i += step) to4[i] = from4[i];
+    for (long long i = pieces * 4 + at; i < n; i += step) to[i] = from[i];
+  };
   // entry i of the stack once the pages given back lie on it
   auto stack_at = [&](int i) -> int {
     if (i < count) return P.free[i];
@@ -120,10 +131,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
     const int needs = sound ? r.need() : 0;
     const bool served = sound && r.fits && (needs == 0 || nd + needs <= have);
     const long long row = (long long)b * P.width;
-    const int kept = served && r.want > r.held ? r.held : P.width;  // entries that stay
-    if (table_copy)
-      for (int i = tid; i < P.width; i += kPlanThreads)
-        if (i < kept || i >= r.want) P.out_table[row + i] = P.table[row + i];
+    if (table_copy) {
+      copy(P.table + row, P.out_table + row, P.width, tid, kPlanThreads);
+      if (served && needs) __syncthreads();  // the new pages go over the copy
+    }
     if (served)
       for (int i = tid; i < needs; i += kPlanThreads) P.out_table[row + r.held + i] = stack_at(have - 1 - (nd + i));
     if (sound)
@@ -146,9 +157,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
   }
   // the stack below the pages given back, and above them
   if (P.out_free != P.free) {
-    const int gap0 = sound ? count : 0, gap1 = sound ? have : 0;
-    for (long long i = (long long)blockIdx.x * kPlanThreads + tid; i < P.capacity; i += (long long)gridDim.x * kPlanThreads)
-      if (i < gap0 || i >= gap1) P.out_free[i] = P.free[i];
+    const int at = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
+    const int gap0 = sound ? count : 0, gap1 = sound ? have : 0, even = min((gap1 + 3) & ~3, P.capacity);
+    copy(P.free, P.out_free, gap0, at, step);
+    for (int i = gap1 + at; i < even; i += step) P.out_free[i] = P.free[i];
+    copy(P.free + even, P.out_free + even, P.capacity - even, at, step);
   }
   // the new count: what is needed, or where that is too much, the longest start of it that is there
   if (blockIdx.x == 0) {
