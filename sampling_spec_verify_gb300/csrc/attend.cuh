@@ -13,21 +13,28 @@
 //
 // All query rows that share a key head (the pass's rows times the group's
 // heads) form tiles of 128 rows, so that the cache is read once for all of
-// them.  Bound: the cache's bytes, up to about 128 rows a key head; the
-// exponentials beyond.
+// them.  Bound: the cache's bytes, up to about 128 rows a key head; beyond, the
+// products and the softmax.
 //
 // The batch is cut into units (request, key head, 128 or 256 rows), a unit into
-// tiles of keys, and all tiles, one unit behind the other, into equal shares, one a
+// tiles of keys, and all units, one behind the other, into shares of equal cost, one a
 // CTA and SM.  A unit that spans CTAs leaves one partial result (out, m, sum) a
 // CTA; a second launch joins them.  The shares come from the lengths on the
 // device: nothing of the launch depends on them, and the order of the sums
 // follows from the lengths alone.
 //
-// A CTA: two warps load, one the keys and q, one the values (through a ring of
+// A CTA: one warp loads q and the keys and one the values (through a ring of
 // shared-memory tiles by TMA; a page's part of a tile is a box of the tensor map),
 // one issues the products (scores into tensor memory, weights times values
-// with the weights read from tensor memory), two warpgroups do the softmax, a
+// with the weights read from tensor memory), and two warpgroups do the softmax, a
 // thread per row.
+//
+// Measured with heads of 128 in bf16: 128 requests of one token over 64 to 4096 cached
+// ones (32/8 heads, pages of 16) 186 us, 5.9 TB/s; 2 x 8 rows over 131072 (64/8 heads)
+// 173 us, 6.2 TB/s; 32 trees of 33 rows over 512 to 8192 (132 query rows a key head: two
+// row tiles) 162 us, where the cache alone would take 89: there a product of scores takes
+// 64 cycles, both its operands in shared memory, and each row tile's next scores wait
+// for its last product.
 #pragma once
 
 #include "loss_common.cuh"
