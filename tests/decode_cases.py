@@ -47,6 +47,10 @@ def attention_case(seed, rows, ctx, Hq, Hkv, D, page, dtype, tree=False, ragged=
         vc[~live] = float("nan")
     if layout == "hnd":
         kc, vc = (t.transpose(1, 2).contiguous().transpose(1, 2) for t in (kc, vc))
+    elif layout == "mixed":  # keys token by token, values head by head
+        vc = vc.transpose(1, 2).contiguous().transpose(1, 2)
+    elif layout == "apart":  # heads that no even dimension continues
+        kc, vc = (torch.cat([t, t[:, :, :, :8]], 3)[..., :D] for t in (kc, vc))
     elif layout == "joint":  # one tensor, keys and values side by side
         joint = torch.stack([kc, vc], 1).contiguous()
         kc, vc = joint[:, 0], joint[:, 1]

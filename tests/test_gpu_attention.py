@@ -56,6 +56,12 @@ CASES = [
     ([0, 4, 0], [9, 700, 9], 4, 2, 96, 48, HF, dict(ragged=True, T=9, spare_rows=130)),
     ([4, 4], [200, 500], 8, 2, 128, 16, BF, dict(layout="hnd")),
     ([4, 4], [200, 500], 8, 2, 64, 16, HF, dict(layout="joint", strided=True, tree=True)),
+    ([4, 4], [200, 500], 8, 2, 128, 16, HF, dict(layout="joint", strided=True)),
+    ([3, 3], [333, 70], 8, 2, 128, 32, BF, dict(layout="mixed", tree=True)),
+    ([3, 3], [333, 70], 8, 2, 256, 32, BF, dict(layout="hnd")),
+    ([3, 3], [333, 70], 8, 2, 192, 64, HF, dict(layout="joint", tree=True)),
+    ([3, 3], [333, 470], 8, 2, 128, 64, BF, dict(layout="apart", tree=True)),
+    ([70, 70], [333, 470], 4, 2, 128, 128, BF, dict(layout="hnd", tree=True)),
     ([9] * 40, list(range(0, 400, 10)), 4, 2, 64, 8, BF, dict(tree=True)),
     ([2], [6000], 4, 1, 128, 160, BF, {}),
     ([20, 20], [300, 170], 30, 2, 192, 16, BF, dict(tree=True)),
