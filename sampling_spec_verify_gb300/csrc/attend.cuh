@@ -859,11 +859,17 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   const int first = blockIdx.x, n = split.last - first + 1;
   const size_t at = m * 128 + r;
   auto slot = [&](int i) { return ((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * L.slot_rows + at; };
+  constexpr int PER = DP / 32, kAhead = 4;
+  // The first parts are asked for with the maxima: most units have no more.
+  float first_parts[kAhead][PER];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+    for (int j = 0; j < PER; ++j) first_parts[i][j] = i < n ? L.part[slot(i) * DP + lane * PER + j] : 0.0f;
   float top = -INFINITY;
   for (int i = lane; i < n; i += 32) top = fmaxf(top, L.stat[slot(i)].x);
   top = redux_max_f32(top);
   const float off = top == -INFINITY ? 0.0f : top;
-  constexpr int PER = DP / 32;
   float acc[PER] = {}, sum = 0.0f, exact = 0.0f;
   for (int i0 = 0; i0 < n; i0 += 32) {
     float wt = 0.0f, z = 0.0f, e = 0.0f;
@@ -875,13 +881,25 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     }
     sum += warp_sum(z);
     exact += warp_sum(e);
+    int from = 0;
+    if (i0 == 0) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, wt, i);
+        if (i < n) {
+#pragma unroll
+          for (int j = 0; j < PER; ++j) acc[j] = fmaf(first_parts[i][j], wi, acc[j]);
+        }
+      }
+      from = kAhead;
+    }
     const int cnt = min(32, n - i0);
 #pragma unroll 4
-    for (int i = 0; i < cnt; ++i) {
+    for (int i = from; i < cnt; ++i) {
       const float wi = __shfl_sync(0xffffffffu, wt, i);
-      const float* from = L.part + slot(i0 + i) * DP + lane * PER;
+      const float* part = L.part + slot(i0 + i) * DP + lane * PER;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) acc[j] = fmaf(from[j], wi, acc[j]);
+      for (int j = 0; j < PER; ++j) acc[j] = fmaf(part[j], wi, acc[j]);
     }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;

@@ -192,7 +192,8 @@ spec_status_t run_attend(const spec_attention_t& A, const AttendPlan& p, uint32_
   ssv::attend_kernel<E, DP, MT><<<grid, Sh::kThreads, Sh::kSmem, st>>>(L);
   if (count_launch(cudaGetLastError()) != cudaSuccess) return SPEC_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)((MT * L.q_rows * L.group + 7) / 8));
+  const int unit_rows = A.T < MT * p.tok ? A.T : MT * p.tok;  // of the pass, at most
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)((unit_rows * L.group + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

@@ -281,3 +281,31 @@ def test_given_scale(ssv):
     check(ssv, c, BF, scale=0.0)
     c["scale"] = -0.2
     check(ssv, c, BF, scale=-0.2)
+
+
+def test_calls_at_once_on_streams_and_threads(ssv):
+    import threading
+
+    cases = [on_gpu(attention_case(20 + i, [4 + i] * 6, [500 * i + 90 * j for j in range(6)], 8, 2, 128, 16, BF, tree=True))
+             for i in range(4)]
+    want = [ssv.tree_attention(*a, **kw).out for a, kw in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[] for _ in cases]
+    for _ in range(10):
+        for i, (a, kw) in enumerate(cases):
+            got[i].append(ssv.tree_attention(*a, stream=streams[i], **kw).out)
+
+    def work(i):  # all threads on the default stream, whose workspace they share
+        a, kw = cases[i]
+        for _ in range(10):
+            got[i].append(ssv.tree_attention(*a, **kw).out)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    for w, outs in zip(want, got):
+        assert len(outs) == 20 and all(torch.equal(w, o) for o in outs)
