@@ -228,8 +228,6 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
   if (blockIdx.x == 0) raise(P.status, bad);  // every slice sees the same
   __syncthreads();
 
-  // Counts that are the same for all rows become what they add, the last bit of its fraction
-  // (2^-23 of it) whether the repetition penalty goes before.
   // The touched tokens in their order, a word of the bitmap a thread.
   int n_list = 0;
   {
@@ -271,6 +269,8 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
     if (own >= 0) own_word = counts[own];
   }
   __syncthreads();
+  // Counts that are the same for all rows become what they add, the last bit of its fraction
+  // (2^-23 of it) whether the repetition penalty goes before.
   for (int q = tid; q < n_list; q += threads) {
     const int v = list[q];
     if ((by_row[v >> 5] >> (v & 31)) & 1u) continue;

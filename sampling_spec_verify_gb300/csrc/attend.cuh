@@ -631,12 +631,14 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           const float grown = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
           const bool grow = live && grown > top && !((grown - top) * L.c <= 8.0f);
           if (grow) {
-            fix = top == -INFINITY ? 0.0f : ex2((top - grown) * L.c);
+            // by the rounded products that the weights are taken off, so that their rounding
+            // (of scores in the hundreds more than a weight's) cancels
+            fix = top == -INFINITY ? 0.0f : ex2(__fmul_rn(top, L.c) - __fmul_rn(grown, L.c));
             top = grown;
             total_w *= fix;
             exact_w *= fix;
           }
-          const float off = top == -INFINITY ? 0.0f : top * L.c;
+          const float off = top == -INFINITY ? 0.0f : __fmul_rn(top, L.c);
           const f32x2 c2 = f2(L.c, L.c), off2 = f2(-off, -off);
           f32x2 s0 = 0, s1 = 0, e0 = 0, e1 = 0;
 #pragma unroll 1
@@ -749,8 +751,8 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
         if (lane == 0) mbar_arrive(bar_join);
         if (!wait(bar_join, seg)) break;
         const float4 other = row_stat[seg & 1][g ^ 1][r];
-        const float both = fmaxf(top, other.x), off = both == -INFINITY ? 0.0f : both;
-        const float f = ex2((top - off) * L.c), fo = ex2((other.x - off) * L.c);
+        const float both = fmaxf(top, other.x), off = both == -INFINITY ? 0.0f : __fmul_rn(both, L.c);
+        const float f = ex2(__fmul_rn(top, L.c) - off), fo = ex2(__fmul_rn(other.x, L.c) - off);
         total_w = total_w * f + other.y * fo;
         exact_w = exact_w * f + other.z * fo;
         top = both;
@@ -814,7 +816,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           __syncwarp();  // the loads are the whole warp's
         }
         if (live && (!kTurns || g == 0)) {
-          const float top2 = top == -INFINITY ? -INFINITY : top * L.c;
+          const float top2 = __fmul_rn(top, L.c);
           if (!whole)
             L.stat[slot] = make_float4(top2, total_w, exact_w, 0.0f);
           else if (A.lse)

@@ -64,7 +64,7 @@ ATTN = dict(q=P, k_new=P, v_new=P, k_cache=P, v_cache=P, out=P, block_table=P, c
 
 @pytest.mark.parametrize("o,want", [
     (dict(B=-1), INVALID), (dict(T=0), INVALID), (dict(rows=-1), INVALID), (dict(rows=5), INVALID),
-    (dict(Hkv=0), INVALID), (dict(Hq=5), INVALID), (dict(D=0), INVALID), (dict(D=60), UNSUPPORTED),
+    (dict(Hkv=0), INVALID), (dict(Hq=5), INVALID), (dict(Hq=258), UNSUPPORTED), (dict(D=0), INVALID), (dict(D=60), UNSUPPORTED),
     (dict(D=264), UNSUPPORTED), (dict(page_size=0), INVALID), (dict(page_size=12), UNSUPPORTED),
     (dict(T=1025, rows=2050), UNSUPPORTED), (dict(table_width=-1), INVALID), (dict(table_stride=8), INVALID),
     (dict(dtype=0), INVALID), (dict(dtype=3), INVALID), (dict(scale=NAN), INVALID), (dict(scale=INF), INVALID),

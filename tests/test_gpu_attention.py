@@ -65,6 +65,7 @@ CASES = [
     ([9] * 40, list(range(0, 400, 10)), 4, 2, 64, 8, BF, dict(tree=True)),
     ([2], [6000], 4, 1, 128, 160, BF, {}),
     ([20, 20], [300, 170], 30, 2, 192, 16, BF, dict(tree=True)),
+    ([6], [2000], 8, 2, 128, 16, BF, dict(spread=4000.0)),
     ([6], [400], 8, 2, 128, 16, HF, dict(spread=40.0)),  # one key takes nearly all of the weight
 ]
 
