@@ -654,31 +654,37 @@ def _loss_buffers(device, handle, given, nbytes, workspace, empties):
     cached per (device, stream) and never zeroed, so they are not the ones of
     the other calls.  Inside a stream capture nothing is cached: the memory
     belongs to the graph."""
+    if given is not None:
+        with torch.cuda.stream(given):
+            return _buffers_here(device, handle, nbytes, workspace, empties)
+    return _buffers_here(device, handle, nbytes, workspace, empties)
+
+
+def _buffers_here(device, handle, nbytes, workspace, empties):
     key = (device.index, handle)
-    with _Nothing() if given is None else torch.cuda.stream(given):
-        capturing = torch.cuda.is_current_stream_capturing()  # of the call's own stream
-        made = [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in empties]
-        status = None
-        if made:
-            if capturing:
-                status = torch.zeros((1,), dtype=torch.int32, device=device)
-            else:
-                block = _STATUS.get(key)
-                if not block:
-                    with torch.inference_mode(False):  # later calls may not be in it, and own their words too
-                        block = list(torch.zeros((_STATUS_WORDS, 1), dtype=torch.int32, device=device).unbind())
-                    _STATUS[key] = block
-                status = block.pop()
-        if workspace is None:
-            if capturing:
+    capturing = torch.cuda.is_current_stream_capturing()  # of the call's own stream
+    made = [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in empties]
+    status = None
+    if made:
+        if capturing:
+            status = torch.zeros((1,), dtype=torch.int32, device=device)
+        else:
+            block = _STATUS.get(key)
+            if not block:
+                with torch.inference_mode(False):  # later calls may not be in it, and own their words too
+                    block = list(torch.zeros((_STATUS_WORDS, 1), dtype=torch.int32, device=device).unbind())
+                _STATUS[key] = block
+            status = block.pop()
+    if workspace is None:
+        if capturing:
+            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        else:
+            workspace = _SCRATCH.get(key)
+            if workspace is None or workspace.numel() < nbytes:
+                _SCRATCH.pop(key, None)
+                workspace = None  # the old one goes before the new one comes
                 workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-            else:
-                workspace = _SCRATCH.get(key)
-                if workspace is None or workspace.numel() < nbytes:
-                    _SCRATCH.pop(key, None)
-                    workspace = None  # the old one goes before the new one comes
-                    workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-                    _SCRATCH[key] = workspace
+                _SCRATCH[key] = workspace
     return status, workspace, made
 
 
@@ -999,7 +1005,8 @@ def _need_strided(t: torch.Tensor, name: str, dtype=None, dims=None, device=None
 
 def _strides(t: torch.Tensor):
     """Strides of all dimensions but the last; one of size 1 is never stepped along."""
-    return [s if n > 1 else t.shape[-1] for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+    shape, strides = t.shape, t.stride()[:-1]
+    return strides if min(shape) > 1 else [s if n > 1 else shape[-1] for n, s in zip(shape, strides)]
 
 
 def _need_pass(t: torch.Tensor, name: str, dtype, shape, ragged: bool, lead: int, device):
@@ -1177,8 +1184,10 @@ def plan_cache(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table: 
     with _held(dev, handle):
         if out is None:
             # no workspace is needed: any tensor stands for it
-            status, _, made = _loss_buffers(dev, handle, stream, 0, block_table, [(s, torch.int32) for s in shapes])
-            out = CachePlan(*made, status)
+            status, _, made = _loss_buffers(dev, handle, stream, 0, block_table, [((B, T), torch.int32)])
+            with _Nothing() if stream is None else torch.cuda.stream(stream):
+                like = torch.empty_like
+                out = CachePlan(like(block_table), like(free_pages), like(free_count), like(context_lens), made[0], status)
         st = L.spec_plan_cache(_at(context_lens), _at(new_lens), _at(block_table), _at(free_pages), _at(free_count), B,
                                T, width, free_pages.numel(), int(page_size), _at(out.block_table), _at(out.free_pages),
                                _at(out.free_count), _at(out.context_lens), _at(out.slots), _at(out.status), handle)
