@@ -12,10 +12,10 @@
 // touched tokens listed; then each row's listed tokens are computed in its stage, a
 // lane per token, and a grammar's bits applied to whole vectors.  Bound: memory, the
 // logits in and out, as long as there is little to compute (128 x 8 x 129280 in bf16 without
-// rules 94 us, 5.6 TB/s); with a grammar, 4000 tokens of history and 300 biases 156 us, by
+// rules 91 us, 5.8 TB/s); with a grammar, 4000 tokens of history and 300 biases 152 us, by
 // instructions and barriers.  The form that passes logits through registers and computes
-// touched ones in between took as long there and a quarter longer for 16 trees of 17 x 50257
-// (78 us against 62), where the touched tokens lie close together.
+// touched ones in between took 157 us there and a quarter longer for 16 trees of 17 x 50257
+// (78 us against 63), where the touched tokens lie close together.
 #pragma once
 
 #include <type_traits>
@@ -27,12 +27,13 @@ namespace ssv {
 
 constexpr int kAdjustThreads = 512;  // at most
 // Threads of a CTA; a word of a row's grammar each.
-inline int adjust_threads(int slice) { return slice > 4096 ? 512 : 256; }
+inline int adjust_threads(int slice) { return slice > 8192 ? 512 : 256; }
 constexpr int kAdjustMaxRows = 1024, kAdjustMaxBiases = 1024;
 constexpr int kAdjustStages = 3, kAdjustNear = 64;
 constexpr uint64_t kAdjustWaitNs = 2000000000ull;
-// Tokens a CTA: 8 KB of logits, or twice that.
-__host__ __device__ constexpr int adjust_slice(int elem) { return 8192 / elem; }
+// Tokens a CTA: 16 KB of logits, or twice that.  (Half of it, and twice the threads for
+// as much, took 3% longer for 128 x 8 x 129280.)
+__host__ __device__ constexpr int adjust_slice(int elem) { return 16384 / elem; }
 
 struct AdjustParams {
   spec_adjust_t a;
@@ -353,12 +354,12 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
       r.out[v] = !keep ? El::neg_inf() : hit ? El::from_f32(computed(i, v, El::to_f32(was))) : was;
     }
     if (!r.vecs) {
-      ok = ok && mbar_wait_bounded(bar0 + 8 * (i % kAdjustStages), (uint32_t)(i / kAdjustStages) & 1u, kAdjustWaitNs);
+      ok = ok && mbar_wait_short(bar0 + 8 * (i % kAdjustStages), (uint32_t)(i / kAdjustStages) & 1u, kAdjustWaitNs);
     } else {
       unsigned char* here = raw + i % kAdjustStages * stage;
       E* x = reinterpret_cast<E*>(here + r.pad);  // by token of the slice
       const int from = r.lead, to = r.lead + r.vecs * PV;
-      ok = mbar_wait_bounded(bar0 + 8 * (i % kAdjustStages), (uint32_t)(i / kAdjustStages) & 1u, kAdjustWaitNs);
+      ok = mbar_wait_short(bar0 + 8 * (i % kAdjustStages), (uint32_t)(i / kAdjustStages) & 1u, kAdjustWaitNs);
       if (ok) {
 #pragma unroll
         for (int u = 0; u < kHold; ++u)

@@ -344,7 +344,7 @@ spec_status_t spec_adjust_logits(const spec_adjust_t* args, uint32_t* dev_status
   int dev = 0;
   const int sms = device_sms(&dev);
   if (!sms) return SPEC_ERR_CUDA;
-  // Slices of 8 KB, twice that where reading the history for each of them would come to
+  // Slices of 16 KB, twice that where reading the history for each of them would come to
   // more than a quarter of the logits' bytes, and shorter ones where requests are few.
   const long long short_slice = ssv::adjust_slice(es), least = 16ll * A.history_width * A.B / ((long long)A.rows * es);
   const long long want = least > short_slice ? 2 * short_slice : short_slice;
