@@ -418,7 +418,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
     const uint32_t idesc_o = mma_idesc_128(kBf16, (A.D + 15) & ~15, true);
     const int ksteps = (A.D + 15) / 16;
     // per result: products with the values issued, known to be done; segments
-    uint32_t base = 0, seg = 0, fixes[2] = {0, 0}, tiles = 0, cnt[2] = {0, 0}, done[2] = {0, 0}, segs[2] = {0, 0};
+    uint32_t slot = 0, phase = 0, seg = 0, fixes[2] = {0, 0}, tiles = 0, cnt[2] = {0, 0}, done[2] = {0, 0}, segs[2] = {0, 0};
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait_short(bar, parity & 1u, kAttendWaitNs));
@@ -434,9 +434,14 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
       }
       return true;
     };
+    // The ring's entries are taken in their order.
+    auto next_entry = [&]() { return wait(bar_full + 8 * slot, phase); };
+    auto pass = [&]() {
+      if (++slot == R) slot = 0, phase ^= 1;
+    };
     // scores of a tile against row tile m, into buffer sb
     auto scores = [&](uint32_t at, int m, int sb) {
-      const uint32_t k0 = ring0 + at % R * Sh::kTile, qm = q0 + m * CH * Sh::kQChunk, d = tmem + sb * NK;
+      const uint32_t k0 = ring0 + at * Sh::kTile, qm = q0 + m * CH * Sh::kQChunk, d = tmem + sb * NK;
       // descriptors count in 16 bytes
       const uint64_t dq = smem_desc(desc_q, qm), dk = smem_desc(desc_k, k0);
       const uint32_t col = (uint32_t)L.col >> 4;
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
       mma_commit(bar_s + 8 * sb);
     };
     auto weigh = [&](uint32_t at, int g, int sb, int keys, bool more) {
-      const uint32_t v0 = ring0 + at % R * Sh::kTile, d = tmem + Sh::kOut + g * DP, p = tmem + sb * NK;
+      const uint32_t v0 = ring0 + at * Sh::kTile, d = tmem + Sh::kOut + g * DP, p = tmem + sb * NK;
       const uint64_t dv = smem_desc(desc_v, v0);
       const uint32_t step = (uint32_t)L.row8 >> 3;
       if (keys == NK) {
@@ -468,14 +473,14 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
       const int t0 = same_in_warp(w.t0), n = same_in_warp(w.t1) - t0, mg = same_in_warp(w.unit) / A.Hkv;
       const int full_tiles = same_in_warp(w.s.full);
       const int tiles_m = MT == 1 ? 1 : min(MT, (same_in_warp(w.s.rows) - mg * tok_unit + L.tok - 1) / L.tok);
-      auto full_at = [&](int place) { return wait(bar_full + 8 * ((base + place) % R), (base + place) / R); };
-      if (!full_at(place_k(0, n)) || !wait(bar_q, seg)) break;
+      if (!next_entry() || !wait(bar_q, seg)) break;
       for (int g = 0; ok && g < GROUPS; ++g) settle(g);
       if (!ok) break;
       tc_fence_after();
       // tiles counts those before this segment: buffers take turns where one group has two
-      for (int m = 0; m < tiles_m; ++m) scores(base, m, MT == 2 ? m : kTurns ? 0 : tiles & 1);
-      mma_commit(bar_empty + 8 * (base % R));
+      for (int m = 0; m < tiles_m; ++m) scores(slot, m, MT == 2 ? m : kTurns ? 0 : tiles & 1);
+      mma_commit(bar_empty + 8 * slot);
+      pass();
       if (n == 1) mma_commit(bar_q_free);
       auto keys_of = [&](int t) {
         if (t < full_tiles) return NK;
@@ -486,9 +491,10 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
       if constexpr (MT == 2) {
         for (int i = 0; ok && i < n; ++i) {
           const int t = t0 + i;
-          const uint32_t this_v = base + place_v(i, n), next_k = base + place_k(i + 1, n);
           if (t >= full_tiles && !wait(bar_fix, fixes[0]++)) break;
-          if (!full_at(place_v(i, n))) break;
+          if (!next_entry()) break;
+          const uint32_t this_v = slot;
+          pass();
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             if (m >= tiles_m || !wait(bar_p + 8 * m, cnt[m])) break;
@@ -497,44 +503,44 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
             weigh(this_v, m, m, keys_of(t), i > 0);
             ++cnt[m];
             if (i + 1 < n) {
-              if ((m == 0 && !full_at(place_k(i + 1, n))) || !settle(m)) break;
+              if ((m == 0 && !next_entry()) || !settle(m)) break;
               tc_fence_after();
-              scores(next_k, m, m);
+              scores(slot, m, m);
             }
           }
           if (!ok) break;
-          mma_commit(bar_empty + 8 * (this_v % R));
+          mma_commit(bar_empty + 8 * this_v);
           if (i + 1 < n) {
-            mma_commit(bar_empty + 8 * (next_k % R));
+            mma_commit(bar_empty + 8 * slot);
+            pass();
             if (i + 2 == n) mma_commit(bar_q_free);
           }
         }
       } else {
         for (int i = 0; ok && i < n; ++i, ++tiles) {
           const int t = t0 + i, g = kTurns ? i & 1 : 0, sb = kTurns ? g : tiles & 1;
-          const uint32_t this_v = base + place_v(i, n);
           if (!settle(kTurns ? g ^ 1 : 0)) break;
           if (i + 1 < n) {
-            const uint32_t next_k = base + place_k(i + 1, n);
-            if (!full_at(place_k(i + 1, n))) break;
+            if (!next_entry()) break;
             tc_fence_after();
-            scores(next_k, 0, sb ^ 1);
-            mma_commit(bar_empty + 8 * (next_k % R));
+            scores(slot, 0, sb ^ 1);
+            mma_commit(bar_empty + 8 * slot);
+            pass();
             if (i + 2 == n) mma_commit(bar_q_free);
           }
           if (t >= full_tiles) {  // one group: two barriers in turn
             if (!wait(bar_fix + 8 * (kTurns ? g : fixes[0] & 1), kTurns ? fixes[g] : fixes[0] >> 1)) break;
             ++fixes[g];
           }
-          if (!full_at(place_v(i, n)) || !wait(bar_p + 8 * sb, kTurns ? cnt[g] : tiles >> 1)) break;
+          if (!next_entry() || !wait(bar_p + 8 * sb, kTurns ? cnt[g] : tiles >> 1)) break;
           if (i == 0 && segs[0] > 0 && !wait(bar_o_free, segs[0] - 1)) break;
           tc_fence_after();
-          weigh(this_v, g, sb, keys_of(t), kTurns ? i > 1 : i > 0);
+          weigh(slot, g, sb, keys_of(t), kTurns ? i > 1 : i > 0);
           ++cnt[g];
-          mma_commit(bar_empty + 8 * (this_v % R));
+          mma_commit(bar_empty + 8 * slot);
+          pass();
         }
       }
-      base += 2 * n;
       for (int m = 0; m < tiles_m; ++m) ++segs[m];
     }
     if (!ok) {
