@@ -62,6 +62,15 @@ CASES = [
     ([3, 3], [333, 70], 8, 2, 192, 64, HF, dict(layout="joint", tree=True)),
     ([3, 3], [333, 470], 8, 2, 128, 64, BF, dict(layout="apart", tree=True)),
     ([70, 70], [333, 470], 4, 2, 128, 128, BF, dict(layout="hnd", tree=True)),
+    ([3], [200], 128, 1, 128, 16, BF, dict(tree=True)),
+    ([2, 2], [150, 64], 100, 1, 64, 16, HF, {}),
+    ([5], [300], 96, 2, 256, 16, BF, dict(tree=True)),
+    ([1024], [70], 1, 1, 16, 8, BF, {}),
+    ([500, 500], [0, 130], 2, 1, 64, 64, HF, dict(tree=True)),
+    ([i % 4 for i in range(450)], [7 * (i % 40) for i in range(450)], 4, 2, 64, 16, BF, dict(ragged=True, tree=True)),
+    ([3, 1], [5000, 9000], 8, 4, 128, 4096, BF, dict(ragged=True)),
+    ([7], [1], 5, 1, 104, 16, HF, dict(tree=True)),
+    ([130], [121], 1, 1, 128, 16, BF, dict(tree=True)),
     ([9] * 40, list(range(0, 400, 10)), 4, 2, 64, 8, BF, dict(tree=True)),
     ([2], [6000], 4, 1, 128, 160, BF, {}),
     ([20, 20], [300, 170], 30, 2, 192, 16, BF, dict(tree=True)),
