@@ -499,6 +499,9 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           for (int m = 0; m < 2; ++m) {
             if (m >= tiles_m || !wait(bar_p + 8 * m, cnt[m])) break;
             if (i == 0 && segs[m] > 0 && !wait(bar_o_free + 8 * m, segs[m] - 1)) break;
+            // one row tile: the second group may still be at its last segment, whose word in
+            // not_finite is the next segment's
+            if (i == 0 && tiles_m == 1 && segs[1] > 0 && !wait(bar_o_free + 8, segs[1] - 1)) break;
             tc_fence_after();
             weigh(this_v, m, m, keys_of(t), i > 0);
             ++cnt[m];

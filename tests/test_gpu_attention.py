@@ -122,6 +122,29 @@ def test_garbage_that_is_not_seen_does_not_enter(ssv):
         assert torch.equal(o.out[:, keep], want.out[:, keep])
 
 
+def test_values_that_are_not_finite_over_many_units_a_cta(ssv):
+    """Units of two row tiles and of one in turn, some with such a value that rows from 5 on see."""
+    rows = [40 if i % 3 == 0 else 3 + 30 * (i % 2) for i in range(1500)]
+    c = attention_case(9, rows, [i % 21 for i in range(1500)], 4, 1, 64, 16, BF, ragged=True)
+    args, kw = on_gpu(c)
+    want = ssv.tree_attention(*args, **kw).out
+    hit = torch.zeros(sum(rows), dtype=torch.bool)
+    at = []
+    for b, n in enumerate(rows):
+        if b % 5 in (0, 3) and n > 5:
+            r = int(c["offsets"][b])
+            at.append(r + 5)
+            hit[r + 5:r + n] = True
+    args[2][torch.tensor(at).cuda(), 0, 17] = float("inf")
+    for _ in range(5):
+        got = ssv.tree_attention(*args, **kw).out
+        torch.cuda.synchronize()
+        assert bool((got[hit.cuda(), :, 17] == float("inf")).all())
+        back = got.clone()
+        back[hit.cuda(), :, 17] = want[hit.cuda(), :, 17]
+        assert torch.equal(back, want)
+
+
 def test_nan_query_stays_in_its_row(ssv):
     c = attention_case(5, [3, 3], [50, 60], 4, 2, 64, 16, HF)
     want = check(ssv, c, HF)
