@@ -596,7 +596,7 @@ typedef struct {
   long long table_stride;
   int B, T, rows, Hq, Hkv, D, pages, page_size, table_width;
   spec_dtype_t dtype;  /* SPEC_BF16 or SPEC_F16 */
-  float scale;         /* of the scores, finite */
+  float scale;         /* of the scores; log2(e) of it finite */
 } spec_attention_t;
 
 /* Attention of a pass's rows over the cache and the pass itself.
@@ -620,6 +620,7 @@ typedef struct {
  * A context length outside [0, table_width * page_size] counts as the nearer
  * bound and sets SPEC_DEV_BAD_OFFSETS.  A page outside [0, pages) reads as
  * zeros and sets SPEC_DEV_BAD_PAGE.
+ * out and lse overlap nothing that is read.
  * The workspace need not be zeroed, and is not left zero. */
 size_t spec_tree_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
 
@@ -681,6 +682,7 @@ typedef struct {
  * not have SPEC_DEV_BAD_OFFSETS; neither writes anything.  Slots have to be distinct:
  * of one that occurs twice, what its token holds afterwards may come from
  * either row.
+ * k_new and v_new may not lie in the cache's own slots.
  * Limits: D a multiple of 8; strides multiples of 8; tensors on 16-byte boundaries;
  * pages * page_size below 2^31. */
 spec_status_t spec_commit_cache(const spec_commit_t* args, uint32_t* dev_status, void* stream);

@@ -220,7 +220,8 @@ spec_status_t spec_tree_attention(const spec_attention_t* args, uint32_t* dev_st
   if (!args) return SPEC_ERR_INVALID_ARG;
   const spec_attention_t& A = *args;
   if (A.B < 0 || A.T < 1 || A.rows < 0 || A.Hkv < 1 || A.Hq < 1 || A.Hq % A.Hkv || A.D < 1 || A.pages < 0 ||
-      A.page_size < 1 || A.table_width < 0 || (A.dtype != SPEC_BF16 && A.dtype != SPEC_F16) || !std::isfinite(A.scale))
+      A.page_size < 1 || A.table_width < 0 || (A.dtype != SPEC_BF16 && A.dtype != SPEC_F16) ||
+      !std::isfinite(A.scale * 1.4426950409f))
     return SPEC_ERR_INVALID_ARG;
   if (!A.row_offsets && (long long)A.B * A.T != A.rows) return SPEC_ERR_INVALID_ARG;
   if (A.D > 256 || A.D % 8 || A.page_size % 8 || A.T > kMaxPassRows || A.Hq / A.Hkv > ssv::kAttendMaxGroup ||

@@ -68,6 +68,7 @@ ATTN = dict(q=P, k_new=P, v_new=P, k_cache=P, v_cache=P, out=P, block_table=P, c
     (dict(D=264), UNSUPPORTED), (dict(page_size=0), INVALID), (dict(page_size=12), UNSUPPORTED),
     (dict(T=1025, rows=2050), UNSUPPORTED), (dict(table_width=-1), INVALID), (dict(table_stride=8), INVALID),
     (dict(dtype=0), INVALID), (dict(dtype=3), INVALID), (dict(scale=NAN), INVALID), (dict(scale=INF), INVALID),
+    (dict(scale=3e38), INVALID),
     (dict(pages=-1), INVALID), (dict(q=None), INVALID), (dict(k_new=None), INVALID), (dict(v_new=None), INVALID),
     (dict(k_cache=None), INVALID), (dict(v_cache=None), INVALID), (dict(out=None), INVALID),
     (dict(block_table=None), INVALID), (dict(context_lens=None), INVALID), (dict(q=ODD), INVALID),
