@@ -1,12 +1,15 @@
 // Attention of a pass's rows over a paged cache and the pass's own keys, on the
 // tensor cores.
 //
-//   s_n = scale q . k_n,  out = sum_n 2^(c s_n - m) v_n / sum_n 2^(c s_n - m),  c = scale log2(e)
+//   s_n = q . k_n,  out = sum_n 2^(c (s_n - m)) v_n / sum_n 2^(c (s_n - m)),  c = scale log2(e)
 //
 // over the cached tokens of the row's request and the rows of the pass that its
-// mask names.  One pass over the keys: m is a running maximum, and where it
-// grows by more than 2^8 the sums so far are rescaled (a smaller growth leaves
-// it behind the maximum, which changes no ratio).  Scores, sums and the result
+// mask names.  One pass over the keys: m is a running maximum, and where a weight
+// would pass 2^8 the sums so far are rescaled (a smaller growth leaves m behind the
+// maximum, which changes no ratio).  m is taken off the scores before they are
+// multiplied by c: one multiplication and addition, c s_n - c m, would round c m first and
+// scale all weights by 2 to the power of that error, which for scores from 2^26 on leaves
+// the weights' range (it took 1% less for 33 rows).  Scores, sums and the result
 // are fp32; the weights are rounded to the operands' 16-bit type for the
 // product with v.  The result is divided by the sum of the rounded weights, so
 // that a row which one key dominates loses nothing; lse takes the sum before rounding.
@@ -577,7 +580,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
       const bool live = tok < rows;
       const bool warp_live = quad * 32 < rows * L.group;
       const int i_row = row0 + tok;
-      float top = -INFINITY, total_w = 0.0f, exact_w = 0.0f;  // m / c; sums of the rounded weights and of the weights
+      float top = -INFINITY, total_w = 0.0f, exact_w = 0.0f;  // m; sums of the rounded weights and of the weights
       for (int i = kTurns ? g : 0; i < n; i += kTurns ? 2 : 1, ++cnt) {
         const bool opening = kTurns ? i < 2 : i == 0;
         const int t = w.t0 + i, sb = GROUPS == 1 ? cnt & 1 : g;
@@ -640,14 +643,12 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           const float grown = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
           const bool grow = live && grown > top && !((grown - top) * L.c <= 8.0f);
           if (grow) {
-            // by the rounded products that the weights are taken off, so that their rounding
-            // (of scores in the hundreds more than a weight's) cancels
-            fix = top == -INFINITY ? 0.0f : ex2(__fmul_rn(top, L.c) - __fmul_rn(grown, L.c));
+            fix = top == -INFINITY ? 0.0f : ex2((top - grown) * L.c);
             top = grown;
             total_w *= fix;
             exact_w *= fix;
           }
-          const float off = top == -INFINITY ? 0.0f : __fmul_rn(top, L.c);
+          const float off = top == -INFINITY ? 0.0f : top;
           const f32x2 c2 = f2(L.c, L.c), off2 = f2(-off, -off);
           f32x2 s0 = 0, s1 = 0, e0 = 0, e1 = 0;
 #pragma unroll 1
@@ -658,7 +659,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
             for (int j = 0; j < 64; j += 2) {
               const int u = j / 32;
               float a, b;
-              f2_split(f2_fma(f2(__uint_as_float(v[u][j % 32]), __uint_as_float(v[u][j % 32 + 1])), c2, off2), a, b);
+              f2_split(f2_mul(f2_add(f2(__uint_as_float(v[u][j % 32]), __uint_as_float(v[u][j % 32 + 1])), off2), c2), a, b);
               a = ex2(a);
               b = ex2(b);
               const uint32_t pair = El::pack(a, b);
@@ -760,8 +761,8 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
         if (lane == 0) mbar_arrive(bar_join);
         if (!wait(bar_join, seg)) break;
         const float4 other = row_stat[seg & 1][g ^ 1][r];
-        const float both = fmaxf(top, other.x), off = both == -INFINITY ? 0.0f : __fmul_rn(both, L.c);
-        const float f = ex2(__fmul_rn(top, L.c) - off), fo = ex2(__fmul_rn(other.x, L.c) - off);
+        const float both = fmaxf(top, other.x), off = both == -INFINITY ? 0.0f : both;
+        const float f = ex2((top - off) * L.c), fo = ex2((other.x - off) * L.c);
         total_w = total_w * f + other.y * fo;
         exact_w = exact_w * f + other.z * fo;
         top = both;
@@ -825,11 +826,10 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           __syncwarp();  // the loads are the whole warp's
         }
         if (live && (!kTurns || g == 0)) {
-          const float top2 = __fmul_rn(top, L.c);
           if (!whole)
-            L.stat[slot] = make_float4(top2, total_w, exact_w, 0.0f);
+            L.stat[slot] = make_float4(top, total_w, exact_w, 0.0f);
           else if (A.lse)
-            A.lse[out_row] = 0.69314718055994531f * (top2 + __log2f(exact_w));
+            A.lse[out_row] = 0.69314718055994531f * fmaf(top, L.c, __log2f(exact_w));
         }
         tc_fence_before();
       }
@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     float wt = 0.0f, z = 0.0f, e = 0.0f;
     if (i0 + lane < n) {
       const float4 st = L.stat[slot(i0 + lane)];
-      wt = ex2(st.x - off);
+      wt = ex2((st.x - off) * L.c);
       z = st.y * wt;
       e = st.z * wt;
     }
@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
 #pragma unroll
   for (int j = 0; j < PER; j += 2)
     if (lane * PER + j < A.D) *(uint32_t*)(to + j) = El::pack(acc[j] * inv, acc[j + 1] * inv);
-  if (A.lse && lane == 0) A.lse[out_row] = 0.69314718055994531f * (off + __log2f(exact));
+  if (A.lse && lane == 0) A.lse[out_row] = 0.69314718055994531f * fmaf(off, L.c, __log2f(exact));
 }
 
 }  // namespace ssv

@@ -342,3 +342,47 @@ def test_calls_at_once_on_streams_and_threads(ssv):
     torch.cuda.synchronize()
     for w, outs in zip(want, got):
         assert len(outs) == 20 and all(torch.equal(w, o) for o in outs)
+
+
+def two_kinds_of_keys(T, ctx, D, page, dtype, top, rest, value_top, value_rest):
+    """One request and head whose queries are 1 in component 0 and 0 elsewhere: the first cached key holds top
+    there, all others rest, and their values are value_top and value_rest throughout."""
+    c = attention_case(3, [T], [ctx], 1, 1, D, page, dtype, poison=False)
+    for k in ("q", "k_new", "k_cache"):
+        c[k].zero_()
+    c["q"][:, 0, 0] = 1.0
+    at = torch.arange(ctx)
+    ids, place = torch.from_numpy(c["table"])[0].long()[at // page], at % page
+    c["k_cache"][ids, place, 0, 0] = torch.where(at < 1, float(top), float(rest)).to(dtype)
+    c["k_new"][:, 0, 0] = float(rest)
+    c["v_cache"][ids, place] = torch.where(at[:, None, None] < 1, float(value_top), float(value_rest)).to(dtype)
+    c["v_new"].fill_(float(value_rest))
+    return c
+
+
+@pytest.mark.parametrize("dtype,exponents", [(BF, (8, 20, 27, 34, 60)), (HF, (8, 20, 26, 29))])
+@pytest.mark.parametrize("T,ctx,D", [(1, 300, 64), (2, 20000, 128), (130, 700, 128), (3, 500, 192)])
+def test_scores_of_any_size(ssv, dtype, exponents, T, ctx, D):
+    """Scores that fp32 holds exactly, of which the largest occurs several times and the next is
+    half of it: the result is those keys' mean, however large they are."""
+    for e in exponents:
+        for m in (1.0, 1.125, 1.375, 1.75):
+            c = two_kinds_of_keys(T, ctx, D, 16, dtype, 0.0, 0.0, 0.0, 1.0)
+            hi, lo = e // 2, e - e // 2
+            c["q"][:, 0, 0] = m * 2.0 ** hi
+            at = torch.arange(ctx)
+            ids, place = torch.from_numpy(c["table"])[0].long()[at // 16], at % 16
+            top = at % 97 == 5
+            c["k_cache"][ids, place, 0, 0] = torch.where(top, 1.25 * 2.0 ** lo, 1.25 * 2.0 ** (lo - 1)).to(dtype)
+            c["v_cache"][ids, place] = torch.where(top, (at % 7).float(), 100.0)[:, None, None].to(dtype)
+            args, kw = on_gpu(c)
+            o = ssv.tree_attention(*args, scale=1.0, want_lse=True, **kw)
+            torch.cuda.synchronize()
+            score = m * 1.25 * 2.0 ** e
+            w = np.where(top.numpy(), 1.0, np.exp(-score / 2))  # below 2^-126 from 2^8 on
+            want = float((w * np.where(top.numpy(), at.numpy() % 7, 100.0)).sum() / w.sum())
+            got = o.out.double().cpu().numpy()
+            # weights of one size round alike; the result's own rounding, sums in fp32
+            assert (np.abs(got - want) <= want * (torch.finfo(dtype).eps / 2 * 1.01 + 2.0 ** -18)).all(), (e, m, want)
+            lse = score + np.log(w.sum())
+            assert (np.abs(o.lse.double().cpu().numpy() - lse) <= 2.0 ** -16 + 2.0 ** -22 * lse).all(), (e, m)
