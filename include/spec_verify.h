@@ -610,8 +610,9 @@ typedef struct {
  * with the keys and values of head h / (Hq / Hkv).  A row that sees nothing,
  * or only scores of -inf, gets out = 0 and lse = -inf.  Keys and values that a
  * row does not see do not enter it, whatever they hold.  Scores and sums are
- * fp32; the weights exp(s - max) are rounded once to dtype for the product
- * with v.
+ * fp32; the weights exp(s - max) are rounded once for the product with v, to
+ * dtype's precision (in fp16 with 2^11 times their size: weights below 2^-25 of
+ * the largest are off by up to 2^-36 of it).
  *
  * Limits: D a multiple of 8, at most 256; Hq a multiple of Hkv, at most 128
  * times it; page_size a multiple of 8; T <= 1024; table_width * page_size below

@@ -1,12 +1,14 @@
 // Attention of a pass's rows over a paged cache and the pass's own keys, on the
 // tensor cores.
 //
-//   s_n = q . k_n,  out = sum_n 2^(c (s_n - m)) v_n / sum_n 2^(c (s_n - m)),  c = scale log2(e)
+//   s_n = q . k_n,  w_n = 2^(c (s_n - m) + h),  out = sum_n w_n v_n / sum_n w_n,  c = scale log2(e)
 //
 // over the cached tokens of the row's request and the rows of the pass that its
 // mask names.  One pass over the keys: m is a running maximum, and where a weight
-// would pass 2^8 the sums so far are rescaled (a smaller growth leaves m behind the
-// maximum, which changes no ratio).  m is taken off the scores before they are
+// would pass 2^(h + kLag) the sums so far are rescaled (a smaller growth leaves m behind
+// the maximum, which changes no ratio).  h is 0 in bf16; in fp16 it uses the range above 1, so that
+// weights keep all bits down to 2^-25 of the largest and are off by at most 2^-36 of it
+// below (with h = 0, a long context of keys of 2^-25 each was lost, or counted twice).  m is taken off the scores before they are
 // multiplied by c: one multiplication and addition, c s_n - c m, would round c m first and
 // scale all weights by 2 to the power of that error, which for scores from 2^26 on leaves
 // the weights' range (it took 1% less for 33 rows).  Scores, sums and the result
@@ -197,6 +199,14 @@ struct AttendWalk {
     }
     return false;
   }
+};
+
+// What a weight's exponent may lag by before the sums are rescaled, and what is added to it: together they
+// stay below fp16's largest exponent, 15, by what the exponential's argument rounds by.
+template <class E>
+struct AttendRange {
+  static constexpr bool kHalf = Elem<E>::kLow != 0xFF80FF80u;
+  static constexpr float kLag = kHalf ? 4.0f : 8.0f, kUp = kHalf ? 11.0f : 0.0f;
 };
 
 template <class E>
@@ -639,9 +649,9 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
                 for (int c = 0; c < 4; ++c)
                   mx[c] = fmaxf(mx[c], fmaxf(__uint_as_float(v[u][j + c]), __uint_as_float(v[u][j + c + 4])));
           }
-          // a larger maximum: the sums so far shrink, unless by less than 2^8
+          // a larger maximum: the sums so far shrink, unless by less than 2^kLag
           const float grown = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-          const bool grow = live && grown > top && !((grown - top) * L.c <= 8.0f);
+          const bool grow = live && grown > top && !((grown - top) * L.c <= AttendRange<E>::kLag);
           if (grow) {
             fix = top == -INFINITY ? 0.0f : ex2((top - grown) * L.c);
             top = grown;
@@ -659,7 +669,8 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
             for (int j = 0; j < 64; j += 2) {
               const int u = j / 32;
               float a, b;
-              f2_split(f2_mul(f2_add(f2(__uint_as_float(v[u][j % 32]), __uint_as_float(v[u][j % 32 + 1])), off2), c2), a, b);
+              const f32x2 d = f2_add(f2(__uint_as_float(v[u][j % 32]), __uint_as_float(v[u][j % 32 + 1])), off2);
+              f2_split(kBf16 ? f2_mul(d, c2) : f2_fma(d, c2, f2(AttendRange<E>::kUp, AttendRange<E>::kUp)), a, b);
               a = ex2(a);
               b = ex2(b);
               const uint32_t pair = El::pack(a, b);
@@ -829,7 +840,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
           if (!whole)
             L.stat[slot] = make_float4(top, total_w, exact_w, 0.0f);
           else if (A.lse)
-            A.lse[out_row] = 0.69314718055994531f * fmaf(top, L.c, __log2f(exact_w));
+            A.lse[out_row] = 0.69314718055994531f * fmaf(top, L.c, __log2f(exact_w) - AttendRange<E>::kUp);
         }
         tc_fence_before();
       }
@@ -919,7 +930,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
 #pragma unroll
   for (int j = 0; j < PER; j += 2)
     if (lane * PER + j < A.D) *(uint32_t*)(to + j) = El::pack(acc[j] * inv, acc[j + 1] * inv);
-  if (A.lse && lane == 0) A.lse[out_row] = 0.69314718055994531f * fmaf(off, L.c, __log2f(exact));
+  if (A.lse && lane == 0) A.lse[out_row] = 0.69314718055994531f * fmaf(off, L.c, __log2f(exact) - AttendRange<E>::kUp);
 }
 
 }  // namespace ssv

@@ -386,3 +386,29 @@ def test_scores_of_any_size(ssv, dtype, exponents, T, ctx, D):
             assert (np.abs(got - want) <= want * (torch.finfo(dtype).eps / 2 * 1.01 + 2.0 ** -18)).all(), (e, m, want)
             lse = score + np.log(w.sum())
             assert (np.abs(o.lse.double().cpu().numpy() - lse) <= 2.0 ** -16 + 2.0 ** -22 * lse).all(), (e, m)
+
+
+@pytest.mark.parametrize("gap", [16.5, 20.5, 24.5, 25.5, 28.25, 30.5])
+@pytest.mark.parametrize("T,D", [(1, 64), (130, 128), (1, 192)])
+def test_many_small_weights_in_fp16(ssv, gap, T, D):
+    """20000 keys of a weight 2^-gap of the largest one, which among fp16's steps of 2^-24 would be off by
+    up to half of itself or gone: weights are rounded at 2^11 times their size, so each is off by 2^-11 of
+    itself or, below the normal range, by 2^-36 of the largest one.  Enough requests that a
+    unit's keys meet in one CTA (over the same pages)."""
+    B, n_cached = 300, 20000
+    c = two_kinds_of_keys(T, n_cached, D, 64, HF, gap, 0.0, 0.0, 1.0)
+    scale = float(np.log(2.0))
+    args, kw = on_gpu(c)
+    for i in (0, 1, 2, 5, 6):
+        args[i] = args[i].repeat(B, *[1] * (args[i].dim() - 1))
+    o = ssv.tree_attention(*args, scale=scale, want_lse=True)
+    torch.cuda.synchronize()
+    n = n_cached + np.arange(T)[:, None, None]  # small weights, the pass's own keys among them
+    w = 2.0 ** -gap
+    want = n * w / (1.0 + n * w)
+    # the weights' rounding and the result's, and n sums in fp32; then what is below the normal ranges
+    tol = (2 * 2.0 ** -11 + n * 2.0 ** -24) * want + n * 2.0 ** -36 + 2.0 ** -25
+    off = np.abs(o.out.double().cpu().numpy() - want) / tol
+    assert off.max() <= 1.0, off.max()
+    lse = gap * np.log(2.0) + np.log1p(n[..., 0] * w)
+    assert (np.abs(o.lse.double().cpu().numpy() - lse) <= n[..., 0] * 2.0 ** -24 + 2.0 ** -22 * lse).all()
