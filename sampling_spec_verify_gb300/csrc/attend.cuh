@@ -785,6 +785,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
       const float inv = whole ? (total_w == 0.0f ? 0.0f : 1.0f / total_w) : 1.0f;
       f0 *= inv;
       f1 *= inv;
+      const bool none = whole && total_w == 0.0f;  // only scores of -inf: zeros, also where they met values of inf
       const bool odd = w.t1 > w.s.full && *(volatile int*)&not_finite[seg & 1] == (int)seg + 1;
       const long long row = w.s.r0 + i_row, out_row = row * A.Hq + kh * L.group + head;
       const size_t slot = ((size_t)cta * 2 + (opens ? 1 : 0)) * L.slot_rows + m * 128 + r;
@@ -821,6 +822,9 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
               }
             }
             if (whole) {
+              if (none)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] = 0.0f;
               E* to = (E*)A.out + out_row * A.D + d;
 #pragma unroll
               for (int j = 0; j < 32; j += 8)
@@ -924,12 +928,12 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
       for (int j = 0; j < PER; ++j) acc[j] = fmaf(part[j], wi, acc[j]);
     }
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float inv = 1.0f / sum;
   const long long out_row = (long long)(split.r0 + i_row) * A.Hq + kh * L.group + head;
   E* to = (E*)A.out + out_row * A.D + lane * PER;
 #pragma unroll
   for (int j = 0; j < PER; j += 2)
-    if (lane * PER + j < A.D) *(uint32_t*)(to + j) = El::pack(acc[j] * inv, acc[j + 1] * inv);
+    if (lane * PER + j < A.D) *(uint32_t*)(to + j) = sum == 0.0f ? 0u : El::pack(acc[j] * inv, acc[j + 1] * inv);
   if (A.lse && lane == 0) A.lse[out_row] = 0.69314718055994531f * fmaf(off, L.c, __log2f(exact) - AttendRange<E>::kUp);
 }
 

@@ -412,3 +412,15 @@ def test_many_small_weights_in_fp16(ssv, gap, T, D):
     assert off.max() <= 1.0, off.max()
     lse = gap * np.log(2.0) + np.log1p(n[..., 0] * w)
     assert (np.abs(o.lse.double().cpu().numpy() - lse) <= n[..., 0] * 2.0 ** -24 + 2.0 ** -22 * lse).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("T,ctx,D", [(1, 100, 64), (2, 30000, 128), (130, 300, 128), (3, 500, 192), (2, 9000, 256)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 1.0])
+def test_only_scores_of_minus_infinity(ssv, dtype, T, ctx, D, value):
+    """Such a row gets zeros and -inf, whatever the values hold."""
+    c = two_kinds_of_keys(T, ctx, D, 16, dtype, float("-inf"), float("-inf"), value, value)
+    args, kw = on_gpu(c)
+    o = ssv.tree_attention(*args, scale=1.0, want_lse=True, **kw)
+    torch.cuda.synchronize()
+    assert not o.out.any() and bool((o.lse == float("-inf")).all()) and int(o.status.item()) == 0
