@@ -358,7 +358,7 @@ __global__ void __launch_bounds__((AttendShape<DP, MT>::kThreads), 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         any = true;
-        if (page < 0 || page >= A.pages) page = L.beyond, bad = SPEC_DEV_BAD_PAGE;
+        if (lane < big + small && (page < 0 || page >= A.pages)) page = L.beyond, bad = SPEC_DEV_BAD_PAGE;
         mbar_expect(full, (uint32_t)(chunks * (big * L.box + (small + rows_new) * 8) * 128));
         auto of_lane = [&](int x, int from) { return (int)__reduce_or_sync(0xffffffffu, lane == from ? (uint32_t)x : 0u); };
         int pl = t * NK % A.page_size, pg = of_lane(page, 0);  // the place is stepped along

@@ -424,3 +424,14 @@ def test_only_scores_of_minus_infinity(ssv, dtype, T, ctx, D, value):
     o = ssv.tree_attention(*args, scale=1.0, want_lse=True, **kw)
     torch.cuda.synchronize()
     assert not o.out.any() and bool((o.lse == float("-inf")).all()) and int(o.status.item()) == 0
+
+
+@pytest.mark.parametrize("rows,Hq,Hkv,D", [([3], 2, 1, 64), ([40], 8, 2, 128), ([5], 2, 1, 192), ([2, 2], 2, 2, 80)])
+def test_no_cache_at_all_raises_nothing(ssv, rows, Hq, Hkv, D):
+    c = attention_case(8, rows, [0] * len(rows), Hq, Hkv, D, 16, BF)
+    args, kw = on_gpu(c)
+    want = ssv.tree_attention(*args, **kw)
+    args[3] = args[4] = torch.empty(0, 16, Hkv, D, dtype=BF, device="cuda")
+    args[5] = torch.empty(len(rows), 0, dtype=torch.int32, device="cuda")
+    o = ssv.tree_attention(*args, **kw)
+    assert torch.equal(o.out, want.out) and int(o.status.item()) == 0 and int(want.status.item()) == 0
