@@ -51,7 +51,7 @@ constexpr int kAdjustMaxHistory = (int)kCountMask;
 // Stages first, on 16-byte boundaries; a stage holds a slice and what its first vector is off one.
 __host__ __device__ inline size_t adjust_stage(int slice, int elem) { return (size_t)slice * elem + 16; }
 inline size_t adjust_smem(int slice, int elem, int biases, int rows) {
-  return kAdjustStages * adjust_stage(slice, elem) + (size_t)slice * 6 + (size_t)slice / 2 + 8 + (size_t)biases * 9 +
+  return kAdjustStages * adjust_stage(slice, elem) + (size_t)slice * 6 + (size_t)slice / 8 * 5 + 8 + (size_t)biases * 9 +
          (size_t)rows * 4 + 64;
 }
 
@@ -82,8 +82,9 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
   const int S = P.slice, tid = threadIdx.x, threads = blockDim.x;  // 256, or 512 for a long slice
   const size_t stage = adjust_stage(S, sizeof(E));
   uint32_t* counts = reinterpret_cast<uint32_t*>(raw + kAdjustStages * stage);  // [S]
-  uint32_t* touched = counts + S;                                               // [S / 32]
-  uint32_t* by_row = touched + S / 32;            // [S / 32] tokens whose count goes by the row
+  uint32_t* touched = counts + S;                 // [S / 32] tokens with a bias, then all whose logits change
+  uint32_t* seen = touched + S / 32;              // [S / 32] tokens of the history
+  uint32_t* by_row = seen + S / 32;               // [S / 32] tokens whose count goes by the row
   uint32_t* grammar[2] = {by_row + S / 32, by_row + S / 16 + 1};  // [S / 32 + 1] a row's bits, two rows in turn
   float* bias = reinterpret_cast<float*>(by_row + 3 * (S / 32) + 2);            // [biases]
   int32_t* bias_id = reinterpret_cast<int32_t*>(bias + A.biases);
@@ -153,14 +154,14 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
   const float inv_rep = 1.0f / rep;  // one rounding more than a division, and no code for it
   const float freq = A.frequency ? A.frequency[b] : 0.0f;
   const float pres = A.presence ? A.presence[b] : 0.0f;
-  for (int i = tid; i < S + S / 16; i += threads) counts[i] = 0;  // touched and by_row too
+  for (int i = tid; i < S + 3 * (S / 32); i += threads) counts[i] = 0;  // touched, seen and by_row too
   for (int i = tid; i < A.biases; i += threads) again[i] = 0;
   __syncthreads();
 
   uint32_t bad = 0;
-  auto mark = [&](int v) {  // most occurrences are of tokens that occurred before
+  auto mark = [&](uint32_t* in, int v) {  // most occurrences are of tokens that occurred before
     const uint32_t bit = 1u << (v & 31);
-    if (!(touched[v >> 5] & bit)) atomicOr(&touched[v >> 5], bit);
+    if (!(in[v >> 5] & bit)) atomicOr(&in[v >> 5], bit);
   };
   if (A.biases > 0) {
     // A token's first place in the list keeps its bias; those of later places are added
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
       if (t < -1 || t >= A.V) bad |= SPEC_DEV_BAD_TOKEN;
       if (t >= v0 && t < v1) {
         atomicMax(&counts[t - v0], (uint32_t)(A.biases - i) << kBiasShift);  // the first place is the largest
-        mark(t - v0);
+        mark(touched, t - v0);
       }
     }
     __syncthreads();
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
             atomicOr(&counts[t[u] - v0], kSeenPrompt);
           else
             atomicAdd(&counts[t[u] - v0], 1u);
-          mark(t[u] - v0);
+          mark(seen, t[u] - v0);
         }
       }
     }
@@ -221,8 +222,7 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
       drafted[j] = here ? t - v0 : -1;
       if (here) {
         atomicOr(&counts[t - v0], kDrafted);
-        mark(t - v0);
-        atomicOr(&by_row[(t - v0) >> 5], 1u << (t & 31));
+        mark(by_row, t - v0);
       }
     }
   }
@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
   // The touched tokens in their order, a word of the bitmap a thread.
   int n_list = 0;
   {
-    const uint32_t word = tid < S / 32 ? touched[tid] : 0u;
+    const uint32_t word = tid < S / 32 ? touched[tid] | seen[tid] | by_row[tid] : 0u;
+    if (tid < S / 32) touched[tid] = word;
     const int lane = tid & 31, wid = tid >> 5;
     int upto = __popc(word);
 #pragma unroll
@@ -270,28 +271,29 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
     if (own >= 0) own_word = counts[own];
   }
   __syncthreads();
-  // Counts that are the same for all rows become what they add, the last bit of its fraction
-  // (2^-23 of it) whether the repetition penalty goes before.
+  auto in = [](const uint32_t* bits, int v) { return ((bits[v >> 5] >> (v & 31)) & 1u) != 0; };
+  // The rule in two steps, each rounded as written, so that a token gives the same bits
+  // whether or not another row drafted it: what a word and c occurrences add to a logit,
+  // and the logit with the penalty and that.
+  auto added = [&](uint32_t w, uint32_t c) {
+    const int at = (int)((w & ~kSeenPrompt) >> kBiasShift);
+    const float add = at ? bias[A.biases - at] : 0.0f;
+    return c ? __fadd_rn(__fmaf_rn(-freq, (float)c, -pres), add) : add;
+  };
+  auto applied = [&](bool penalty, float add, float x) {
+    const float y = __fmul_rn(x, x > 0.0f ? inv_rep : rep);
+    return __fadd_rn(penalty ? y : x, add);
+  };
+  // Counts that are the same for all rows become what they add.
   for (int q = tid; q < n_list; q += threads) {
     const int v = list[q];
-    if ((by_row[v >> 5] >> (v & 31)) & 1u) continue;
-    const uint32_t w = counts[v], c = w & kCountMask;
-    const int at = (int)((w & ~kSeenPrompt) >> kBiasShift);
-    float add = at ? bias[A.biases - at] : 0.0f;
-    if (c) add = -freq * (float)c - pres + add;
-    counts[v] = (__float_as_uint(add) & ~1u) | (c || (w & kSeenPrompt) ? 1u : 0u);
+    if (in(by_row, v)) continue;
+    const uint32_t w = counts[v];
+    counts[v] = __float_as_uint(added(w, w & kCountMask));
   }
   __syncthreads();
-  auto short_rule = [&](uint32_t word, float x) {
-    const float y = x * (x > 0.0f ? inv_rep : rep);
-    return (word & 1u ? y : x) + __uint_as_float(word & ~1u);
-  };
   auto counted = [&](uint32_t w, uint32_t c, float x) {  // the whole rule, of c occurrences
-    if (c || (w & kSeenPrompt)) x *= x > 0.0f ? inv_rep : rep;
-    const int at = (int)((w & ~kSeenPrompt) >> kBiasShift);
-    float add = at ? bias[A.biases - at] : 0.0f;
-    if (c) add = -freq * (float)c - pres + add;
-    return x + add;
+    return applied(c || (w & kSeenPrompt), added(w, c), x);
   };
   auto rule = [&](int i, int v, float x) {  // row i, token v of the slice that goes by the row
     const uint32_t w = counts[v];
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
     return counted(w, c, x);
   };
   auto computed = [&](int i, int v, float x) {
-    return (by_row[v >> 5] >> (v & 31)) & 1u ? rule(i, v, x) : short_rule(counts[v], x);
+    return in(by_row, v) ? rule(i, v, x) : applied(in(seen, v), __uint_as_float(counts[v]), x);
   };
 
   // A row's bits of the slice are read while the row before it is at work, a word a thread.
@@ -323,14 +325,15 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
   }
   // A thread's first listed tokens stay in registers over the rows: token, what it adds.
   constexpr int kHold = 4;
-  int held_at[kHold];
-  uint32_t held[kHold];
+  int held_at[kHold];  // -1: none, -2: goes by the row
+  float held[kHold];
+  uint32_t held_seen = 0;  // a bit each
 #pragma unroll
   for (int u = 0; u < kHold; ++u) {
     const int q = tid + u * threads, v = q < n_list ? list[q] : -1;
-    const bool slow = v >= 0 && ((by_row[v >> 5] >> (v & 31)) & 1u);
-    held_at[u] = slow ? ~(v + 1) : v;  // below -1: goes by the row
-    held[u] = v >= 0 ? counts[v] : 0;
+    held_at[u] = v >= 0 && in(by_row, v) ? -2 : v;
+    held[u] = v >= 0 ? __uint_as_float(counts[v]) : 0.0f;
+    held_seen |= v >= 0 && in(seen, v) ? 1u << u : 0u;
   }
   auto read_edge = [&](int i) {
     const Row r = row_at(i);
@@ -350,8 +353,7 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
       const int v = q < r.lead ? q : q + r.vecs * PV;
       const E was = q == tid ? first : r.in[v];
       const bool keep = !allow || ((allow[v >> 5] >> (v & 31)) & 1u);
-      const bool hit = (touched[v >> 5] >> (v & 31)) & 1u;
-      r.out[v] = !keep ? El::neg_inf() : hit ? El::from_f32(computed(i, v, El::to_f32(was))) : was;
+      r.out[v] = !keep ? El::neg_inf() : in(touched, v) ? El::from_f32(computed(i, v, El::to_f32(was))) : was;
     }
     if (!r.vecs) {
       ok = ok && mbar_wait_short(bar0 + 8 * (i % kAdjustStages), (uint32_t)(i / kAdjustStages) & 1u, kAdjustWaitNs);
@@ -362,11 +364,10 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
       ok = mbar_wait_short(bar0 + 8 * (i % kAdjustStages), (uint32_t)(i / kAdjustStages) & 1u, kAdjustWaitNs);
       if (ok) {
 #pragma unroll
-        for (int u = 0; u < kHold; ++u)
-          if (held_at[u] >= from && held_at[u] < to) {
-            E* at = x + held_at[u];
-            *at = El::from_f32(short_rule(held[u], El::to_f32(*at)));
-          }
+        for (int u = 0; u < kHold; ++u) {
+          const int v = held_at[u];
+          if (v >= from && v < to) x[v] = El::from_f32(applied((held_seen >> u) & 1u, held[u], El::to_f32(x[v])));
+        }
         if (own >= from && own < to)
           x[own] = El::from_f32(counted(own_word, (own_word & kCountMask) + __popcll(sees[i] & own_rows), El::to_f32(x[own])));
         bool slow = false;
@@ -376,14 +377,13 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
 #pragma unroll 1
           for (int q = tid; q < min(n_list, kHold * threads); q += threads) {
             const int v = list[q];
-            if (((by_row[v >> 5] >> (v & 31)) & 1u) && v >= from && v < to) x[v] = El::from_f32(rule(i, v, El::to_f32(x[v])));
+            if (in(by_row, v) && v >= from && v < to) x[v] = El::from_f32(rule(i, v, El::to_f32(x[v])));
           }
         }
 #pragma unroll 1
         for (int q = tid + kHold * threads; q < n_list; q += threads) {
           const int v = list[q];
-          const bool goes = (by_row[v >> 5] >> (v & 31)) & 1u;
-          if (v >= from && v < to && !(goes && near)) x[v] = El::from_f32(computed(i, v, El::to_f32(x[v])));
+          if (v >= from && v < to && !(near && in(by_row, v))) x[v] = El::from_f32(computed(i, v, El::to_f32(x[v])));
         }
       }
       if (allow) {

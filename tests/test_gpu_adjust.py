@@ -177,3 +177,42 @@ def test_same_bits_in_a_graph_and_on_a_stream(ssv):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(o, eager)
+
+
+def bits_of(t):
+    return t.contiguous().view(torch.int32).cpu()
+
+
+def test_a_bias_alone_is_added_whole(ssv):
+    """z = 0: the result is the bias, to its last bit, in a long slice's list as in a short one."""
+    for V, n in ((50, 40), (20000, 1000), (3000, 1024)):
+        c = case(11, [1, 1], V, 1, F, prompts=False)
+        rng = np.random.default_rng(V)
+        c["z"].zero_()
+        word = rng.integers(0, 2 ** 32, size=(2, n), dtype=np.uint64).astype(np.uint32)
+        word[:, :6] = [1, 0x3DCCCCCD, 0x7F800001, 0x80000001, 0x7FC00001, 0xFF800000]
+        c.update(tokens=np.array([-1, -1]), lens=np.array([0, 0]), repetition=None, frequency=None, presence=None,
+                 bias_ids=np.stack([rng.permutation(V)[:n] for _ in range(2)]), bias=word.view(np.float32))
+        got, st = call(ssv, c, False)
+        got, want = bits_of(got).numpy().view(np.uint32), word
+        for b in range(2):
+            have = got[b][c["bias_ids"][b]]
+            nan = np.isnan(want[b].view(np.float32))
+            zero = want[b] == 0x80000000  # 0 + -0
+            assert (np.isnan(have.view(np.float32)) == nan).all()
+            assert (have == want[b])[~nan & ~zero].all() and st == 0
+
+
+def test_a_row_that_is_not_seen_changes_no_bit(ssv):
+    """Row 0 of a tree with and without a sibling, which it does not see, that drafts the tokens that have biases,
+    penalties and a place in the history."""
+    for V, rows in ((3000, 70), (5001, 9), (40000, 33)):
+        c = case(12, [rows, rows], V, 500, F, biases=200, tree=True)
+        c["mask"][:] = np.eye(rows, dtype=np.uint8)
+        rng = np.random.default_rng(rows)
+        c["tokens"] = np.where(rng.uniform(size=2 * rows) < 0.5, c["history"].ravel()[:2 * rows], c["bias_ids"].ravel()[:2 * rows])
+        alone = dict(c, tokens=c["tokens"].copy())
+        keep = [0, rows]
+        alone["tokens"][[i for i in range(2 * rows) if i not in keep]] = -1
+        got, want = call(ssv, c, False)[0], call(ssv, alone, False)[0]
+        assert torch.equal(bits_of(got)[keep], bits_of(want)[keep])
