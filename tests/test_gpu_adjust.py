@@ -216,3 +216,22 @@ def test_a_row_that_is_not_seen_changes_no_bit(ssv):
         alone["tokens"][[i for i in range(2 * rows) if i not in keep]] = -1
         got, want = call(ssv, c, False)[0], call(ssv, alone, False)[0]
         assert torch.equal(bits_of(got)[keep], bits_of(want)[keep])
+
+
+@pytest.mark.parametrize("rep", [1.1, 1.3, 3.0, 0.7, 7e-40, 3e38, 1e-42])
+def test_the_repetition_penalty_divides(ssv, rep):
+    """Bit by bit z / r above zero and z r elsewhere, for tokens of the history, drafted ones and those
+    in no vector."""
+    V = 1003
+    c = case(13, [2, 1], V, 900, F, T=2)
+    c = dict(c, repetition=np.full(2, rep, dtype=np.float32), frequency=None, presence=None)
+    c["z"].mul_(1e-3 if rep > 1e-30 else 1e-39)
+    got, st = call(ssv, c, True)
+    r = torch.tensor(rep, dtype=torch.float32)
+    for b, at in ((0, 0), (0, 1), (1, 2)):
+        seen = torch.zeros(V, dtype=torch.bool)
+        seen[torch.from_numpy(c["history"][b, :c["lens"][b]]).long()] = True
+        seen[torch.from_numpy(c["tokens"][c["offsets"][b]:at + 1]).long()] = True
+        z = c["z"][at]
+        want = torch.where(seen, torch.where(z > 0, z / r, z * r), z)
+        assert torch.equal(got[at].cpu(), want) and st == 0
