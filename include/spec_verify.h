@@ -649,7 +649,9 @@ spec_status_t spec_tree_attention(const spec_attention_t* args, uint32_t* dev_st
  * out_count [1], out_lens [B] int32 (written): the new count and lengths; not
  *   the inputs.
  * slots [B, T] int32 (written): page * page_size + place of the appended
- *   tokens, then -1.
+ *   tokens, then -1.  A page below 0, or one whose slot is beyond 2^31 - 1, gives its
+ *   tokens the slot 2^31 - 1, which no cache has (spec_commit_cache refuses it), and sets
+ *   SPEC_DEV_BAD_PAGE.
  * A request with context_lens or the new length outside [0, table_width *
  * page_size], or with new_lens > T, is left as it was and sets
  * SPEC_DEV_BAD_OFFSETS.  A free_count outside [0, capacity], or pages given

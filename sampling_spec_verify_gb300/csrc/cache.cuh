@@ -19,6 +19,7 @@ struct PlanParams {
 };
 
 constexpr int kPlanThreads = 256;
+constexpr int kNoSlot = 0x7FFFFFFF;  // beyond every cache: pages * page_size < 2^31
 
 // A request's pages before and after the step.
 struct PlanRequest {
@@ -139,15 +140,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
       for (int i = tid; i < needs; i += kPlanThreads) P.out_table[row + r.held + i] = stack_at(have - 1 - (nd + i));
     if (sound)
       for (int i = tid; i < r.back(); i += kPlanThreads) P.out_free[count + bk + i] = P.table[row + r.want + i];
+    bool no_slot = false;
     for (int i = tid; i < P.T; i += kPlanThreads) {
       int slot = -1;
       if (served && i < added) {
         const int pos = len + i, p = pos / P.page;
         const int page = p < r.held ? P.table[row + p] : stack_at(have - 1 - (nd + p - r.held));
-        slot = page * P.page + (pos - p * P.page);
+        // ids come from the caller: one that no cache has may wrap to another page's slot in 32 bits
+        const long long at = (long long)page * P.page + (pos - p * P.page);
+        const bool named = page >= 0 && at <= kNoSlot;
+        slot = named ? (int)at : kNoSlot;
+        no_slot |= !named;
       }
       P.slots[(long long)b * P.T + i] = slot;
     }
+    if (no_slot && P.status) atomicOr(P.status, SPEC_DEV_BAD_PAGE);
     if (tid == 0) {
       P.out_lens[b] = served ? len + added : len;
       const uint32_t bits = (!r.fits || !sound ? SPEC_DEV_BAD_OFFSETS : 0u) |

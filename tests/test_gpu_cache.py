@@ -160,3 +160,34 @@ def test_commit_skips_what_cannot_be(ssv):
                 if 0 <= slots[b][i] < 16 and 0 <= r0 <= r1 <= B * T and 0 <= row < r1 - r0:
                     want[slots[b][i]] = kn[r0 + row]
         assert torch.equal(kc.view(16, 2, D), want)
+
+
+def test_pages_that_no_slot_can_name(ssv):
+    """Ids below 0, or whose slots pass 2^31 - 1, in a table's last page and on the stack: the tokens get a
+    slot that a commit refuses, not one of another page (2^28 * 16 wraps to 0) and not -1."""
+    big = 2 ** 31 - 1
+    for page_id in (-1, -2 ** 31, 2 ** 28, 2 ** 28 + 1, 2 ** 27, big):
+        table = np.array([[3, page_id, -1], [5, -1, -1], [6, 7, -1]])
+        free = [9, page_id, -1, -1]
+        for in_place in (False, True):
+            # request 0 goes on in its last page, 1 takes the stack's top, 2 stays
+            o = run(ssv, [20, 14, 18], [2, 4, 0], table, free, 2, 16, 5, in_place)
+            assert int(o.status.item()) == ssv.DEV_BAD_PAGE
+            assert o.slots.tolist() == [[big, big, -1, -1, -1], [5 * 16 + 14, 5 * 16 + 15, big, big, -1], [-1] * 5]
+            assert o.context_lens.tolist() == [22, 18, 18] and o.free_count.item() == 1
+            assert o.block_table[1].tolist() == [5, page_id, -1]
+            kn, vn = (torch.randn(3, 5, 1, 8, device=DEV).bfloat16() for _ in range(2))
+            kc, vc = (torch.zeros(8, 16, 1, 8, device=DEV).bfloat16() for _ in range(2))
+            st = torch.zeros(1, dtype=torch.int32, device=DEV)
+            ssv.commit_cache(kn, vn, kc, vc, o.slots, status=st)
+            torch.cuda.synchronize()
+            assert st.item() == ssv.DEV_BAD_PAGE
+            want = torch.zeros_like(kc).view(128, 1, 8)
+            want[94:96] = kn[1, :2]
+            assert torch.equal(kc.view(128, 1, 8), want)
+    # the last slots that 32 bits hold
+    o = run(ssv, [14], [2], np.array([[2 ** 27 - 1]]), [-1], 0, 16, 2)
+    assert o.slots.tolist() == [[2 ** 31 - 2, 2 ** 31 - 1]] and int(o.status.item()) == 0
+    # given back, they name no slot
+    o = run(ssv, [20], [-10], np.array([[3, -5]]), [-1], 0, 16, 2)
+    assert o.free_pages.tolist() == [-5] and int(o.status.item()) == 0
