@@ -731,11 +731,12 @@ spec_status_t spec_adjust_logits(const spec_adjust_t* args, uint32_t* dev_status
 /* ------------------------------------------------------------------------ */
 /* Failure-path self-test of the bounded wait.
  *
- * Launches one warp that waits, with the same bounded mbarrier wait the
- * sweep uses on its bulk copies, for a phase of a fresh shared-memory
- * mbarrier that nothing ever completes.  No copy is in flight.  After
- * limit_ns nanoseconds of wall time the wait gives up, and the kernel ORs
- * SPEC_DEV_TIMEOUT into *dev_status and returns.  Tests use it to check that
+ * Launches two warps.  The second one waits, with the same bounded mbarrier
+ * wait the sweep uses on its bulk copies, for a phase of a fresh shared-memory
+ * mbarrier that nothing ever completes; the first one's wait ends at once.  No
+ * copy is in flight.  After limit_ns nanoseconds of wall time the wait gives
+ * up; the block's first thread learns of it as in the logit rules, ORs
+ * SPEC_DEV_TIMEOUT into *dev_status, and the kernel returns.  Tests use it to check that
  * a wait that runs out is reported on the status word and that the context
  * stays usable afterwards.
  * limit_ns   in [1, 10^10] (10 s).

@@ -1319,8 +1319,9 @@ def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor, history: torch.Ten
 def selftest_bounded_wait(limit_ns: int = 2_000_000, *, status: Optional[torch.Tensor] = None,
                           device="cuda", stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Failure-path self-test of the library's bounded wait (see
-    spec_selftest_bounded_wait in the C header): one warp waits on an
-    mbarrier that nothing completes and gives up after ``limit_ns``.  Returns
+    spec_selftest_bounded_wait in the C header): a warp waits on an
+    mbarrier that nothing completes and gives up after ``limit_ns``; a thread
+    of another warp reports it.  Returns
     the int32 status word, which holds DEV_TIMEOUT once the stream has run the
     test."""
     L = lib()

@@ -412,7 +412,8 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) adjust_kernel(const __grid_
       fence_proxy_async_smem();
     }
     if (allow && i + 1 < rows) keep_bits(i + 1);
-    if (!__syncthreads_and(ok)) break;
+    ok = block_waited(ok);
+    if (!ok) break;
     if (tid == 0) {
       if (r.vecs) {
         bulk_store(r.out + r.lead, stages0 + (uint32_t)(i % kAdjustStages * stage) + r.pad + r.lead * (uint32_t)sizeof(E),

@@ -111,6 +111,11 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// Whether the waits of all threads of the block ended in time.  All threads get the
+// same answer, so that the one that reports a wait that ran out, and waits for the copies in
+// flight, knows of any thread's.
+__device__ __forceinline__ bool block_waited(bool mine) { return __syncthreads_and(mine) != 0; }
+
 // ---- bulk copies --------------------------------------------------------------
 
 // L2 policy for data that is read exactly once.

@@ -288,3 +288,15 @@ def test_arguments(calls, call, o):
     with pytest.raises((ValueError, TypeError)):
         call(**o)
     assert calls.n == 0
+
+
+def test_the_rules_threads_share_their_verdict_on_a_wait():
+    """A wait that runs out in any thread ends the kernel's loop over rows, and thread 0 has to report
+    it and to wait for the copies in flight.  No GPU test can make one thread's wait run out
+    there, so this one reads the source: the loop ends by the block's answer, kept in the variable that
+    thread 0 asks behind it."""
+    text = open(os.path.join(os.path.dirname(ssv.__file__), "csrc", "adjust.cuh")).read()
+    loop = text[text.index("bool ok = true;\n  for (int i = 0; i < rows; ++i)"):]
+    assert "ok = block_waited(ok);\n    if (!ok) break;" in loop
+    assert "__syncthreads_and" not in text and loop.count("break;") == 1
+    assert "if (!ok) {\n      raise(P.status, SPEC_DEV_TIMEOUT);" in loop

@@ -80,3 +80,15 @@ def test_invalid_limits_are_refused(ssv):
             ssv.selftest_bounded_wait(bad, status=st)
     torch.cuda.synchronize()
     assert int(st.item()) == 0
+
+
+def test_a_wait_of_another_warp_than_the_reporting_one_is_reported(ssv):
+    """The self-test's first warp, whose thread 0 reports, waits on a phase that is complete: what it reports
+    is the second warp's wait, which it knows of by the block's common answer."""
+    for limit in (1000, 500_000):
+        st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        for _ in range(20):
+            st.zero_()
+            ssv.selftest_bounded_wait(limit, status=st)
+            assert int(st.item()) == ssv.DEV_TIMEOUT
+    _small_verify_matches_oracle(ssv)
