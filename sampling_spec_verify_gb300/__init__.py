@@ -1119,6 +1119,8 @@ def tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_
         empties = [(q_shape, dt), (q_shape[:-1], torch.float32)] if want_lse else [(q_shape, dt)]
     else:
         _need(out.out, "out.out", dtype=dt, shape=q.shape, device=dev)
+        if want_lse and out.lse is None:
+            raise ValueError("want_lse: out.lse is missing")
         _need_out(out.lse, "lse", torch.float32, q.shape[:-1], dev)
         _need_out(out.status, "status", torch.int32, (1,), dev)
     if workspace is not None:

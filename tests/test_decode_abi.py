@@ -300,3 +300,13 @@ def test_the_rules_threads_share_their_verdict_on_a_wait():
     assert "ok = block_waited(ok);\n    if (!ok) break;" in loop
     assert "__syncthreads_and" not in text and loop.count("break;") == 1
     assert "if (!ok) {\n      raise(P.status, SPEC_DEV_TIMEOUT);" in loop
+
+
+def test_lse_that_has_no_place_is_refused(calls):
+    out = lambda lse: ssv.AttentionOutput(Fake(2, 3, 4, 64, dtype=H), lse, Fake(1))  # noqa: E731
+    with pytest.raises(ValueError, match="lse"):
+        attn(out=out(None), want_lse=True)
+    assert calls.n == 0
+    attn(out=out(Fake(2, 3, 4, dtype=torch.float32)), want_lse=True)
+    attn(out=out(None))
+    assert calls.n == 2
