@@ -725,7 +725,7 @@ typedef struct {
  * prompt lengths beyond the history count as the nearer bound and set
  * SPEC_DEV_BAD_OFFSETS.  Rows that nothing is allowed for become -inf
  * throughout.
- * Limits: T <= 1024, biases <= 1024, history_width < 2^19, V <= 2^24. */
+ * Limits: B <= 65535, T <= 1024, biases <= 1024, history_width < 2^19, V <= 2^24. */
 spec_status_t spec_adjust_logits(const spec_adjust_t* args, uint32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------ */

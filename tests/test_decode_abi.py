@@ -310,3 +310,10 @@ def test_lse_that_has_no_place_is_refused(calls):
     attn(out=out(Fake(2, 3, 4, dtype=torch.float32)), want_lse=True)
     attn(out=out(None))
     assert calls.n == 2
+
+
+def test_adjust_refuses_more_than_65535_requests(L):
+    a = struct(ADJUST_T, ADJUST, dict(B=65536, T=1, rows=65536))
+    assert L.spec_adjust_logits(ctypes.byref(a), None, None) == UNSUPPORTED
+    text = open(os.path.join(os.path.dirname(ssv.__file__), "..", "include", "spec_verify.h")).read()
+    assert "B <= 65535" in text.split("Sampling rules on the logits")[1].split("spec_adjust_logits(")[0]
