@@ -38,11 +38,6 @@ __device__ __forceinline__ PlanRequest plan_request(const PlanParams& P, int len
   return r;
 }
 
-// Sums of the pages given back and needed; both below 2^31 for tables that exist.
-struct PlanSums {
-  long long back, need;
-};
-
 // Request by request: pages given back go on the stack at count + (those of the
 // requests before it), pages needed come from count + (all given back) - 1 -
 // (those needed before it).  Every CTA sums the whole batch's lengths for
@@ -50,6 +45,8 @@ struct PlanSums {
 // requests, so that one launch does without a pass over the batch before it;
 // no CTA writes what another one reads, also in place: tables keep the entries
 // of pages given back, and pushes lie above the stack's old top.
+// Sums of pages are 32 bits: a request gives back or needs at most a row of the table, and
+// the host refuses tables of 2^31 entries.
 // Bound: latency at ordinary sizes (8 requests 4.5 us), else the copy of table and stack
 // (1024 requests with 2048 pages each, 34 MB: 17 us), which a call in place leaves out.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) {
