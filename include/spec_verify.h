@@ -614,6 +614,10 @@ typedef struct {
  * dtype's precision (in fp16 with 2^11 times their size: weights below 2^-25 of
  * the largest are off by up to 2^-36 of it).
  *
+ * No gradients.  T decides how the work is laid out: beyond 128 / (Hq / Hkv)
+ * (rounded down) requests of few rows take up to a third longer, so that a batch of
+ * single tokens and a few large trees is better off in two calls.
+ *
  * Limits: D a multiple of 8, at most 256; Hq a multiple of Hkv, at most 128
  * times it; page_size a multiple of 8; T <= 1024; table_width * page_size below
  * 2^31; strides multiples of 8 and below 2^39; tensors on 16-byte boundaries,
@@ -720,6 +724,7 @@ typedef struct {
  *   z += the biases listed for v, less frequency * c(v) + presence where c(v) > 0
  *   z  = -inf                                      where v is not allowed
  * in fp32 (the biases added up in their order), rounded once to dtype.  Untouched logits are copied bit by bit.
+ * No gradients.
  * Tokens, history and bias ids outside [0, V) count for nothing and set
  * SPEC_DEV_BAD_TOKEN (-1 as a row's token or a bias id does not); history or
  * prompt lengths beyond the history count as the nearer bound and set

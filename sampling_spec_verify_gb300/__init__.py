@@ -1088,7 +1088,8 @@ def tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_
     int32 [B, width]; context_lens int32 [B]; mask uint8 [B, T, T] (``tree_mask``
     of the rows' parent map; None: a chain).  ``scale`` is 1 / sqrt(D) unless
     given.  Only the last dimension has to be contiguous; the others lie
-    multiples of 8 elements apart."""
+    multiples of 8 elements apart.  The result carries no gradient, whatever the
+    arguments require."""
     L = lib()
     ragged = row_offsets is not None
     _need_strided(q, "q", dims=3 if ragged else 4)
@@ -1266,7 +1267,7 @@ def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor, history: torch.Ten
     and presence float32 [B]; bias_ids int32 [B, n] and bias float32 [B, n];
     allowed int32 [B, T, ceil(V / 32)] bits; mask uint8 [B, T, T] (a tree; None: a
     chain).  ``out`` may be ``logits`` (in place); ``status`` is an optional int32
-    [1] device word."""
+    [1] device word.  The result carries no gradient, whatever the arguments require."""
     L = lib()
     ragged = row_offsets is not None
     _need(logits, "logits")

@@ -12,10 +12,10 @@
 // touched tokens listed; then each row's listed tokens are computed in its stage, a
 // lane per token, and a grammar's bits applied to whole vectors.  Bound: memory, the
 // logits in and out, as long as there is little to compute (128 x 8 x 129280 in bf16 without
-// rules 91 us, 5.8 TB/s); with a grammar, 4000 tokens of history and 300 biases 152 us, by
-// instructions and barriers.  The form that passes logits through registers and computes
-// touched ones in between took 157 us there and a quarter longer for 16 trees of 17 x 50257
-// (78 us against 63), where the touched tokens lie close together.
+// rules 90 us, 5.9 TB/s); with a grammar, 4000 tokens of history and 300 biases 152 us, by the
+// barriers between lanes per token and vectors (0.43 of the issue slots).  The form that passes
+// logits through registers and computes touched ones in between took 157 us there and 78 us
+// for 16 trees of 17 x 50257 (69 so), where the touched tokens lie close together.
 #pragma once
 
 #include <type_traits>

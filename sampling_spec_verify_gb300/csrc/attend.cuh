@@ -5,16 +5,22 @@
 //
 // over the cached tokens of the row's request and the rows of the pass that its
 // mask names.  One pass over the keys: m is a running maximum, and where a weight
-// would pass 2^(h + kLag) the sums so far are rescaled (a smaller growth leaves m behind
-// the maximum, which changes no ratio).  h is 0 in bf16; in fp16 it uses the range above 1, so that
-// weights keep all bits down to 2^-25 of the largest and are off by at most 2^-36 of it
-// below (with h = 0, a long context of keys of 2^-25 each was lost, or counted twice).  m is taken off the scores before they are
-// multiplied by c: one multiplication and addition, c s_n - c m, would round c m first and
-// scale all weights by 2 to the power of that error, which for scores from 2^26 on leaves
-// the weights' range (it took 1% less for 33 rows).  Scores, sums and the result
-// are fp32; the weights are rounded to the operands' 16-bit type for the
-// product with v.  The result is divided by the sum of the rounded weights, so
-// that a row which one key dominates loses nothing; lse takes the sum before rounding.
+// would pass 2^(h + kLag) the sums so far are rescaled (a smaller growth leaves m
+// behind the maximum, which changes no ratio).
+//
+// m is taken off the scores before they are multiplied by c.  c s_n - c m in one
+// multiplication and addition would round c m first and scale all weights by 2 to the
+// power of that error, which for scores from 2^26 on leaves the weights' range (it took 1%
+// less for 33 rows).
+//
+// Scores, sums and the result are fp32.  The weights are rounded once to the operands'
+// 16-bit type, which the tensor cores ask for both factors of the product with v: the
+// result is off its 64-bit value by 2.3e-3 of its size in bf16 where rounding it alone
+// would be 1.7e-3 (1.7e-4 and 1.5e-4 in fp16).  h is 0 in bf16; in fp16 it is 11,
+// so that weights keep all bits down to 2^-25 of the largest and are off by at most 2^-36 of
+// it below (with h = 0, the keys of a long context with 2^-25 each were lost, or
+// counted twice).  The result is divided by the sum of the rounded weights, so that a row
+// which one key dominates loses nothing; lse takes the sum before rounding.
 //
 // All query rows that share a key head (the pass's rows times the group's
 // heads) form tiles of 128 rows, so that the cache is read once for all of
@@ -35,11 +41,12 @@
 // thread per row.
 //
 // Measured with heads of 128 in bf16: 128 requests of one token over 64 to 4096 cached
-// ones (32/8 heads, pages of 16) 186 us, 5.9 TB/s; 2 x 8 rows over 131072 (64/8 heads)
-// 173 us, 6.2 TB/s; 32 trees of 33 rows over 512 to 8192 (132 query rows a key head: two
-// row tiles) 162 us, where the cache alone would take 89: there a product of scores takes
-// 64 cycles, both its operands in shared memory, and each row tile's next scores wait
-// for its last product.
+// ones (32/8 heads, pages of 16) 187 us, 5.8 TB/s; 2 x 8 rows over 131072 (64/8 heads)
+// 169 us, 6.4 TB/s; 32 trees of 33 rows over 512 to 8192 (132 query rows a key head: two
+// row tiles) 153 us, where the cache alone would take 89.  With two row tiles a group has
+// one buffer of scores, so that a tile's scores, softmax and product follow each other and
+// the tensor cores work 45% of the time; their products, of 256 rows of which 132 are live, would
+// take 76 us at the measured rate.
 #pragma once
 
 #include "loss_common.cuh"

@@ -47,8 +47,8 @@ __device__ __forceinline__ PlanRequest plan_request(const PlanParams& P, int len
 // of pages given back, and pushes lie above the stack's old top.
 // Sums of pages are 32 bits: a request gives back or needs at most a row of the table, and
 // the host refuses tables of 2^31 entries.
-// Bound: latency at ordinary sizes (8 requests 4.5 us), else the copy of table and stack
-// (1024 requests with 2048 pages each, 34 MB: 17 us), which a call in place leaves out.
+// Bound: latency at ordinary sizes (8 requests 4.8 us), else the copy of table and stack
+// (1024 requests with 2048 pages each, 34 MB: 15 us warm, 18 cold), which a call in place leaves out.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) {
   __shared__ int back_at[kPlanThreads + 1];  // given back before each thread's requests
   __shared__ int need_at[kPlanThreads + 1];

@@ -67,7 +67,10 @@ struct AttendPlan {
 };
 // Rows of 128 query rows and two such tiles a CTA where a request's pass may have
 // more of them (one tile: the cache would be read again for the second).  A head
-// beyond 128 fills the tensor memory with one tile.
+// beyond 128 fills the tensor memory with one tile.  T, the most rows of a request, decides for
+// the whole batch, whose lengths only the device knows: units of one row tile then leave the second
+// group idle (128 single tokens over 64 to 4096 cached ones, 32/8 heads: 200 us in
+// a graph for T = 1, 255 for T = 33, 263 with one request of 33 rows among them).
 AttendPlan attend_plan(int T, int group, int D, void* base) {
   AttendPlan p = {};
   p.dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
